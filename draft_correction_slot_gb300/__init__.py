@@ -64,7 +64,38 @@ EXPORTED = ("dcoco_version", "dcoco_status_string", "dcoco_create", "dcoco_weigh
             "dcoco_selftest_wait_timeout",
             "dcoco_weights_destroy", "dcoco_destroy", "dcoco_kernel_launches",
             "dcoco_stage_timing", "dcoco_stage_read", "dcoco_stage_name", "dcoco_topk_noalloc",
-            "dcoco_topk_noalloc_plan", "dcoco_verify_stochastic", "dcoco_host_range_covers")
+            "dcoco_topk_noalloc_plan", "dcoco_verify_stochastic", "dcoco_host_range_covers",
+            "dcoco_tree_create", "dcoco_tree_attention", "dcoco_tree_commit", "dcoco_tree_status",
+            "dcoco_tree_launches", "dcoco_tree_destroy", "dcoco_sample", "dcoco_distill_loss",
+            "dcoco_distill_grad", "dcoco_distill_step")
+
+DCOCO_BF16, DCOCO_FP16, DCOCO_FP32 = 0, 1, 2
+_DTYPE = {torch.bfloat16: DCOCO_BF16, torch.float16: DCOCO_FP16, torch.float32: DCOCO_FP32}
+
+
+class dcoco_tree_config(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("max_batch", "max_tree", "q_heads", "kv_heads", "head_dim", "page_size",
+                                       "max_pages", "dtype")]
+
+
+def _strided(name, *axes):
+    return [(name, C.c_void_p)] + [(f"{name}_stride_{a}", C.c_int64) for a in axes]
+
+
+class dcoco_tree_attention_args(C.Structure):
+    _fields_ = (_strided("q", "n", "t", "h") + _strided("k_new", "n", "t", "h") + _strided("v_new", "n", "t", "h")
+                + _strided("k_cache", "page", "token", "h") + _strided("v_cache", "page", "token", "h")
+                + [("page_table", C.c_void_p), ("page_table_stride", C.c_int64), ("ctx_len", C.c_void_p),
+                   ("tree_len", C.c_void_p), ("tree_mask", C.c_void_p), ("tree_mask_stride_n", C.c_int64),
+                   ("num_pages", C.c_int), ("scale", C.c_float)])
+
+
+class dcoco_tree_commit_args(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("tokens", "parents", "sampled", "tree_len", "ctx_len", "page_table")]
+                + [("page_table_stride", C.c_int64)]
+                + _strided("k_new", "l", "n", "t", "h") + _strided("v_new", "l", "n", "t", "h")
+                + _strided("k_cache", "l", "page", "token", "h") + _strided("v_cache", "l", "page", "token", "h")
+                + [("num_pages", C.c_int), ("layers", C.c_int)])
 
 
 def _load():
@@ -103,6 +134,20 @@ def _load():
                                    C.POINTER(C.c_int)]
     L.dcoco_stage_name.argtypes = [C.c_void_p, C.c_int]
     L.dcoco_stage_name.restype = C.c_char_p
+    P, I, I64, F = C.c_void_p, C.c_int, C.c_int64, C.c_float
+    L.dcoco_tree_create.argtypes = [C.POINTER(dcoco_tree_config), C.POINTER(P)]
+    L.dcoco_tree_attention.argtypes = [P, I, I, C.POINTER(dcoco_tree_attention_args), P, P, P]
+    L.dcoco_tree_commit.argtypes = [P, I, I, C.POINTER(dcoco_tree_commit_args), P, P, P, P, P]
+    L.dcoco_tree_status.argtypes = [P]
+    L.dcoco_tree_launches.argtypes = [P]
+    L.dcoco_tree_launches.restype = C.c_longlong
+    L.dcoco_tree_destroy.argtypes = [P]
+    L.dcoco_tree_destroy.restype = None
+    L.dcoco_sample.argtypes = [I, I, P, I, I64, P, P, P, P, P, P, P, P]
+    teacher = [I, I, P, I, I64, I, P, P, P, F]
+    L.dcoco_distill_loss.argtypes = teacher + [P, P, P]
+    L.dcoco_distill_grad.argtypes = teacher + [P, P, P, I64, P]
+    L.dcoco_distill_step.argtypes = teacher + [P, P, P, P, I64, P]
     return L
 
 
@@ -289,6 +334,252 @@ def dcoco_stage_read(handle) -> tuple[dict, int]:
 def dcoco_stage_name(handle, s: int) -> str | None:
     r = _lib.dcoco_stage_name(handle, s)
     return None if r is None else r.decode()
+
+
+# ------------------------------------------------------------------ the target's side of a drafted block
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dense(t, name: str, shape: tuple, dtype, none_ok: bool = False):
+    """A contiguous CUDA tensor of that shape and type (or None): its pointer."""
+    if t is None:
+        _need(none_ok, f"{name} is required")
+        return None
+    _need(t.dtype == dtype and t.is_cuda and t.shape == shape and t.is_contiguous(),
+          f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _heads(t, name: str, shape: tuple, dtype):
+    """A CUDA tensor whose last axis (a head's elements) is dense: (pointer, the other axes' strides)."""
+    _need(t.dtype == dtype and t.is_cuda and t.shape == shape, f"{name} must be a CUDA {dtype} tensor of shape {shape}")
+    st = t.stride()
+    _need(st[-1] == 1, f"the elements of a head must be dense in {name}")
+    # the stride of an axis of one element says nothing: any value addresses it
+    return (t.data_ptr(), *(0 if n == 1 else x for n, x in zip(shape[:-1], st)))
+
+
+class _TreeHandle(C.c_void_p):
+    """A dcoco_tree_handle and the sizes it was made for."""
+    sizes: tuple = ()
+
+
+def dcoco_tree_create(max_batch: int, max_tree: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
+                      max_pages: int, dtype: torch.dtype = torch.bfloat16) -> _TreeHandle:
+    """Handle of the tree calls for one attention layout; see include/dcoco.h."""
+    cfg = dcoco_tree_config(max_batch, max_tree, q_heads, kv_heads, head_dim, page_size, max_pages,
+                            _DTYPE.get(dtype, -1))
+    h = _TreeHandle()
+    _check(_lib.dcoco_tree_create(C.byref(cfg), C.byref(h)), "dcoco_tree_create")
+    h.sizes = (q_heads, kv_heads, head_dim, page_size, max_pages, dtype)
+    return h
+
+
+def _page_table(page_table, batch: int, max_pages: int):
+    _need(page_table.dtype == torch.int32 and page_table.is_cuda and page_table.dim() == 2
+          and page_table.shape[0] == batch and page_table.shape[1] >= max_pages and page_table.stride(1) == 1,
+          f"page_table must be a CUDA int32 tensor of shape ({batch}, >= {max_pages}) with dense rows")
+    return page_table.data_ptr(), (page_table.stride(0) if batch > 1 else max(page_table.stride(0), max_pages))
+
+
+def dcoco_tree_attention(handle, batch: int, q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, *, out,
+                         tree_mask=None, tree_len=None, lse=None, scale: float | None = None, stream=None) -> None:
+    """Attention of batch trees of q.shape[1] nodes over a paged cache and the trees themselves.
+
+    q [batch, nodes, q_heads, D], k_new and v_new [batch, nodes, kv_heads, D], k_cache and v_cache
+    [pages, page_size, kv_heads, D] may be views (the last axis dense, strides multiples of 8);
+    page_table [batch, max_pages], ctx_len and tree_len [batch] int32; tree_mask int32 words
+    [batch or 1, nodes, ceil(nodes / 32)] (tree_mask() makes them from parents; None: causal);
+    out [batch, nodes, q_heads, D] and lse fp32 [batch, nodes, q_heads] are written.  scale: 1/sqrt(D)."""
+    hq, hkv, d, page, max_pages, dt = handle.sizes
+    nodes, pages = q.shape[1], k_cache.shape[0]
+    new, pool = (batch, nodes, hkv, d), (pages, page, hkv, d)
+    mask_ptr, mask_stride = None, 0
+    if tree_mask is not None:
+        words = (nodes + 31) // 32
+        n = batch if tree_mask.dim() == 3 and tree_mask.shape[0] == batch else 1
+        mask_ptr = _dense(tree_mask, "tree_mask", (n, nodes, words), torch.int32)
+        mask_stride = nodes * words if n == batch else 0
+    args = dcoco_tree_attention_args(
+        *_heads(q, "q", (batch, nodes, hq, d), dt), *_heads(k_new, "k_new", new, dt),
+        *_heads(v_new, "v_new", new, dt), *_heads(k_cache, "k_cache", pool, dt),
+        *_heads(v_cache, "v_cache", pool, dt), *_page_table(page_table, batch, max_pages),
+        _dense(ctx_len, "ctx_len", (batch,), torch.int32), _dense(tree_len, "tree_len", (batch,), torch.int32, True),
+        mask_ptr, mask_stride, pages, d ** -0.5 if scale is None else scale)
+    _check(_lib.dcoco_tree_attention(handle, batch, nodes, C.byref(args), _dense(out, "out", (batch, nodes, hq, d), dt),
+                                     _dense(lse, "lse", (batch, nodes, hq), torch.float32, True), _stream(stream)),
+           "dcoco_tree_attention")
+
+
+def dcoco_tree_commit(handle, batch: int, tokens, parents, sampled, k_new, v_new, k_cache, v_cache, page_table,
+                      ctx_len, *, path, accept_len, next_token, new_len, tree_len=None, stream=None) -> None:
+    """Walk each tree along the target's tokens and append the path's K/V to the cache of every layer.
+
+    tokens, parents, sampled and path int32 [batch, nodes]; k_new and v_new [layers, batch, nodes, kv_heads, D],
+    k_cache and v_cache [layers, pages, page_size, kv_heads, D]; the others int32 [batch]."""
+    _, hkv, d, page, max_pages, dt = handle.sizes
+    nodes, layers, pages = tokens.shape[1], k_cache.shape[0], k_cache.shape[1]
+    i32, tree, one = torch.int32, (batch, nodes), (batch,)
+    new, pool = (layers, batch, nodes, hkv, d), (layers, pages, page, hkv, d)
+    args = dcoco_tree_commit_args(
+        _dense(tokens, "tokens", tree, i32), _dense(parents, "parents", tree, i32),
+        _dense(sampled, "sampled", tree, i32), _dense(tree_len, "tree_len", one, i32, True),
+        _dense(ctx_len, "ctx_len", one, i32), *_page_table(page_table, batch, max_pages),
+        *_heads(k_new, "k_new", new, dt), *_heads(v_new, "v_new", new, dt),
+        *_heads(k_cache, "k_cache", pool, dt), *_heads(v_cache, "v_cache", pool, dt), pages, layers)
+    _check(_lib.dcoco_tree_commit(handle, batch, nodes, C.byref(args), _dense(path, "path", tree, i32),
+                                  _dense(accept_len, "accept_len", one, i32),
+                                  _dense(next_token, "next_token", one, i32), _dense(new_len, "new_len", one, i32),
+                                  _stream(stream)), "dcoco_tree_commit")
+
+
+def dcoco_tree_status(handle) -> int:
+    return _lib.dcoco_tree_status(handle)
+
+
+def dcoco_tree_launches(handle) -> int:
+    return int(_lib.dcoco_tree_launches(handle))
+
+
+def dcoco_tree_destroy(handle) -> None:
+    _lib.dcoco_tree_destroy(handle)
+
+
+def _logit_rows(logits, name: str = "logits"):
+    """[rows, vocab] with dense rows: (rows, vocab, pointer, dtype code, row stride)."""
+    _need(logits.dim() == 2 and logits.is_cuda and logits.dtype in (torch.bfloat16, torch.float32)
+          and logits.stride(1) == 1, f"{name} must be a CUDA bf16 or fp32 [rows, vocab] tensor with dense rows")
+    rows, vocab = logits.shape
+    stride = logits.stride(0) if rows > 1 else max(logits.stride(0), (vocab + 7) // 8 * 8)
+    return rows, vocab, logits.data_ptr(), _DTYPE[logits.dtype], stride
+
+
+def dcoco_sample(logits, u, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
+                 stream=None) -> None:
+    """One token per row of logits [rows, vocab] (bf16 or fp32, row stride a multiple of 8), from uniforms u
+    [rows]; temperature, top_p, min_p fp32 and top_k int32 [rows] or None; tokens int32, logprob fp32 [rows]."""
+    rows, vocab, ptr, dt, stride = _logit_rows(logits)
+    one, f32 = (rows,), torch.float32
+    _check(_lib.dcoco_sample(rows, vocab, ptr, dt, stride, _dense(temperature, "temperature", one, f32, True),
+                             _dense(top_k, "top_k", one, torch.int32, True), _dense(top_p, "top_p", one, f32, True),
+                             _dense(min_p, "min_p", one, f32, True), _dense(u, "u", one, f32),
+                             _dense(tokens, "tokens", one, torch.int32), _dense(logprob, "logprob", one, f32, True),
+                             _stream(stream)), "dcoco_sample")
+
+
+def _teacher(logits, teacher_ids, teacher_logits, teacher_lse, temperature):
+    rows, vocab, ptr, dt, stride = _logit_rows(logits)
+    _need(teacher_ids.dim() == 2, "teacher_ids must be [rows, topk]")
+    k, f32 = teacher_ids.shape[1], torch.float32
+    return (rows, vocab, ptr, dt, stride, k, _dense(teacher_ids, "teacher_ids", (rows, k), torch.int32),
+            _dense(teacher_logits, "teacher_logits", (rows, k), f32),
+            _dense(teacher_lse, "teacher_lse", (rows,), f32, True), float(temperature))
+
+
+def _grad_rows(grad, logits):
+    _need(grad.shape == logits.shape and grad.dtype == logits.dtype, "grad must have the logits' shape and type")
+    rows = _logit_rows(grad, "grad")
+    return rows[2], rows[4]
+
+
+def dcoco_distill_loss(logits, teacher_ids, teacher_logits, *, loss, lse, teacher_lse=None, temperature: float = 1.0,
+                       stream=None) -> None:
+    """Per-row distillation loss (and the log-sum-exp that the gradient needs) of logits [rows, vocab] against
+    the teacher's top logits: teacher_ids int32, teacher_logits fp32 [rows, topk]; see include/dcoco.h."""
+    t = _teacher(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    one = (t[0],)
+    _check(_lib.dcoco_distill_loss(*t, _dense(loss, "loss", one, torch.float32), _dense(lse, "lse", one, torch.float32),
+                                   _stream(stream)), "dcoco_distill_loss")
+
+
+def dcoco_distill_grad(logits, teacher_ids, teacher_logits, lse, grad_loss, *, grad, teacher_lse=None,
+                       temperature: float = 1.0, stream=None) -> None:
+    """Gradient with respect to the logits, times grad_loss [rows], from the loss call's lse.  grad has the
+    logits' shape and type and may be the logits themselves; hand it on with logits.backward(grad)."""
+    t = _teacher(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    one = (t[0],)
+    _check(_lib.dcoco_distill_grad(*t, _dense(lse, "lse", one, torch.float32),
+                                   _dense(grad_loss, "grad_loss", one, torch.float32), *_grad_rows(grad, logits),
+                                   _stream(stream)), "dcoco_distill_grad")
+
+
+def dcoco_distill_step(logits, teacher_ids, teacher_logits, grad_loss, *, loss, lse, grad, teacher_lse=None,
+                       temperature: float = 1.0, stream=None) -> None:
+    """Loss and gradient in one pass over the logits (the rows' grad_loss known beforehand, e.g. 1 / rows)."""
+    t = _teacher(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    one, f32 = (t[0],), torch.float32
+    _check(_lib.dcoco_distill_step(*t, _dense(grad_loss, "grad_loss", one, f32), _dense(loss, "loss", one, f32),
+                                   _dense(lse, "lse", one, f32), *_grad_rows(grad, logits), _stream(stream)),
+           "dcoco_distill_step")
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """Mask words of trees given by parents [batch, nodes] (-1: a root): node t sees its ancestors and itself."""
+    n, t = parents.shape
+    up = parents.long()
+    words = (t + 31) // 32
+    sees = torch.zeros(n, t, words * 32, dtype=torch.bool, device=parents.device)
+    sees[:, :, :t] = torch.eye(t, dtype=torch.bool, device=parents.device)
+    for i in range(1, t):  # a parent's row is complete before its children's
+        row = sees.gather(1, up[:, i].clamp(min=0).view(n, 1, 1).expand(n, 1, words * 32))[:, 0]
+        sees[:, i] |= row & (up[:, i] >= 0)[:, None]
+    bits = (sees.view(n, t, words, 32).long() << torch.arange(32, device=parents.device)).sum(-1)
+    return torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(torch.int32)
+
+
+class TreeVerifier:
+    """Owns a tree handle; allocates output tensors per call.  One step of the target on a drafted tree:
+    attention() in every layer, sample() on the nodes' logits, commit() for all layers at once."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, max_pages: int, max_batch: int = 32,
+                 max_tree: int = 64, dtype: torch.dtype = torch.bfloat16):
+        self.handle = dcoco_tree_create(max_batch, max_tree, q_heads, kv_heads, head_dim, page_size, max_pages, dtype)
+
+    def close(self):
+        if getattr(self, "handle", None) is not None:
+            dcoco_tree_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def attention(self, q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, tree_mask=None, tree_len=None,
+                  scale=None, stream=None):
+        """-> (out [N, T, q_heads, D], lse [N, T, q_heads])"""
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        dcoco_tree_attention(self.handle, q.shape[0], q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, out=out,
+                             tree_mask=tree_mask, tree_len=tree_len, lse=lse, scale=scale, stream=stream)
+        return out, lse
+
+    def sample(self, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+        """logits [N, T, V] -> (tokens [N, T] int32, logprob [N, T]); u and the parameters [N, T] (or None)."""
+        n, t, v = logits.shape
+        flat = [None if x is None else x.reshape(n * t) for x in (temperature, top_k, top_p, min_p)]
+        tokens = torch.empty(n, t, dtype=torch.int32, device=logits.device)
+        logprob = torch.empty(n, t, dtype=torch.float32, device=logits.device)
+        dcoco_sample(logits.view(n * t, v), u.reshape(n * t), tokens.view(n * t), temperature=flat[0], top_k=flat[1],
+                     top_p=flat[2], min_p=flat[3], logprob=logprob.view(n * t), stream=stream)
+        return tokens, logprob
+
+    def commit(self, tokens, parents, sampled, k_new, v_new, k_cache, v_cache, page_table, ctx_len, tree_len=None,
+               stream=None):
+        """-> dict(path [N, T], accept_len [N], next_token [N], new_len [N]); the caches are written."""
+        n, t = tokens.shape
+        out = {"path": torch.empty(n, t, dtype=torch.int32, device=tokens.device)}
+        for name in ("accept_len", "next_token", "new_len"):
+            out[name] = torch.empty(n, dtype=torch.int32, device=tokens.device)
+        dcoco_tree_commit(self.handle, n, tokens, parents, sampled, k_new, v_new, k_cache, v_cache, page_table, ctx_len,
+                          tree_len=tree_len, stream=stream, **out)
+        return out
+
+    def status(self) -> int:
+        return dcoco_tree_status(self.handle)
 
 
 # ------------------------------------------------------------------ convenience wrapper

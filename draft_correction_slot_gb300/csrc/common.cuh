@@ -13,6 +13,8 @@ namespace dc {
 enum : int {
   kErrBadCandidateId = 1,   // a gathered token id was outside [0, V)
   kErrTimeout = 2,          // a bounded wait inside a kernel expired
+  kErrBadLength = 4,        // a context or tree length was out of range
+  kErrBadPage = 8,          // a page number was outside the pool, or a position past the page table
 };
 
 // ---- bf16 bit helpers ------------------------------------------------------

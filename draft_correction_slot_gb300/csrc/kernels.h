@@ -193,6 +193,73 @@ cudaError_t launch_verify_stochastic(const uint16_t *target, int64_t stride, int
                                      unsigned *req_count, int32_t *accept_len, int32_t *next_token,
                                      cudaStream_t st);
 
+// ---------------------------------------------------------------- tree attention
+// Strides in elements; see dcoco_tree_attention.  `group` query heads a K/V
+// head; rows of a K/V head are packed t * group + j.
+struct TreeAttnParams {
+  const uint16_t *q, *k_new, *v_new, *k_cache, *v_cache;
+  int64_t q_sn, q_st, q_sh, kn_sn, kn_st, kn_sh, vn_sn, vn_st, vn_sh;
+  int64_t kc_sp, kc_st, kc_sh, vc_sp, vc_st, vc_sh;
+  const int32_t *page_table;
+  int64_t pt_stride;
+  const int32_t *ctx_len, *tree_len, *tree_mask;  // tree_len, tree_mask: or null
+  int64_t mask_sn;
+  int num_pages, max_pages, page_shift;
+  int N, T, kv_heads, group, head_dim;
+  bool f16;
+  float scale;
+  uint16_t *out;  // [N][T][kv_heads * group][head_dim]
+  float *lse;     // [N][T][kv_heads * group] or null
+  int *err;
+};
+cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t st);
+
+// ---------------------------------------------------------------- tree commit
+struct TreeCommitParams {
+  const int32_t *tokens, *parents, *sampled, *tree_len, *ctx_len, *page_table;
+  int64_t pt_stride;
+  const uint16_t *k_new, *v_new;
+  uint16_t *k_cache, *v_cache;
+  int64_t kn_sl, kn_sn, kn_st, kn_sh, vn_sl, vn_sn, vn_st, vn_sh;
+  int64_t kc_sl, kc_sp, kc_st, kc_sh, vc_sl, vc_sp, vc_st, vc_sh;
+  int num_pages, max_pages, page_shift, layers;
+  int N, T, kv_heads, head_dim;
+  int32_t *path, *accept_len, *next_token, *new_len;
+  int *err;
+};
+cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t st);
+
+// ---------------------------------------------------------------- sampling
+// See dcoco_sample.  `f32`: fp32 logits, else bf16.
+struct SampleParams {
+  const void *logits;
+  int64_t stride;
+  int rows, V;
+  const float *temperature;
+  const int32_t *top_k;
+  const float *top_p, *min_p, *u;
+  int32_t *tokens;
+  float *logprob;
+};
+cudaError_t launch_sample(const SampleParams &p, bool f32, cudaStream_t st);
+
+// ---------------------------------------------------------------- distillation
+// See dcoco_distill_loss / _grad / _step.  grad null: the loss alone; loss
+// null: the gradient alone, from lse; both: one pass.
+struct DistillParams {
+  const void *logits;
+  int64_t stride;
+  int rows, V, K;
+  const int32_t *ids;
+  const float *teacher, *teacher_lse;
+  float temperature;
+  const float *grad_loss;
+  float *loss, *lse;
+  void *grad;
+  int64_t grad_stride;
+};
+cudaError_t launch_distill(const DistillParams &p, bool f32, cudaStream_t st);
+
 // One CTA waits (tc::mbar_wait, limit_ns) on an mbarrier nothing completes:
 // the wait expires and ORs kErrTimeout into *err.
 cudaError_t launch_wait_timeout(unsigned long long limit_ns, int *err, cudaStream_t st);

@@ -316,6 +316,197 @@ const char *dcoco_stage_name(const dcoco_handle *h, int s);
 void dcoco_weights_destroy(dcoco_weights *w);
 void dcoco_destroy(dcoco_handle *h);
 
+/* ====================================================================
+ * The target's side of a drafted block: attention of a drafted tree over a
+ * paged K/V cache, the target's tokens, the commit of the accepted path, and
+ * the loss that trains the drafter on the target's top logits.
+ *
+ * A drafted tree of T nodes per request: node 0 is the anchor (the last
+ * committed token, whose K/V is not in the cache yet), every node t > 0 has a
+ * parent among the nodes before it.  A chain of draft slots is the tree with
+ * parent t - 1; single-token decoding is T = 1.  The conventions above hold
+ * (status codes, streams, ownership, determinism, no dependence on the batch).
+ * ==================================================================== */
+
+/* Element types of the calls below. */
+#define DCOCO_BF16 0
+#define DCOCO_FP16 1
+#define DCOCO_FP32 2
+
+typedef struct dcoco_tree_handle dcoco_tree_handle; /* sizes + device workspace */
+
+typedef struct {
+  int max_batch; /* largest batch of any call, 1..4096                         */
+  int max_tree;  /* most nodes of a tree, 1..256                               */
+  int q_heads;   /* query heads, a multiple of kv_heads, <= 1024; q_heads / kv_heads <= 128 */
+  int kv_heads;  /* K/V heads, >= 1                                            */
+  int head_dim;  /* 64 or 128                                                  */
+  int page_size; /* tokens of a cache page, a power of two, 16..1024           */
+  int max_pages; /* page-table entries of a request, >= 1; max_pages * page_size
+                    is the longest context, at most 2^30                       */
+  int dtype;     /* DCOCO_BF16 or DCOCO_FP16: q, K, V and the outputs          */
+} dcoco_tree_config;
+
+/* Inputs of dcoco_tree_attention (device pointers).  The head_dim elements of
+ * a head are contiguous; every other stride is given, in elements: positive, a
+ * multiple of 8 and below 2^39 (any value where the axis has one entry); bases
+ * are 16-byte aligned. */
+typedef struct {
+  const void *q; /* [n][t][head] */
+  int64_t q_stride_n, q_stride_t, q_stride_h;
+  const void *k_new; /* K of the tree's nodes, [n][t][kv head] */
+  int64_t k_new_stride_n, k_new_stride_t, k_new_stride_h;
+  const void *v_new;
+  int64_t v_new_stride_n, v_new_stride_t, v_new_stride_h;
+  const void *k_cache; /* [page][token][kv head], any order of strides */
+  int64_t k_cache_stride_page, k_cache_stride_token, k_cache_stride_h;
+  const void *v_cache;
+  int64_t v_cache_stride_page, v_cache_stride_token, v_cache_stride_h;
+  const int32_t *page_table; /* [n][max_pages]: token c of request n is row c % page_size
+                                of page page_table[n][c / page_size]; entries past the
+                                context are not read */
+  int64_t page_table_stride; /* entries between requests, >= max_pages */
+  const int32_t *ctx_len;    /* [n] committed tokens, 0..max_pages * page_size */
+  const int32_t *tree_len;   /* [n] nodes of each tree, 0..nodes; NULL: all have `nodes` */
+  const int32_t *tree_mask;  /* [n][t][ceil(nodes / 32)] words: bit j % 32 of word j / 32 set:
+                                node t sees node j.  NULL: node t sees nodes 0..t */
+  int64_t tree_mask_stride_n; /* words between requests; 0: one mask for all */
+  int num_pages;             /* pages of the cache pool */
+  float scale;               /* of q.k, finite (1 / sqrt(head_dim)) */
+} dcoco_tree_attention_args;
+
+/* Validate `cfg` and allocate the workspace on the current device.  Errors:
+ * EINVAL, EUNSUPPORTED (head_dim, dtype, group or page size outside the set
+ * above), ENOMEM, ECUDA.  Validation happens before any CUDA call. */
+int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out);
+
+/* Attention of `batch` trees of up to `nodes` nodes:
+ *   out[n][t][h] = sum_j e^{s_j} v_j / sum_j e^{s_j},  s_j = scale q.k_j,
+ * over the whole context of request n and the nodes j < tree_len[n] that the
+ * mask shows to node t; query head h reads K/V head h / (q_heads / kv_heads).
+ * K/V of tokens that a node does not see never reach its output, whatever
+ * they hold (infinities and NaN included).  A node that sees nothing, and a
+ * node t >= tree_len[n], gets out = 0 and lse = -inf.
+ *   out: [batch][nodes][q_heads][head_dim], dense, the handle's dtype.
+ *   lse: fp32 [batch][nodes][q_heads], natural log of the sum; NULL = not wanted.
+ * Scores, sums and the running output are fp32; the weights e^{s - m} are
+ * rounded to the dtype before they meet V.  Never allocates, never
+ * synchronises.  batch == 0 or nodes == 0 is a no-op.  Errors: EINVAL (null or
+ * misaligned pointer, bad stride, num_pages < 1, nodes outside
+ * [0, max_tree], scale not finite), EBATCH, ECUDA.  Lengths and page numbers
+ * are device data: one out of range is clamped, never followed out of the
+ * buffers, and recorded in the handle's status word (that request's output
+ * then has no meaning). */
+int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_attention_args *in,
+                         void *out, float *lse, void *stream);
+
+/* Inputs of dcoco_tree_commit (device pointers; strides as above). */
+typedef struct {
+  const int32_t *tokens;   /* [n][nodes] the nodes' tokens (node 0: the anchor) */
+  const int32_t *parents;  /* [n][nodes] parent node, less than the node; -1 at node 0 */
+  const int32_t *sampled;  /* [n][nodes] the target's token after each node */
+  const int32_t *tree_len; /* [n] or NULL, as above */
+  const int32_t *ctx_len;  /* [n] */
+  const int32_t *page_table;
+  int64_t page_table_stride;
+  const void *k_new; /* [layer][n][t][kv head] */
+  int64_t k_new_stride_l, k_new_stride_n, k_new_stride_t, k_new_stride_h;
+  const void *v_new;
+  int64_t v_new_stride_l, v_new_stride_n, v_new_stride_t, v_new_stride_h;
+  void *k_cache; /* [layer][page][token][kv head] */
+  int64_t k_cache_stride_l, k_cache_stride_page, k_cache_stride_token, k_cache_stride_h;
+  void *v_cache;
+  int64_t v_cache_stride_l, v_cache_stride_page, v_cache_stride_token, v_cache_stride_h;
+  int num_pages;
+  int layers;
+} dcoco_tree_commit_args;
+
+/* Accept the path the target agrees with, and append its K/V to the cache.
+ * From node 0 on, the walk goes to the lowest child whose token is the
+ * target's token after the current node, as long as there is one.
+ *   path: int32 [batch][nodes], the nodes of the path (node 0 first), then -1
+ *   accept_len: int32 [batch], accepted draft tokens (the path without node 0)
+ *   next_token: int32 [batch], the target's token after the path's last node
+ *   new_len: int32 [batch], ctx_len + accept_len + 1
+ * K/V of the path's nodes go to cache positions ctx_len .. new_len - 1 of
+ * every layer.  A request with tree_len 0 commits nothing (accept_len 0,
+ * next_token -1, new_len = ctx_len).  No page may belong to two requests.
+ * A position past the page table, or a page outside [0, num_pages), is not
+ * written and is recorded in the status word.  Outputs and inputs do not
+ * overlap (new_len == ctx_len: EINVAL).  One launch for all layers.  Errors: as
+ * dcoco_tree_attention; layers outside 1..65535: EINVAL. */
+int dcoco_tree_commit(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_commit_args *in,
+                      int32_t *path, int32_t *accept_len, int32_t *next_token, int32_t *new_len, void *stream);
+
+/* As dcoco_get_device_status, for a tree handle: DCOCO_EDEVICE if a kernel
+ * recorded a length or page out of range or a bounded wait that expired since
+ * the last call. */
+int dcoco_tree_status(dcoco_tree_handle *h);
+
+/* Kernels launched by this handle since it was created; -1 for NULL. */
+long long dcoco_tree_launches(const dcoco_tree_handle *h);
+
+/* NULL is allowed.  Synchronises the device before freeing. */
+void dcoco_tree_destroy(dcoco_tree_handle *h);
+
+/* One token per row from the target's logits, with random numbers that the
+ * caller draws.  logits: [rows][row_stride] of dtype DCOCO_BF16 or DCOCO_FP32,
+ * the first `vocab` of each row; 16-byte aligned, row_stride >= vocab a
+ * multiple of 8.  Per row (device arrays of `rows` entries; NULL = off):
+ *   temperature t (NULL: 1): z_v = (x_v - max x) / t.  t <= 0: the token of
+ *     the largest logit (lowest id), logprob 0; the filters do not matter.
+ *   top_k k: the k best tokens stay (value descending, id ascending); k <= 0: all.
+ *   top_p p: of those, in that order, a token stays if the mass (e^z) of the
+ *     tokens before it is less than p times the mass of all of them; p >= 1:
+ *     all stay; p <= 0: the best one.
+ *   min_p q: of those, the tokens with e^z >= q stay; q <= 0: all; q > 1: as 1.
+ *   u, required, in [0, 1): the token is the smallest id whose cumulative mass
+ *     of kept tokens, in id order, exceeds u times the kept mass.
+ * tokens: int32 [rows].  logprob: fp32 [rows], log of the token's share of the
+ * kept mass; NULL = not wanted.  A logit of NaN counts as -inf; -inf has no
+ * mass; +inf takes the whole mass (shared by all +inf).  A row with nothing
+ * above -inf gives token -1 and logprob -inf.  A NaN parameter counts as off
+ * (u: as 0).
+ * The order and the sums do not depend on rows or timing.  One launch, no
+ * workspace.  rows == 0 is a no-op.  Errors: EINVAL (null or misaligned
+ * pointers, vocab outside 1..2^20, stride, dtype, rows < 0), ECUDA. */
+int dcoco_sample(int rows, int vocab, const void *logits, int dtype, int64_t row_stride,
+                 const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                 const float *u, int32_t *tokens, float *logprob, void *stream);
+
+/* Distillation of the drafter from the target's top logits.  Per row r:
+ *   p_k = e^{t_k / T} / sum_j e^{t_j / T}       (teacher_lse NULL), or
+ *   p_k = e^{t_k / T - teacher_lse[r]}          (the teacher's log-sum-exp of
+ *         its logits / T over the whole vocabulary: sum p may be below 1)
+ *   q = softmax(x / T) over the vocabulary
+ *   loss = T^2 sum_k p_k (log p_k - log q_{id_k})
+ *   d loss / d x_v = T ((sum p) q_v - sum_{k: id_k = v} p_k)
+ * logits: [rows][row_stride], DCOCO_BF16 or DCOCO_FP32, 16-byte aligned,
+ * row_stride >= vocab a multiple of 8.  teacher_ids int32 [rows][topk] in
+ * [0, vocab); another id (-1) is padding and left out; teacher_logits fp32
+ * [rows][topk].  Terms with p_k = 0 count as 0; a row of padding alone has
+ * loss 0 and gradient 0.  topk 1..1024; temperature > 0, finite.  A row's
+ * logits are finite or -inf with a finite maximum.
+ *   loss, lse: fp32 [rows]; lse is the log-sum-exp of x / T, for _grad.
+ *   grad_loss: fp32 [rows], the gradient of each row's loss.
+ *   grad: [rows][grad_stride], the logits' dtype; the first `vocab` of each
+ *     row are written (grad_stride >= vocab a multiple of 8); may be `logits`
+ *     itself (same stride).  A row whose grad_loss is 0 gets zeros.
+ * _step does _loss and _grad in one pass over the logits.  Sums are fp32;
+ * outputs do not depend on rows or timing.  One launch each, no workspace.
+ * rows == 0 is a no-op.  Errors: EINVAL, ECUDA. */
+int dcoco_distill_loss(int rows, int vocab, const void *logits, int dtype, int64_t row_stride, int topk,
+                       const int32_t *teacher_ids, const float *teacher_logits, const float *teacher_lse,
+                       float temperature, float *loss, float *lse, void *stream);
+int dcoco_distill_grad(int rows, int vocab, const void *logits, int dtype, int64_t row_stride, int topk,
+                       const int32_t *teacher_ids, const float *teacher_logits, const float *teacher_lse,
+                       float temperature, const float *lse, const float *grad_loss, void *grad,
+                       int64_t grad_stride, void *stream);
+int dcoco_distill_step(int rows, int vocab, const void *logits, int dtype, int64_t row_stride, int topk,
+                       const int32_t *teacher_ids, const float *teacher_logits, const float *teacher_lse,
+                       float temperature, const float *grad_loss, float *loss, float *lse, void *grad,
+                       int64_t grad_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
