@@ -211,7 +211,31 @@ struct TreeAttnParams {
   uint16_t *out;  // [N][T][kv_heads * group][head_dim]
   float *lse;     // [N][T][kv_heads * group] or null
   int *err;
+  // rows of a K/V head in tiles of tile_nodes nodes (tile_rows = tile_nodes *
+  // group <= 128 rows); tree_box: nodes of a K/V copy
+  int mtiles, tile_nodes, tile_rows, tree_box;
+  // chunks (see tree_chunk_tiles): (request, head, row tile) items of a full
+  // batch, SMs, the largest chunk, the most chunks of a request
+  int items, sms, chunk_cap, max_chunks;
+  float4 *part_o;   // [item][max_chunks][head_dim / 4][tile_rows]
+  float2 *part_ml;  // [item][max_chunks][tile_rows] (log2 reference, sum)
+  int *counts;      // [item], zero between calls
 };
+constexpr int kTreeTile = 128;  // tokens of a K/V tile
+struct TreeAttnMaps {
+  CUtensorMap q, k_new, v_new, k_cache, v_cache;
+};
+// Tiles of a chunk for a request of nt tiles: as few as spread a full batch
+// of such requests over the SMs, at most `cap` (so that requests of unlike
+// lengths balance), and at least nt / kTreeMaxChunks.
+constexpr int kTreeMaxChunks = 64;
+__host__ __device__ inline int tree_chunk_tiles(int nt, int items, int sms, int cap) {
+  const long long want = ((long long)nt * items + sms - 1) / sms;
+  int c = want < cap ? (int)want : cap;
+  const int least = (nt + kTreeMaxChunks - 1) / kTreeMaxChunks;
+  if (c < least) c = least;
+  return c < 1 ? 1 : c;
+}
 cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t st);
 
 // ---------------------------------------------------------------- tree commit

@@ -13,8 +13,13 @@
 struct dcoco_tree_handle {
   dcoco_tree_config cfg;
   int device = 0;
-  int page_shift = 0;
-  int *err = nullptr;  // device status word
+  int page_shift = 0, sms = 1;
+  int chunk_cap = 1, max_chunks = 1;  // see TreeAttnParams
+  void *block = nullptr;              // one device allocation: status word, counters, partial results
+  size_t counts_bytes = 0;
+  int *err = nullptr, *counts = nullptr;
+  float2 *part_ml = nullptr;
+  float4 *part_o = nullptr;
   cudaStream_t last_stream = nullptr;
   long long launches = 0;
 };
@@ -46,6 +51,17 @@ int validate_tree_config(const dcoco_tree_config *c) {
   return DCOCO_OK;
 }
 
+// Rows of a K/V head (nodes x group) in tiles of at most 128, whole nodes each.
+struct RowTiles {
+  int tile_nodes, tile_rows, mtiles;
+  RowTiles(const dcoco_tree_config &c, int nodes) {
+    const int group = c.q_heads / c.kv_heads, most = 128 / group;
+    tile_nodes = nodes < most ? nodes : most;
+    tile_rows = tile_nodes * group;
+    mtiles = (nodes + tile_nodes - 1) / tile_nodes;
+  }
+};
+
 int check_distill(int rows, int vocab, const void *logits, int dtype, int64_t row_stride, int topk,
                   const int32_t *ids, const float *teacher, float temperature) {
   if (rows < 0 || vocab < 1 || vocab > (1 << 20) || topk < 1 || topk > 1024) return DCOCO_EINVAL;
@@ -68,18 +84,43 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
   if (!h) return DCOCO_ENOMEM;
   h->cfg = *cfg;
   while ((1 << h->page_shift) < cfg->page_size) ++h->page_shift;
-  if (cudaGetDevice(&h->device) != cudaSuccess) {
+  if (cudaGetDevice(&h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
     delete h;
     return DCOCO_ECUDA;
   }
-  if (cudaMalloc(&h->err, sizeof(int)) != cudaSuccess) {
+  // Chunk sizes.  One request at a time: whatever spreads it over the SMs.
+  // More: at most 16 tiles (2048 tokens), since requests differ in length.
+  const int64_t max_tiles = ((int64_t)cfg->page_size * cfg->max_pages + dc::kTreeTile - 1) / dc::kTreeTile +
+                            (cfg->max_tree + dc::kTreeTile - 1) / dc::kTreeTile;
+  h->chunk_cap = cfg->max_batch == 1 ? 1 << 30 : 16;
+  const RowTiles rt(*cfg, cfg->max_tree);
+  const int64_t scan = max_tiles < 2048 ? max_tiles : 2048;
+  for (int nt = 1; nt <= scan; ++nt) {
+    const int per = dc::tree_chunk_tiles(nt, cfg->max_batch * cfg->kv_heads, h->sms, h->chunk_cap);
+    const int n = (nt + per - 1) / per;
+    if (n > h->max_chunks) h->max_chunks = n;
+  }
+  if (max_tiles > scan) h->max_chunks = dc::kTreeMaxChunks;
+  const size_t items = (size_t)cfg->max_batch * cfg->kv_heads * rt.mtiles;
+  const size_t rows = h->max_chunks > 1 ? items * h->max_chunks * rt.tile_rows : 0;
+  h->counts_bytes = items * sizeof(int);
+  const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+  const size_t at_ml = up(256 + h->counts_bytes), at_o = at_ml + up(rows * sizeof(float2));
+  const size_t bytes = at_o + rows * cfg->head_dim * sizeof(float);
+  if (cudaMalloc(&h->block, bytes) != cudaSuccess) {
     cudaGetLastError();
     delete h;
     return DCOCO_ENOMEM;
   }
-  if (cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  char *base = static_cast<char *>(h->block);
+  h->err = reinterpret_cast<int *>(base);
+  h->counts = reinterpret_cast<int *>(base + 256);
+  h->part_ml = reinterpret_cast<float2 *>(base + at_ml);
+  h->part_o = reinterpret_cast<float4 *>(base + at_o);
+  if (cudaMemset(base, 0, 256 + h->counts_bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
-    cudaFree(h->err);
+    cudaFree(h->block);
     delete h;
     return DCOCO_ECUDA;
   }
@@ -122,6 +163,12 @@ int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco
   p.f16 = c.dtype == DCOCO_FP16;
   p.scale = a->scale;
   p.out = (uint16_t *)out, p.lse = lse, p.err = h->err;
+  const RowTiles rt(c, nodes);
+  p.mtiles = rt.mtiles, p.tile_nodes = rt.tile_nodes, p.tile_rows = rt.tile_rows;
+  p.tree_box = nodes < dc::kTreeTile ? (nodes + 7) / 8 * 8 : dc::kTreeTile;
+  p.items = c.max_batch * c.kv_heads * rt.mtiles, p.sms = h->sms;
+  p.chunk_cap = h->chunk_cap, p.max_chunks = h->max_chunks;
+  p.part_o = h->part_o, p.part_ml = h->part_ml, p.counts = h->counts;
   h->last_stream = static_cast<cudaStream_t>(stream);
   ++h->launches;
   return cuda_status(dc::launch_tree_attention(p, h->last_stream));
@@ -174,7 +221,8 @@ int dcoco_tree_status(dcoco_tree_handle *h) {
   int flag = 0;
   if (cudaMemcpy(&flag, h->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return DCOCO_ECUDA;
   if (flag != 0) {
-    if (cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess) return DCOCO_ECUDA;
+    // a block that gave up left its item's count behind
+    if (cudaMemset(h->block, 0, 256 + h->counts_bytes) != cudaSuccess) return DCOCO_ECUDA;
     return DCOCO_EDEVICE;
   }
   return DCOCO_OK;
@@ -185,7 +233,7 @@ long long dcoco_tree_launches(const dcoco_tree_handle *h) { return h ? h->launch
 void dcoco_tree_destroy(dcoco_tree_handle *h) {
   if (!h) return;
   cudaDeviceSynchronize();
-  cudaFree(h->err);
+  cudaFree(h->block);
   delete h;
 }
 
