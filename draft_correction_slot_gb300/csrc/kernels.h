@@ -237,6 +237,9 @@ __host__ __device__ inline int tree_chunk_tiles(int nt, int items, int sms, int 
   return c < 1 ? 1 : c;
 }
 cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t st);
+// The kernel for at most 64 rows a K/V head (one row tile).
+cudaError_t launch_tree_attention_few(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid,
+                                      cudaStream_t st);
 
 // ---------------------------------------------------------------- tree commit
 struct TreeCommitParams {

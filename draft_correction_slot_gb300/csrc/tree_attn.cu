@@ -23,25 +23,16 @@
 // each leaves its unnormalised output with its maximum and sum, and the last
 // to finish joins them in chunk order.
 //
-// Roles: warps 0-3 softmax and output (thread = row = TMEM lane), warp 4 TMA,
-// warp 5 the tensor core.
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "kernels.h"
-#include "tc.cuh"
+// Roles: warps 0-3 softmax and output (thread = row = TMEM lane), warp 4 the
+// tensor core, warps 5-6 TMA.
+#include "tree_attn.cuh"
 
 namespace dc {
 namespace {
 
-using namespace tc;
-
-constexpr float kLn2 = 0.693147180559945f;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kTile = kTreeTile;      // tokens of a K/V tile
 constexpr int kSoftWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + 2);
-constexpr float kRescale = 8.f;       // log2 growth of a row's maximum before the output is rescaled
+constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
 
 template <int D>
 struct Geom {
@@ -49,142 +40,12 @@ struct Geom {
   static constexpr uint32_t kHalfBytes = kTile * 128;    // a tile's column block
   static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
   static constexpr int kNK = D == 128 ? 2 : 4, kNV = D == 128 ? 3 : 4;  // K and V stages
-  static constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + kNK * kTileBytes;
+  static constexpr uint32_t kQHalf = kHalfBytes, kQBytes = kTileBytes;
+  static constexpr uint32_t kQ = 0, kK = 2 * kQBytes, kV = kK + kNK * kTileBytes;
   static constexpr uint32_t kSmem = kV + kNV * kTileBytes;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <bool F16>
-__device__ __forceinline__ float unpack_lo(uint32_t w) {
-  if constexpr (F16) return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
-  else return __uint_as_float(w << 16);
-}
-// Whether either 16-bit element of w is an infinity or NaN.
-template <bool F16>
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
-  return (w & e) == e || ((w >> 16) & e) == e;
-}
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-// D[tmem] += A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Descriptor of a V tile as the B operand with its rows (tokens) along K and
-// its columns along N (N-major, 128-byte swizzle): 8-token groups 1024 bytes
-// apart, 64-column blocks kHalfBytes apart.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((kTile * 128) >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// ---------------------------------------------------------------- units
-struct Unit {
-  int n, h, mt, chunk, nchunks;  // request, K/V head, row tile, chunk of the request's nchunks
-  int ctx, len;                  // clamped lengths
-  int tile0, ntiles, nctx;       // first tile, tiles (0: no live rows), context tiles of the request
-};
-
-// Every gridDim-th unit in the order (request, chunk, head, row tile), warp
-// by warp without communication: 32 requests' lengths at a time in the lanes.
-struct UnitIter {
-  const TreeAttnParams &p;
-  int lane, base = 0, n0 = 0, u;
-  int ctx = 0, len = 0, chunks = 0, before = 0, upto = 0, window = 0;
-  __device__ UnitIter(const TreeAttnParams &p_, bool flag) : p(p_), lane(threadIdx.x & 31), u(blockIdx.x) { load(flag); }
-  __device__ void load(bool flag) {
-    const int n = n0 + lane;
-    chunks = 0;
-    if (n < p.N) {
-      const int capacity = p.max_pages << p.page_shift;
-      ctx = p.ctx_len[n];
-      len = p.tree_len ? p.tree_len[n] : p.T;
-      if ((ctx < 0 || ctx > capacity || len < 0 || len > p.T) && flag) atomicOr(p.err, kErrBadLength);
-      ctx = min(max(ctx, 0), capacity);
-      len = len < 0 ? 0 : min(len, p.T);
-      const int nt = len > 0 ? (ctx + kTile - 1) / kTile + (len + kTile - 1) / kTile : 0;
-      const int per = tree_chunk_tiles(nt, p.items, p.sms, p.chunk_cap);
-      chunks = nt > 0 ? (nt + per - 1) / per : 1;
-    }
-    const int count = chunks * p.kv_heads * p.mtiles;
-    int s = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(DC_FULL_MASK, s, o);
-      if (lane >= o) s += y;
-    }
-    upto = s;
-    before = s - count;
-    window = __shfl_sync(DC_FULL_MASK, s, 31);
-  }
-  __device__ bool next(Unit &w, bool flag = false) {
-    while (u - base >= window) {
-      base += window;
-      n0 += 32;
-      if (n0 >= p.N) return false;
-      load(flag);
-    }
-    const int rel = u - base;
-    const int src = __ffs(__ballot_sync(DC_FULL_MASK, upto > rel)) - 1;
-    int i = rel - __shfl_sync(DC_FULL_MASK, before, src);
-    w.n = n0 + src;
-    w.ctx = __shfl_sync(DC_FULL_MASK, ctx, src);
-    w.len = __shfl_sync(DC_FULL_MASK, len, src);
-    w.nchunks = __shfl_sync(DC_FULL_MASK, chunks, src);
-    w.mt = i % p.mtiles, i /= p.mtiles;
-    w.h = i % p.kv_heads, w.chunk = i / p.kv_heads;
-    w.nctx = (w.ctx + kTile - 1) / kTile;
-    const int nt = w.mt * p.tile_nodes < w.len ? w.nctx + (w.len + kTile - 1) / kTile : 0;
-    w.tile0 = (int)((int64_t)nt * w.chunk / w.nchunks);  // chunks as even as they come
-    w.ntiles = (int)((int64_t)nt * (w.chunk + 1) / w.nchunks) - w.tile0;
-    u += gridDim.x;
-    return true;
-  }
-};
-
-struct Bars {
-  unsigned long long q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
+struct Bars : RingBars {
   unsigned long long s_full[2], p_full[2], pv_done[2], o_free, soft, done;
 };
 
@@ -201,94 +62,36 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_last;
   __shared__ uint32_t s_odd[4];  // tree tile: nodes whose V holds an infinity or NaN
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&b.q_full[i]), 1);
-      mbar_init(smem_u32(&b.q_empty[i]), 1);
       mbar_init(smem_u32(&b.s_full[i]), 1);
       mbar_init(smem_u32(&b.p_full[i]), kSoftWarps);
       mbar_init(smem_u32(&b.pv_done[i]), 1);
     }
-    for (int i = 0; i < G::kNK; ++i) mbar_init(smem_u32(&b.k_full[i]), 1), mbar_init(smem_u32(&b.k_empty[i]), 1);
-    for (int i = 0; i < G::kNV; ++i) mbar_init(smem_u32(&b.v_full[i]), 1), mbar_init(smem_u32(&b.v_empty[i]), 1);
+    init_ring<G>(b);
     mbar_init(smem_u32(&b.o_free), kSoftWarps);
     mbar_init(smem_u32(&b.soft), kSoftWarps);
     mbar_init(smem_u32(&b.done), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(&s_tmem), 512);
+  // rows past the unit's are zeros: what lies there would set off rescales
+  for (uint32_t i = tid * 16; i < 2 * G::kQBytes; i += kThreads * 16)
+    *reinterpret_cast<uint4 *>(smem + G::kQ + i) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(DC_FULL_MASK, s_tmem, 0);
   int g = 0, live = 0;  // tiles and units with tiles that this role has begun
 
-  if (warp == kSoftWarps) {
-    // ------------------------------------------------------------ TMA
-    UnitIter it(p, blockIdx.x == 0);
-    Unit w;
-    const int page_size = 1 << p.page_shift;
-    const int box = min(page_size, kTile);       // tokens of one copy
-    const int boxes = kTile / box;               // copies of a tile's column block
-    bool ok = true;
-    while (ok && it.next(w, blockIdx.x == 0)) {
-      if (w.ntiles == 0) continue;
-      const int qb = live & 1;
-      if (live >= 2) ok = mbar_wait(smem_u32(&b.q_empty[qb]), ((live >> 1) - 1) & 1, &s_abort, p.err);
-      ok = __all_sync(DC_FULL_MASK, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(&b.q_full[qb]), (uint32_t)(G::kHalves * p.tile_nodes * p.group * 128));
-        for (int c = 0; c < G::kHalves; ++c)
-          tma_load_4d(sbase + G::kQ + qb * G::kTileBytes + c * G::kHalfBytes, &maps.q, c * 64, w.h * p.group,
-                      w.mt * p.tile_nodes, w.n, smem_u32(&b.q_full[qb]));
-      }
-      ++live;
-      for (int i = 0; ok && i < w.ntiles; ++i, ++g) {
-        const int tile = w.tile0 + i;
-        const bool tree = tile >= w.nctx;
-        // this lane's copy: column block lane / boxes, tokens lane % boxes
-        const int tok0 = (tree ? tile - w.nctx : tile) * kTile;
-        const int c = lane / boxes, r = lane % boxes;
-        int page = 0, used = boxes;
-        if (!tree) {
-          used = min(boxes, (w.ctx - tok0 + box - 1) / box);
-          if (r < used && c < G::kHalves) {
-            page = __ldg(p.page_table + w.n * p.pt_stride + ((tok0 + r * box) >> p.page_shift));
-            if (page < 0 || page >= p.num_pages) {
-              atomicOr(p.err, kErrBadPage);
-              page = 0;
-            }
-          }
-        }
-        const uint32_t bytes = tree ? (uint32_t)(G::kHalves * p.tree_box * 128) : (uint32_t)(G::kHalves * used * box * 128);
-        const bool mine = tree ? lane < G::kHalves : (c < G::kHalves && r < used);
-        auto copy = [&](uint32_t dst, uint32_t bar, const CUtensorMap *cache, const CUtensorMap *fresh) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-          __syncwarp();
-          if (!mine) return;
-          if (tree) tma_load_4d(dst + lane * G::kHalfBytes, fresh, lane * 64, tok0, w.h, w.n, bar);
-          else tma_load_4d(dst + c * G::kHalfBytes + r * box * 128, cache, c * 64, tok0 & (page_size - 1), w.h, page, bar);
-        };
-        const int ks = g % G::kNK, vs = g % G::kNV;
-        if (g >= G::kNK) ok = mbar_wait(smem_u32(&b.k_empty[ks]), (g / G::kNK - 1) & 1, &s_abort, p.err);
-        ok = __all_sync(DC_FULL_MASK, ok);
-        if (!ok) break;
-        copy(sbase + G::kK + ks * G::kTileBytes, smem_u32(&b.k_full[ks]), &maps.k_cache, &maps.k_new);
-        if (g >= G::kNV) ok = mbar_wait(smem_u32(&b.v_empty[vs]), (g / G::kNV - 1) & 1, &s_abort, p.err);
-        ok = __all_sync(DC_FULL_MASK, ok);
-        if (!ok) {
-          if (lane == 0) mbar_drain(smem_u32(&b.k_full[ks]), (g / G::kNK) & 1);
-          break;
-        }
-        copy(sbase + G::kV + vs * G::kTileBytes, smem_u32(&b.v_full[vs]), &maps.v_cache, &maps.v_new);
-      }
-    }
-  } else if (warp == kSoftWarps + 1) {
+  if (warp >= kLoadWarp) {
+    load_tiles<G>(p, maps, sbase, b, warp - kLoadWarp, &s_abort, g, live);
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ tensor core
     constexpr uint32_t kIdS = F16 ? idesc_f16(128, kTile) : idesc_bf16(128, kTile);
     constexpr uint32_t kIdO = (F16 ? idesc_f16(128, D) : idesc_bf16(128, D)) | (1u << 16);  // B is N-major
@@ -298,49 +101,54 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
     // O (+)= P V of tile t, the first of the block's unit number `unit` if `first`
     auto pv = [&](int t, bool first, int unit) {
       const int vs = t % G::kNV;
-      if (!mbar_wait(smem_u32(&b.v_full[vs]), (t / G::kNV) & 1, &s_abort, p.err) ||
-          (first && unit > 0 && !mbar_wait(smem_u32(&b.o_free), (unit - 1) & 1, &s_abort, p.err)) ||
-          !mbar_wait(smem_u32(&b.p_full[t & 1]), (t >> 1) & 1, &s_abort, p.err))
-        return false;
+      const bool go = bar_wait(smem_u32(&b.v_full[vs]), (t / G::kNV) & 1, &s_abort, p.err) &&
+                      (!first || unit == 0 || bar_wait(smem_u32(&b.o_free), (unit - 1) & 1, &s_abort, p.err)) &&
+                      bar_wait(smem_u32(&b.p_full[t & 1]), (t >> 1) & 1, &s_abort, p.err);
+      if (!__all_sync(DC_FULL_MASK, go)) return false;
       tc_fence_after();
-      const uint32_t sv = sbase + G::kV + vs * G::kTileBytes;
+      const uint32_t sv = mn_major_lo(sbase + G::kV + vs * G::kTileBytes);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(tmem + kO, tmem + kP + (t & 1) * 64 + k * 8, v_desc(sv + k * 2048), kIdO, (!first || k > 0) ? 1u : 0u);
-      mma_commit(smem_u32(&b.v_empty[vs]));
-      mma_commit(smem_u32(&b.pv_done[t & 1]));
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts(tmem + kO, tmem + kP + (t & 1) * 64 + k * 8, sv + k * (2048 >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
+        mma_commit(smem_u32(&b.v_empty[vs]));
+        mma_commit(smem_u32(&b.pv_done[t & 1]));
+      }
+      __syncwarp();
       return true;
     };
     bool prev_first = false;
     int prev_unit = 0;
-    while (__all_sync(DC_FULL_MASK, ok) && it.next(w)) {
+    while (ok && it.next(w)) {
       if (w.ntiles == 0) continue;
-      if (lane == 0) {
-        const int qb = live & 1;
-        ok = mbar_wait(smem_u32(&b.q_full[qb]), (live >> 1) & 1, &s_abort, p.err);
-        for (int i = 0; ok && i < w.ntiles; ++i, ++g) {
-          const int ks = g % G::kNK;
-          ok = mbar_wait(smem_u32(&b.k_full[ks]), (g / G::kNK) & 1, &s_abort, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sq = sbase + G::kQ + qb * G::kTileBytes, sk = sbase + G::kK + ks * G::kTileBytes;
+      const int qb = live & 1;
+      ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (live >> 1) & 1, &s_abort, p.err));
+      for (int i = 0; ok && i < w.ntiles; ++i, ++g) {
+        const int ks = g % G::kNK;
+        ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.k_full[ks]), (g / G::kNK) & 1, &s_abort, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sq = k_major_lo(sbase + G::kQ + qb * G::kQBytes);
+        const uint32_t sk = k_major_lo(sbase + G::kK + ks * G::kTileBytes);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * G::kHalfBytes + (k & 3) * 32;
-            mma_bf16(tmem + kS + (g & 1) * 128, sw128_desc(sq + off), sw128_desc(sk + off), kIdS, k > 0 ? 1u : 0u);
+            const uint32_t off = ((k >> 2) * G::kHalfBytes + (k & 3) * 32) >> 4;
+            mma_ss(tmem + kS + (g & 1) * 128, sq + off, sk + off, kIdS, k > 0 ? 1u : 0u);
           }
           mma_commit(smem_u32(&b.s_full[g & 1]));
           mma_commit(smem_u32(&b.k_empty[ks]));
           if (i == w.ntiles - 1) mma_commit(smem_u32(&b.q_empty[qb]));
-          if (g > 0) ok = pv(g - 1, prev_first, prev_unit);
-          prev_first = i == 0, prev_unit = live;
         }
+        __syncwarp();
+        if (g > 0) ok = pv(g - 1, prev_first, prev_unit);
+        prev_first = i == 0, prev_unit = live;
       }
       ++live;
     }
-    if (lane == 0) {
-      if (ok && g > 0) pv(g - 1, prev_first, prev_unit);
-      mma_commit(smem_u32(&b.done));  // nothing is in flight when the block frees its TMEM
+    if (ok && g > 0) pv(g - 1, prev_first, prev_unit);
+    if (elect_one()) {  // the lane that issued: nothing is in flight when the block frees its TMEM
+      mma_commit(smem_u32(&b.done));
       mbar_drain(smem_u32(&b.done), 0);
     }
     __syncwarp();
@@ -361,7 +169,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
     auto meet = [&] {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&b.soft));
-      const bool met = mbar_wait(smem_u32(&b.soft), syncs++ & 1, &s_abort, p.err);
+      const bool met = bar_wait(smem_u32(&b.soft), syncs++ & 1, &s_abort, p.err);
       return (bool)__all_sync(DC_FULL_MASK, met);
     };
     while (ok && it.next(w)) {
@@ -376,38 +184,12 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
         const bool tree = tile >= w.nctx;
         const int tok0 = (tree ? tile - w.nctx : tile) * kTile;
         const int valid = min(kTile, (tree ? w.len : w.ctx) - tok0);
-        ok = mbar_wait(smem_u32(&b.s_full[g & 1]), (g >> 1) & 1, &s_abort, p.err);
+        ok = bar_wait(smem_u32(&b.s_full[g & 1]), (g >> 1) & 1, &s_abort, p.err);
         if (valid < kTile || tree) {
-          // V rows past the end hold what a page or a copy left there: zeros
-          // in their place, since a zero weight does not cancel an infinity
-          ok = ok && mbar_wait(smem_u32(&b.v_full[g % G::kNV]), (g / G::kNV) & 1, &s_abort, p.err);
+          ok = ok && bar_wait(smem_u32(&b.v_full[g % G::kNV]), (g / G::kNV) & 1, &s_abort, p.err);
           ok = __all_sync(DC_FULL_MASK, ok);
           if (!ok) break;
-          const uint32_t sv = G::kV + (g % G::kNV) * G::kTileBytes + row * 128;  // token `row`
-          bool bad = false;
-          if (row >= valid) {
-#pragma unroll
-            for (int e = 0; e < D / 8; ++e)
-              *reinterpret_cast<uint4 *>(smem + sv + (e >> 3) * G::kHalfBytes + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-          } else if (tree) {
-            // a node's infinities and NaN stay out of the product (they would
-            // reach nodes that do not see it) and are added at the end
-            for (int e = 0; e < D / 8; ++e) {
-              uint4 *v = reinterpret_cast<uint4 *>(smem + sv + (e >> 3) * G::kHalfBytes + (e & 7) * 16);
-              const uint4 x = *v;
-              uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-              bool any = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (nonfinite2<F16>(xs[k])) {
-                  if (nonfinite2<F16>(xs[k] & 0xFFFFu)) xs[k] &= 0xFFFF0000u;
-                  if (nonfinite2<F16>(xs[k] >> 16)) xs[k] &= 0xFFFFu;
-                  any = true;
-                }
-              if (any) *v = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-              bad |= any;
-            }
-          }
+          const bool bad = clean_v_row<D, F16>(smem + G::kV + (g % G::kNV) * G::kTileBytes + row * 128, row < valid, tree);
           if (tree) {
             const uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
             ok = meet();  // the previous tree tile's bits have been read
@@ -417,56 +199,55 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
           fence_proxy_async();
         }
         if (g >= 2)  // P's columns are free
-          ok = ok && mbar_wait(smem_u32(&b.pv_done[g & 1]), ((g >> 1) - 1) & 1, &s_abort, p.err);
+          ok = ok && bar_wait(smem_u32(&b.pv_done[g & 1]), ((g >> 1) - 1) & 1, &s_abort, p.err);
         ok = __all_sync(DC_FULL_MASK, ok);
         if (!ok) break;
         tc_fence_after();
-        float v[kTile];
         const uint32_t ts = trow + kS + (g & 1) * 128, tp = trow + kP + (g & 1) * 64;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x[32];
-          tmem_ld32(ts + q * 32, x);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[q * 32 + k] = x[k];
-        }
-        if (flip | zero) {
-#pragma unroll
-          for (int k = 0; k < kTile; ++k) v[k] = zero ? 0.f : -v[k];
-        }
-        if (valid < kTile || tree) {
-          uint32_t see[4];
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // tokens of the tile that this row sees
+        const bool masked = valid < kTile || tree;
+        if (masked) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int left = valid - q * 32;  // tokens of this word that exist
             see[q] = left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
           }
           if (tree) {
-            const int words = (p.T + 31) / 32, w0 = tok0 / 32;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              uint32_t m = 0;
-              if (live_row && w0 + q < words) {
-                if (p.tree_mask) {
-                  m = (uint32_t)__ldg(p.tree_mask + w.n * p.mask_sn + (int64_t)node * words + w0 + q);
-                } else {
-                  const int left = node + 1 - (w0 + q) * 32;  // nodes 0..node
-                  m = left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
-                }
-              }
-              see[q] &= m;
+              see[q] &= tree_sees(p, w.n, w.len, live_row ? node : w.len, tok0 / 32 + q);
               const uint32_t o = see[q] & s_odd[q];
               if (tok0 == 0) odd[q] = o;
               else odd[4 + q] = o;
               any_odd |= o != 0;
             }
           }
-#pragma unroll
-          for (int k = 0; k < kTile; ++k) v[k] = (see[k >> 5] >> (k & 31)) & 1u ? v[k] : -INFINITY;
         }
+        // 64 scores at a time (all 128 would not fit the registers): the
+        // maximum over both halves, then the weights of the second half, still
+        // held, and of the first, read from TMEM again.
+        float v[64];
+        auto load = [&](int half) {
+          tmem_ld64(ts + half * 64, v);
+          if (flip | zero) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k) v[k] = zero ? 0.f : -v[k];
+          }
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k) {
+              const uint32_t word = half == 0 ? see[k >> 5] : see[2 + (k >> 5)];
+              v[k] = (word >> (k & 31)) & 1u ? v[k] : -INFINITY;
+            }
+          }
+        };
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < kTile; ++k) m4[k & 3] = fmaxf(m4[k & 3], v[k]);
+        for (int half = 0; half < 2; ++half) {
+          load(half);
+#pragma unroll
+          for (int k = 0; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], v[k]);
+        }
         const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
         if (i == 0) {
           mref = mt;
@@ -475,7 +256,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
           if (__any_sync(DC_FULL_MASK, grow)) {
             const float f = grow ? ex2(mref - mt) : 1.f;
             if (grow) mref = mt, l *= f;
-            ok = mbar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
+            ok = bar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
             ok = __all_sync(DC_FULL_MASK, ok);
             if (!ok) break;
             tc_fence_after();
@@ -494,11 +275,12 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
         const float mb = mref == -INFINITY ? 0.f : mref;
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 1; q >= 0; --q) {
+          if (q == 0) load(0);
           uint32_t y[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float a = ex2(fmaf(v[q * 64 + 2 * k], c, -mb)), d = ex2(fmaf(v[q * 64 + 2 * k + 1], c, -mb));
+            const float a = ex2(fmaf(v[2 * k], c, -mb)), d = ex2(fmaf(v[2 * k + 1], c, -mb));
             l4[(2 * k) & 3] += a;
             l4[(2 * k + 1) & 3] += d;
             y[k] = pack2<F16>(a, d);
@@ -528,7 +310,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
           }
       };
       if (w.ntiles > 0) {
-        ok = mbar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
+        ok = bar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
         ok = __all_sync(DC_FULL_MASK, ok);
         if (!ok) break;
         tc_fence_after();
@@ -635,14 +417,8 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s_abort && tid == kSoftWarps * 32) {  // copies in flight land before the block gives its memory back
-    for (int t = max(0, g - 4); t < g; ++t) {
-      if (t >= g - G::kNK) mbar_drain(smem_u32(&b.k_full[t % G::kNK]), (t / G::kNK) & 1);
-      if (t >= g - G::kNV) mbar_drain(smem_u32(&b.v_full[t % G::kNV]), (t / G::kNV) & 1);
-    }
-    for (int t = max(0, live - 2); t < live; ++t) mbar_drain(smem_u32(&b.q_full[t & 1]), (t >> 1) & 1);
-  }
-  if (warp == kSoftWarps + 1) tmem_dealloc(tmem, 512);
+  if (s_abort && warp >= kLoadWarp && lane == 0) drain_copies<G>(b, warp - kLoadWarp, g, live);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -681,13 +457,12 @@ bool encode_4d(CUtensorMap *map, bool f16, const void *base, int D, int na, int6
 }
 
 template <int D, bool F16>
-cudaError_t launch(const TreeAttnParams &p, const TreeAttnMaps &maps, cudaStream_t st) {
+cudaError_t launch(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid, cudaStream_t st) {
   const size_t smem = Geom<D>::kSmem + 1024;
   const cudaError_t e =
       cudaFuncSetAttribute(k_tree_attn<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t most = (int64_t)p.N * p.kv_heads * p.mtiles * p.max_chunks;
-  k_tree_attn<D, F16><<<(unsigned)(most < p.sms ? most : p.sms), kThreads, smem, st>>>(p, maps);
+  k_tree_attn<D, F16><<<grid, kThreads, smem, st>>>(p, maps);
   return cudaGetLastError();
 }
 
@@ -702,9 +477,12 @@ cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t st) {
       !encode_4d(&maps.k_cache, p.f16, p.k_cache, D, page, p.kc_st, heads, p.kc_sh, p.num_pages, p.kc_sp, box, 1) ||
       !encode_4d(&maps.v_cache, p.f16, p.v_cache, D, page, p.vc_st, heads, p.vc_sh, p.num_pages, p.vc_sp, box, 1))
     return cudaErrorInvalidValue;
+  const int64_t most = (int64_t)p.N * p.kv_heads * p.mtiles * p.max_chunks;
+  const unsigned grid = (unsigned)(most < p.sms ? most : p.sms);
+  if (p.tile_rows <= 64 && p.mtiles == 1) return launch_tree_attention_few(p, maps, grid, st);
   if (p.head_dim == 128)
-    return p.f16 ? launch<128, true>(p, maps, st) : launch<128, false>(p, maps, st);
-  return p.f16 ? launch<64, true>(p, maps, st) : launch<64, false>(p, maps, st);
+    return p.f16 ? launch<128, true>(p, maps, grid, st) : launch<128, false>(p, maps, grid, st);
+  return p.f16 ? launch<64, true>(p, maps, grid, st) : launch<64, false>(p, maps, grid, st);
 }
 
 }  // namespace dc

@@ -1,0 +1,504 @@
+// tree_attn_few.cu -- tree attention when a K/V head has at most 64 query
+// rows (nodes x group), single-token decoding among them.
+//
+// The products are turned round: S^T = K Q^T (M = the tile's 128 tokens, N =
+// the rows, padded to 16, 32 or 64) and O^T += V^T P^T (M = the head's
+// elements, N = the rows).  So a tile costs 128 x rows exponentials, where
+// rows in M cost 128 x 128 whatever their number, and each of the four softmax
+// warps has 32 tokens of every row to itself.  P^T goes to shared memory, a
+// token's row of N weights the 128 bytes of a swizzle row.
+//
+// A row's reference (the maximum when last taken) is common to the four
+// warps; its sum is kept per thread, over the thread's tokens, until the
+// unit's end.  Per tile the warps only vote whether any score has outgrown its
+// row's reference by 2^8; then, and on a unit's first tile, the references are
+// taken anew across the block and O^T is rescaled.
+//
+// Roles: warps 0-3 softmax (thread = token = TMEM lane) and output (thread =
+// element), warp 4 the tensor core, warps 5-6 TMA.  After an expired wait the
+// softmax warps run their loops to the end without waiting or storing, so
+// that their block barriers stay complete.
+#include "tree_attn.cuh"
+
+namespace dc {
+namespace {
+
+constexpr int kSoft = 128;              // softmax threads
+constexpr int kMmaWarp = kSoft / 32, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = kSoft + 32 + 32 * kLoadWarps;
+constexpr float kNone = -1e30f;         // reference of a row that has seen nothing: any score outgrows it
+
+template <int D, int N>
+struct GeomFew {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kHalfBytes = kTile * 128;
+  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kNK = D == 128 ? 2 : 4, kNV = D == 128 ? 3 : 4;
+  static constexpr uint32_t kQHalf = N * 128, kQBytes = kHalves * kQHalf;
+  static constexpr uint32_t kPBytes = kTile * 128;
+  // V before P: for head_dim 64 the product reads 64 rows of M past each V
+  // stage (their results are not used), which have to be shared memory of ours
+  static constexpr uint32_t kK = 0, kV = kK + kNK * kTileBytes, kP = kV + kNV * kTileBytes;
+  static constexpr uint32_t kQ = kP + 2 * kPBytes;
+  static constexpr uint32_t kSmem = kQ + 2 * kQBytes;
+  static constexpr uint32_t kTmem = N == 16 ? 64 : N == 32 ? 128 : 256;
+  static constexpr uint32_t kS = 0, kO = 2 * N;  // TMEM columns: S^T of even and odd tiles, O^T
+};
+
+struct BarsFew : RingBars {
+  unsigned long long s_full[2], p_full[2], pv_done[2], o_free, done;
+};
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
+  if constexpr (N == 64) {
+    tmem_ld64(addr, v);
+  } else if constexpr (N == 32) {
+    tmem_ld32(addr, v);
+  } else {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 16)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"f"(
+            v[i]),
+        "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]), "f"(v[i + 6]), "f"(v[i + 7]),
+        "f"(v[i + 8]), "f"(v[i + 9]), "f"(v[i + 10]), "f"(v[i + 11]), "f"(v[i + 12]), "f"(v[i + 13]), "f"(v[i + 14]),
+        "f"(v[i + 15]), "r"(addr + i)
+        : "memory");
+  tmem_st_wait();
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\n"
+      "setp.ne.u32 p, %1, 0;\n"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n"
+      "selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+// Maximum over the warp by one integer reduction; NaN counts as -inf.
+__device__ __forceinline__ float warp_fmax(float x) {
+  const int b = __float_as_int(x != x ? -INFINITY : x);
+  const int m = __reduce_max_sync(DC_FULL_MASK, b ^ ((b >> 31) & 0x7FFFFFFF));
+  return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
+}
+
+template <int D, int N, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
+  using G = GeomFew<D, N>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) BarsFew b;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_last;
+  __shared__ uint32_t s_odd[4];              // tree tile: nodes whose V holds an infinity or NaN
+  __shared__ __align__(16) float s_mb[N];    // the rows' references (log2 units)
+  __shared__ __align__(16) float s_f[N];     // rescale factors; at the end 1 / sum
+  __shared__ __align__(16) float s_part[4][N];
+  const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
+  const uint32_t sbase = smem_u32(smem);
+
+  if (tid == 0) {
+    init_ring<G>(b);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&b.s_full[i]), 1);
+      mbar_init(smem_u32(&b.p_full[i]), kSoft / 32);
+      mbar_init(smem_u32(&b.pv_done[i]), 1);
+    }
+    mbar_init(smem_u32(&b.o_free), kSoft / 32);
+    mbar_init(smem_u32(&b.done), 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // rows past the unit's are zeros: their scores are 0 and outgrow nothing
+  for (uint32_t i = tid * 16; i < 2 * G::kQBytes; i += kThreads * 16)
+    *reinterpret_cast<uint4 *>(smem + G::kQ + i) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), G::kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(DC_FULL_MASK, s_tmem, 0);
+  int g = 0, live = 0;  // tiles and units with tiles that this role has begun
+
+  if (warp >= kLoadWarp) {
+    load_tiles<G>(p, maps, sbase, b, warp - kLoadWarp, &s_abort, g, live);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ tensor core
+    constexpr uint32_t kIdS = F16 ? idesc_f16(128, N) : idesc_bf16(128, N);
+    constexpr uint32_t kIdO = kIdS | (1u << 15) | (1u << 16);  // A is M-major, B is N-major
+    UnitIter it(p, false);
+    Unit w;
+    bool ok = true;
+    // O^T (+)= V^T P^T of tile t, the first of the block's unit number `unit` if `first`
+    auto pv = [&](int t, bool first, int unit) {
+      const int vs = t % G::kNV;
+      const bool go = bar_wait(smem_u32(&b.v_full[vs]), (t / G::kNV) & 1, &s_abort, p.err) &&
+                      (!first || unit == 0 || bar_wait(smem_u32(&b.o_free), (unit - 1) & 1, &s_abort, p.err)) &&
+                      bar_wait(smem_u32(&b.p_full[t & 1]), (t >> 1) & 1, &s_abort, p.err);
+      if (!__all_sync(DC_FULL_MASK, go)) return false;
+      tc_fence_after();
+      const uint32_t sv = mn_major_lo(sbase + G::kV + vs * G::kTileBytes);
+      const uint32_t sp = mn_major_lo(sbase + G::kP + (t & 1) * G::kPBytes);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ss(tmem + G::kO, sv + k * (2048 >> 4), sp + k * (2048 >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
+        mma_commit(smem_u32(&b.v_empty[vs]));
+        mma_commit(smem_u32(&b.pv_done[t & 1]));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool prev_first = false;
+    int prev_unit = 0;
+    while (ok && it.next(w)) {
+      if (w.ntiles == 0) continue;
+      const int qb = live & 1;
+      ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (live >> 1) & 1, &s_abort, p.err));
+      for (int i = 0; ok && i < w.ntiles; ++i, ++g) {
+        const int ks = g % G::kNK;
+        ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.k_full[ks]), (g / G::kNK) & 1, &s_abort, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sq = k_major_lo(sbase + G::kQ + qb * G::kQBytes);
+        const uint32_t sk = k_major_lo(sbase + G::kK + ks * G::kTileBytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + G::kS + (g & 1) * N, sk + (((k >> 2) * G::kHalfBytes + (k & 3) * 32) >> 4),
+                   sq + (((k >> 2) * G::kQHalf + (k & 3) * 32) >> 4), kIdS, k > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&b.s_full[g & 1]));
+          mma_commit(smem_u32(&b.k_empty[ks]));
+          if (i == w.ntiles - 1) mma_commit(smem_u32(&b.q_empty[qb]));
+        }
+        __syncwarp();
+        if (g > 0) ok = pv(g - 1, prev_first, prev_unit);
+        prev_first = i == 0, prev_unit = live;
+      }
+      ++live;
+    }
+    if (ok && g > 0) pv(g - 1, prev_first, prev_unit);
+    if (elect_one()) {  // the lane that issued: nothing is in flight when the block frees its TMEM
+      mma_commit(smem_u32(&b.done));
+      mbar_drain(smem_u32(&b.done), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, output
+    UnitIter it(p, false);
+    Unit w;
+    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    const int heads = p.kv_heads * p.group, R = p.tile_rows;
+    float c = p.scale * kLog2e;
+    const bool flip = c < 0.f, zero = c == 0.f;
+    c = zero ? 1.f : fabsf(c);
+    bool ok = true;
+    auto wait = [&](unsigned long long *bar, int phase) {
+      if (ok) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(bar), phase & 1, &s_abort, p.err));
+    };
+    while (it.next(w)) {
+      const int node0 = w.mt * p.tile_nodes;
+      float l[N];  // the rows' sums over this thread's tokens
+#pragma unroll
+      for (int k = 0; k < N; ++k) l[k] = 0.f;
+      uint32_t odd[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // nodes with an infinity or NaN in V
+      bool any_odd = false;
+      for (int i = 0; i < w.ntiles; ++i, ++g) {
+        const int tile = w.tile0 + i;
+        const bool tree = tile >= w.nctx;
+        const int tok0 = (tree ? tile - w.nctx : tile) * kTile;
+        const int valid = min(kTile, (tree ? w.len : w.ctx) - tok0);
+        wait(&b.s_full[g & 1], g >> 1);
+        if (valid < kTile || tree) {
+          wait(&b.v_full[g % G::kNV], g / G::kNV);
+          bool bad = false;
+          if (ok) bad = clean_v_row<D, F16>(smem + G::kV + (g % G::kNV) * G::kTileBytes + tid * 128, tid < valid, tree);
+          if (tree) {
+            const uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
+            if (lane == 0) s_odd[warp] = bits;
+            soft_sync();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t o = s_odd[q];
+              if (tok0 == 0) odd[q] = o;
+              else odd[4 + q] = o;
+              any_odd |= o != 0;
+            }
+            soft_sync();
+          }
+        }
+        if (g >= 2) wait(&b.pv_done[g & 1], (g >> 1) - 1);  // P's buffer is free
+        tc_fence_after();
+        float v[N];
+        tmem_ld<N>(trow + G::kS + (g & 1) * N, v);
+        if (flip | zero) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) v[k] = zero ? 0.f : -v[k];
+        }
+        if (tree) {
+          // this warp's 32 nodes are one word of each row's mask
+          int node = node0, head = 0;
+          uint32_t word = tree_sees(p, w.n, w.len, node, tok0 / 32 + warp);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            v[k] = k < R && ((word >> lane) & 1u) ? v[k] : -INFINITY;
+            if (++head == p.group) {
+              head = 0, ++node;
+              if (k + 1 < R) word = tree_sees(p, w.n, w.len, node, tok0 / 32 + warp);
+            }
+          }
+        } else if (tid >= valid) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) v[k] = -INFINITY;
+        }
+        bool renew = i == 0;
+        if (!renew) {
+          float grow = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < N; k += 4) {
+            const float4 mb = *reinterpret_cast<const float4 *>(&s_mb[k]);
+            grow = fmaxf(grow, fmaxf(fmaf(v[k], c, -mb.x), fmaf(v[k + 1], c, -mb.y)));
+            grow = fmaxf(grow, fmaxf(fmaf(v[k + 2], c, -mb.z), fmaf(v[k + 3], c, -mb.w)));
+          }
+          renew = soft_any(grow > kRescale);
+        }
+        if (renew) {
+          // the rows' maxima over the tile, and references from them
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const float m = warp_fmax(v[k]);
+            if (lane == (k & 31)) s_part[warp][k] = m;
+          }
+          soft_sync();
+          if (tid < N) {
+            const float m = fmaxf(fmaxf(s_part[0][tid], s_part[1][tid]), fmaxf(s_part[2][tid], s_part[3][tid])) * c;
+            const float old = i == 0 ? kNone : s_mb[tid];
+            const bool up = m > old + kRescale;
+            s_mb[tid] = up ? m : old;
+            s_f[tid] = up ? ex2(old - m) : 1.f;
+          }
+          soft_sync();
+          if (i > 0) {
+            wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
+            tc_fence_after();
+            float o[N];
+            tmem_ld<N>(trow + G::kO, o);
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(&s_f[k]);
+              o[k] *= f.x, o[k + 1] *= f.y, o[k + 2] *= f.z, o[k + 3] *= f.w;
+              l[k] *= f.x, l[k + 1] *= f.y, l[k + 2] *= f.z, l[k + 3] *= f.w;
+            }
+            tmem_st<N>(trow + G::kO, o);
+          }
+        }
+        uint8_t *prow = smem + G::kP + (g & 1) * G::kPBytes + tid * 128;
+#pragma unroll
+        for (int k = 0; k < N; k += 8) {
+          const float4 m0 = *reinterpret_cast<const float4 *>(&s_mb[k]), m1 = *reinterpret_cast<const float4 *>(&s_mb[k + 4]);
+          const float e0 = ex2(fmaf(v[k], c, -m0.x)), e1 = ex2(fmaf(v[k + 1], c, -m0.y));
+          const float e2 = ex2(fmaf(v[k + 2], c, -m0.z)), e3 = ex2(fmaf(v[k + 3], c, -m0.w));
+          const float e4 = ex2(fmaf(v[k + 4], c, -m1.x)), e5 = ex2(fmaf(v[k + 5], c, -m1.y));
+          const float e6 = ex2(fmaf(v[k + 6], c, -m1.z)), e7 = ex2(fmaf(v[k + 7], c, -m1.w));
+          l[k] += e0, l[k + 1] += e1, l[k + 2] += e2, l[k + 3] += e3;
+          l[k + 4] += e4, l[k + 5] += e5, l[k + 6] += e6, l[k + 7] += e7;
+          *reinterpret_cast<uint4 *>(prow + (((k >> 3) ^ (tid & 7)) * 16)) =
+              make_uint4(pack2<F16>(e0, e1), pack2<F16>(e2, e3), pack2<F16>(e4, e5), pack2<F16>(e6, e7));
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&b.p_full[g & 1]));
+      }
+      // -------------------------------------------------------- the unit's output
+      if (w.ntiles == 0) {
+        // no live row: the first chunk writes the zeros
+        if (w.chunk == 0 && ok) {
+          for (int k = warp; k < R; k += 4) {
+            const int node = node0 + k / p.group;
+            if (node >= p.T) break;
+            const int64_t row = ((int64_t)w.n * p.T + node) * heads + w.h * p.group + k % p.group;
+            for (int e = lane; e < D / 2; e += 32) reinterpret_cast<uint32_t *>(p.out + row * D)[e] = 0u;
+            if (p.lse && lane == 0) p.lse[row] = -INFINITY;
+          }
+        }
+        continue;
+      }
+      // the rows' sums over the warp, then over the block
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float s = warp_sum(l[k]);
+        if (lane == (k & 31)) s_part[warp][k] = s;
+      }
+      wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
+      tc_fence_after();
+      soft_sync();
+      const bool whole = w.nchunks == 1;
+      const int64_t item = ((int64_t)w.n * p.kv_heads + w.h) * p.mtiles + w.mt;
+      const int64_t slot = (item * p.max_chunks + w.chunk) * R;  // this chunk's rows
+      float *part = reinterpret_cast<float *>(p.part_o);         // [item][chunk][row][D]
+      if (tid < R && ok) {
+        const float sum = (s_part[0][tid] + s_part[1][tid]) + (s_part[2][tid] + s_part[3][tid]);
+        const int node = node0 + tid / p.group;
+        if (whole) {
+          const bool some = node < w.len && sum != 0.f;
+          s_f[tid] = some ? 1.f / sum : 0.f;
+          if (p.lse && node < p.T)
+            p.lse[((int64_t)w.n * p.T + node) * heads + w.h * p.group + tid % p.group] =
+                some ? (s_mb[tid] + __log2f(sum)) * kLn2 : -INFINITY;
+        } else {
+          p.part_ml[slot + tid] = make_float2(s_mb[tid], sum);
+        }
+      }
+      soft_sync();
+      float o[N];
+      tmem_ld<N>(trow + G::kO, o);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free));
+      ++live;
+      if (any_odd && tid < D) {
+        // infinities and NaN of the nodes that a row sees
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q)
+#pragma unroll 1
+          for (uint32_t r = odd[q]; r; r &= r - 1) {
+            const int j = __ffs(r) - 1;
+            const uint32_t e = p.v_new[w.n * p.vn_sn + (q * 32 + j) * p.vn_st + w.h * p.vn_sh + tid];
+            if (!nonfinite2<F16>(e)) continue;
+            const float f = unpack_lo<F16>(e);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+              if (k < R && ((tree_sees(p, w.n, w.len, node0 + k / p.group, q) >> j) & 1u)) o[k] += f;
+          }
+      }
+      __syncwarp();
+      if (tid < D && ok) {
+        int node = node0, head = 0;
+        uint16_t *out = p.out + (((int64_t)w.n * p.T + node0) * heads + w.h * p.group) * D + tid;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          if (k < R) {
+            if (whole) {
+              if (node < p.T) {
+                const float f = s_f[k];
+                out[head * D] = (uint16_t)pack2<F16>(f == 0.f ? 0.f : o[k] * f, 0.f);
+              }
+              if (++head == p.group) head = 0, ++node, out += (int64_t)heads * D;
+            } else {
+              part[(slot + k) * D + tid] = o[k];
+            }
+          }
+        }
+      }
+      if (!whole) {
+        __threadfence();
+        soft_sync();
+        if (tid == 0) s_last = ok && atomicAdd(&p.counts[item], 1) == w.nchunks - 1;
+        soft_sync();
+        if (s_last) {
+          __threadfence();
+          if (tid == 0) p.counts[item] = 0;
+          // each chunk's weight in its row, in P's buffers (the products that
+          // read them are done); s_f: 1 / sum
+          float *wt = reinterpret_cast<float *>(smem + G::kP);  // [chunk][N]
+          const int64_t first = item * p.max_chunks * R;
+          if (tid < R) {
+            float M = kNone, L = 0.f;
+            for (int k = 0; k < w.nchunks; ++k) M = fmaxf(M, __ldcg(&p.part_ml[first + (int64_t)k * R + tid]).x);
+            for (int k = 0; k < w.nchunks; ++k) {
+              const float2 a = __ldcg(&p.part_ml[first + (int64_t)k * R + tid]);
+              const float f = ex2(a.x - M);
+              wt[k * N + tid] = f;
+              L = fmaf(f, a.y, L);
+            }
+            const int node = node0 + tid / p.group;
+            const bool some = node < w.len && L != 0.f;
+            s_f[tid] = some ? 1.f / L : 0.f;
+            if (p.lse && node < p.T)
+              p.lse[((int64_t)w.n * p.T + node) * heads + w.h * p.group + tid % p.group] =
+                  some ? (M + __log2f(L)) * kLn2 : -INFINITY;
+          }
+          soft_sync();
+          constexpr int kRowsAtOnce = 128 / D;  // threads per element
+          const int d = tid % D, r0 = tid / D;
+          for (int k0 = r0; k0 < R; k0 += 16 * kRowsAtOnce) {
+            float acc[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+            for (int k = 0; k < w.nchunks; ++k) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int row = k0 + e * kRowsAtOnce;
+                if (row < R) acc[e] = fmaf(wt[k * N + row], __ldcg(&part[(first + (int64_t)k * R + row) * D + d]), acc[e]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int row = k0 + e * kRowsAtOnce, node = node0 + row / p.group;
+              if (row < R && node < p.T) {
+                const float f = s_f[row];
+                p.out[(((int64_t)w.n * p.T + node) * heads + w.h * p.group + row % p.group) * D + d] =
+                    (uint16_t)pack2<F16>(f == 0.f ? 0.f : acc[e] * f, 0.f);
+              }
+            }
+          }
+          soft_sync();  // the weights have been read before the next tile's P
+        }
+      }
+      soft_sync();  // s_f and s_mb are free for the next unit
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (s_abort && warp >= kLoadWarp && lane == 0) drain_copies<G>(b, warp - kLoadWarp, g, live);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, G::kTmem);
+}
+
+template <int D, int N, bool F16>
+cudaError_t launch(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid, cudaStream_t st) {
+  const size_t smem = GeomFew<D, N>::kSmem + 1024;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_tree_attn_few<D, N, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k_tree_attn_few<D, N, F16><<<grid, kThreads, smem, st>>>(p, maps);
+  return cudaGetLastError();
+}
+
+template <int D, bool F16>
+cudaError_t launch_n(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid, cudaStream_t st) {
+  return p.tile_rows <= 16   ? launch<D, 16, F16>(p, maps, grid, st)
+         : p.tile_rows <= 32 ? launch<D, 32, F16>(p, maps, grid, st)
+                             : launch<D, 64, F16>(p, maps, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_attention_few(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid,
+                                      cudaStream_t st) {
+  if (p.head_dim == 128) return p.f16 ? launch_n<128, true>(p, maps, grid, st) : launch_n<128, false>(p, maps, grid, st);
+  return p.f16 ? launch_n<64, true>(p, maps, grid, st) : launch_n<64, false>(p, maps, grid, st);
+}
+
+}  // namespace dc
