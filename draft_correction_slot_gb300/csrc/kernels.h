@@ -217,9 +217,8 @@ struct TreeAttnParams {
   // chunks (see tree_chunk_tiles): (request, head, row tile) items of a full
   // batch, SMs, the largest chunk, the most chunks of a request
   int items, sms, chunk_cap, max_chunks;
-  float4 *part_o;   // [item][max_chunks][head_dim / 4][tile_rows]
+  float4 *part_o;   // [item][max_chunks][tile_rows][head_dim], fp32
   float2 *part_ml;  // [item][max_chunks][tile_rows] (log2 reference, sum)
-  int *counts;      // [item], zero between calls
 };
 constexpr int kTreeTile = 128;  // tokens of a K/V tile
 struct TreeAttnMaps {

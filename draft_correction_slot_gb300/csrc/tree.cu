@@ -3,6 +3,7 @@
 // handle-free sampling and distillation entries.
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include <cmath>
 #include <initializer_list>
 #include <new>
@@ -15,9 +16,8 @@ struct dcoco_tree_handle {
   int device = 0;
   int page_shift = 0, sms = 1;
   int chunk_cap = 1, max_chunks = 1;  // see TreeAttnParams
-  void *block = nullptr;              // one device allocation: status word, counters, partial results
-  size_t counts_bytes = 0;
-  int *err = nullptr, *counts = nullptr;
+  void *block = nullptr;              // one device allocation: status word, partial results
+  int *err = nullptr;
   float2 *part_ml = nullptr;
   float4 *part_o = nullptr;
   cudaStream_t last_stream = nullptr;
@@ -93,8 +93,9 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
   // More: at most 16 tiles (2048 tokens), since requests differ in length.
   const int64_t max_tiles = ((int64_t)cfg->page_size * cfg->max_pages + dc::kTreeTile - 1) / dc::kTreeTile +
                             (cfg->max_tree + dc::kTreeTile - 1) / dc::kTreeTile;
-  h->chunk_cap = cfg->max_batch == 1 ? 1 << 30 : 16;
   const RowTiles rt(*cfg, cfg->max_tree);
+  h->chunk_cap = cfg->max_batch == 1 ? 1 << 30 : 16;
+  if (getenv("DC_CAP")) h->chunk_cap = atoi(getenv("DC_CAP"));
   const int64_t scan = max_tiles < 2048 ? max_tiles : 2048;
   for (int nt = 1; nt <= scan; ++nt) {
     const int per = dc::tree_chunk_tiles(nt, cfg->max_batch * cfg->kv_heads, h->sms, h->chunk_cap);
@@ -104,9 +105,8 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
   if (max_tiles > scan) h->max_chunks = dc::kTreeMaxChunks;
   const size_t items = (size_t)cfg->max_batch * cfg->kv_heads * rt.mtiles;
   const size_t rows = h->max_chunks > 1 ? items * h->max_chunks * rt.tile_rows : 0;
-  h->counts_bytes = items * sizeof(int);
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-  const size_t at_ml = up(256 + h->counts_bytes), at_o = at_ml + up(rows * sizeof(float2));
+  const size_t at_ml = 256, at_o = at_ml + up(rows * sizeof(float2));
   const size_t bytes = at_o + rows * cfg->head_dim * sizeof(float);
   if (cudaMalloc(&h->block, bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -115,10 +115,9 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
   }
   char *base = static_cast<char *>(h->block);
   h->err = reinterpret_cast<int *>(base);
-  h->counts = reinterpret_cast<int *>(base + 256);
   h->part_ml = reinterpret_cast<float2 *>(base + at_ml);
   h->part_o = reinterpret_cast<float4 *>(base + at_o);
-  if (cudaMemset(base, 0, 256 + h->counts_bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (cudaMemset(base, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     cudaFree(h->block);
     delete h;
@@ -168,9 +167,9 @@ int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco
   p.tree_box = nodes < dc::kTreeTile ? (nodes + 7) / 8 * 8 : dc::kTreeTile;
   p.items = c.max_batch * c.kv_heads * rt.mtiles, p.sms = h->sms;
   p.chunk_cap = h->chunk_cap, p.max_chunks = h->max_chunks;
-  p.part_o = h->part_o, p.part_ml = h->part_ml, p.counts = h->counts;
+  p.part_o = h->part_o, p.part_ml = h->part_ml;
   h->last_stream = static_cast<cudaStream_t>(stream);
-  ++h->launches;
+  h->launches += h->max_chunks > 1 ? 2 : 1;
   return cuda_status(dc::launch_tree_attention(p, h->last_stream));
 }
 
@@ -221,8 +220,7 @@ int dcoco_tree_status(dcoco_tree_handle *h) {
   int flag = 0;
   if (cudaMemcpy(&flag, h->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return DCOCO_ECUDA;
   if (flag != 0) {
-    // a block that gave up left its item's count behind
-    if (cudaMemset(h->block, 0, 256 + h->counts_bytes) != cudaSuccess) return DCOCO_ECUDA;
+    if (cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess) return DCOCO_ECUDA;
     return DCOCO_EDEVICE;
   }
   return DCOCO_OK;

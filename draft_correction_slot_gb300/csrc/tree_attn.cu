@@ -20,11 +20,12 @@
 // result does not depend on the batch.  A unit is a (request, K/V head, row
 // tile, chunk); a persistent block an SM takes every gridDim-th unit, and its
 // products run on across unit borders.  Where a request has several chunks,
-// each leaves its unnormalised output with its maximum and sum, and the last
-// to finish joins them in chunk order.
+// each leaves its unnormalised output with its reference and sum, and a second
+// kernel joins them.
 //
 // Roles: warps 0-3 softmax and output (thread = row = TMEM lane), warp 4 the
 // tensor core, warps 5-6 TMA.
+#include "launch.h"
 #include "tree_attn.cuh"
 
 namespace dc {
@@ -32,7 +33,7 @@ namespace {
 
 constexpr int kSoftWarps = 4;
 constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 
 template <int D>
 struct Geom {
@@ -60,7 +61,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) Bars b;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_last;
+  __shared__ int s_abort;
   __shared__ uint32_t s_odd[4];  // tree tile: nodes whose V holds an infinity or NaN
   const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
@@ -88,6 +89,8 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(DC_FULL_MASK, s_tmem, 0);
   int g = 0, live = 0;  // tiles and units with tiles that this role has begun
+
+  pdl_trigger();
 
   if (warp >= kLoadWarp) {
     load_tiles<G>(p, maps, sbase, b, warp - kLoadWarp, &s_abort, g, live);
@@ -344,8 +347,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
       } else {
         const int64_t item = ((int64_t)w.n * p.kv_heads + w.h) * p.mtiles + w.mt;
         const int R = p.tile_rows;
-        float4 *part = p.part_o + (item * p.max_chunks + w.chunk) * (D / 4) * R;  // [D / 4][rows]: rows adjacent
-        float2 *ml = p.part_ml + item * p.max_chunks * R;
+        float *part = reinterpret_cast<float *>(p.part_o) + ((item * p.max_chunks + w.chunk) * R + row) * D;
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           float x[32];
@@ -354,57 +356,13 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
           if (used) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              part[(q * 8 + k) * R + row] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+              reinterpret_cast<float4 *>(part)[q * 8 + k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
           }
           __syncwarp();
         }
-        if (used) ml[w.chunk * R + row] = make_float2(mref, l);
-        __threadfence();
-        ok = meet();
-        if (!ok) break;
-        if (tid == 0) s_last = atomicAdd(&p.counts[item], 1) == w.nchunks - 1;
-        ok = meet();
-        if (!ok) break;
-        if (s_last) {
-          __threadfence();
-          if (tid == 0) p.counts[item] = 0;
-          if (mine) {
-            float M = -INFINITY, L = 0.f;
-            for (int k = 0; k < w.nchunks; ++k) M = fmaxf(M, __ldcg(&ml[k * R + row]).x);
-            auto weight = [&](int k) {
-              const float2 a = __ldcg(&ml[k * R + row]);
-              return a.x == -INFINITY && a.y == 0.f ? 0.f : ex2(a.x - M);
-            };
-            for (int k = 0; k < w.nchunks; ++k) L = fmaf(weight(k), __ldcg(&ml[k * R + row]).y, L);
-            const bool some = live_row && L != 0.f;
-            const float inv = some ? 1.f / L : 0.f;
-            const float4 *po = p.part_o + item * p.max_chunks * (D / 4) * R + row;
-#pragma unroll 1
-            for (int d = 0; d < D / 4; d += 8) {
-              float4 acc[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-              for (int k = 0; some && k < w.nchunks; ++k) {
-                const float f = weight(k);
-                if (f == 0.f) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 o = __ldcg(po + ((int64_t)k * (D / 4) + d + e) * R);
-                  acc[e].x = fmaf(f, o.x, acc[e].x), acc[e].y = fmaf(f, o.y, acc[e].y);
-                  acc[e].z = fmaf(f, o.z, acc[e].z), acc[e].w = fmaf(f, o.w, acc[e].w);
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 a = acc[2 * e], d2 = acc[2 * e + 1];
-                reinterpret_cast<uint4 *>(out)[d / 2 + e] =
-                    make_uint4(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv),
-                               pack2<F16>(d2.x * inv, d2.y * inv), pack2<F16>(d2.z * inv, d2.w * inv));
-              }
-            }
-            if (p.lse) p.lse[orow] = some ? (M + __log2f(L)) * kLn2 : -INFINITY;
-          }
-        }
+        if (used)
+          p.part_ml[(item * p.max_chunks + w.chunk) * R + row] =
+              mref == -INFINITY ? make_float2(kNone, l) : make_float2(mref, l);
       }
       if (w.ntiles > 0) {
         tc_fence_before();
@@ -419,6 +377,64 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   tc_fence_after();
   if (s_abort && warp >= kLoadWarp && lane == 0) drain_copies<G>(b, warp - kLoadWarp, g, live);
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the chunks of each row: sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,
+// M = max m_k, in chunk order.  One warp a row, its elements over the lanes.
+// (Inside the attention kernel the last block of an item would do this alone:
+// at 128 KB of partial results 7 us, and some blocks had four of them to do;
+// spread over the SMs the join of 32 requests of 16 nodes takes 4 us.)
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) k_tree_join(const TreeAttnParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, heads = p.kv_heads * p.group;
+  const int64_t orow = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (orow >= (int64_t)p.N * p.T * heads) return;
+  const int hq = (int)(orow % heads), node = (int)(orow / heads % p.T), n = (int)(orow / heads / p.T);
+  int ctx, len;
+  const int nchunks = request_chunks(p, n, ctx, len);
+  if (nchunks <= 1 || node / p.tile_nodes * p.tile_nodes >= len) return;  // written by the unit itself
+  const int h = hq / p.group, mt = node / p.tile_nodes;
+  const int row = (node - mt * p.tile_nodes) * p.group + hq - h * p.group, R = p.tile_rows;
+  const int64_t item = ((int64_t)n * p.kv_heads + h) * p.mtiles + mt;
+  const float *po = reinterpret_cast<const float *>(p.part_o) + (item * p.max_chunks * R + row) * D + lane * E;
+  const float2 *ml = p.part_ml + item * p.max_chunks * R + row;
+  pdl_wait();
+  float2 a[2];  // chunks lane and 32 + lane (at most kTreeMaxChunks)
+  for (int q = 0; q < 2; ++q) a[q] = q * 32 + lane < nchunks ? __ldcg(&ml[(int64_t)(q * 32 + lane) * R]) : make_float2(kNone, 0.f);
+  const float M = warp_max(fmaxf(a[0].x, a[1].x));
+  const float w[2] = {ex2(a[0].x - M), ex2(a[1].x - M)};
+  const float L = warp_sum(w[0] * a[0].y + w[1] * a[1].y);
+  float acc[E] = {};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int k1 = min(nchunks, q * 32 + 32);
+#pragma unroll 8
+    for (int k = q * 32; k < k1; ++k) {
+      const float f = __shfl_sync(DC_FULL_MASK, w[q], k & 31);
+      const float *src = po + (int64_t)k * R * D;
+      if constexpr (E == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+        acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
+        acc[2] = fmaf(f, x.z, acc[2]), acc[3] = fmaf(f, x.w, acc[3]);
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+        acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
+      }
+    }
+  }
+  const bool some = node < len && L != 0.f;
+  const float inv = some ? 1.f / L : 0.f;
+  uint32_t *out = reinterpret_cast<uint32_t *>(p.out + orow * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = some ? pack2<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
+  if (p.lse && lane == 0) p.lse[orow] = some ? (M + __log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int D, bool F16>
+cudaError_t launch_join(const TreeAttnParams &p, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.N * p.T * p.kv_heads * p.group;
+  return launch_ex(k_tree_join<D, F16>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, true, 0, p);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -479,10 +495,13 @@ cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int64_t most = (int64_t)p.N * p.kv_heads * p.mtiles * p.max_chunks;
   const unsigned grid = (unsigned)(most < p.sms ? most : p.sms);
-  if (p.tile_rows <= 64 && p.mtiles == 1) return launch_tree_attention_few(p, maps, grid, st);
-  if (p.head_dim == 128)
-    return p.f16 ? launch<128, true>(p, maps, grid, st) : launch<128, false>(p, maps, grid, st);
-  return p.f16 ? launch<64, true>(p, maps, grid, st) : launch<64, false>(p, maps, grid, st);
+  cudaError_t e;
+  if (p.tile_rows <= 64 && p.mtiles == 1) e = launch_tree_attention_few(p, maps, grid, st);
+  else if (p.head_dim == 128) e = p.f16 ? launch<128, true>(p, maps, grid, st) : launch<128, false>(p, maps, grid, st);
+  else e = p.f16 ? launch<64, true>(p, maps, grid, st) : launch<64, false>(p, maps, grid, st);
+  if (e != cudaSuccess || p.max_chunks == 1) return e;
+  if (p.head_dim == 128) return p.f16 ? launch_join<128, true>(p, st) : launch_join<128, false>(p, st);
+  return p.f16 ? launch_join<64, true>(p, st) : launch_join<64, false>(p, st);
 }
 
 }  // namespace dc

@@ -142,6 +142,19 @@ struct Unit {
   int tile0, ntiles, nctx;       // first tile, tiles (0: no live rows), context tiles of the request
 };
 
+// Lengths of request n, clamped, and its chunks (at least 1).
+__device__ __forceinline__ int request_chunks(const TreeAttnParams &p, int n, int &ctx, int &len, bool flag = false) {
+  const int capacity = p.max_pages << p.page_shift;
+  ctx = p.ctx_len[n];
+  len = p.tree_len ? p.tree_len[n] : p.T;
+  if ((ctx < 0 || ctx > capacity || len < 0 || len > p.T) && flag) atomicOr(p.err, kErrBadLength);
+  ctx = min(max(ctx, 0), capacity);
+  len = len < 0 ? 0 : min(len, p.T);
+  const int nt = len > 0 ? (ctx + kTile - 1) / kTile + (len + kTile - 1) / kTile : 0;
+  const int per = tree_chunk_tiles(nt, p.items, p.sms, p.chunk_cap);
+  return nt > 0 ? (nt + per - 1) / per : 1;
+}
+
 // Every gridDim-th unit in the order (request, chunk, head, row tile), warp
 // by warp without communication: 32 requests' lengths at a time in the lanes.
 struct UnitIter {
@@ -152,17 +165,7 @@ struct UnitIter {
   __device__ void load(bool flag) {
     const int n = n0 + lane;
     chunks = 0;
-    if (n < p.N) {
-      const int capacity = p.max_pages << p.page_shift;
-      ctx = p.ctx_len[n];
-      len = p.tree_len ? p.tree_len[n] : p.T;
-      if ((ctx < 0 || ctx > capacity || len < 0 || len > p.T) && flag) atomicOr(p.err, kErrBadLength);
-      ctx = min(max(ctx, 0), capacity);
-      len = len < 0 ? 0 : min(len, p.T);
-      const int nt = len > 0 ? (ctx + kTile - 1) / kTile + (len + kTile - 1) / kTile : 0;
-      const int per = tree_chunk_tiles(nt, p.items, p.sms, p.chunk_cap);
-      chunks = nt > 0 ? (nt + per - 1) / per : 1;
-    }
+    if (n < p.N) chunks = request_chunks(p, n, ctx, len, flag);
     const int count = chunks * p.kv_heads * p.mtiles;
     int s = count;
 #pragma unroll
@@ -287,6 +290,8 @@ __device__ __forceinline__ void drain_copies(RingBars &b, int role, int g, int l
   if (role == 0)
     for (int t = max(0, live - 2); t < live; ++t) mbar_drain(smem_u32(&b.q_full[t & 1]), (t >> 1) & 1);
 }
+
+constexpr float kNone = -1e30f;  // reference of a row that has seen nothing: any score outgrows it
 
 template <class G>
 __device__ __forceinline__ void init_ring(RingBars &b) {

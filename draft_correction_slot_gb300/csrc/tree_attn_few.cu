@@ -10,9 +10,10 @@
 //
 // A row's reference (the maximum when last taken) is common to the four
 // warps; its sum is kept per thread, over the thread's tokens, until the
-// unit's end.  Per tile the warps only vote whether any score has outgrown its
-// row's reference by 2^8; then, and on a unit's first tile, the references are
-// taken anew across the block and O^T is rescaled.
+// unit's end.  A unit's first references are the best of four tokens' scores; per
+// tile the warps only vote whether any score has outgrown its row's reference
+// by 2^8, and only then the references are taken anew (the maxima across the
+// block) and O^T is rescaled.
 //
 // Roles: warps 0-3 softmax (thread = token = TMEM lane) and output (thread =
 // element), warp 4 the tensor core, warps 5-6 TMA.  After an expired wait the
@@ -25,8 +26,7 @@ namespace {
 
 constexpr int kSoft = 128;              // softmax threads
 constexpr int kMmaWarp = kSoft / 32, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = kSoft + 32 + 32 * kLoadWarps;
-constexpr float kNone = -1e30f;         // reference of a row that has seen nothing: any score outgrows it
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 
 template <int D, int N>
 struct GeomFew {
@@ -101,6 +101,31 @@ __device__ __forceinline__ float warp_fmax(float x) {
   return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
 }
 
+// dst[k] = sum of v[k] over the warp: at each step a lane hands half of its
+// columns to its partner (62 shuffles for 64 columns instead of 320).
+template <int N>
+__device__ __forceinline__ void warp_col_sums(float (&v)[N], float *dst) {
+  const int lane = threadIdx.x & 31;
+  int col = 0;  // first column this lane still holds
+#pragma unroll
+  for (int o = 16, n = N / 2; o > 0; o >>= 1, n >>= 1) {
+    if (n > 0) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        const float mine = up ? v[n + k] : v[k], other = up ? v[k] : v[n + k];
+        v[k] = mine + __shfl_xor_sync(DC_FULL_MASK, other, o);
+      }
+      if (up) col += n;
+    } else {
+      v[0] += __shfl_xor_sync(DC_FULL_MASK, v[0], o);
+    }
+  }
+  constexpr int kLeft = N >= 32 ? N / 32 : 1;
+#pragma unroll
+  for (int k = 0; k < kLeft; ++k) dst[col + k] = v[k];
+}
+
 template <int D, int N, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
@@ -109,7 +134,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) BarsFew b;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_last;
+  __shared__ int s_abort;
   __shared__ uint32_t s_odd[4];              // tree tile: nodes whose V holds an infinity or NaN
   __shared__ __align__(16) float s_mb[N];    // the rows' references (log2 units)
   __shared__ __align__(16) float s_f[N];     // rescale factors; at the end 1 / sum
@@ -139,6 +164,8 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(DC_FULL_MASK, s_tmem, 0);
   int g = 0, live = 0;  // tiles and units with tiles that this role has begun
+
+  pdl_trigger();
 
   if (warp >= kLoadWarp) {
     load_tiles<G>(p, maps, sbase, b, warp - kLoadWarp, &s_abort, g, live);
@@ -271,17 +298,28 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
 #pragma unroll
           for (int k = 0; k < N; ++k) v[k] = -INFINITY;
         }
-        bool renew = i == 0;
-        if (!renew) {
-          float grow = -INFINITY;
+        if (i == 0) {
+          // a unit begins with the best of four tokens' scores as the references
+          if (lane == 0) {
 #pragma unroll
-          for (int k = 0; k < N; k += 4) {
-            const float4 mb = *reinterpret_cast<const float4 *>(&s_mb[k]);
-            grow = fmaxf(grow, fmaxf(fmaf(v[k], c, -mb.x), fmaf(v[k + 1], c, -mb.y)));
-            grow = fmaxf(grow, fmaxf(fmaf(v[k + 2], c, -mb.z), fmaf(v[k + 3], c, -mb.w)));
+            for (int k = 0; k < N; k += 4)
+              *reinterpret_cast<float4 *>(&s_part[warp][k]) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
-          renew = soft_any(grow > kRescale);
+          soft_sync();
+          if (tid < N) {
+            const float m = fmaxf(fmaxf(s_part[0][tid], s_part[1][tid]), fmaxf(s_part[2][tid], s_part[3][tid])) * c;
+            s_mb[tid] = fabsf(m) < INFINITY ? m : kNone;
+          }
+          soft_sync();
         }
+        float grow = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+          const float4 mb = *reinterpret_cast<const float4 *>(&s_mb[k]);
+          grow = fmaxf(grow, fmaxf(fmaf(v[k], c, -mb.x), fmaf(v[k + 1], c, -mb.y)));
+          grow = fmaxf(grow, fmaxf(fmaf(v[k + 2], c, -mb.z), fmaf(v[k + 3], c, -mb.w)));
+        }
+        const bool renew = soft_any(grow > kRescale);
         if (renew) {
           // the rows' maxima over the tile, and references from them
 #pragma unroll
@@ -292,8 +330,8 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
           soft_sync();
           if (tid < N) {
             const float m = fmaxf(fmaxf(s_part[0][tid], s_part[1][tid]), fmaxf(s_part[2][tid], s_part[3][tid])) * c;
-            const float old = i == 0 ? kNone : s_mb[tid];
-            const bool up = m > old + kRescale;
+            const float old = s_mb[tid];
+            const bool up = m > old;
             s_mb[tid] = up ? m : old;
             s_f[tid] = up ? ex2(old - m) : 1.f;
           }
@@ -345,11 +383,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
         continue;
       }
       // the rows' sums over the warp, then over the block
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float s = warp_sum(l[k]);
-        if (lane == (k & 31)) s_part[warp][k] = s;
-      }
+      warp_col_sums<N>(l, s_part[warp]);
       wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
       tc_fence_after();
       soft_sync();
@@ -409,61 +443,6 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
               part[(slot + k) * D + tid] = o[k];
             }
           }
-        }
-      }
-      if (!whole) {
-        __threadfence();
-        soft_sync();
-        if (tid == 0) s_last = ok && atomicAdd(&p.counts[item], 1) == w.nchunks - 1;
-        soft_sync();
-        if (s_last) {
-          __threadfence();
-          if (tid == 0) p.counts[item] = 0;
-          // each chunk's weight in its row, in P's buffers (the products that
-          // read them are done); s_f: 1 / sum
-          float *wt = reinterpret_cast<float *>(smem + G::kP);  // [chunk][N]
-          const int64_t first = item * p.max_chunks * R;
-          if (tid < R) {
-            float M = kNone, L = 0.f;
-            for (int k = 0; k < w.nchunks; ++k) M = fmaxf(M, __ldcg(&p.part_ml[first + (int64_t)k * R + tid]).x);
-            for (int k = 0; k < w.nchunks; ++k) {
-              const float2 a = __ldcg(&p.part_ml[first + (int64_t)k * R + tid]);
-              const float f = ex2(a.x - M);
-              wt[k * N + tid] = f;
-              L = fmaf(f, a.y, L);
-            }
-            const int node = node0 + tid / p.group;
-            const bool some = node < w.len && L != 0.f;
-            s_f[tid] = some ? 1.f / L : 0.f;
-            if (p.lse && node < p.T)
-              p.lse[((int64_t)w.n * p.T + node) * heads + w.h * p.group + tid % p.group] =
-                  some ? (M + __log2f(L)) * kLn2 : -INFINITY;
-          }
-          soft_sync();
-          constexpr int kRowsAtOnce = 128 / D;  // threads per element
-          const int d = tid % D, r0 = tid / D;
-          for (int k0 = r0; k0 < R; k0 += 16 * kRowsAtOnce) {
-            float acc[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-            for (int k = 0; k < w.nchunks; ++k) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int row = k0 + e * kRowsAtOnce;
-                if (row < R) acc[e] = fmaf(wt[k * N + row], __ldcg(&part[(first + (int64_t)k * R + row) * D + d]), acc[e]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int row = k0 + e * kRowsAtOnce, node = node0 + row / p.group;
-              if (row < R && node < p.T) {
-                const float f = s_f[row];
-                p.out[(((int64_t)w.n * p.T + node) * heads + w.h * p.group + row % p.group) * D + d] =
-                    (uint16_t)pack2<F16>(f == 0.f ? 0.f : acc[e] * f, 0.f);
-              }
-            }
-          }
-          soft_sync();  // the weights have been read before the next tile's P
         }
       }
       soft_sync();  // s_f and s_mb are free for the next unit
