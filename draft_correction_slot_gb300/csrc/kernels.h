@@ -207,6 +207,7 @@ struct TreeAttnParams {
   int num_pages, max_pages, page_shift;
   int N, T, kv_heads, group, head_dim;
   bool f16;
+  bool few;  // at most 64 rows a K/V head: launch_tree_attention_few's kernel
   float scale;
   uint16_t *out;  // [N][T][kv_heads * group][head_dim]
   float *lse;     // [N][T][kv_heads * group] or null
@@ -217,8 +218,9 @@ struct TreeAttnParams {
   // chunks (see tree_chunk_tiles): (request, head, row tile) items of a full
   // batch, SMs, the largest chunk, the most chunks of a request
   int items, sms, chunk_cap, max_chunks;
-  float4 *part_o;   // [item][max_chunks][tile_rows][head_dim], fp32
-  float2 *part_ml;  // [item][max_chunks][tile_rows] (log2 reference, sum)
+  int part_rows;    // tile_rows as the partial results are laid out: padded by the kernel for few rows
+  float4 *part_o;   // [item][max_chunks][part_rows][head_dim], fp32
+  float2 *part_ml;  // [item][max_chunks][part_rows] (log2 reference, sum)
 };
 constexpr int kTreeTile = 128;  // tokens of a K/V tile
 struct TreeAttnMaps {
@@ -236,7 +238,9 @@ __host__ __device__ inline int tree_chunk_tiles(int nt, int items, int sms, int 
   return c < 1 ? 1 : c;
 }
 cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t st);
-// The kernel for at most 64 rows a K/V head (one row tile).
+// The kernel for at most 64 rows a K/V head (one row tile), padded to
+// tree_few_rows.
+inline int tree_few_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 cudaError_t launch_tree_attention_few(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid,
                                       cudaStream_t st);
 

@@ -53,12 +53,15 @@ int validate_tree_config(const dcoco_tree_config *c) {
 
 // Rows of a K/V head (nodes x group) in tiles of at most 128, whole nodes each.
 struct RowTiles {
-  int tile_nodes, tile_rows, mtiles;
+  int tile_nodes, tile_rows, mtiles, part_rows;
+  bool few;
   RowTiles(const dcoco_tree_config &c, int nodes) {
     const int group = c.q_heads / c.kv_heads, most = 128 / group;
     tile_nodes = nodes < most ? nodes : most;
     tile_rows = tile_nodes * group;
     mtiles = (nodes + tile_nodes - 1) / tile_nodes;
+    few = mtiles == 1 && tile_rows <= 64;
+    part_rows = few ? dc::tree_few_rows(tile_rows) : tile_rows;
   }
 };
 
@@ -104,7 +107,8 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
   }
   if (max_tiles > scan) h->max_chunks = dc::kTreeMaxChunks;
   const size_t items = (size_t)cfg->max_batch * cfg->kv_heads * rt.mtiles;
-  const size_t rows = h->max_chunks > 1 ? items * h->max_chunks * rt.tile_rows : 0;
+  // (a call on fewer nodes has no more rows than this: at most 64 where it has one tile of them)
+  const size_t rows = items * h->max_chunks * rt.part_rows;
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t at_ml = 256, at_o = at_ml + up(rows * sizeof(float2));
   const size_t bytes = at_o + rows * cfg->head_dim * sizeof(float);
@@ -164,12 +168,13 @@ int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco
   p.out = (uint16_t *)out, p.lse = lse, p.err = h->err;
   const RowTiles rt(c, nodes);
   p.mtiles = rt.mtiles, p.tile_nodes = rt.tile_nodes, p.tile_rows = rt.tile_rows;
+  p.part_rows = rt.part_rows, p.few = rt.few;
   p.tree_box = nodes < dc::kTreeTile ? (nodes + 7) / 8 * 8 : dc::kTreeTile;
   p.items = c.max_batch * c.kv_heads * rt.mtiles, p.sms = h->sms;
   p.chunk_cap = h->chunk_cap, p.max_chunks = h->max_chunks;
   p.part_o = h->part_o, p.part_ml = h->part_ml;
   h->last_stream = static_cast<cudaStream_t>(stream);
-  h->launches += h->max_chunks > 1 ? 2 : 1;
+  h->launches += 2;
   return cuda_status(dc::launch_tree_attention(p, h->last_stream));
 }
 

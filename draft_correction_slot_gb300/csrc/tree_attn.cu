@@ -19,9 +19,9 @@
 // by a rule on the handle's sizes and the request's own length, so that a
 // result does not depend on the batch.  A unit is a (request, K/V head, row
 // tile, chunk); a persistent block an SM takes every gridDim-th unit, and its
-// products run on across unit borders.  Where a request has several chunks,
-// each leaves its unnormalised output with its reference and sum, and a second
-// kernel joins them.
+// products run on across unit borders.  Each unit leaves its rows'
+// unnormalised output with their references and sums, and a second kernel
+// joins the chunks.
 //
 // Roles: warps 0-3 softmax and output (thread = row = TMEM lane), warp 4 the
 // tensor core, warps 5-6 TMA.
@@ -83,6 +83,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   for (uint32_t i = tid * 16; i < 2 * G::kQBytes; i += kThreads * 16)
     *reinterpret_cast<uint4 *>(smem + G::kQ + i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
+  if (warp == kLoadWarp && lane == 0) prefetch_maps(maps);
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
   tc_fence_before();
   __syncthreads();
@@ -161,7 +162,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
     Unit w;
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
     const int row = tid;                          // row of the tile: node row / group, head row % group
-    const int rnode = row / p.group, rhead = row - rnode * p.group;
+    const int rnode = row / p.group;
     const bool used = row < p.tile_rows;
     float c = p.scale * kLog2e;
     const bool flip = c < 0.f, zero = c == 0.f;
@@ -298,78 +299,44 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
       }
       if (!ok) break;
       // -------------------------------------------------------- the unit's output
-      const int64_t orow = ((int64_t)w.n * p.T + node) * (p.kv_heads * p.group) + w.h * p.group + rhead;
-      uint32_t *out = reinterpret_cast<uint32_t *>(p.out + orow * D);
-      auto add_odd = [&](float (&x)[32], int d0) {  // infinities and NaN of the seen nodes
+      if (w.ntiles == 0) continue;
+      ok = bar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
+      ok = __all_sync(DC_FULL_MASK, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const int64_t item = ((int64_t)w.n * p.kv_heads + w.h) * p.mtiles + w.mt;
+      const int64_t slot = (item * p.max_chunks + w.chunk) * p.part_rows + row;
+      float *part = reinterpret_cast<float *>(p.part_o) + slot * D;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float x[32];
+        tmem_ld32(trow + kO + q * 32, x);
+        if (used) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<float4 *>(part)[q * 8 + k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        }
+        __syncwarp();
+      }
+      if (used) p.part_ml[slot] = make_float2(mref == -INFINITY ? kNone : mref, l);
+      if (any_odd) {
+        // infinities and NaN of the nodes that the row sees
 #pragma unroll 1
         for (int q = 0; q < 8; ++q)
           for (uint32_t r = odd[q]; r; r &= r - 1) {
             const uint16_t *vn = p.v_new + w.n * p.vn_sn + (q * 32 + __ffs(r) - 1) * p.vn_st + w.h * p.vn_sh;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const uint32_t e = vn[d0 + k];
-              if (nonfinite2<F16>(e)) x[k] += unpack_lo<F16>(e);
-            }
-          }
-      };
-      if (w.ntiles > 0) {
-        ok = bar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
-        ok = __all_sync(DC_FULL_MASK, ok);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      if (w.nchunks == 1 || w.ntiles == 0) {
-        // whole: normalise and write.  (A unit without tiles has no live row;
-        // its first chunk writes the zeros.)
-        if (w.chunk == 0 || w.ntiles > 0) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            float x[32];
-            if (w.ntiles > 0) {
-              tmem_ld32(trow + kO + q * 32, x);
-              if (any_odd) add_odd(x, q * 32);
+            for (int k = 0; k < D; ++k) {
+              const uint32_t e = vn[k];
+              if (nonfinite2<F16>(e)) part[k] += unpack_lo<F16>(e);
             }
-            if (mine) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (live_row && l != 0.f)
-                  y = make_uint4(pack2<F16>(x[8 * k] * inv, x[8 * k + 1] * inv), pack2<F16>(x[8 * k + 2] * inv, x[8 * k + 3] * inv),
-                                 pack2<F16>(x[8 * k + 4] * inv, x[8 * k + 5] * inv), pack2<F16>(x[8 * k + 6] * inv, x[8 * k + 7] * inv));
-                reinterpret_cast<uint4 *>(out)[q * 4 + k] = y;
-              }
-            }
-            __syncwarp();
           }
-          if (mine && p.lse) p.lse[orow] = live_row && l != 0.f ? (mref + __log2f(l)) * kLn2 : -INFINITY;
-        }
-      } else {
-        const int64_t item = ((int64_t)w.n * p.kv_heads + w.h) * p.mtiles + w.mt;
-        const int R = p.tile_rows;
-        float *part = reinterpret_cast<float *>(p.part_o) + ((item * p.max_chunks + w.chunk) * R + row) * D;
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          float x[32];
-          tmem_ld32(trow + kO + q * 32, x);
-          if (any_odd) add_odd(x, q * 32);
-          if (used) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              reinterpret_cast<float4 *>(part)[q * 8 + k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-          }
-          __syncwarp();
-        }
-        if (used)
-          p.part_ml[(item * p.max_chunks + w.chunk) * R + row] =
-              mref == -INFINITY ? make_float2(kNone, l) : make_float2(mref, l);
       }
-      if (w.ntiles > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&b.o_free));
-        ++live;
-      }
+      __syncwarp();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&b.o_free));
+      ++live;
     }
   }
   tc_fence_before();
@@ -379,11 +346,12 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Joins the chunks of each row: sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,
-// M = max m_k, in chunk order.  One warp a row, its elements over the lanes.
-// (Inside the attention kernel the last block of an item would do this alone:
-// at 128 KB of partial results 7 us, and some blocks had four of them to do;
-// spread over the SMs the join of 32 requests of 16 nodes takes 4 us.)
+// The output of each row from its chunks: sum_k 2^(m_k - M) O_k / sum_k
+// 2^(m_k - M) l_k, M = max m_k, in chunk order; zeros for a node past the
+// tree's length and for one that saw nothing.  One warp a row, its elements
+// over the lanes.  (Joining inside the attention kernel, by the last block of
+// an item, took that block 7 us for 64 rows and four chunks, and some blocks
+// had four items to join.)
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) k_tree_join(const TreeAttnParams p) {
   constexpr int E = D / 32;
@@ -393,22 +361,22 @@ __global__ void __launch_bounds__(256) k_tree_join(const TreeAttnParams p) {
   const int hq = (int)(orow % heads), node = (int)(orow / heads % p.T), n = (int)(orow / heads / p.T);
   int ctx, len;
   const int nchunks = request_chunks(p, n, ctx, len);
-  if (nchunks <= 1 || node / p.tile_nodes * p.tile_nodes >= len) return;  // written by the unit itself
   const int h = hq / p.group, mt = node / p.tile_nodes;
-  const int row = (node - mt * p.tile_nodes) * p.group + hq - h * p.group, R = p.tile_rows;
+  const int row = (node - mt * p.tile_nodes) * p.group + hq - h * p.group, R = p.part_rows;
   const int64_t item = ((int64_t)n * p.kv_heads + h) * p.mtiles + mt;
   const float *po = reinterpret_cast<const float *>(p.part_o) + (item * p.max_chunks * R + row) * D + lane * E;
   const float2 *ml = p.part_ml + item * p.max_chunks * R + row;
   pdl_wait();
   float2 a[2];  // chunks lane and 32 + lane (at most kTreeMaxChunks)
-  for (int q = 0; q < 2; ++q) a[q] = q * 32 + lane < nchunks ? __ldcg(&ml[(int64_t)(q * 32 + lane) * R]) : make_float2(kNone, 0.f);
+  const int live = node < len ? nchunks : 0;
+  for (int q = 0; q < 2; ++q) a[q] = q * 32 + lane < live ? __ldcg(&ml[(int64_t)(q * 32 + lane) * R]) : make_float2(kNone, 0.f);
   const float M = warp_max(fmaxf(a[0].x, a[1].x));
   const float w[2] = {ex2(a[0].x - M), ex2(a[1].x - M)};
   const float L = warp_sum(w[0] * a[0].y + w[1] * a[1].y);
   float acc[E] = {};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int k1 = min(nchunks, q * 32 + 32);
+    const int k1 = min(live, q * 32 + 32);
 #pragma unroll 8
     for (int k = q * 32; k < k1; ++k) {
       const float f = __shfl_sync(DC_FULL_MASK, w[q], k & 31);
@@ -496,10 +464,10 @@ cudaError_t launch_tree_attention(const TreeAttnParams &p, cudaStream_t st) {
   const int64_t most = (int64_t)p.N * p.kv_heads * p.mtiles * p.max_chunks;
   const unsigned grid = (unsigned)(most < p.sms ? most : p.sms);
   cudaError_t e;
-  if (p.tile_rows <= 64 && p.mtiles == 1) e = launch_tree_attention_few(p, maps, grid, st);
+  if (p.few) e = launch_tree_attention_few(p, maps, grid, st);
   else if (p.head_dim == 128) e = p.f16 ? launch<128, true>(p, maps, grid, st) : launch<128, false>(p, maps, grid, st);
   else e = p.f16 ? launch<64, true>(p, maps, grid, st) : launch<64, false>(p, maps, grid, st);
-  if (e != cudaSuccess || p.max_chunks == 1) return e;
+  if (e != cudaSuccess) return e;
   if (p.head_dim == 128) return p.f16 ? launch_join<128, true>(p, st) : launch_join<128, false>(p, st);
   return p.f16 ? launch_join<64, true>(p, st) : launch_join<64, false>(p, st);
 }

@@ -203,6 +203,13 @@ struct UnitIter {
 };
 
 
+__device__ __forceinline__ void prefetch_maps(const TreeAttnMaps &maps) {
+  const CUtensorMap *m[] = {&maps.q, &maps.k_cache, &maps.v_cache, &maps.k_new, &maps.v_new};
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m[i])) : "memory");
+}
+
 struct RingBars {
   unsigned long long q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
 };

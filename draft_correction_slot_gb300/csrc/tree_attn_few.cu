@@ -15,6 +15,8 @@
 // by 2^8, and only then the references are taken anew (the maxima across the
 // block) and O^T is rescaled.
 //
+// Every unit leaves its result to the join kernel (tree_attn.cu).
+//
 // Roles: warps 0-3 softmax (thread = token = TMEM lane) and output (thread =
 // element), warp 4 the tensor core, warps 5-6 TMA.  After an expired wait the
 // softmax warps run their loops to the end without waiting or storing, so
@@ -42,11 +44,11 @@ struct GeomFew {
   static constexpr uint32_t kQ = kP + 2 * kPBytes;
   static constexpr uint32_t kSmem = kQ + 2 * kQBytes;
   static constexpr uint32_t kTmem = N == 16 ? 64 : N == 32 ? 128 : 256;
-  static constexpr uint32_t kS = 0, kO = 2 * N;  // TMEM columns: S^T of even and odd tiles, O^T
+  static constexpr uint32_t kS = 0, kO = 2 * N;  // TMEM columns: S^T of even and odd tiles, O^T of even and odd units
 };
 
 struct BarsFew : RingBars {
-  unsigned long long s_full[2], p_full[2], pv_done[2], o_free, done;
+  unsigned long long s_full[2], p_full[2], pv_done[2], o_free[2], done;
 };
 
 template <int N>
@@ -136,9 +138,10 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ uint32_t s_odd[4];              // tree tile: nodes whose V holds an infinity or NaN
-  __shared__ __align__(16) float s_mb[N];    // the rows' references (log2 units)
-  __shared__ __align__(16) float s_f[N];     // rescale factors; at the end 1 / sum
+  __shared__ __align__(16) float s_mb[N];  // the rows' references (log2 units)
+  __shared__ __align__(16) float s_f[N];   // rescale factors
   __shared__ __align__(16) float s_part[4][N];
+  uint32_t(*const s_word)[N] = reinterpret_cast<uint32_t(*)[N]>(s_part);  // mask words (a tile's step between uses of s_part)
   const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
 
@@ -148,8 +151,8 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
       mbar_init(smem_u32(&b.s_full[i]), 1);
       mbar_init(smem_u32(&b.p_full[i]), kSoft / 32);
       mbar_init(smem_u32(&b.pv_done[i]), 1);
+      mbar_init(smem_u32(&b.o_free[i]), kSoft / 32);
     }
-    mbar_init(smem_u32(&b.o_free), kSoft / 32);
     mbar_init(smem_u32(&b.done), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -158,6 +161,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
   for (uint32_t i = tid * 16; i < 2 * G::kQBytes; i += kThreads * 16)
     *reinterpret_cast<uint4 *>(smem + G::kQ + i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
+  if (warp == kLoadWarp && lane == 0) prefetch_maps(maps);
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), G::kTmem);
   tc_fence_before();
   __syncthreads();
@@ -180,7 +184,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
     auto pv = [&](int t, bool first, int unit) {
       const int vs = t % G::kNV;
       const bool go = bar_wait(smem_u32(&b.v_full[vs]), (t / G::kNV) & 1, &s_abort, p.err) &&
-                      (!first || unit == 0 || bar_wait(smem_u32(&b.o_free), (unit - 1) & 1, &s_abort, p.err)) &&
+                      (!first || unit < 2 || bar_wait(smem_u32(&b.o_free[unit & 1]), ((unit >> 1) - 1) & 1, &s_abort, p.err)) &&
                       bar_wait(smem_u32(&b.p_full[t & 1]), (t >> 1) & 1, &s_abort, p.err);
       if (!__all_sync(DC_FULL_MASK, go)) return false;
       tc_fence_after();
@@ -189,7 +193,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_ss(tmem + G::kO, sv + k * (2048 >> 4), sp + k * (2048 >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
+          mma_ss(tmem + G::kO + (unit & 1) * N, sv + k * (2048 >> 4), sp + k * (2048 >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
         mma_commit(smem_u32(&b.v_empty[vs]));
         mma_commit(smem_u32(&b.pv_done[t & 1]));
       }
@@ -235,7 +239,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
     UnitIter it(p, false);
     Unit w;
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-    const int heads = p.kv_heads * p.group, R = p.tile_rows;
+    const int R = p.tile_rows;
     float c = p.scale * kLog2e;
     const bool flip = c < 0.f, zero = c == 0.f;
     c = zero ? 1.f : fabsf(c);
@@ -243,13 +247,57 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
     auto wait = [&](unsigned long long *bar, int phase) {
       if (ok) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(bar), phase & 1, &s_abort, p.err));
     };
+    // A unit's output, unnormalised, leaves for the join after the first tile
+    // of the unit that follows, whose products go to the other half of O, so
+    // that the tensor core and the copies go on meanwhile.
+    Unit done = {};
+    int done_g = -1, done_unit = 0;                  // that unit's last tile (-1: none), its number
+    bool any_odd = false, done_odd = false;
+    uint32_t odd[8] = {}, odd_done[8] = {};          // nodes with an infinity or NaN in V
+    auto slot_of = [&](const Unit &u) {              // the unit's rows among the partial results
+      const int64_t item = ((int64_t)u.n * p.kv_heads + u.h) * p.mtiles + u.mt;
+      return (item * p.max_chunks + u.chunk) * N;
+    };
+    auto finish = [&] {
+      const int par = done_unit & 1;
+      wait(&b.pv_done[done_g & 1], done_g >> 1);
+      tc_fence_after();
+      float o[N];
+      tmem_ld<N>(trow + G::kO + par * N, o);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free[par]));
+      float *part = reinterpret_cast<float *>(p.part_o) + slot_of(done) * D + tid;  // [row][D]
+      if (tid < D && ok) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) part[k * D] = o[k];
+        if (done_odd) {
+          // infinities and NaN of the nodes that a row sees
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q)
+#pragma unroll 1
+            for (uint32_t r = odd_done[q]; r; r &= r - 1) {
+              const int j = __ffs(r) - 1;
+              const uint32_t e = p.v_new[done.n * p.vn_sn + (q * 32 + j) * p.vn_st + done.h * p.vn_sh + tid];
+              if (!nonfinite2<F16>(e)) continue;
+#pragma unroll 1
+              for (int k = 0; k < R; ++k)
+                if ((tree_sees(p, done.n, done.len, done.mt * p.tile_nodes + k / p.group, q) >> j) & 1u)
+                  part[k * D] += unpack_lo<F16>(e);
+            }
+        }
+      }
+      __syncwarp();
+      done_g = -1;
+    };
     while (it.next(w)) {
+      if (w.ntiles == 0) continue;
       const int node0 = w.mt * p.tile_nodes;
+      ++live;
       float l[N];  // the rows' sums over this thread's tokens
 #pragma unroll
       for (int k = 0; k < N; ++k) l[k] = 0.f;
-      uint32_t odd[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // nodes with an infinity or NaN in V
-      bool any_odd = false;
+      any_odd = false;
       for (int i = 0; i < w.ntiles; ++i, ++g) {
         const int tile = w.tile0 + i;
         const bool tree = tile >= w.nctx;
@@ -267,7 +315,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t o = s_odd[q];
-              if (tok0 == 0) odd[q] = o;
+              if (tok0 == 0) odd[q] = o, odd[4 + q] = 0;
               else odd[4 + q] = o;
               any_odd |= o != 0;
             }
@@ -283,17 +331,19 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
           for (int k = 0; k < N; ++k) v[k] = zero ? 0.f : -v[k];
         }
         if (tree) {
-          // this warp's 32 nodes are one word of each row's mask
-          int node = node0, head = 0;
-          uint32_t word = tree_sees(p, w.n, w.len, node, tok0 / 32 + warp);
+          // this warp's 32 nodes are one word of each row's mask: lane k fetches row k's
+          for (int k = lane; k < N; k += 32)
+            s_word[warp][k] = k < R ? tree_sees(p, w.n, w.len, node0 + k / p.group, tok0 / 32 + warp) : 0u;
+          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < N; ++k) {
-            v[k] = k < R && ((word >> lane) & 1u) ? v[k] : -INFINITY;
-            if (++head == p.group) {
-              head = 0, ++node;
-              if (k + 1 < R) word = tree_sees(p, w.n, w.len, node, tok0 / 32 + warp);
-            }
+          for (int k = 0; k < N; k += 4) {
+            const uint4 word = *reinterpret_cast<const uint4 *>(&s_word[warp][k]);
+            v[k] = (word.x >> lane) & 1u ? v[k] : -INFINITY;
+            v[k + 1] = (word.y >> lane) & 1u ? v[k + 1] : -INFINITY;
+            v[k + 2] = (word.z >> lane) & 1u ? v[k + 2] : -INFINITY;
+            v[k + 3] = (word.w >> lane) & 1u ? v[k + 3] : -INFINITY;
           }
+          __syncwarp();
         } else if (tid >= valid) {
 #pragma unroll
           for (int k = 0; k < N; ++k) v[k] = -INFINITY;
@@ -340,14 +390,15 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
             wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
             tc_fence_after();
             float o[N];
-            tmem_ld<N>(trow + G::kO, o);
+            const uint32_t to = trow + G::kO + ((live - 1) & 1) * N;
+            tmem_ld<N>(to, o);
 #pragma unroll
             for (int k = 0; k < N; k += 4) {
               const float4 f = *reinterpret_cast<const float4 *>(&s_f[k]);
               o[k] *= f.x, o[k + 1] *= f.y, o[k + 2] *= f.z, o[k + 3] *= f.w;
               l[k] *= f.x, l[k + 1] *= f.y, l[k + 2] *= f.z, l[k + 3] *= f.w;
             }
-            tmem_st<N>(trow + G::kO, o);
+            tmem_st<N>(to, o);
           }
         }
         uint8_t *prow = smem + G::kP + (g & 1) * G::kPBytes + tid * 128;
@@ -367,86 +418,19 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(smem_u32(&b.p_full[g & 1]));
+        if (i == 0 && done_g >= 0) finish();
       }
-      // -------------------------------------------------------- the unit's output
-      if (w.ntiles == 0) {
-        // no live row: the first chunk writes the zeros
-        if (w.chunk == 0 && ok) {
-          for (int k = warp; k < R; k += 4) {
-            const int node = node0 + k / p.group;
-            if (node >= p.T) break;
-            const int64_t row = ((int64_t)w.n * p.T + node) * heads + w.h * p.group + k % p.group;
-            for (int e = lane; e < D / 2; e += 32) reinterpret_cast<uint32_t *>(p.out + row * D)[e] = 0u;
-            if (p.lse && lane == 0) p.lse[row] = -INFINITY;
-          }
-        }
-        continue;
-      }
-      // the rows' sums over the warp, then over the block
       warp_col_sums<N>(l, s_part[warp]);
-      wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
-      tc_fence_after();
       soft_sync();
-      const bool whole = w.nchunks == 1;
-      const int64_t item = ((int64_t)w.n * p.kv_heads + w.h) * p.mtiles + w.mt;
-      const int64_t slot = (item * p.max_chunks + w.chunk) * R;  // this chunk's rows
-      float *part = reinterpret_cast<float *>(p.part_o);         // [item][chunk][row][D]
-      if (tid < R && ok) {
-        const float sum = (s_part[0][tid] + s_part[1][tid]) + (s_part[2][tid] + s_part[3][tid]);
-        const int node = node0 + tid / p.group;
-        if (whole) {
-          const bool some = node < w.len && sum != 0.f;
-          s_f[tid] = some ? 1.f / sum : 0.f;
-          if (p.lse && node < p.T)
-            p.lse[((int64_t)w.n * p.T + node) * heads + w.h * p.group + tid % p.group] =
-                some ? (s_mb[tid] + __log2f(sum)) * kLn2 : -INFINITY;
-        } else {
-          p.part_ml[slot + tid] = make_float2(s_mb[tid], sum);
-        }
-      }
+      if (tid < N && ok)
+        p.part_ml[slot_of(w) + tid] =
+            make_float2(s_mb[tid], (s_part[0][tid] + s_part[1][tid]) + (s_part[2][tid] + s_part[3][tid]));
       soft_sync();
-      float o[N];
-      tmem_ld<N>(trow + G::kO, o);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free));
-      ++live;
-      if (any_odd && tid < D) {
-        // infinities and NaN of the nodes that a row sees
-#pragma unroll 1
-        for (int q = 0; q < 8; ++q)
-#pragma unroll 1
-          for (uint32_t r = odd[q]; r; r &= r - 1) {
-            const int j = __ffs(r) - 1;
-            const uint32_t e = p.v_new[w.n * p.vn_sn + (q * 32 + j) * p.vn_st + w.h * p.vn_sh + tid];
-            if (!nonfinite2<F16>(e)) continue;
-            const float f = unpack_lo<F16>(e);
+      done = w, done_g = g - 1, done_unit = live - 1, done_odd = any_odd;
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-              if (k < R && ((tree_sees(p, w.n, w.len, node0 + k / p.group, q) >> j) & 1u)) o[k] += f;
-          }
-      }
-      __syncwarp();
-      if (tid < D && ok) {
-        int node = node0, head = 0;
-        uint16_t *out = p.out + (((int64_t)w.n * p.T + node0) * heads + w.h * p.group) * D + tid;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          if (k < R) {
-            if (whole) {
-              if (node < p.T) {
-                const float f = s_f[k];
-                out[head * D] = (uint16_t)pack2<F16>(f == 0.f ? 0.f : o[k] * f, 0.f);
-              }
-              if (++head == p.group) head = 0, ++node, out += (int64_t)heads * D;
-            } else {
-              part[(slot + k) * D + tid] = o[k];
-            }
-          }
-        }
-      }
-      soft_sync();  // s_f and s_mb are free for the next unit
+      for (int q = 0; q < 8; ++q) odd_done[q] = odd[q];
     }
+    if (done_g >= 0) finish();
   }
   tc_fence_before();
   __syncthreads();
@@ -467,8 +451,8 @@ cudaError_t launch(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned g
 
 template <int D, bool F16>
 cudaError_t launch_n(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid, cudaStream_t st) {
-  return p.tile_rows <= 16   ? launch<D, 16, F16>(p, maps, grid, st)
-         : p.tile_rows <= 32 ? launch<D, 32, F16>(p, maps, grid, st)
+  return p.part_rows == 16   ? launch<D, 16, F16>(p, maps, grid, st)
+         : p.part_rows == 32 ? launch<D, 32, F16>(p, maps, grid, st)
                              : launch<D, 64, F16>(p, maps, grid, st);
 }
 

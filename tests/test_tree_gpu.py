@@ -158,6 +158,31 @@ def test_attention_shapes(env, i, dtype):
     assert v.status() == dc.DCOCO_OK
 
 
+@pytest.mark.parametrize("T,H,g,D,page", [(1, 4, 4, 64, 32), (3, 4, 5, 128, 16), (16, 4, 2, 64, 16), (12, 4, 5, 128, 64),
+                                          (30, 4, 4, 128, 64), (70, 3, 4, 64, 128)])
+def test_attention_more_units_than_blocks(env, T, H, g, D, page):
+    """Each block takes several units, of one tile and of many, with empty ones between."""
+    torch, dc = env
+    rng = np.random.default_rng(T)
+    ctx = [int(rng.choice([0, 1, 100, 128, 400, 900, 2500, 4500])) for _ in range(70)]
+    a = Attn(torch, T, ctx, T, H, g, D, page, torch.bfloat16, tree_len=[int(rng.choice([0, 1, T, T])) for _ in ctx])
+    v = a.verifier(dc)
+    out, lse = a.run(v)
+    assert v.status() == dc.DCOCO_OK
+    again, lse2 = a.run(v)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    heads = H * g
+    for n in rng.choice(70, 12, replace=False):  # the 64-bit reference of every request would take minutes
+        b = Attn.__new__(Attn)
+        b.__dict__.update(a.__dict__)
+        one = slice(n, n + 1)
+        b.q, b.k_new, b.v_new = a.q[one], a.k_new[one], a.v_new[one]
+        b.table, b.ctx, b.sees, b.len = a.table[one], a.ctx[one], a.sees[one], a.len[one]
+        b.check(out[one], lse[one])
+    dead = torch.tensor([[t >= a.len[n] for t in range(T)] for n in range(70)], device="cuda")
+    assert (out[dead] == 0).all() and int(torch.isneginf(lse[dead]).sum()) == int(dead.sum()) * heads
+
+
 @pytest.mark.parametrize("mask", ["causal", "random", "none"])
 @pytest.mark.parametrize("ctx", [[0, 0, 0], [37, 128, 1]])
 @pytest.mark.parametrize("T", [1, 9, 40, 129])
