@@ -4,21 +4,24 @@
 // The products are turned round: S^T = K Q^T (M = the tile's 128 tokens, N =
 // the rows, padded to 16, 32 or 64) and O^T += V^T P^T (M = the head's
 // elements, N = the rows).  So a tile costs 128 x rows exponentials, where
-// rows in M cost 128 x 128 whatever their number, and each of the four softmax
-// warps has 32 tokens of every row to itself.  P^T goes to shared memory, a
+// rows in M cost 128 x 128 whatever their number.  Two softmax groups of four
+// warps have half of the rows each, and each of their warps 32 tokens of every
+// row of its group: two warps a scheduler hide each other's latencies (with
+// one group a tile's step took 2800 cycles, as long as its 64 KB take to
+// arrive, and nothing was left to make up for the unit borders).  P^T goes to shared memory, a
 // token's row of N weights the 128 bytes of a swizzle row.
 //
-// A row's reference (the maximum when last taken) is common to the four
+// A row's reference (the maximum when last taken) is common to its group's
 // warps; its sum is kept per thread, over the thread's tokens, until the
 // unit's end.  A unit's first references are the best of four tokens' scores; per
-// tile the warps only vote whether any score has outgrown its row's reference
+// tile a group's warps only vote whether any score has outgrown its row's reference
 // by 2^8, and only then the references are taken anew (the maxima across the
-// block) and O^T is rescaled.
+// group) and the rows' O^T is rescaled.
 //
 // Every unit leaves its result to the join kernel (tree_attn.cu).
 //
-// Roles: warps 0-3 softmax (thread = token = TMEM lane) and output (thread =
-// element), warp 4 the tensor core, warps 5-6 TMA.  After an expired wait the
+// Roles: warps 0-7 softmax (thread = token = TMEM lane) and output (thread =
+// element), warp 8 the tensor core, warps 9-10 TMA.  After an expired wait the
 // softmax warps run their loops to the end without waiting or storing, so
 // that their block barriers stay complete.
 #include "tree_attn.cuh"
@@ -26,7 +29,7 @@
 namespace dc {
 namespace {
 
-constexpr int kSoft = 128;              // softmax threads
+constexpr int kGroup = 128, kSoft = 2 * kGroup;  // softmax threads of a group, of both
 constexpr int kMmaWarp = kSoft / 32, kLoadWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 
@@ -51,48 +54,50 @@ struct BarsFew : RingBars {
   unsigned long long s_full[2], p_full[2], pv_done[2], o_free[2], done;
 };
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
-  if constexpr (N == 64) {
-    tmem_ld64(addr, v);
-  } else if constexpr (N == 32) {
+// 32 lanes x C consecutive columns, C = 8, 16 or 32.
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[C]) {
+  if constexpr (C == 32) {
     tmem_ld32(addr, v);
-  } else {
-    uint32_t r[16];
+  } else if constexpr (C == 16) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+        : "r"(addr)
+        : "memory");
   }
 }
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[N]) {
+template <int C>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[C]) {
 #pragma unroll
-  for (int i = 0; i < N; i += 16)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"f"(
-            v[i]),
-        "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]), "f"(v[i + 6]), "f"(v[i + 7]),
-        "f"(v[i + 8]), "f"(v[i + 9]), "f"(v[i + 10]), "f"(v[i + 11]), "f"(v[i + 12]), "f"(v[i + 13]), "f"(v[i + 14]),
-        "f"(v[i + 15]), "r"(addr + i)
-        : "memory");
+  for (int i = 0; i < C; i += 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(v[i]), "f"(v[i + 1]),
+                 "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]), "f"(v[i + 6]), "f"(v[i + 7]), "r"(addr + i)
+                 : "memory");
   tmem_st_wait();
 }
 
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool soft_any(bool x) {
+// The threads of a softmax group meet; the softmax threads of both.
+__device__ __forceinline__ void soft_sync(int group) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+__device__ __forceinline__ void both_sync() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(int group, bool x) {
   uint32_t r;
   asm volatile(
       "{\n.reg .pred p, q;\n"
       "setp.ne.u32 p, %1, 0;\n"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n"
       "selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "r"(1 + group)
       : "memory");
   return r != 0;
 }
@@ -104,7 +109,7 @@ __device__ __forceinline__ float warp_fmax(float x) {
 }
 
 // dst[k] = sum of v[k] over the warp: at each step a lane hands half of its
-// columns to its partner (62 shuffles for 64 columns instead of 320).
+// columns to its partner (31 shuffles for 32 columns instead of 160).
 template <int N>
 __device__ __forceinline__ void warp_col_sums(float (&v)[N], float *dst) {
   const int lane = threadIdx.x & 31;
@@ -137,7 +142,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
   __shared__ __align__(8) BarsFew b;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ uint32_t s_odd[4];              // tree tile: nodes whose V holds an infinity or NaN
+  __shared__ uint32_t s_odd[2][8];           // nodes whose V holds an infinity or NaN, of even and odd units
   __shared__ __align__(16) float s_mb[N];  // the rows' references (log2 units)
   __shared__ __align__(16) float s_f[N];   // rescale factors
   __shared__ __align__(16) float s_part[4][N];
@@ -238,7 +243,9 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
     // ------------------------------------------------------------ softmax, output
     UnitIter it(p, false);
     Unit w;
-    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    constexpr int C = N / 2;  // this group's rows: columns col0 .. col0 + C - 1
+    const int group = warp >> 2, quad = warp & 3, t = tid & (kGroup - 1), col0 = group * C;
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + col0;
     const int R = p.tile_rows;
     float c = p.scale * kLog2e;
     const bool flip = c < 0.f, zero = c == 0.f;
@@ -252,8 +259,7 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
     // that the tensor core and the copies go on meanwhile.
     Unit done = {};
     int done_g = -1, done_unit = 0;                  // that unit's last tile (-1: none), its number
-    bool any_odd = false, done_odd = false;
-    uint32_t odd[8] = {}, odd_done[8] = {};          // nodes with an infinity or NaN in V
+    bool seen_tree = false, done_tree = false;       // the unit has tree tiles: its s_odd holds
     auto slot_of = [&](const Unit &u) {              // the unit's rows among the partial results
       const int64_t item = ((int64_t)u.n * p.kv_heads + u.h) * p.mtiles + u.mt;
       return (item * p.max_chunks + u.chunk) * N;
@@ -262,27 +268,27 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
       const int par = done_unit & 1;
       wait(&b.pv_done[done_g & 1], done_g >> 1);
       tc_fence_after();
-      float o[N];
-      tmem_ld<N>(trow + G::kO + par * N, o);
+      float o[C];
+      tmem_ld<C>(trow + G::kO + par * N, o);
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free[par]));
-      float *part = reinterpret_cast<float *>(p.part_o) + slot_of(done) * D + tid;  // [row][D]
-      if (tid < D && ok) {
+      float *part = reinterpret_cast<float *>(p.part_o) + (slot_of(done) + col0) * D + t;  // [row][D]
+      if (t < D && ok) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) part[k * D] = o[k];
-        if (done_odd) {
+        for (int k = 0; k < C; ++k) part[k * D] = o[k];
+        if (done_tree) {
           // infinities and NaN of the nodes that a row sees
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q)
+          for (int q = 0; q < (p.T + 31) / 32; ++q)
 #pragma unroll 1
-            for (uint32_t r = odd_done[q]; r; r &= r - 1) {
+            for (uint32_t r = s_odd[par][q]; r; r &= r - 1) {
               const int j = __ffs(r) - 1;
-              const uint32_t e = p.v_new[done.n * p.vn_sn + (q * 32 + j) * p.vn_st + done.h * p.vn_sh + tid];
+              const uint32_t e = p.v_new[done.n * p.vn_sn + (q * 32 + j) * p.vn_st + done.h * p.vn_sh + t];
               if (!nonfinite2<F16>(e)) continue;
 #pragma unroll 1
-              for (int k = 0; k < R; ++k)
-                if ((tree_sees(p, done.n, done.len, done.mt * p.tile_nodes + k / p.group, q) >> j) & 1u)
+              for (int k = 0; k < C && col0 + k < R; ++k)
+                if ((tree_sees(p, done.n, done.len, done.mt * p.tile_nodes + (col0 + k) / p.group, q) >> j) & 1u)
                   part[k * D] += unpack_lo<F16>(e);
             }
         }
@@ -294,10 +300,10 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
       if (w.ntiles == 0) continue;
       const int node0 = w.mt * p.tile_nodes;
       ++live;
-      float l[N];  // the rows' sums over this thread's tokens
+      float l[C];  // the rows' sums over this thread's tokens
 #pragma unroll
-      for (int k = 0; k < N; ++k) l[k] = 0.f;
-      any_odd = false;
+      for (int k = 0; k < C; ++k) l[k] = 0.f;
+      seen_tree = false;
       for (int i = 0; i < w.ntiles; ++i, ++g) {
         const int tile = w.tile0 + i;
         const bool tree = tile >= w.nctx;
@@ -305,114 +311,118 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
         const int valid = min(kTile, (tree ? w.len : w.ctx) - tok0);
         wait(&b.s_full[g & 1], g >> 1);
         if (valid < kTile || tree) {
-          wait(&b.v_full[g % G::kNV], g / G::kNV);
-          bool bad = false;
-          if (ok) bad = clean_v_row<D, F16>(smem + G::kV + (g % G::kNV) * G::kTileBytes + tid * 128, tid < valid, tree);
-          if (tree) {
-            const uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
-            if (lane == 0) s_odd[warp] = bits;
-            soft_sync();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t o = s_odd[q];
-              if (tok0 == 0) odd[q] = o, odd[4 + q] = 0;
-              else odd[4 + q] = o;
-              any_odd |= o != 0;
+          if (group == 0) {  // the first group cleans V for both
+            wait(&b.v_full[g % G::kNV], g / G::kNV);
+            bool bad = false;
+            if (ok) bad = clean_v_row<D, F16>(smem + G::kV + (g % G::kNV) * G::kTileBytes + t * 128, t < valid, tree);
+            if (tree) {
+              const uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
+              both_sync();  // the words' last readers (two units back) are done
+              if (lane == 0) s_odd[(live - 1) & 1][tok0 / 32 + warp] = bits;
             }
-            soft_sync();
+          } else if (tree) {
+            both_sync();
           }
+          if (tree) both_sync();
+          seen_tree |= tree;
         }
         if (g >= 2) wait(&b.pv_done[g & 1], (g >> 1) - 1);  // P's buffer is free
         tc_fence_after();
-        float v[N];
-        tmem_ld<N>(trow + G::kS + (g & 1) * N, v);
-        if (flip | zero) {
+        float v[C];
+        // once, or once more when a score has outgrown its row's reference
+        for (bool renew = false;;) {
+          tmem_ld<C>(trow + G::kS + (g & 1) * N, v);
+          if (flip | zero) {
 #pragma unroll
-          for (int k = 0; k < N; ++k) v[k] = zero ? 0.f : -v[k];
-        }
-        if (tree) {
-          // this warp's 32 nodes are one word of each row's mask: lane k fetches row k's
-          for (int k = lane; k < N; k += 32)
-            s_word[warp][k] = k < R ? tree_sees(p, w.n, w.len, node0 + k / p.group, tok0 / 32 + warp) : 0u;
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < N; k += 4) {
-            const uint4 word = *reinterpret_cast<const uint4 *>(&s_word[warp][k]);
-            v[k] = (word.x >> lane) & 1u ? v[k] : -INFINITY;
-            v[k + 1] = (word.y >> lane) & 1u ? v[k + 1] : -INFINITY;
-            v[k + 2] = (word.z >> lane) & 1u ? v[k + 2] : -INFINITY;
-            v[k + 3] = (word.w >> lane) & 1u ? v[k + 3] : -INFINITY;
+            for (int k = 0; k < C; ++k) v[k] = zero ? 0.f : -v[k];
           }
-          __syncwarp();
-        } else if (tid >= valid) {
-#pragma unroll
-          for (int k = 0; k < N; ++k) v[k] = -INFINITY;
-        }
-        if (i == 0) {
-          // a unit begins with the best of four tokens' scores as the references
-          if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < N; k += 4)
-              *reinterpret_cast<float4 *>(&s_part[warp][k]) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-          }
-          soft_sync();
-          if (tid < N) {
-            const float m = fmaxf(fmaxf(s_part[0][tid], s_part[1][tid]), fmaxf(s_part[2][tid], s_part[3][tid])) * c;
-            s_mb[tid] = fabsf(m) < INFINITY ? m : kNone;
-          }
-          soft_sync();
-        }
-        float grow = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < N; k += 4) {
-          const float4 mb = *reinterpret_cast<const float4 *>(&s_mb[k]);
-          grow = fmaxf(grow, fmaxf(fmaf(v[k], c, -mb.x), fmaf(v[k + 1], c, -mb.y)));
-          grow = fmaxf(grow, fmaxf(fmaf(v[k + 2], c, -mb.z), fmaf(v[k + 3], c, -mb.w)));
-        }
-        const bool renew = soft_any(grow > kRescale);
-        if (renew) {
-          // the rows' maxima over the tile, and references from them
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            const float m = warp_fmax(v[k]);
-            if (lane == (k & 31)) s_part[warp][k] = m;
-          }
-          soft_sync();
-          if (tid < N) {
-            const float m = fmaxf(fmaxf(s_part[0][tid], s_part[1][tid]), fmaxf(s_part[2][tid], s_part[3][tid])) * c;
-            const float old = s_mb[tid];
-            const bool up = m > old;
-            s_mb[tid] = up ? m : old;
-            s_f[tid] = up ? ex2(old - m) : 1.f;
-          }
-          soft_sync();
-          if (i > 0) {
-            wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
-            tc_fence_after();
-            float o[N];
-            const uint32_t to = trow + G::kO + ((live - 1) & 1) * N;
-            tmem_ld<N>(to, o);
-#pragma unroll
-            for (int k = 0; k < N; k += 4) {
-              const float4 f = *reinterpret_cast<const float4 *>(&s_f[k]);
-              o[k] *= f.x, o[k + 1] *= f.y, o[k + 2] *= f.z, o[k + 3] *= f.w;
-              l[k] *= f.x, l[k + 1] *= f.y, l[k + 2] *= f.z, l[k + 3] *= f.w;
+          if (tree) {
+            // this warp's 32 nodes are one word of each row's mask: lane k fetches row k's
+            if (lane < C) {
+              const int row = col0 + lane;
+              s_word[quad][row] = row < R ? tree_sees(p, w.n, w.len, node0 + row / p.group, tok0 / 32 + quad) : 0u;
             }
-            tmem_st<N>(to, o);
-          }
-        }
-        uint8_t *prow = smem + G::kP + (g & 1) * G::kPBytes + tid * 128;
+            __syncwarp();
 #pragma unroll
-        for (int k = 0; k < N; k += 8) {
-          const float4 m0 = *reinterpret_cast<const float4 *>(&s_mb[k]), m1 = *reinterpret_cast<const float4 *>(&s_mb[k + 4]);
-          const float e0 = ex2(fmaf(v[k], c, -m0.x)), e1 = ex2(fmaf(v[k + 1], c, -m0.y));
-          const float e2 = ex2(fmaf(v[k + 2], c, -m0.z)), e3 = ex2(fmaf(v[k + 3], c, -m0.w));
-          const float e4 = ex2(fmaf(v[k + 4], c, -m1.x)), e5 = ex2(fmaf(v[k + 5], c, -m1.y));
-          const float e6 = ex2(fmaf(v[k + 6], c, -m1.z)), e7 = ex2(fmaf(v[k + 7], c, -m1.w));
-          l[k] += e0, l[k + 1] += e1, l[k + 2] += e2, l[k + 3] += e3;
-          l[k + 4] += e4, l[k + 5] += e5, l[k + 6] += e6, l[k + 7] += e7;
-          *reinterpret_cast<uint4 *>(prow + (((k >> 3) ^ (tid & 7)) * 16)) =
-              make_uint4(pack2<F16>(e0, e1), pack2<F16>(e2, e3), pack2<F16>(e4, e5), pack2<F16>(e6, e7));
+            for (int k = 0; k < C; k += 4) {
+              const uint4 word = *reinterpret_cast<const uint4 *>(&s_word[quad][col0 + k]);
+              v[k] = (word.x >> lane) & 1u ? v[k] : -INFINITY;
+              v[k + 1] = (word.y >> lane) & 1u ? v[k + 1] : -INFINITY;
+              v[k + 2] = (word.z >> lane) & 1u ? v[k + 2] : -INFINITY;
+              v[k + 3] = (word.w >> lane) & 1u ? v[k + 3] : -INFINITY;
+            }
+            __syncwarp();
+          } else if (t >= valid) {
+#pragma unroll
+            for (int k = 0; k < C; ++k) v[k] = -INFINITY;
+          }
+          if (renew) {
+            // references from the rows' maxima over the tile; l and O^T follow
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+              const float m = warp_fmax(v[k]);
+              if (lane == k) s_part[quad][col0 + k] = m;
+            }
+            soft_sync(group);
+            if (t < C) {
+              const int k = col0 + t;
+              const float m = fmaxf(fmaxf(s_part[0][k], s_part[1][k]), fmaxf(s_part[2][k], s_part[3][k])) * c;
+              const float old = s_mb[k];
+              s_mb[k] = fmaxf(old, m);
+              s_f[k] = m > old ? ex2(old - m) : 1.f;
+            }
+            soft_sync(group);
+#pragma unroll
+            for (int k = 0; k < C; ++k) l[k] *= s_f[col0 + k];
+            if (i > 0) {
+              wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
+              tc_fence_after();
+              float o[C];
+              const uint32_t to = trow + G::kO + ((live - 1) & 1) * N;
+              tmem_ld<C>(to, o);
+#pragma unroll
+              for (int k = 0; k < C; ++k) o[k] *= s_f[col0 + k];
+              tmem_st<C>(to, o);
+            }
+          } else if (i == 0) {
+            // a unit begins with the best of four tokens' scores as the references
+            if (lane == 0) {
+#pragma unroll
+              for (int k = 0; k < C; k += 4)
+                *reinterpret_cast<float4 *>(&s_part[quad][col0 + k]) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            }
+            soft_sync(group);
+            if (t < C) {
+              const int k = col0 + t;
+              const float m = fmaxf(fmaxf(s_part[0][k], s_part[1][k]), fmaxf(s_part[2][k], s_part[3][k])) * c;
+              s_mb[k] = fabsf(m) < INFINITY ? m : kNone;
+            }
+            soft_sync(group);
+          }
+          // exponents against the references, in v's place
+          float grow[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < C; k += 4) {
+            const float4 mb = *reinterpret_cast<const float4 *>(&s_mb[col0 + k]);
+            v[k] = fmaf(v[k], c, -mb.x), v[k + 1] = fmaf(v[k + 1], c, -mb.y);
+            v[k + 2] = fmaf(v[k + 2], c, -mb.z), v[k + 3] = fmaf(v[k + 3], c, -mb.w);
+            grow[0] = fmaxf(grow[0], v[k]), grow[1] = fmaxf(grow[1], v[k + 1]);
+            grow[2] = fmaxf(grow[2], v[k + 2]), grow[3] = fmaxf(grow[3], v[k + 3]);
+          }
+          if (renew || !soft_any(group, fmaxf(fmaxf(grow[0], grow[1]), fmaxf(grow[2], grow[3])) > kRescale)) break;
+          renew = true;
+        }
+        uint8_t *prow = smem + G::kP + (g & 1) * G::kPBytes + t * 128;
+#pragma unroll
+        for (int k = 0; k < C; k += 8) {
+          float e[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            e[x] = ex2(v[k + x]);
+            l[k + x] += e[x];
+          }
+          *reinterpret_cast<uint4 *>(prow + ((((col0 + k) >> 3) ^ (t & 7)) * 16)) =
+              make_uint4(pack2<F16>(e[0], e[1]), pack2<F16>(e[2], e[3]), pack2<F16>(e[4], e[5]), pack2<F16>(e[6], e[7]));
         }
         fence_proxy_async();
         tc_fence_before();
@@ -420,15 +430,14 @@ k_tree_attn_few(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps map
         if (lane == 0 && ok) mbar_arrive(smem_u32(&b.p_full[g & 1]));
         if (i == 0 && done_g >= 0) finish();
       }
-      warp_col_sums<N>(l, s_part[warp]);
-      soft_sync();
-      if (tid < N && ok)
-        p.part_ml[slot_of(w) + tid] =
-            make_float2(s_mb[tid], (s_part[0][tid] + s_part[1][tid]) + (s_part[2][tid] + s_part[3][tid]));
-      soft_sync();
-      done = w, done_g = g - 1, done_unit = live - 1, done_odd = any_odd;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) odd_done[q] = odd[q];
+      warp_col_sums<C>(l, s_part[quad] + col0);
+      soft_sync(group);
+      if (t < C && ok) {
+        const int k = col0 + t;
+        p.part_ml[slot_of(w) + k] = make_float2(s_mb[k], (s_part[0][k] + s_part[1][k]) + (s_part[2][k] + s_part[3][k]));
+      }
+      soft_sync(group);
+      done = w, done_g = g - 1, done_unit = live - 1, done_tree = seen_tree;
     }
     if (done_g >= 0) finish();
   }
