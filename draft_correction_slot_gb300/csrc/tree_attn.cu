@@ -8,12 +8,18 @@
 // All T * group query rows of a K/V head share that head's K and V, so a tile
 // of up to 128 of them is the M of two tensor-core products over each tile of
 // 128 tokens: S = Q K^T (both from shared memory, accumulated in TMEM) and
-// O += P V with P = e^{S - m} rounded to the inputs' type and kept in
-// TMEM.  K and V arrive by TMA, a page's tokens a copy, and are read
-// once; the running maximum and sum stay in the registers of the thread that
-// owns the row.  The running output is rescaled only when a row's maximum has
-// grown by more than 2^8 since the last time (the weights stay below 2^8,
-// their relative rounding is the same), which keeps it in TMEM nearly always.
+// O += P V with P = e^{S - m} rounded to the inputs' type, over half of S's
+// own columns.  K and V arrive by TMA, a page's tokens a copy, and are read
+// once a row tile.
+//
+// Two softmax groups of four warps take the tiles in turn, each with its own
+// S, running reference, sum and O, so that one's exponentials run under the
+// other's products (one group alone took 2870 cycles a tile, the products
+// 1024); at a unit's end their two outputs are weighed together.  A thread
+// owns a row: reference and sum stay in its registers.  A tile's weights are
+// taken against the reference at hand; only when a score has outgrown it by
+// 2^8 the reference is raised, O rescaled and the tile done again (below that
+// the weights' relative rounding is the same).
 //
 // The tiles of a request (context first, then the tree) are cut into chunks,
 // by a rule on the handle's sizes and the request's own length, so that a
@@ -23,17 +29,22 @@
 // unnormalised output with their references and sums, and a second kernel
 // joins the chunks.
 //
-// Roles: warps 0-3 softmax and output (thread = row = TMEM lane), warp 4 the
-// tensor core, warps 5-6 TMA.
+// Roles: warps 0-7 softmax and output (thread = row = TMEM lane), warp 8 the
+// tensor core, warps 9-10 TMA.  After an expired wait the softmax warps run
+// their loops to the end without waiting or storing, so that their block
+// barriers stay complete.
 #include "launch.h"
 #include "tree_attn.cuh"
 
 namespace dc {
 namespace {
 
-constexpr int kSoftWarps = 4;
+constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kThreads = 384;           // three warpgroups; warp 11 only completes the third
+// Registers a thread: 168 at launch (65,536 / 384 in steps of 8), then 224 for
+// the two softmax warpgroups and 56 for the third: 2 x 224 + 56 = 3 x 168.
+constexpr int kSoftRegs = 224, kOtherRegs = 56;
 
 template <int D>
 struct Geom {
@@ -44,39 +55,53 @@ struct Geom {
   static constexpr uint32_t kQHalf = kHalfBytes, kQBytes = kTileBytes;
   static constexpr uint32_t kQ = 0, kK = 2 * kQBytes, kV = kK + kNK * kTileBytes;
   static constexpr uint32_t kSmem = kV + kNV * kTileBytes;
+  static_assert(kSmem + 3072 <= 232448, "");
 };
 
 struct Bars : RingBars {
-  unsigned long long s_full[2], p_full[2], pv_done[2], o_free, soft, done;
+  unsigned long long s_full[2], p_full[2], pv_done[2], o_free, done;
 };
 
-// TMEM columns: S of even and odd tiles, O, P of even and odd tiles.
-constexpr uint32_t kS = 0, kO = 256, kP = 384;
+// TMEM columns, of even and odd tiles: S, whose upper half P takes over; O.
+constexpr uint32_t kS = 0, kP = 64, kO = 256;
+
+struct Small {
+  Bars bars;
+  uint32_t tmem;
+  int abort;
+  uint32_t odd[2][8];  // nodes whose V holds an infinity or NaN, of even and odd units
+  float2 ml[2][128];   // a unit's (reference, sum) of the rows, of either group
+};
+static_assert(sizeof(Small) <= 3072, "");
+
+__device__ __forceinline__ void both_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
   using G = Geom<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) Bars b;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  __shared__ uint32_t s_odd[4];  // tree tile: nodes whose V holds an infinity or NaN
+  // all of the shared memory there is: the ring at its (1024-byte aligned) base, then Small
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small &sm = *reinterpret_cast<Small *>(smem + G::kSmem);
+  Bars &b = sm.bars;
+  uint32_t &s_tmem = sm.tmem;
   const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // never: there is no static shared memory before it
+    if (tid == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&b.s_full[i]), 1);
-      mbar_init(smem_u32(&b.p_full[i]), kSoftWarps);
+      mbar_init(smem_u32(&b.p_full[i]), kSoftWarps / 2);
       mbar_init(smem_u32(&b.pv_done[i]), 1);
     }
     init_ring<G>(b);
     mbar_init(smem_u32(&b.o_free), kSoftWarps);
-    mbar_init(smem_u32(&b.soft), kSoftWarps);
     mbar_init(smem_u32(&b.done), 1);
-    s_abort = 0;
+    sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // rows past the unit's are zeros: what lies there would set off rescales
@@ -93,8 +118,12 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
 
   pdl_trigger();
 
-  if (warp >= kLoadWarp) {
-    load_tiles<G>(p, maps, sbase, b, warp - kLoadWarp, &s_abort, g, live);
+  if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+
+  if (warp >= kLoadWarp + kLoadWarps) {
+  } else if (warp >= kLoadWarp) {
+    load_tiles<G>(p, maps, sbase, b, warp - kLoadWarp, &sm.abort, g, live);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ tensor core
     constexpr uint32_t kIdS = F16 ? idesc_f16(128, kTile) : idesc_bf16(128, kTile);
@@ -102,19 +131,19 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
     UnitIter it(p, false);
     Unit w;
     bool ok = true;
-    // O (+)= P V of tile t, the first of the block's unit number `unit` if `first`
+    // O (+)= P V of tile t, one of the first two (the groups' first) of the block's unit number `unit` if `first`
     auto pv = [&](int t, bool first, int unit) {
       const int vs = t % G::kNV;
-      const bool go = bar_wait(smem_u32(&b.v_full[vs]), (t / G::kNV) & 1, &s_abort, p.err) &&
-                      (!first || unit == 0 || bar_wait(smem_u32(&b.o_free), (unit - 1) & 1, &s_abort, p.err)) &&
-                      bar_wait(smem_u32(&b.p_full[t & 1]), (t >> 1) & 1, &s_abort, p.err);
+      const bool go = bar_wait(smem_u32(&b.v_full[vs]), (t / G::kNV) & 1, &sm.abort, p.err) &&
+                      (!first || unit == 0 || bar_wait(smem_u32(&b.o_free), (unit - 1) & 1, &sm.abort, p.err)) &&
+                      bar_wait(smem_u32(&b.p_full[t & 1]), (t >> 1) & 1, &sm.abort, p.err);
       if (!__all_sync(DC_FULL_MASK, go)) return false;
       tc_fence_after();
       const uint32_t sv = mn_major_lo(sbase + G::kV + vs * G::kTileBytes);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + kO, tmem + kP + (t & 1) * 64 + k * 8, sv + k * (2048 >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
+          mma_ts(tmem + kO + (t & 1) * 128, tmem + kP + (t & 1) * 128 + k * 8, sv + k * (2048 >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
         mma_commit(smem_u32(&b.v_empty[vs]));
         mma_commit(smem_u32(&b.pv_done[t & 1]));
       }
@@ -126,10 +155,12 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
     while (ok && it.next(w)) {
       if (w.ntiles == 0) continue;
       const int qb = live & 1;
-      ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (live >> 1) & 1, &s_abort, p.err));
+      ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (live >> 1) & 1, &sm.abort, p.err));
       for (int i = 0; ok && i < w.ntiles; ++i, ++g) {
         const int ks = g % G::kNK;
-        ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.k_full[ks]), (g / G::kNK) & 1, &s_abort, p.err));
+        // S's columns hold the weights of two tiles ago until their product is done
+        ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.k_full[ks]), (g / G::kNK) & 1, &sm.abort, p.err) &&
+                                          (g < 2 || bar_wait(smem_u32(&b.pv_done[g & 1]), ((g >> 1) - 1) & 1, &sm.abort, p.err)));
         if (!ok) break;
         tc_fence_after();
         const uint32_t sq = k_major_lo(sbase + G::kQ + qb * G::kQBytes);
@@ -146,7 +177,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
         }
         __syncwarp();
         if (g > 0) ok = pv(g - 1, prev_first, prev_unit);
-        prev_first = i == 0, prev_unit = live;
+        prev_first = i < 2, prev_unit = live;
       }
       ++live;
     }
@@ -160,189 +191,191 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
     // ------------------------------------------------------------ softmax, output
     UnitIter it(p, false);
     Unit w;
-    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-    const int row = tid;                          // row of the tile: node row / group, head row % group
+    const int group = warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;             // row of the tile: node row / p.group
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     const int rnode = row / p.group;
     const bool used = row < p.tile_rows;
     float c = p.scale * kLog2e;
     const bool flip = c < 0.f, zero = c == 0.f;
     c = zero ? 1.f : fabsf(c);
-    int syncs = 0;
     bool ok = true;
-    // the four warps meet (a bounded wait, unlike bar.sync: a warp that gave up does not come)
-    auto meet = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&b.soft));
-      const bool met = bar_wait(smem_u32(&b.soft), syncs++ & 1, &s_abort, p.err);
-      return (bool)__all_sync(DC_FULL_MASK, met);
+    auto wait = [&](unsigned long long *bar, int phase) {
+      if (ok) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(bar), phase & 1, &sm.abort, p.err));
     };
-    while (ok && it.next(w)) {
-      const int node = w.mt * p.tile_nodes + rnode;
-      const bool mine = used && node < p.T;       // a row of the output
-      const bool live_row = mine && node < w.len;
-      float mref = -INFINITY, l = 0.f;            // reference (log2 units) and sum of this row
-      uint32_t odd[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // seen nodes with an infinity or NaN in V
-      bool any_odd = false;
+    while (it.next(w)) {
+      if (w.ntiles == 0) continue;
+      const int node = w.mt * p.tile_nodes + rnode, par = live & 1;
+      const bool live_row = used && node < w.len;
+      float ref = kNone, l = 0.f;                 // reference (log2 units) and sum of this row
+      bool seen_tree = false;
       for (int i = 0; i < w.ntiles; ++i, ++g) {
         const int tile = w.tile0 + i;
         const bool tree = tile >= w.nctx;
+        seen_tree |= tree;
+        if ((g & 1) != group) continue;
         const int tok0 = (tree ? tile - w.nctx : tile) * kTile;
         const int valid = min(kTile, (tree ? w.len : w.ctx) - tok0);
-        ok = bar_wait(smem_u32(&b.s_full[g & 1]), (g >> 1) & 1, &s_abort, p.err);
-        if (valid < kTile || tree) {
-          ok = ok && bar_wait(smem_u32(&b.v_full[g % G::kNV]), (g / G::kNV) & 1, &s_abort, p.err);
-          ok = __all_sync(DC_FULL_MASK, ok);
-          if (!ok) break;
-          const bool bad = clean_v_row<D, F16>(smem + G::kV + (g % G::kNV) * G::kTileBytes + row * 128, row < valid, tree);
-          if (tree) {
-            const uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
-            ok = meet();  // the previous tree tile's bits have been read
-            if (lane == 0) s_odd[warp] = bits;
-            ok = ok && meet();
-          }
-          fence_proxy_async();
-        }
-        if (g >= 2)  // P's columns are free
-          ok = ok && bar_wait(smem_u32(&b.pv_done[g & 1]), ((g >> 1) - 1) & 1, &s_abort, p.err);
-        ok = __all_sync(DC_FULL_MASK, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t ts = trow + kS + (g & 1) * 128, tp = trow + kP + (g & 1) * 64;
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // tokens of the tile that this row sees
+        wait(&b.s_full[group], g >> 1);
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};   // tokens of the tile that this row sees
         const bool masked = valid < kTile || tree;
         if (masked) {
+          wait(&b.v_full[g % G::kNV], g / G::kNV);
+          bool bad = false;
+          if (ok)
+            bad = clean_v_row<D, F16>(smem + G::kV + (g % G::kNV) * G::kTileBytes + row * 128, row < valid, tree);
+          fence_proxy_async();
+          const uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
+          if (tree && lane == 0) sm.odd[par][tok0 / 32 + quad] = bits;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int left = valid - q * 32;  // tokens of this word that exist
-            see[q] = left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
-          }
-          if (tree) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              see[q] &= tree_sees(p, w.n, w.len, live_row ? node : w.len, tok0 / 32 + q);
-              const uint32_t o = see[q] & s_odd[q];
-              if (tok0 == 0) odd[q] = o;
-              else odd[4 + q] = o;
-              any_odd |= o != 0;
-            }
+            const int left = valid - q * 32;      // tokens of this word that exist
+            see[q] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+            if (tree) see[q] = tree_sees(p, w.n, w.len, live_row ? node : w.len, tok0 / 32 + q);
           }
         }
-        // 64 scores at a time (all 128 would not fit the registers): the
-        // maximum over both halves, then the weights of the second half, still
-        // held, and of the first, read from TMEM again.
-        float v[64];
-        auto load = [&](int half) {
-          tmem_ld64(ts + half * 64, v);
-          if (flip | zero) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k) v[k] = zero ? 0.f : -v[k];
-          }
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k) {
-              const uint32_t word = half == 0 ? see[k >> 5] : see[2 + (k >> 5)];
-              v[k] = (word >> (k & 31)) & 1u ? v[k] : -INFINITY;
-            }
-          }
-        };
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          load(half);
-#pragma unroll
-          for (int k = 0; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], v[k]);
-        }
-        const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-        if (i == 0) {
-          mref = mt;
-        } else {
-          const bool grow = mt > mref + kRescale;  // from -inf: any finite maximum
-          if (__any_sync(DC_FULL_MASK, grow)) {
-            const float f = grow ? ex2(mref - mt) : 1.f;
-            if (grow) mref = mt, l *= f;
-            ok = bar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
-            ok = __all_sync(DC_FULL_MASK, ok);
-            if (!ok) break;
-            tc_fence_after();
+        tc_fence_after();
+        const uint32_t ts = trow + kS + group * 128;
+        uint32_t pk[2][32];                       // the tile's weights, packed
+        // once, or once more when a score has outgrown the reference
+        float sum;
+        for (bool renew = i < 2;; renew = true) {
+          float top = -INFINITY;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          if (renew) {
+            // the row's maximum over the tile
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              float x[32];
-              uint32_t y[32];
-              tmem_ld32(trow + kO + q * 32, x);
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t word = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+              float v[32];
+              tmem_ld32(ts + q * 32, v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(x[k] * f);
-              tmem_st32(trow + kO + q * 32, y);
+              for (int k = 0; k < 32; ++k) {
+                const float x = zero ? 0.f : flip ? -v[k] : v[k];
+                top = fmaxf(top, (word >> k) & 1u ? x : -INFINITY);
+              }
             }
-            tmem_st_wait();
-          }
-        }
-        const float mb = mref == -INFINITY ? 0.f : mref;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+            top *= c;
+            if (i < 2) {
+              ref = top > kNone ? top : kNone;
+            } else {
+              const float f = top > ref ? ex2(ref - top) : 1.f;
+              ref = fmaxf(ref, top);
+              l *= f;
+              // this group's last product is done (S was written after it)
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                float x[32];
+                uint32_t y[32];
+                tmem_ld32(trow + kO + group * 128 + q * 32, x);
 #pragma unroll
-        for (int q = 1; q >= 0; --q) {
-          if (q == 0) load(0);
-          uint32_t y[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float a = ex2(fmaf(v[2 * k], c, -mb)), d = ex2(fmaf(v[2 * k + 1], c, -mb));
-            l4[(2 * k) & 3] += a;
-            l4[(2 * k + 1) & 3] += d;
-            y[k] = pack2<F16>(a, d);
+                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(x[k] * f);
+                tmem_st32(trow + kO + group * 128 + q * 32, y);
+              }
+              tmem_st_wait();
+            }
+            top = -INFINITY;
           }
-          tmem_st32(tp + q * 32, y);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float v[16];
+            tmem_ld<16>(ts + q * 16, v);
+            if (flip | zero) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = zero ? 0.f : -v[k];
+            }
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = (see[q >> 1] >> ((q & 1) * 16 + k)) & 1u ? v[k] : -INFINITY;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              v[k] = fmaf(v[k], c, -ref);
+              top = fmaxf(top, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float a = ex2(v[2 * k]), d = ex2(v[2 * k + 1]);
+              s4[(2 * k) & 3] += a;
+              s4[(2 * k + 1) & 3] += d;
+              pk[q >> 2][(q & 3) * 8 + k] = pack2<F16>(a, d);
+            }
+          }
+          sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          if (renew || !__any_sync(DC_FULL_MASK, top > kRescale)) break;
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l += sum;
+        tmem_st32(trow + kP + group * 128, pk[0]);
+        tmem_st32(trow + kP + group * 128 + 32, pk[1]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&b.p_full[g & 1]));
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&b.p_full[group]));
       }
-      if (!ok) break;
       // -------------------------------------------------------- the unit's output
-      if (w.ntiles == 0) continue;
-      ok = bar_wait(smem_u32(&b.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, &s_abort, p.err);
-      ok = __all_sync(DC_FULL_MASK, ok);
-      if (!ok) break;
+      // Each group weighs half of the columns of both O together.
+      const int last = g - 1, g0 = g - w.ntiles;  // the unit's last and first tile
+      const bool lone = w.ntiles == 1;            // only group g0 & 1 had a tile
+      if (!lone || group == (g0 & 1)) {
+        sm.ml[group][row] = make_float2(ref, l);
+        const int mine = (last & 1) == group ? last : last - 1;
+        wait(&b.pv_done[group], mine >> 1);
+      }
+      both_sync();
       tc_fence_after();
+      const float2 other = sm.ml[group ^ 1][row];
+      const float M = fmaxf(ref, other.x), f = ex2(ref - M), fo = ex2(other.x - M);
       const int64_t item = ((int64_t)w.n * p.kv_heads + w.h) * p.mtiles + w.mt;
       const int64_t slot = (item * p.max_chunks + w.chunk) * p.part_rows + row;
-      float *part = reinterpret_cast<float *>(p.part_o) + slot * D;
+      float *part = reinterpret_cast<float *>(p.part_o) + slot * D + group * (D / 2);
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        float x[32];
-        tmem_ld32(trow + kO + q * 32, x);
-        if (used) {
+      for (int q = 0; q < D / 64; ++q) {
+        const uint32_t col = trow + kO + group * (D / 2) + q * 32;
+        float x[32], y[32];
+        if (lone) {
+          tmem_ld32(col + (g0 & 1) * 128, x);
+        } else {
+          tmem_ld32(col + group * 128, x);
+          tmem_ld32(col + (group ^ 1) * 128, y);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = fmaf(y[k], fo, x[k] * f);
+        }
+        if (used && ok) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             reinterpret_cast<float4 *>(part)[q * 8 + k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
         __syncwarp();
       }
-      if (used) p.part_ml[slot] = make_float2(mref == -INFINITY ? kNone : mref, l);
-      if (any_odd) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free));
+      if (group == 0 && used && ok)
+        p.part_ml[slot] = lone ? ((g0 & 1) ? other : make_float2(ref, l)) : make_float2(M, fmaf(other.y, fo, l * f));
+      if (seen_tree && live_row && ok) {
         // infinities and NaN of the nodes that the row sees
 #pragma unroll 1
-        for (int q = 0; q < 8; ++q)
-          for (uint32_t r = odd[q]; r; r &= r - 1) {
-            const uint16_t *vn = p.v_new + w.n * p.vn_sn + (q * 32 + __ffs(r) - 1) * p.vn_st + w.h * p.vn_sh;
+        for (int q = max(0, w.tile0 - w.nctx) * 4; q < (w.tile0 + w.ntiles - w.nctx) * 4 && q < (p.T + 31) / 32; ++q)
 #pragma unroll 1
-            for (int k = 0; k < D; ++k) {
+          for (uint32_t r = sm.odd[par][q]; r; r &= r - 1) {
+            const int jn = q * 32 + __ffs(r) - 1;
+            if (!((tree_sees(p, w.n, w.len, node, q) >> (jn & 31)) & 1u)) continue;
+            const uint16_t *vn = p.v_new + w.n * p.vn_sn + jn * p.vn_st + w.h * p.vn_sh + group * (D / 2);
+#pragma unroll 1
+            for (int k = 0; k < D / 2; ++k) {
               const uint32_t e = vn[k];
               if (nonfinite2<F16>(e)) part[k] += unpack_lo<F16>(e);
             }
           }
       }
       __syncwarp();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&b.o_free));
       ++live;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s_abort && warp >= kLoadWarp && lane == 0) drain_copies<G>(b, warp - kLoadWarp, g, live);
+  if (sm.abort && warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps && lane == 0) drain_copies<G>(b, warp - kLoadWarp, g, live);
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -442,7 +475,7 @@ bool encode_4d(CUtensorMap *map, bool f16, const void *base, int D, int na, int6
 
 template <int D, bool F16>
 cudaError_t launch(const TreeAttnParams &p, const TreeAttnMaps &maps, unsigned grid, cudaStream_t st) {
-  const size_t smem = Geom<D>::kSmem + 1024;
+  const size_t smem = Geom<D>::kSmem + sizeof(Small);
   const cudaError_t e =
       cudaFuncSetAttribute(k_tree_attn<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

@@ -105,22 +105,27 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_
       "r"(tmem_a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
-// 32 lanes x 64 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-  uint32_t r[64];
-#define R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-      : R8(0), R8(8), R8(16), R8(24), R8(32), R8(40), R8(48), R8(56)
-      : "r"(taddr));
-#undef R8
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+// 32 lanes x C consecutive columns, C = 8, 16 or 32.
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[C]) {
+  if constexpr (C == 32) {
+    tmem_ld32(addr, v);
+  } else if constexpr (C == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+        : "r"(addr)
+        : "memory");
+  }
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -155,17 +160,36 @@ __device__ __forceinline__ int request_chunks(const TreeAttnParams &p, int n, in
   return nt > 0 ? (nt + per - 1) / per : 1;
 }
 
-// Every gridDim-th unit in the order (request, chunk, head, row tile), warp
-// by warp without communication: 32 requests' lengths at a time in the lanes.
+// This block's units, warp by warp without communication: 32 requests' lengths
+// at a time in the lanes, those with the largest chunks first; units in the
+// order (request, chunk, head, row tile), dealt to the blocks to and fro.
+// (Dealt in request order and one way, the fullest of 152 blocks had 20 % more
+// tiles than the mean for 32 requests of 1000 to 8000 tokens; now 13 %.)
 struct UnitIter {
   const TreeAttnParams &p;
-  int lane, base = 0, n0 = 0, u;
+  int lane, base = 0, n0 = 0, round = 0, req = 0;
   int ctx = 0, len = 0, chunks = 0, before = 0, upto = 0, window = 0;
-  __device__ UnitIter(const TreeAttnParams &p_, bool flag) : p(p_), lane(threadIdx.x & 31), u(blockIdx.x) { load(flag); }
+  __device__ UnitIter(const TreeAttnParams &p_, bool flag) : p(p_), lane(threadIdx.x & 31) { load(flag); }
   __device__ void load(bool flag) {
-    const int n = n0 + lane;
+    req = n0 + lane;
     chunks = 0;
-    if (n < p.N) chunks = request_chunks(p, n, ctx, len, flag);
+    if (req < p.N) chunks = request_chunks(p, req, ctx, len, flag);
+    // sort the lanes by their tiles a chunk
+    const int tiles = (ctx + kTile - 1) / kTile + (len + kTile - 1) / kTile;
+    const int key = chunks > 0 ? len > 0 ? (tiles + chunks - 1) / chunks : 0 : -1;
+    int rank = 0, src = 0;
+#pragma unroll 8
+    for (int o = 0; o < 32; ++o) {
+      const int k = __shfl_sync(DC_FULL_MASK, key, o);
+      rank += k > key || (k == key && o < lane);
+    }
+#pragma unroll 8
+    for (int o = 0; o < 32; ++o)
+      if (__shfl_sync(DC_FULL_MASK, rank, o) == lane) src = o;
+    req = __shfl_sync(DC_FULL_MASK, req, src);
+    ctx = __shfl_sync(DC_FULL_MASK, ctx, src);
+    len = __shfl_sync(DC_FULL_MASK, len, src);
+    chunks = __shfl_sync(DC_FULL_MASK, chunks, src);
     const int count = chunks * p.kv_heads * p.mtiles;
     int s = count;
 #pragma unroll
@@ -178,6 +202,7 @@ struct UnitIter {
     window = __shfl_sync(DC_FULL_MASK, s, 31);
   }
   __device__ bool next(Unit &w, bool flag = false) {
+    const int u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     while (u - base >= window) {
       base += window;
       n0 += 32;
@@ -187,7 +212,7 @@ struct UnitIter {
     const int rel = u - base;
     const int src = __ffs(__ballot_sync(DC_FULL_MASK, upto > rel)) - 1;
     int i = rel - __shfl_sync(DC_FULL_MASK, before, src);
-    w.n = n0 + src;
+    w.n = __shfl_sync(DC_FULL_MASK, req, src);
     w.ctx = __shfl_sync(DC_FULL_MASK, ctx, src);
     w.len = __shfl_sync(DC_FULL_MASK, len, src);
     w.nchunks = __shfl_sync(DC_FULL_MASK, chunks, src);
@@ -197,7 +222,7 @@ struct UnitIter {
     const int nt = w.mt * p.tile_nodes < w.len ? w.nctx + (w.len + kTile - 1) / kTile : 0;
     w.tile0 = (int)((int64_t)nt * w.chunk / w.nchunks);  // chunks as even as they come
     w.ntiles = (int)((int64_t)nt * (w.chunk + 1) / w.nchunks) - w.tile0;
-    u += gridDim.x;
+    ++round;
     return true;
   }
 };

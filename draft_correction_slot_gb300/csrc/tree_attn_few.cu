@@ -54,28 +54,6 @@ struct BarsFew : RingBars {
   unsigned long long s_full[2], p_full[2], pv_done[2], o_free[2], done;
 };
 
-// 32 lanes x C consecutive columns, C = 8, 16 or 32.
-template <int C>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[C]) {
-  if constexpr (C == 32) {
-    tmem_ld32(addr, v);
-  } else if constexpr (C == 16) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-        : "r"(addr)
-        : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-        : "r"(addr)
-        : "memory");
-  }
-}
 template <int C>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[C]) {
 #pragma unroll
