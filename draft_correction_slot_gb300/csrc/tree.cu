@@ -3,7 +3,6 @@
 // handle-free sampling and distillation entries.
 #include <cuda_runtime.h>
 
-#include <cstdlib>
 #include <cmath>
 #include <initializer_list>
 #include <new>
@@ -15,7 +14,7 @@ struct dcoco_tree_handle {
   dcoco_tree_config cfg;
   int device = 0;
   int page_shift = 0, sms = 1;
-  int chunk_cap = 1, max_chunks = 1;  // see TreeAttnParams
+  int max_chunks = 1;     // see TreeAttnParams
   void *block = nullptr;              // one device allocation: status word, partial results
   int *err = nullptr;
   float2 *part_ml = nullptr;
@@ -65,6 +64,14 @@ struct RowTiles {
   }
 };
 
+// The largest chunk in tiles.  One request at a time: whatever spreads it over
+// the SMs.  Several differ in length, and small chunks balance them, but each
+// costs its block a unit border and leaves a partial result.  Measured: 32
+// requests x 16 nodes, 64 rows, to 8000 tokens: 136 / 133 / 133 us at 8 / 16 /
+// 32 tiles; 24 x 1, 4 rows, to 16001: 114 / 103 / 105 us; 8 x 64, three tiles
+// of 125 rows, to 32000: 490 / 359 / 304 us.
+int chunk_cap(const dcoco_tree_config &c, bool few) { return c.max_batch == 1 ? 1 << 30 : few ? 16 : 32; }
+
 int check_distill(int rows, int vocab, const void *logits, int dtype, int64_t row_stride, int topk,
                   const int32_t *ids, const float *teacher, float temperature) {
   if (rows < 0 || vocab < 1 || vocab > (1 << 20) || topk < 1 || topk > 1024) return DCOCO_EINVAL;
@@ -92,16 +99,12 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
     delete h;
     return DCOCO_ECUDA;
   }
-  // Chunk sizes.  One request at a time: whatever spreads it over the SMs.
-  // More: at most 16 tiles (2048 tokens), since requests differ in length.
   const int64_t max_tiles = ((int64_t)cfg->page_size * cfg->max_pages + dc::kTreeTile - 1) / dc::kTreeTile +
                             (cfg->max_tree + dc::kTreeTile - 1) / dc::kTreeTile;
   const RowTiles rt(*cfg, cfg->max_tree);
-  h->chunk_cap = cfg->max_batch == 1 ? 1 << 30 : 16;
-  if (getenv("DC_CAP")) h->chunk_cap = atoi(getenv("DC_CAP"));
   const int64_t scan = max_tiles < 2048 ? max_tiles : 2048;
   for (int nt = 1; nt <= scan; ++nt) {
-    const int per = dc::tree_chunk_tiles(nt, cfg->max_batch * cfg->kv_heads, h->sms, h->chunk_cap);
+    const int per = dc::tree_chunk_tiles(nt, cfg->max_batch * cfg->kv_heads, h->sms, chunk_cap(*cfg, true));
     const int n = (nt + per - 1) / per;
     if (n > h->max_chunks) h->max_chunks = n;
   }
@@ -171,7 +174,7 @@ int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco
   p.part_rows = rt.part_rows, p.few = rt.few;
   p.tree_box = nodes < dc::kTreeTile ? (nodes + 7) / 8 * 8 : dc::kTreeTile;
   p.items = c.max_batch * c.kv_heads * rt.mtiles, p.sms = h->sms;
-  p.chunk_cap = h->chunk_cap, p.max_chunks = h->max_chunks;
+  p.chunk_cap = chunk_cap(c, rt.few), p.max_chunks = h->max_chunks;
   p.part_o = h->part_o, p.part_ml = h->part_ml;
   h->last_stream = static_cast<cudaStream_t>(stream);
   h->launches += 2;

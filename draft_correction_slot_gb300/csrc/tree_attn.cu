@@ -274,33 +274,34 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
               }
               tmem_st_wait();
             }
-            top = -INFINITY;
           }
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t raw[2][32];
+          tmem_ld32_start(ts, raw[0]);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float v[16];
-            tmem_ld<16>(ts + q * 16, v);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t(&r)[32] = raw[q & 1];
+            tmem_ld_wait(r);
+            if (q < 3) tmem_ld32_start(ts + (q + 1) * 32, raw[(q + 1) & 1]);  // in flight during this part's arithmetic
             if (flip | zero) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = zero ? 0.f : -v[k];
+              for (int k = 0; k < 32; ++k) r[k] = zero ? 0u : r[k] ^ 0x80000000u;
             }
             if (masked) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = (see[q >> 1] >> ((q & 1) * 16 + k)) & 1u ? v[k] : -INFINITY;
+              for (int k = 0; k < 32; ++k) r[k] = (see[q] >> k) & 1u ? r[k] : 0xFF800000u;
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              v[k] = fmaf(v[k], c, -ref);
-              top = fmaxf(top, v[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float a = ex2(v[2 * k]), d = ex2(v[2 * k + 1]);
+              const float x = fmaf(__uint_as_float(r[2 * k]), c, -ref), y = fmaf(__uint_as_float(r[2 * k + 1]), c, -ref);
+              t4[k & 3] = fmaxf(t4[k & 3], fmaxf(x, y));
+              const float a = ex2(x), d = ex2(y);
               s4[(2 * k) & 3] += a;
               s4[(2 * k + 1) & 3] += d;
-              pk[q >> 2][(q & 3) * 8 + k] = pack2<F16>(a, d);
+              pk[q >> 1][(q & 1) * 16 + k] = pack2<F16>(a, d);
             }
           }
+          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
           if (renew || !__any_sync(DC_FULL_MASK, top > kRescale)) break;
         }

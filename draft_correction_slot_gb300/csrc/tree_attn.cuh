@@ -127,6 +127,24 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[C]) {
         : "memory");
   }
 }
+// A load in flight: 32 columns; its registers are the caller's only after
+// tmem_ld_wait.
+#define DC_R8(c, i) c(r[i]), c(r[i + 1]), c(r[i + 2]), c(r[i + 3]), c(r[i + 4]), c(r[i + 5]), c(r[i + 6]), c(r[i + 7])
+#define DC_R32(c) DC_R8(c, 0), DC_R8(c, 8), DC_R8(c, 16), DC_R8(c, 24)
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : DC_R32("=r")
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : DC_R32("+r")::"memory");
+}
+#undef DC_R32
+#undef DC_R8
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -174,6 +192,8 @@ struct UnitIter {
     req = n0 + lane;
     chunks = 0;
     if (req < p.N) chunks = request_chunks(p, req, ctx, len, flag);
+    scan();
+    if (p.N <= 32 && window <= (int)gridDim.x) return;  // one unit a block at most
     // sort the lanes by their tiles a chunk
     const int tiles = (ctx + kTile - 1) / kTile + (len + kTile - 1) / kTile;
     const int key = chunks > 0 ? len > 0 ? (tiles + chunks - 1) / chunks : 0 : -1;
@@ -190,6 +210,9 @@ struct UnitIter {
     ctx = __shfl_sync(DC_FULL_MASK, ctx, src);
     len = __shfl_sync(DC_FULL_MASK, len, src);
     chunks = __shfl_sync(DC_FULL_MASK, chunks, src);
+    scan();
+  }
+  __device__ void scan() {  // units before and up to each lane's request, in the window
     const int count = chunks * p.kv_heads * p.mtiles;
     int s = count;
 #pragma unroll
