@@ -7,19 +7,43 @@
 // min-p is a bound on d.  The token is the smallest id whose cumulative kept
 // weight exceeds u times the kept total.
 //
+// One cluster of blocks a row.  Its blocks bring their slices of the row into
+// shared memory once (DRAM sees every logit once) and take from there:
+//   the maximum;
+//   a histogram of d, its linear bins a 2048th of the row's range, merged
+//     over the cluster: of each 16-byte vector's best token for top-k (the
+//     k-th best vector bounds the k-th best token from below), of all tokens
+//     for top-p;
+//   the few candidates around the border, collected in the first block;
+//   and, unless top-k leaves only those, the weights: summed over all tokens,
+//     over those surely kept, and per 1024 tokens for the draw.
+// The first block sorts the candidates, finds the border exactly, and draws:
+// the 1024 tokens by their sums, then the token in them.
+// What this does not cover (top_k over kTopkMost of a larger vocabulary,
+// borders with more tokens around them than the list holds, infinite
+// logits) the first block does alone by bisection over the row, ~100 passes.
+//
 // Weights are summed as 64-bit integers in units of 2^-40 (V <= 2^20 of them
-// stay below 2^60): the sums are exact, so neither the threads' order nor
-// how a row is split over them can change a token.
-// One block a row; the last value and id are found by bisection, a pass over
-// the row each step.
+// stay below 2^60), up to 32 of one thread's first in fp32: the same sums
+// whatever the cluster's size and the blocks' timing.  e^{-d / t} is taken as
+// 2^-z with z = d / (t ln 2) carried with its rounding error: a row's border
+// can lie where a token has 10^-6 of the mass, and a bias of 10^-7 common to
+// all weights beyond it would move it.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 
 namespace dc {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 typedef unsigned long long u64;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBins = 2048;      // histogram bins
+constexpr int kList = 2048;      // candidates the list holds
+constexpr int kTopkMost = 1024;  // largest top_k of the candidate path
+constexpr int kChunk = 1024;     // tokens of a partial sum (one warp)
+constexpr int kMostBlocks = 8;   // blocks of a cluster
+constexpr size_t kMostSlice = 96 * 1024;  // bytes of a slice held in shared memory
 
 // Larger key <=> larger value; -0 and +0 share a key, NaN counts as -inf.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -27,6 +51,7 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return x != x ? 0x007FFFFFu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+// Sum over the block; s: kWarps entries.
 __device__ __forceinline__ u64 block_sum(u64 v, u64 *s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -67,46 +92,12 @@ struct SampleRow {
   }
 };
 
-template <bool F32>
-__global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
-  __shared__ u64 s_red[kWarps];
-  const int row = blockIdx.x, tid = threadIdx.x, V = p.V;
-  SampleRow<F32> r;
-  r.x = static_cast<const char *>(p.logits) + row * p.stride * (F32 ? 4 : 2);
-  // the maximum and its lowest id, as one integer
-  u64 best = 0;
-  for (int v = tid; v < V; v += kThreads) {
-    const u64 k = (u64)order_key(r.value(v)) << 32 | (uint32_t)(V - v);
-    best = k > best ? k : best;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const u64 k = __shfl_xor_sync(DC_FULL_MASK, best, o);
-    best = k > best ? k : best;
-  }
-  if ((tid & 31) == 0) s_red[tid >> 5] = best;
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w) best = s_red[w] > best ? s_red[w] : best;
-  const int arg = V - (int)(uint32_t)best;
-  r.mx = r.value(arg);
-  float t = p.temperature ? p.temperature[row] : 1.f;
-  if (t != t) t = 1.f;
-  if (r.mx == -INFINITY || t <= 0.f) {
-    if (tid == 0) {
-      p.tokens[row] = r.mx == -INFINITY ? -1 : arg;
-      if (p.logprob) p.logprob[row] = r.mx == -INFINITY ? -INFINITY : 0.f;
-    }
-    return;
-  }
-  const double c = 1.4426950408889634 / fmax((double)t, 1e-30);
-  r.ch = (float)c, r.cl = (float)(c - (double)r.ch);
-  int k = p.top_k ? p.top_k[row] : 0;
-  if (k <= 0 || k > V) k = V;
-  float tp = p.top_p ? p.top_p[row] : 1.f, mp = p.min_p ? p.min_p[row] : 0.f;
-  if (tp != tp) tp = 1.f;
-  r.dmax = mp > 0.f ? __double2float_rd(fmax(0.0, -(double)t * log((double)fminf(mp, 1.f)))) : INFINITY;
-  r.key = 0, r.last = V;
 
+// The general path: the border's value by bisection on the key, its id by
+// bisection on the id, a pass over the row each step.  One block.
+template <bool F32>
+__device__ __noinline__ int sample_general(SampleRow<F32> r, int V, int k, float tp, float u, u64 *s_red, u64 *kept) {
+  const int tid = threadIdx.x;
   // The shortest prefix of the order for which `over` (monotone in the
   // prefix) of its count and mass holds: its last value by bisection on the
   // key, then its last id.
@@ -158,8 +149,6 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
     if (r.kept(f, v)) total += r.weight(f);
   }
   total = block_sum(total, s_red);
-  float u = p.u[row];
-  if (!(u > 0.f)) u = 0.f;
   u64 target = (u64)((double)u * (double)total);  // below `total`
   if (target >= total) target = total - 1;
   int a = 0, b = V - 1;
@@ -173,19 +162,668 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
     if (block_sum(m, s_red) > target) b = mid;
     else a = mid + 1;
   }
-  if (tid == 0) {
-    p.tokens[row] = a;
-    const float x = r.value(a), d = x == r.mx ? 0.f : r.mx - x;
-    if (p.logprob) p.logprob[row] = (float)(-(double)d / fmax((double)t, 1e-30) - log((double)total * 0x1p-40));
+  *kept = total;
+  return a;
+}
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// Address of this block's shared `p` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer(const void *p, int rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ void put32(uint32_t at, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void put64(uint32_t at, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t get32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t add32(uint32_t at, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(at), "r"(v) : "memory");
+  return old;
+}
+
+// Inclusive scan over the block (T: u64, double or int); s: kWarps entries.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(DC_FULL_MASK, v, o);
+    if (lane >= o) v += y;
   }
+  __syncthreads();
+  if (lane == 31) s[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v += s[w];
+  return v;
+}
+// The lowest thread with `hit`, and its values; -1 if none.
+__device__ __forceinline__ int block_first(bool hit, int *s) {
+  __syncthreads();
+  if (threadIdx.x == 0) *s = kThreads;
+  __syncthreads();
+  if (hit) atomicMin(s, (int)threadIdx.x);
+  __syncthreads();
+  return *s == kThreads ? -1 : *s;
+}
+
+// Sorts list[0, n) descending (n a power of two), the whole block.
+__device__ __forceinline__ void sort_desc(u64 *list, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
+        const int a = 2 * j * (i / j) + i % j, b = a + j;
+        const u64 x = list[a], y = list[b];
+        if ((x < y) == ((a & k) == 0)) list[a] = y, list[b] = x;
+      }
+    }
+  __syncthreads();
+}
+
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What a block is told by the first one.
+struct Orders {
+  int step;        // kCollect, kWeigh (and collect), kStop
+  float from, to;  // bins (as floats): collect [from, to), weigh as surely kept what lies before `from`
+};
+enum { kStop, kCollect, kWeigh };
+
+struct SampleShared {
+  u64 red[kWarps];
+  double redd[kWarps];
+  int redi[kWarps];
+  int first;
+  float mx[kMostBlocks], low[kMostBlocks];
+  uint32_t arg[kMostBlocks];
+  u64 sure[kMostBlocks], all[kMostBlocks];
+  uint32_t listed;
+  Orders orders;
+};
+
+// E logits of a 16-byte vector as floats.
+template <bool F32>
+__device__ __forceinline__ void unpack(const uint4 &w, float (&f)[F32 ? 4 : 8]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) f[i] = __uint_as_float(x[i]);
+    else f[2 * i] = __uint_as_float(x[i] << 16), f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 3)
+k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) {
+  constexpr int E = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ SampleShared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.z, V = p.V;
+  u64 *list = reinterpret_cast<u64 *>(smem);                 // [kList]; before the candidates: the histogram
+  uint32_t *hist = reinterpret_cast<uint32_t *>(smem);       // [kBins]
+  u64 *chunk_all = list + kList;                             // [chunks_all], the first block's: kept weight a chunk
+  const int share = kBins / blocks;                          // merged bins that each block holds
+  uint32_t *merged = reinterpret_cast<uint32_t *>(chunk_all + (chunks_all + 1) / 2 * 2);  // (16-byte steps: `data` is read in vectors)
+  uint8_t *data = reinterpret_cast<uint8_t *>(merged + share);
+  const int64_t row = blockIdx.x;
+  const uint8_t *src = static_cast<const uint8_t *>(p.logits) + row * p.stride * kSize;
+  const int v0 = rank * slice, v1 = min(V, v0 + slice), nv = max(0, v1 - v0);
+  const int nch = (nv + kChunk - 1) / kChunk, vecs = nch * (kChunk / E);
+  cluster_arrive();  // (this block is there)
+
+  // A vector of the slice, whole and without NaN: past the end, and where a logit is NaN, -inf.
+  auto fetch = [&](int i) {
+    const int at = v0 + i * E;
+    uint4 w;
+    if (at + E <= V) {
+      w = ld_stream_v4(src + (int64_t)at * kSize);
+    } else {
+      uint32_t x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (F32) {
+          x[q] = at + q < V ? reinterpret_cast<const uint32_t *>(src)[at + q] : 0xFF800000u;
+        } else {
+          const uint32_t a = at + 2 * q < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q] : 0xFF80u;
+          const uint32_t b = at + 2 * q + 1 < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q + 1] : 0xFF80u;
+          x[q] = a | b << 16;
+        }
+      }
+      w = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (F32) {
+        if ((x[q] & 0x7FFFFFFFu) > 0x7F800000u) x[q] = 0xFF800000u;
+      } else {
+        if ((x[q] & 0x7FFFu) > 0x7F80u) x[q] = (x[q] & 0xFFFF0000u) | 0xFF80u;
+        if ((x[q] & 0x7FFF0000u) > 0x7F800000u) x[q] = (x[q] & 0xFFFFu) | 0xFF800000u;
+      }
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+  };
+  auto vec = [&](int i) { return held ? reinterpret_cast<const uint4 *>(data)[i] : fetch(i); };
+  // a vector's largest logit
+  auto best_of = [&](const uint4 &w) {
+    float f[E];
+    unpack<F32>(w, f);
+    float m = f[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) m = fmaxf(m, f[e]);
+    return m;
+  };
+
+  // ---------------------------------------------------------------- the maximum
+  // `low`: the least of the vectors' maxima, which sets the histogram's range
+  float mx = -INFINITY, low = INFINITY;
+  for (int i0 = tid; i0 < vecs; i0 += 4 * kThreads) {
+    uint4 w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i0 + q * kThreads < vecs) w[q] = fetch(i0 + q * kThreads);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (i0 + q * kThreads >= vecs) continue;
+      if (held) reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] = w[q];
+      const float m = best_of(w[q]);
+      mx = fmaxf(mx, m);
+      low = fminf(low, m == -INFINITY ? INFINITY : m);
+    }
+  }
+  mx = warp_max(mx), low = -warp_max(-low);
+  if (lane == 0) s.redd[warp] = mx, s.red[warp] = __float_as_uint(low);
+  for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+  if (tid == 0) s.listed = 0;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, (float)s.redd[w]), low = fminf(low, __uint_as_float((uint32_t)s.red[w]));
+  cluster_wait();  // every block of the cluster is there
+  if (tid < blocks) {
+    put32(peer(&s.mx[rank], tid), __float_as_uint(mx));
+    put32(peer(&s.low[rank], tid), __float_as_uint(low));
+  }
+  cluster_sync();
+  for (int b = 0; b < blocks; ++b) mx = fmaxf(mx, s.mx[b]), low = fminf(low, s.low[b]);
+
+  // ---------------------------------------------------------------- the row's parameters
+  float t = p.temperature ? p.temperature[row] : 1.f;
+  if (t != t) t = 1.f;
+  int k = p.top_k ? p.top_k[row] : 0;
+  if (k <= 0 || k > V) k = V;
+  float tp = p.top_p ? p.top_p[row] : 1.f, mp = p.min_p ? p.min_p[row] : 0.f, u = p.u[row];
+  if (tp != tp) tp = 1.f;
+  if (!(u > 0.f)) u = 0.f;
+  if (mx == -INFINITY) {
+    if (rank == 0 && tid == 0) {
+      p.tokens[row] = -1;
+      if (p.logprob) p.logprob[row] = -INFINITY;
+    }
+    return;
+  }
+  if (t <= 0.f) {
+    // the lowest id of the maximum
+    uint32_t arg = 0xFFFFFFFFu;
+    for (int i = tid; i < vecs; i += kThreads) {
+      float f[E];
+      unpack<F32>(vec(i), f);
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (f[e] == mx) arg = min(arg, (uint32_t)(v0 + i * E + e));
+    }
+    arg = __reduce_min_sync(DC_FULL_MASK, arg);
+    __syncthreads();
+    if (lane == 0) s.redi[warp] = (int)arg;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) arg = min(arg, (uint32_t)s.redi[w]);
+    if (tid == 0) put32(peer(&s.arg[rank], 0), arg);
+    cluster_sync();
+    if (rank == 0 && tid == 0) {
+      for (int b = 0; b < blocks; ++b) arg = min(arg, s.arg[b]);
+      p.tokens[row] = (int)arg;
+      if (p.logprob) p.logprob[row] = 0.f;
+    }
+    return;
+  }
+  SampleRow<F32> r;
+  r.x = src;
+  r.mx = mx;
+  const double td = fmax((double)t, 1e-30), c = 1.4426950408889634 / td;
+  r.ch = (float)c, r.cl = (float)(c - (double)r.ch);
+  r.dmax = mp > 0.f ? __double2float_rd(fmax(0.0, -(double)t * log((double)fminf(mp, 1.f)))) : INFINITY;
+  r.key = 0, r.last = V;
+
+  // ---------------------------------------------------------------- which way
+  const bool small = V <= kList;                       // everything is a candidate
+  const bool by_list = small || (k < V && k <= kTopkMost);
+  const bool by_mass = !by_list && k == V && tp < 1.f;
+  const bool whole = k == V && tp >= 1.f && !small;    // min-p at most
+  bool general = !(by_list || by_mass || whole) || mx == INFINITY;
+  // bins of d, 1.5 times the range down to the least vector maximum
+  const float range = 1.5f * fmaxf(mx - low, 1e-6f), scale = (float)kBins / range;
+  if (!small && !whole && !(range < 1e30f)) general = true;
+  if (!general && (by_mass || (by_list && !small))) {
+    // histogram
+    for (int i = tid; i < vecs; i += kThreads) {
+      const uint4 w = vec(i);
+      if (by_list) {
+        const float m = best_of(w);
+        if (m > -INFINITY) atomicAdd(&hist[min((int)((mx - m) * scale), kBins - 1)], 1u);
+      } else {
+        float f[E];
+        unpack<F32>(w, f);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (f[e] > -INFINITY) atomicAdd(&hist[(int)fminf((mx - f[e]) * scale, (float)(kBins - 1))], 1u);
+      }
+    }
+    cluster_sync();
+    for (int i = tid; i < share; i += kThreads) {
+      uint32_t n = 0;
+      for (int b = 0; b < blocks; ++b) n += get32(peer(&hist[rank * share + i], b));
+      merged[i] = n;
+    }
+    cluster_sync();
+  }
+
+  // The first block decides; the others do as told, any number of times.
+  constexpr int kPer = kBins / kThreads;
+  u64 sure_all = 0, all_all = 0;  // (first block) weight surely kept, and of all tokens
+  int tries = 0;
+  int b1 = 0, b2 = kBins;         // (first block) bins collected: [b1, b2)
+  while (true) {
+    if (rank == 0) {
+      Orders o{kStop, 0.f, 0.f};
+      if (general) {
+      } else if (whole) {
+        o = Orders{kWeigh, INFINITY, INFINITY};
+      } else if (small) {
+        o = Orders{kCollect, 0.f, INFINITY};
+      } else {
+        // this thread's bins
+        int n[kPer], sum = 0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const int bin = tid * kPer + q;
+          n[q] = (int)get32(peer(&merged[bin % share], bin / share));
+          sum += n[q];
+        }
+        if (by_list) {
+          // the bin where the vectors' count reaches k: its tokens and the better ones hold the k best
+          int upto = block_scan(sum, s.redi) - sum, bin = kBins - 1;
+          bool hit = false;
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            if (!hit && upto < k && upto + n[q] >= k) hit = true, bin = tid * kPer + q;
+            upto += n[q];
+          }
+          const int who = block_first(hit, &s.first);
+          if (tid == max(who, 0)) s.redi[0] = who < 0 ? kBins : bin + 1;
+          __syncthreads();
+          const int to = s.redi[0];
+          o = Orders{kCollect, 0.f, to >= kBins ? INFINITY : (float)to};
+        } else {
+          // masses by the bins' middles; after a first try, from its exact masses on
+          double m[kPer], mass = 0.;
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            m[q] = n[q] ? (double)n[q] * ex2_approx(-((float)(tid * kPer + q) + 0.5f) / scale * r.ch) : 0.;
+            mass += m[q];
+          }
+          const double cum = block_scan(mass, s.redd);
+          __syncthreads();
+          if (tid == kThreads - 1) s.redd[0] = cum;
+          __syncthreads();
+          const double total = tries ? (double)all_all * 0x1p-40 : s.redd[0];
+          double shift = 0.;  // what an exact mass says the middles' are off by, at bin b1
+          if (tries) {
+            __syncthreads();
+            if (tid == b1 / kPer) {
+              double before = cum - mass;
+              for (int q = 0; q < b1 % kPer; ++q) before += m[q];
+              s.redd[1] = (double)sure_all * 0x1p-40 - before;
+            }
+            __syncthreads();
+            shift = s.redd[1];
+          }
+          const double need = fmax((double)tp, 0.) * total;
+          double before = cum - mass + shift;
+          int bin = kBins - 1;
+          bool hit = false;
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            if (!hit && before + m[q] >= need) hit = true, bin = tid * kPer + q;
+            before += m[q];
+          }
+          const int who = block_first(hit, &s.first);
+          __syncthreads();
+          if (tid == max(who, 0)) s.redi[0] = who < 0 ? kBins - 1 : bin;
+          __syncthreads();
+          bin = s.redi[0];
+          // as many bins around it as three quarters of the list take: the
+          // counts before each bin go where the draw's sums will be
+          int upto = block_scan(sum, s.redi) - sum;
+          uint32_t *cnt = reinterpret_cast<uint32_t *>(list);  // [kBins + 1] (the histogram is merged)
+          __syncthreads();
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            cnt[tid * kPer + q] = (uint32_t)upto;
+            upto += n[q];
+          }
+          if (tid == kThreads - 1) cnt[kBins] = (uint32_t)upto;
+          __syncthreads();
+          int wide = 0;  // the widest 2^i - 1 bins to both sides that fit
+          for (int x = 1; x < kBins; x = 2 * x + 1) {
+            if (cnt[min(kBins, bin + x + 1)] - cnt[max(0, bin - x)] > kList * 3 / 4) break;
+            wide = x;
+          }
+          b1 = max(0, bin - wide), b2 = min(kBins, bin + wide + 1);
+          const uint32_t inside = cnt[b2] - cnt[b1];
+          __syncthreads();
+          if (inside > kList || tries == 4) general = true;
+          else o = Orders{kWeigh, (float)b1, b2 >= kBins ? INFINITY : (float)b2};
+        }
+      }
+      if (tid == 0) s.listed = 0;
+      if (tid < blocks) {
+        put32(peer(&s.orders.step, tid), (uint32_t)o.step);
+        put32(peer(&s.orders.from, tid), __float_as_uint(o.from));
+        put32(peer(&s.orders.to, tid), __float_as_uint(o.to));
+      }
+    }
+    cluster_sync();
+    const Orders o = s.orders;
+    if (o.step == kStop) {
+      if (rank != 0) return;
+      break;
+    }
+    // ---------------------------------------------------------------- the pass over the tokens
+    const uint32_t list0 = peer(list, 0), listed0 = peer(&s.listed, 0);
+    auto collect = [&](float x, int v) {
+      const uint32_t at = add32(listed0, 1u);
+      if (at < kList) put64(list0 + at * 8, (u64)order_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)v));
+    };
+    if (o.step == kCollect) {
+      for (int i = tid; i < vecs; i += kThreads) {
+        const uint4 w = vec(i);
+        const float m = best_of(w);
+        if (m > -INFINITY && (mx - m) * scale < o.to) {
+          float f[E];
+          unpack<F32>(w, f);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (f[e] > -INFINITY && (mx - f[e]) * scale < o.to) collect(f[e], v0 + i * E + e);
+        }
+      }
+    } else {
+      const float dfar = fminf(45.f / r.ch, 3e38f);  // beyond it a weight rounds to nothing
+      const float dkeep = fminf(r.dmax, dfar);
+      u64 sure = 0, all = 0;
+      for (int ch = warp; ch < nch; ch += kWarps) {
+        float kept = 0.f, certain = 0.f, total = 0.f;  // of this lane's 32 tokens
+#pragma unroll
+        for (int q = 0; q < kChunk / E / 32; ++q) {
+          const int i = ch * (kChunk / E) + q * 32 + lane;
+          float f[E];
+          unpack<F32>(vec(i), f);
+          float w1[E], w2[E], w3[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float d = mx - f[e], zh = d * r.ch;
+            const float zl = fmaf(d, r.cl, fmaf(d, r.ch, -zh));
+            const float w0 = ex2_approx(-zh);
+            const float w = d < dfar ? fmaf(-0.693147180559945f * w0, zl, w0) : 0.f;
+            const float bin = d * scale;
+            w3[e] = w;
+            w2[e] = bin < o.from ? w : 0.f;
+            w1[e] = d <= dkeep ? w2[e] : 0.f;
+            if (bin >= o.from && bin < o.to && f[e] > -INFINITY) collect(f[e], v0 + i * E + e);
+          }
+#pragma unroll
+          for (int o2 = E / 2; o2 > 0; o2 >>= 1)
+#pragma unroll
+            for (int e = 0; e < o2; ++e) w1[e] += w1[e + o2], w2[e] += w2[e + o2], w3[e] += w3[e + o2];
+          kept += w1[0], certain += w2[0], total += w3[0];
+        }
+        u64 x = __float2ull_rn(kept * 1099511627776.f);
+#pragma unroll
+        for (int o2 = 16; o2 > 0; o2 >>= 1) x += __shfl_xor_sync(DC_FULL_MASK, x, o2);
+        if (lane == 0) put64(peer(&chunk_all[v0 / kChunk + ch], 0), x);
+        if (by_mass) {
+          sure += __float2ull_rn(certain * 1099511627776.f);
+          all += __float2ull_rn(total * 1099511627776.f);
+        }
+      }
+      if (by_mass) {
+        sure = block_sum(sure, s.red);
+        all = block_sum(all, s.red);
+        if (tid == 0) {
+          put64(peer(&s.sure[rank], 0), sure);
+          put64(peer(&s.all[rank], 0), all);
+        }
+      }
+    }
+    cluster_sync();
+    if (by_list || whole) {
+      if (rank != 0) return;
+      break;
+    }
+    // by mass: is the border among the candidates?
+    ++tries;
+    if (rank == 0) {
+      sure_all = all_all = 0;
+      for (int b = 0; b < blocks; ++b) sure_all += s.sure[b], all_all += s.all[b];
+      const int n = (int)min(s.listed, (uint32_t)kList);
+      u64 m = 0;
+      for (int i = tid; i < n; i += kThreads) m += r.weight(key_value((uint32_t)(list[i] >> 32)));
+      m = block_sum(m, s.red);
+      const double need = fmax((double)tp, 0.) * (double)all_all;
+      const bool in = s.listed <= kList && ((double)sure_all < need || sure_all == 0) && (double)(sure_all + m) >= need;
+      __syncthreads();
+      if (in) {
+        // it is: the others are done
+        if (tid < blocks) put32(peer(&s.orders.step, tid), kStop);
+      } else if (tid < blocks) {
+        put32(peer(&s.orders.step, tid), kWeigh);
+      }
+    }
+    cluster_sync();
+    if (s.orders.step == kStop) {
+      if (rank != 0) return;
+      break;
+    }
+    __syncthreads();
+  }
+
+  // ---------------------------------------------------------------- the draw (first block)
+  int token = -1;
+  u64 total = 0;
+  if (!general && by_list && s.listed > kList) general = true;
+  if (general) {
+    token = sample_general<F32>(r, V, k, tp, u, s.red, &total);
+  } else {
+    // candidates in order
+    int n = whole ? 0 : (int)s.listed, pad = 1;
+    while (pad < n) pad <<= 1;
+    for (int i = n + tid; i < pad; i += kThreads) list[i] = 0;
+    if (n > 0) sort_desc(list, pad);
+    const auto weight_at = [&](int i) { return r.weight(key_value((uint32_t)(list[i] >> 32))); };
+    // the first `m` of them stay: the shortest prefix with mass `need`
+    int m = n;
+    if (by_list) m = min(n, k);
+    const int per = (n + kThreads - 1) / kThreads;
+    if (n > 0 && tp < 1.f) {
+      u64 mine = 0;
+      for (int q = 0; q < per; ++q) {
+        const int i = tid * per + q;
+        if (i < m) mine += weight_at(i);
+      }
+      const u64 upto = block_scan(mine, s.red);
+      __syncthreads();
+      if (tid == kThreads - 1) s.red[0] = upto;
+      __syncthreads();
+      const double need = fmax((double)tp, 0.) * (by_list ? (double)s.red[0] : (double)all_all);
+      u64 cum = (by_list ? 0 : sure_all) + upto - mine;
+      int at = -1;
+      for (int q = 0; q < per && at < 0; ++q) {
+        const int i = tid * per + q;
+        if (i >= m) break;
+        cum += weight_at(i);
+        if ((double)cum >= need) at = i + 1;
+      }
+      const int who = block_first(at > 0, &s.first);
+      __syncthreads();
+      if (tid == max(who, 0)) s.redi[0] = who < 0 ? m : at;
+      __syncthreads();
+      m = s.redi[0];
+    }
+    if (by_list) {
+      // the kept ones, by id, and the draw among them
+      for (int i = tid; i < pad; i += kThreads) {
+        const u64 e = list[i];
+        const float x = key_value((uint32_t)(e >> 32));
+        const bool keep = i < m && (x == mx || mx - x <= r.dmax);
+        list[i] = keep ? (e & 0xFFFFFFFFull) << 32 | (e >> 32) : 0;  // ids are stored complemented: descending is by id
+      }
+      sort_desc(list, pad);
+      const auto by_id = [&](int i) { return list[i] ? r.weight(key_value((uint32_t)list[i])) : 0; };
+      u64 mine = 0;
+      for (int q = 0; q < per; ++q)
+        if (tid * per + q < n) mine += by_id(tid * per + q);
+      const u64 upto = block_scan(mine, s.red);
+      __syncthreads();
+      if (tid == kThreads - 1) s.red[0] = upto;
+      __syncthreads();
+      total = s.red[0];
+      u64 target = (u64)((double)u * (double)total);
+      if (target >= total) target = total - 1;
+      u64 cum = upto - mine;
+      int at = -1;
+      for (int q = 0; q < per && at < 0; ++q) {
+        const int i = tid * per + q;
+        if (i >= n) break;
+        cum += by_id(i);
+        if (cum > target) at = i;
+      }
+      const int who = block_first(at >= 0, &s.first);
+      if (tid == who) s.redi[0] = (int)(0xFFFFFFFFu - (uint32_t)(list[at] >> 32));
+      __syncthreads();
+      token = s.redi[0];
+    } else {
+      if (by_mass) {
+        // the kept candidates join their chunks; the border as a rule for any token
+        for (int i = tid; i < m; i += kThreads) {
+          const float x = key_value((uint32_t)(list[i] >> 32));
+          if (x == mx || mx - x <= r.dmax) atomicAdd(&chunk_all[(0xFFFFFFFFu - (uint32_t)list[i]) / kChunk], weight_at(i));
+        }
+        r.key = (uint32_t)(list[m - 1] >> 32), r.last = (int)(0xFFFFFFFFu - (uint32_t)list[m - 1]);
+        __syncthreads();
+      }
+      u64 mine = 0;
+      const int cper = (chunks_all + kThreads - 1) / kThreads;
+      for (int q = 0; q < cper; ++q)
+        if (tid * cper + q < chunks_all) mine += chunk_all[tid * cper + q];
+      const u64 upto = block_scan(mine, s.red);
+      __syncthreads();
+      if (tid == kThreads - 1) s.red[0] = upto;
+      __syncthreads();
+      total = s.red[0];
+      u64 target = (u64)((double)u * (double)total);
+      if (target >= total) target = total - 1;
+      u64 cum = upto - mine;
+      int at = -1;
+      for (int q = 0; q < cper && at < 0; ++q) {
+        const int i = tid * cper + q;
+        if (i >= chunks_all) break;
+        if (cum + chunk_all[i] > target) at = i;
+        else cum += chunk_all[i];
+      }
+      const int who = block_first(at >= 0, &s.first);
+      if (tid == who) s.redi[0] = at, s.red[0] = target - cum;
+      __syncthreads();
+      const int v = s.redi[0] * kChunk + tid * (kChunk / kThreads);
+      target = s.red[0];
+      // in the chunk
+      u64 w[kChunk / kThreads], sum = 0;
+#pragma unroll
+      for (int q = 0; q < kChunk / kThreads; ++q) {
+        const float x = v + q < V ? r.value(v + q) : -INFINITY;
+        w[q] = v + q < V && x > -INFINITY && r.kept(x, v + q) ? r.weight(x) : 0;
+        sum += w[q];
+      }
+      u64 before = block_scan(sum, s.red) - sum;
+      int found = -1, last = -1;
+#pragma unroll
+      for (int q = 0; q < kChunk / kThreads; ++q) {
+        before += w[q];
+        if (w[q] > 0) {
+          last = v + q;
+          if (found < 0 && before > target) found = v + q;
+        }
+      }
+      const int got = block_first(found >= 0, &s.first);
+      if (got >= 0) {
+        if (tid == got) s.redi[0] = found;
+      } else {
+        // the chunk's sum, rounded 32 tokens at a time, was above its tokens': the last one
+        if (tid == 0) s.redi[0] = -1;
+        __syncthreads();
+        if (last >= 0) atomicMax(&s.redi[0], last);
+      }
+      __syncthreads();
+      token = s.redi[0];
+    }
+  }
+  if (tid == 0) {
+    p.tokens[row] = token;
+    const float x = r.value(min(max(token, 0), V - 1)), d = x == mx ? 0.f : mx - x;
+    if (p.logprob) p.logprob[row] = (float)(-(double)d / td - log((double)total * 0x1p-40));
+  }
+}
+
+template <bool F32>
+cudaError_t launch(const SampleParams &p, cudaStream_t st) {
+  constexpr int kSize = F32 ? 4 : 2;
+  // blocks of a cluster: slices of about 40 KB, so that several clusters share
+  // the SMs and one's copies run under another's arithmetic
+  const int64_t bytes = (int64_t)p.V * kSize;
+  int blocks = 1;
+  while (blocks < kMostBlocks && bytes > blocks * (40 << 10)) blocks *= 2;
+  const int chunks = (p.V + kChunk - 1) / kChunk, slice = (chunks + blocks - 1) / blocks * kChunk;
+  const bool held = (size_t)slice * kSize <= kMostSlice;
+  const size_t smem = kList * 8 + (size_t)(chunks + 1) / 2 * 16 + kBins / blocks * 4 + (held ? (size_t)slice * kSize : 0);
+  const cudaError_t e = cudaFuncSetAttribute(k_sample<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(kList * 8 + 8192 + kBins * 4 + kMostSlice));
+  if (e != cudaSuccess) return e;
+  return launch_ex(k_sample<F32>, dim3((unsigned)p.rows, 1, (unsigned)blocks), dim3(kThreads), smem, st, false,
+                   (unsigned)blocks, p, blocks, slice, (int)held, chunks);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleParams &p, bool f32, cudaStream_t st) {
-  if (f32) k_sample<true><<<p.rows, kThreads, 0, st>>>(p);
-  else k_sample<false><<<p.rows, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return f32 ? launch<true>(p, st) : launch<false>(p, st);
 }
 
 }  // namespace dc
