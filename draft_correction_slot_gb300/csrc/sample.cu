@@ -40,6 +40,7 @@ typedef unsigned long long u64;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBins = 2048;      // histogram bins
 constexpr int kList = 2048;      // candidates the list holds
+constexpr int kOwn = kList;      // candidates one block may have of them
 constexpr int kTopkMost = 1024;  // largest top_k of the candidate path
 constexpr int kChunk = 1024;     // tokens of a partial sum (one warp)
 constexpr int kMostBlocks = 8;   // blocks of a cluster
@@ -221,16 +222,20 @@ __device__ __forceinline__ int block_first(bool hit, int *s) {
   return *s == kThreads ? -1 : *s;
 }
 
-// Sorts list[0, n) descending (n a power of two), the whole block.
+// Sorts list[0, n) descending (n a power of two), the whole block.  Pairs
+// closer than 64 stay within a warp's 64 entries: those steps need no block
+// barrier.
 __device__ __forceinline__ void sort_desc(u64 *list, int n) {
+  __syncthreads();
   for (int k = 2; k <= n; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
       for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int a = 2 * j * (i / j) + i % j, b = a + j;
+        const int a = ((i & ~(j - 1)) << 1) | (i & (j - 1)), b = a + j;
         const u64 x = list[a], y = list[b];
         if ((x < y) == ((a & k) == 0)) list[a] = y, list[b] = x;
       }
+      if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
+      else __syncwarp();
     }
   __syncthreads();
 }
@@ -251,15 +256,22 @@ struct Orders {
 };
 enum { kStop, kCollect, kWeigh };
 
+// The least integer that is at least p * mass.
+__device__ __forceinline__ u64 share_of(float p, u64 mass) {
+  return (u64)ceil((double)fmaxf(p, 0.f) * (double)mass);
+}
+
 struct SampleShared {
   u64 red[kWarps];
-  double redd[kWarps];
+  float redf[kWarps];
   int redi[kWarps];
   int first;
   float mx[kMostBlocks], low[kMostBlocks];
   uint32_t arg[kMostBlocks];
   u64 sure[kMostBlocks], all[kMostBlocks];
-  uint32_t listed;
+  uint32_t listed;      // (first block) candidates of the cluster
+  uint32_t mine, base;  // candidates of this block, and where they go in the first block's list
+  float dmax;
   Orders orders;
 };
 
@@ -283,7 +295,8 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.z, V = p.V;
   u64 *list = reinterpret_cast<u64 *>(smem);                 // [kList]; before the candidates: the histogram
   uint32_t *hist = reinterpret_cast<uint32_t *>(smem);       // [kBins]
-  u64 *chunk_all = list + kList;                             // [chunks_all], the first block's: kept weight a chunk
+  u64 *own = list + kList;                                   // [kOwn] this block's candidates
+  u64 *chunk_all = own + kOwn;                             // [chunks_all], the first block's: kept weight a chunk
   const int share = kBins / blocks;                          // merged bins that each block holds
   uint32_t *merged = reinterpret_cast<uint32_t *>(chunk_all + (chunks_all + 1) / 2 * 2);  // (16-byte steps: `data` is read in vectors)
   uint8_t *data = reinterpret_cast<uint8_t *>(merged + share);
@@ -328,24 +341,25 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
   auto vec = [&](int i) { return held ? reinterpret_cast<const uint4 *>(data)[i] : fetch(i); };
   // a vector's largest logit
   auto best_of = [&](const uint4 &w) {
-    float f[E];
-    unpack<F32>(w, f);
-    float m = f[0];
-#pragma unroll
-    for (int e = 1; e < E; ++e) m = fmaxf(m, f[e]);
-    return m;
+    if constexpr (F32) {
+      return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    } else {
+      const uint32_t m = bf16x2_max(bf16x2_max(w.x, w.y), bf16x2_max(w.z, w.w));
+      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
   };
 
   // ---------------------------------------------------------------- the maximum
   // `low`: the least of the vectors' maxima, which sets the histogram's range
   float mx = -INFINITY, low = INFINITY;
-  for (int i0 = tid; i0 < vecs; i0 += 4 * kThreads) {
-    uint4 w[4];
+  constexpr int kAtOnce = 10;  // vectors a thread has in flight: a 40 KB slice at once
+  for (int i0 = tid; i0 < vecs; i0 += kAtOnce * kThreads) {
+    uint4 w[kAtOnce];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < kAtOnce; ++q)
       if (i0 + q * kThreads < vecs) w[q] = fetch(i0 + q * kThreads);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kAtOnce; ++q) {
       if (i0 + q * kThreads >= vecs) continue;
       if (held) reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] = w[q];
       const float m = best_of(w[q]);
@@ -354,11 +368,22 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
     }
   }
   mx = warp_max(mx), low = -warp_max(-low);
-  if (lane == 0) s.redd[warp] = mx, s.red[warp] = __float_as_uint(low);
+  if (lane == 0) s.redf[warp] = mx, s.redi[warp] = __float_as_int(low);
   for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-  if (tid == 0) s.listed = 0;
+  float t = p.temperature ? p.temperature[row] : 1.f;
+  if (t != t) t = 1.f;
+  int k = p.top_k ? p.top_k[row] : 0;
+  if (k <= 0 || k > V) k = V;
+  float tp = p.top_p ? p.top_p[row] : 1.f, u = p.u[row];
+  const float mp = p.min_p ? p.min_p[row] : 0.f;
+  if (tp != tp) tp = 1.f;
+  if (!(u > 0.f)) u = 0.f;
+  if (tid == 0) {  // (one thread: 256 would keep the few 64-bit units busy for 6 us)
+    s.listed = s.mine = 0;
+    s.dmax = mp > 0.f ? __double2float_rd(fmax(0.0, -(double)t * log((double)fminf(mp, 1.f)))) : INFINITY;
+  }
   __syncthreads();
-  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, (float)s.redd[w]), low = fminf(low, __uint_as_float((uint32_t)s.red[w]));
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s.redf[w]), low = fminf(low, __int_as_float(s.redi[w]));
   cluster_wait();  // every block of the cluster is there
   if (tid < blocks) {
     put32(peer(&s.mx[rank], tid), __float_as_uint(mx));
@@ -367,14 +392,6 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
   cluster_sync();
   for (int b = 0; b < blocks; ++b) mx = fmaxf(mx, s.mx[b]), low = fminf(low, s.low[b]);
 
-  // ---------------------------------------------------------------- the row's parameters
-  float t = p.temperature ? p.temperature[row] : 1.f;
-  if (t != t) t = 1.f;
-  int k = p.top_k ? p.top_k[row] : 0;
-  if (k <= 0 || k > V) k = V;
-  float tp = p.top_p ? p.top_p[row] : 1.f, mp = p.min_p ? p.min_p[row] : 0.f, u = p.u[row];
-  if (tp != tp) tp = 1.f;
-  if (!(u > 0.f)) u = 0.f;
   if (mx == -INFINITY) {
     if (rank == 0 && tid == 0) {
       p.tokens[row] = -1;
@@ -409,9 +426,12 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
   SampleRow<F32> r;
   r.x = src;
   r.mx = mx;
-  const double td = fmax((double)t, 1e-30), c = 1.4426950408889634 / td;
-  r.ch = (float)c, r.cl = (float)(c - (double)r.ch);
-  r.dmax = mp > 0.f ? __double2float_rd(fmax(0.0, -(double)t * log((double)fminf(mp, 1.f)))) : INFINITY;
+  // log2 e / t in two floats: the quotient, and the quotient of what it leaves
+  const float ts = fmaxf(t, 1e-30f);
+  r.ch = __fdiv_rn(1.44269502f, ts);
+  r.cl = __fdiv_rn(fmaf(-r.ch, ts, 1.44269502f) + 1.92596303e-8f, ts);
+  if (!(ts < 3e38f)) r.ch = r.cl = 0.f;
+  r.dmax = s.dmax;
   r.key = 0, r.last = V;
 
   // ---------------------------------------------------------------- which way
@@ -484,31 +504,25 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
           const int to = s.redi[0];
           o = Orders{kCollect, 0.f, to >= kBins ? INFINITY : (float)to};
         } else {
+          const float per_bin = range / (float)kBins * r.ch;
           // masses by the bins' middles; after a first try, from its exact masses on
-          double m[kPer], mass = 0.;
+          float m[kPer], mass = 0.f;
 #pragma unroll
           for (int q = 0; q < kPer; ++q) {
-            m[q] = n[q] ? (double)n[q] * ex2_approx(-((float)(tid * kPer + q) + 0.5f) / scale * r.ch) : 0.;
+            m[q] = n[q] ? (float)n[q] * ex2_approx(-((float)(tid * kPer + q) + 0.5f) * per_bin) : 0.f;
             mass += m[q];
           }
-          const double cum = block_scan(mass, s.redd);
+          const float cum = block_scan(mass, s.redf);
           __syncthreads();
-          if (tid == kThreads - 1) s.redd[0] = cum;
-          __syncthreads();
-          const double total = tries ? (double)all_all * 0x1p-40 : s.redd[0];
-          double shift = 0.;  // what an exact mass says the middles' are off by, at bin b1
-          if (tries) {
-            __syncthreads();
-            if (tid == b1 / kPer) {
-              double before = cum - mass;
-              for (int q = 0; q < b1 % kPer; ++q) before += m[q];
-              s.redd[1] = (double)sure_all * 0x1p-40 - before;
-            }
-            __syncthreads();
-            shift = s.redd[1];
+          if (tid == kThreads - 1) s.redf[0] = cum;
+          if (tries && tid == b1 / kPer) {  // what an exact mass says the middles' are off by, at bin b1
+            float before = cum - mass;
+            for (int q = 0; q < b1 % kPer; ++q) before += m[q];
+            s.redf[1] = __ull2float_rn(sure_all) * 0x1p-40f - before;
           }
-          const double need = fmax((double)tp, 0.) * total;
-          double before = cum - mass + shift;
+          __syncthreads();
+          const float need = fmaxf(tp, 0.f) * (tries ? __ull2float_rn(all_all) * 0x1p-40f : s.redf[0]);
+          float before = cum - mass + (tries ? s.redf[1] : 0.f);
           int bin = kBins - 1;
           bool hit = false;
 #pragma unroll
@@ -547,6 +561,7 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
       }
       if (tid == 0) s.listed = 0;
       if (tid < blocks) {
+        put32(peer(&s.mine, tid), 0u);
         put32(peer(&s.orders.step, tid), (uint32_t)o.step);
         put32(peer(&s.orders.from, tid), __float_as_uint(o.from));
         put32(peer(&s.orders.to, tid), __float_as_uint(o.to));
@@ -559,10 +574,11 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
       break;
     }
     // ---------------------------------------------------------------- the pass over the tokens
-    const uint32_t list0 = peer(list, 0), listed0 = peer(&s.listed, 0);
+    // candidates gather in this block, then go to the first one's list together
+    // (one by one, each would wait for the reply from the other block's memory)
     auto collect = [&](float x, int v) {
-      const uint32_t at = add32(listed0, 1u);
-      if (at < kList) put64(list0 + at * 8, (u64)order_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)v));
+      const uint32_t at = atomicAdd(&s.mine, 1u);
+      if (at < kOwn) own[at] = (u64)order_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)v);
     };
     if (o.step == kCollect) {
       for (int i = tid; i < vecs; i += kThreads) {
@@ -579,6 +595,14 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
     } else {
       const float dfar = fminf(45.f / r.ch, 3e38f);  // beyond it a weight rounds to nothing
       const float dkeep = fminf(r.dmax, dfar);
+      const bool min_p = r.dmax < INFINITY;
+      auto tree_sum = [](float(&w)[E]) {
+#pragma unroll
+        for (int h = E / 2; h > 0; h >>= 1)
+#pragma unroll
+          for (int e = 0; e < h; ++e) w[e] += w[e + h];
+        return w[0];
+      };
       u64 sure = 0, all = 0;
       for (int ch = warp; ch < nch; ch += kWarps) {
         float kept = 0.f, certain = 0.f, total = 0.f;  // of this lane's 32 tokens
@@ -587,25 +611,38 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
           const int i = ch * (kChunk / E) + q * 32 + lane;
           float f[E];
           unpack<F32>(vec(i), f);
-          float w1[E], w2[E], w3[E];
+          float w1[E], w3[E];
+          bool any = false;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const float d = mx - f[e], zh = d * r.ch;
             const float zl = fmaf(d, r.cl, fmaf(d, r.ch, -zh));
             const float w0 = ex2_approx(-zh);
-            const float w = d < dfar ? fmaf(-0.693147180559945f * w0, zl, w0) : 0.f;
+            w3[e] = d < dfar ? fmaf(-0.693147180559945f * w0, zl, w0) : 0.f;
             const float bin = d * scale;
-            w3[e] = w;
-            w2[e] = bin < o.from ? w : 0.f;
-            w1[e] = d <= dkeep ? w2[e] : 0.f;
-            if (bin >= o.from && bin < o.to && f[e] > -INFINITY) collect(f[e], v0 + i * E + e);
+            w1[e] = bin < o.from ? w3[e] : 0.f;
+            any |= bin >= o.from && bin < o.to;
           }
+          if (any) {
 #pragma unroll
-          for (int o2 = E / 2; o2 > 0; o2 >>= 1)
+            for (int e = 0; e < E; ++e) {
+              const float bin = (mx - f[e]) * scale;
+              if (bin >= o.from && bin < o.to && f[e] > -INFINITY) collect(f[e], v0 + i * E + e);
+            }
+          }
+          if (min_p) {  // the draw leaves out what min-p does; the border counts it
+            float w2[E];
 #pragma unroll
-            for (int e = 0; e < o2; ++e) w1[e] += w1[e + o2], w2[e] += w2[e + o2], w3[e] += w3[e + o2];
-          kept += w1[0], certain += w2[0], total += w3[0];
+            for (int e = 0; e < E; ++e) {
+              w2[e] = w1[e];
+              w1[e] = mx - f[e] <= dkeep ? w1[e] : 0.f;
+            }
+            certain += tree_sum(w2);
+          }
+          kept += tree_sum(w1);
+          if (by_mass) total += tree_sum(w3);
         }
+        if (!min_p) certain = kept;
         u64 x = __float2ull_rn(kept * 1099511627776.f);
 #pragma unroll
         for (int o2 = 16; o2 > 0; o2 >>= 1) x += __shfl_xor_sync(DC_FULL_MASK, x, o2);
@@ -624,6 +661,16 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
         }
       }
     }
+    if (!whole) {
+      __syncthreads();
+      if (tid == 0) s.base = s.mine > 0 ? add32(peer(&s.listed, 0), s.mine <= kOwn ? s.mine : kList + 1u) : 0;
+      __syncthreads();
+      if (s.mine <= kOwn) {
+        const uint32_t list0 = peer(list, 0);
+        for (uint32_t i = tid; i < s.mine; i += kThreads)
+          if (s.base + i < kList) put64(list0 + (s.base + i) * 8, own[i]);
+      }
+    }
     cluster_sync();
     if (by_list || whole) {
       if (rank != 0) return;
@@ -638,8 +685,8 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
       u64 m = 0;
       for (int i = tid; i < n; i += kThreads) m += r.weight(key_value((uint32_t)(list[i] >> 32)));
       m = block_sum(m, s.red);
-      const double need = fmax((double)tp, 0.) * (double)all_all;
-      const bool in = s.listed <= kList && ((double)sure_all < need || sure_all == 0) && (double)(sure_all + m) >= need;
+      const u64 need = share_of(tp, all_all);
+      const bool in = s.listed <= kList && (sure_all < need || sure_all == 0) && sure_all + m >= need;
       __syncthreads();
       if (in) {
         // it is: the others are done
@@ -683,14 +730,14 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
       __syncthreads();
       if (tid == kThreads - 1) s.red[0] = upto;
       __syncthreads();
-      const double need = fmax((double)tp, 0.) * (by_list ? (double)s.red[0] : (double)all_all);
+      const u64 need = share_of(tp, by_list ? s.red[0] : all_all);
       u64 cum = (by_list ? 0 : sure_all) + upto - mine;
       int at = -1;
       for (int q = 0; q < per && at < 0; ++q) {
         const int i = tid * per + q;
         if (i >= m) break;
         cum += weight_at(i);
-        if ((double)cum >= need) at = i + 1;
+        if (cum >= need) at = i + 1;
       }
       const int who = block_first(at > 0, &s.first);
       __syncthreads();
@@ -798,7 +845,7 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
   if (tid == 0) {
     p.tokens[row] = token;
     const float x = r.value(min(max(token, 0), V - 1)), d = x == mx ? 0.f : mx - x;
-    if (p.logprob) p.logprob[row] = (float)(-(double)d / td - log((double)total * 0x1p-40));
+    if (p.logprob) p.logprob[row] = -(d / ts) - logf(__ull2float_rn(total) * 0x1p-40f);
   }
 }
 
@@ -812,9 +859,9 @@ cudaError_t launch(const SampleParams &p, cudaStream_t st) {
   while (blocks < kMostBlocks && bytes > blocks * (40 << 10)) blocks *= 2;
   const int chunks = (p.V + kChunk - 1) / kChunk, slice = (chunks + blocks - 1) / blocks * kChunk;
   const bool held = (size_t)slice * kSize <= kMostSlice;
-  const size_t smem = kList * 8 + (size_t)(chunks + 1) / 2 * 16 + kBins / blocks * 4 + (held ? (size_t)slice * kSize : 0);
+  const size_t smem = (kList + kOwn) * 8 + (size_t)(chunks + 1) / 2 * 16 + kBins / blocks * 4 + (held ? (size_t)slice * kSize : 0);
   const cudaError_t e = cudaFuncSetAttribute(k_sample<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)(kList * 8 + 8192 + kBins * 4 + kMostSlice));
+                                             (int)((kList + kOwn) * 8 + 8192 + kBins * 4 + kMostSlice));
   if (e != cudaSuccess) return e;
   return launch_ex(k_sample<F32>, dim3((unsigned)p.rows, 1, (unsigned)blocks), dim3(kThreads), smem, st, false,
                    (unsigned)blocks, p, blocks, slice, (int)held, chunks);
