@@ -16,15 +16,15 @@
 //     for top-p;
 //   the few candidates around the border, collected in the first block;
 //   and, unless top-k leaves only those, the weights: summed over all tokens,
-//     over those surely kept, and per 1024 tokens for the draw.
+//     over those surely kept, and per 512 tokens for the draw.
 // The first block sorts the candidates, finds the border exactly, and draws:
-// the 1024 tokens by their sums, then the token in them.
+// the 512 tokens by their sums, then the token in them.
 // What this does not cover (top_k over kTopkMost of a larger vocabulary,
 // borders with more tokens around them than the list holds, infinite
 // logits) the first block does alone by bisection over the row, ~100 passes.
 //
 // Weights are summed as 64-bit integers in units of 2^-40 (V <= 2^20 of them
-// stay below 2^60), up to 32 of one thread's first in fp32: the same sums
+// stay below 2^60), up to 16 of one thread's first in fp32: the same sums
 // whatever the cluster's size and the blocks' timing.  e^{-d / t} is taken as
 // 2^-z with z = d / (t ln 2) carried with its rounding error: a row's border
 // can lie where a token has 10^-6 of the mass, and a bias of 10^-7 common to
@@ -40,9 +40,8 @@ typedef unsigned long long u64;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBins = 2048;      // histogram bins
 constexpr int kList = 2048;      // candidates the list holds
-constexpr int kOwn = kList;      // candidates one block may have of them
 constexpr int kTopkMost = 1024;  // largest top_k of the candidate path
-constexpr int kChunk = 1024;     // tokens of a partial sum (one warp)
+constexpr int kChunk = 512;      // tokens of a partial sum (one warp)
 constexpr int kMostBlocks = 8;   // blocks of a cluster
 constexpr size_t kMostSlice = 96 * 1024;  // bytes of a slice held in shared memory
 
@@ -286,17 +285,16 @@ __device__ __forceinline__ void unpack(const uint4 &w, float (&f)[F32 ? 4 : 8]) 
   }
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kThreads, 3)
-k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) {
+template <bool F32, bool HELD>
+__global__ void __launch_bounds__(kThreads, 4)
+k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   constexpr int E = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ SampleShared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.z, V = p.V;
   u64 *list = reinterpret_cast<u64 *>(smem);                 // [kList]; before the candidates: the histogram
   uint32_t *hist = reinterpret_cast<uint32_t *>(smem);       // [kBins]
-  u64 *own = list + kList;                                   // [kOwn] this block's candidates
-  u64 *chunk_all = own + kOwn;                             // [chunks_all], the first block's: kept weight a chunk
+  u64 *chunk_all = list + kList;                             // [chunks_all], the first block's: kept weight a chunk
   const int share = kBins / blocks;                          // merged bins that each block holds
   uint32_t *merged = reinterpret_cast<uint32_t *>(chunk_all + (chunks_all + 1) / 2 * 2);  // (16-byte steps: `data` is read in vectors)
   uint8_t *data = reinterpret_cast<uint8_t *>(merged + share);
@@ -338,7 +336,10 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
     }
     return make_uint4(x[0], x[1], x[2], x[3]);
   };
-  auto vec = [&](int i) { return held ? reinterpret_cast<const uint4 *>(data)[i] : fetch(i); };
+  auto vec = [&](int i) {
+    if constexpr (HELD) return reinterpret_cast<const uint4 *>(data)[i];
+    else return fetch(i);
+  };
   // a vector's largest logit
   auto best_of = [&](const uint4 &w) {
     if constexpr (F32) {
@@ -361,7 +362,7 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q) {
       if (i0 + q * kThreads >= vecs) continue;
-      if (held) reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] = w[q];
+      if constexpr (HELD) reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] = w[q];
       const float m = best_of(w[q]);
       mx = fmaxf(mx, m);
       low = fminf(low, m == -INFINITY ? INFINITY : m);
@@ -574,11 +575,19 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
       break;
     }
     // ---------------------------------------------------------------- the pass over the tokens
-    // candidates gather in this block, then go to the first one's list together
-    // (one by one, each would wait for the reply from the other block's memory)
-    auto collect = [&](float x, int v) {
-      const uint32_t at = atomicAdd(&s.mine, 1u);
-      if (at < kOwn) own[at] = (u64)order_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)v);
+    // candidates gather in this block's list, then go to the first one's (one
+    // by one, each would wait for the reply from the other block's memory)
+    uint32_t *count = rank == 0 ? &s.listed : &s.mine;
+    // the tokens of vector i whose bits are set
+    auto collect = [&](int i, uint32_t bits) {
+      uint32_t at = atomicAdd(count, (uint32_t)__popc(bits));
+      for (; bits; bits &= bits - 1, ++at) {
+        const int e = __ffs(bits) - 1, v = v0 + i * E + e;
+        float x;
+        if constexpr (HELD) x = F32 ? reinterpret_cast<const float *>(data)[i * E + e] : bf16_bits_to_float(reinterpret_cast<const uint16_t *>(data)[i * E + e]);
+        else x = r.value(v);
+        if (at < kList) list[at] = (u64)order_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)v);
+      }
     };
     if (o.step == kCollect) {
       for (int i = tid; i < vecs; i += kThreads) {
@@ -587,9 +596,10 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
         if (m > -INFINITY && (mx - m) * scale < o.to) {
           float f[E];
           unpack<F32>(w, f);
+          uint32_t bits = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (f[e] > -INFINITY && (mx - f[e]) * scale < o.to) collect(f[e], v0 + i * E + e);
+          for (int e = 0; e < E; ++e) bits |= f[e] > -INFINITY && (mx - f[e]) * scale < o.to ? 1u << e : 0u;
+          collect(i, bits);
         }
       }
     } else {
@@ -605,14 +615,14 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
       };
       u64 sure = 0, all = 0;
       for (int ch = warp; ch < nch; ch += kWarps) {
-        float kept = 0.f, certain = 0.f, total = 0.f;  // of this lane's 32 tokens
-#pragma unroll
+        float kept = 0.f, certain = 0.f, total = 0.f;  // of this lane's 16 tokens
+#pragma unroll 1
         for (int q = 0; q < kChunk / E / 32; ++q) {
           const int i = ch * (kChunk / E) + q * 32 + lane;
           float f[E];
           unpack<F32>(vec(i), f);
           float w1[E], w3[E];
-          bool any = false;
+          uint32_t bits = 0;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const float d = mx - f[e], zh = d * r.ch;
@@ -621,15 +631,9 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
             w3[e] = d < dfar ? fmaf(-0.693147180559945f * w0, zl, w0) : 0.f;
             const float bin = d * scale;
             w1[e] = bin < o.from ? w3[e] : 0.f;
-            any |= bin >= o.from && bin < o.to;
+            bits |= bin >= o.from && bin < o.to ? 1u << e : 0u;  // (bin of -inf is infinite, or no number)
           }
-          if (any) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const float bin = (mx - f[e]) * scale;
-              if (bin >= o.from && bin < o.to && f[e] > -INFINITY) collect(f[e], v0 + i * E + e);
-            }
-          }
+          if (bits) collect(i, bits);
           if (min_p) {  // the draw leaves out what min-p does; the border counts it
             float w2[E];
 #pragma unroll
@@ -661,14 +665,14 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
         }
       }
     }
-    if (!whole) {
+    if (!whole && rank != 0) {
       __syncthreads();
-      if (tid == 0) s.base = s.mine > 0 ? add32(peer(&s.listed, 0), s.mine <= kOwn ? s.mine : kList + 1u) : 0;
+      if (tid == 0) s.base = s.mine > 0 ? add32(peer(&s.listed, 0), s.mine <= kList ? s.mine : kList + 1u) : 0;
       __syncthreads();
-      if (s.mine <= kOwn) {
+      if (s.mine <= kList) {
         const uint32_t list0 = peer(list, 0);
         for (uint32_t i = tid; i < s.mine; i += kThreads)
-          if (s.base + i < kList) put64(list0 + (s.base + i) * 8, own[i]);
+          if (s.base + i < kList) put64(list0 + (s.base + i) * 8, list[i]);
       }
     }
     cluster_sync();
@@ -833,7 +837,7 @@ k_sample(const SampleParams p, int blocks, int slice, int held, int chunks_all) 
       if (got >= 0) {
         if (tid == got) s.redi[0] = found;
       } else {
-        // the chunk's sum, rounded 32 tokens at a time, was above its tokens': the last one
+        // the chunk's sum, rounded 16 tokens at a time, was above its tokens': the last one
         if (tid == 0) s.redi[0] = -1;
         __syncthreads();
         if (last >= 0) atomicMax(&s.redi[0], last);
@@ -859,12 +863,12 @@ cudaError_t launch(const SampleParams &p, cudaStream_t st) {
   while (blocks < kMostBlocks && bytes > blocks * (40 << 10)) blocks *= 2;
   const int chunks = (p.V + kChunk - 1) / kChunk, slice = (chunks + blocks - 1) / blocks * kChunk;
   const bool held = (size_t)slice * kSize <= kMostSlice;
-  const size_t smem = (kList + kOwn) * 8 + (size_t)(chunks + 1) / 2 * 16 + kBins / blocks * 4 + (held ? (size_t)slice * kSize : 0);
-  const cudaError_t e = cudaFuncSetAttribute(k_sample<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)((kList + kOwn) * 8 + 8192 + kBins * 4 + kMostSlice));
+  const size_t smem = kList * 8 + (size_t)(chunks + 1) / 2 * 16 + kBins / blocks * 4 + (held ? (size_t)slice * kSize : 0);
+  const auto kernel = held ? k_sample<F32, true> : k_sample<F32, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(k_sample<F32>, dim3((unsigned)p.rows, 1, (unsigned)blocks), dim3(kThreads), smem, st, false,
-                   (unsigned)blocks, p, blocks, slice, (int)held, chunks);
+  return launch_ex(kernel, dim3((unsigned)p.rows, 1, (unsigned)blocks), dim3(kThreads), smem, st, false, (unsigned)blocks,
+                   p, blocks, slice, chunks);
 }
 
 }  // namespace
