@@ -39,11 +39,11 @@ namespace {
 typedef unsigned long long u64;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBins = 2048;      // histogram bins
-constexpr int kList = 2048;      // candidates the list holds
-constexpr int kTopkMost = 1024;  // largest top_k of the candidate path
+constexpr int kList = 1088;      // candidates the list holds (its 8704 bytes also hold the histogram)
+constexpr int kTopkMost = 512;   // largest top_k of the candidate path
 constexpr int kChunk = 512;      // tokens of a partial sum (one warp)
 constexpr int kMostBlocks = 8;   // blocks of a cluster
-constexpr size_t kMostSlice = 96 * 1024;  // bytes of a slice held in shared memory
+constexpr size_t kMostSlice = 40 * 1024;  // bytes of a slice held in shared memory (four blocks an SM)
 
 // Larger key <=> larger value; -0 and +0 share a key, NaN counts as -inf.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -251,7 +251,7 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // What a block is told by the first one.
 struct Orders {
   int step;        // kCollect, kWeigh (and collect), kStop
-  float from, to;  // bins (as floats): collect [from, to), weigh as surely kept what lies before `from`
+  float from, to;  // distances from the maximum: collect [from, to), weigh as surely kept what is nearer than `from`
 };
 enum { kStop, kCollect, kWeigh };
 
@@ -273,6 +273,18 @@ struct SampleShared {
   float dmax;
   Orders orders;
 };
+
+// Maxima that a NaN goes through.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 // E logits of a 16-byte vector as floats.
 template <bool F32>
@@ -304,26 +316,25 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   const int nch = (nv + kChunk - 1) / kChunk, vecs = nch * (kChunk / E);
   cluster_arrive();  // (this block is there)
 
-  // A vector of the slice, whole and without NaN: past the end, and where a logit is NaN, -inf.
+  // A vector of the slice; past the vocabulary's end: -inf.
   auto fetch = [&](int i) {
     const int at = v0 + i * E;
-    uint4 w;
-    if (at + E <= V) {
-      w = ld_stream_v4(src + (int64_t)at * kSize);
-    } else {
-      uint32_t x[4];
+    if (at + E <= V) return ld_stream_v4(src + (int64_t)at * kSize);
+    uint32_t x[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if constexpr (F32) {
-          x[q] = at + q < V ? reinterpret_cast<const uint32_t *>(src)[at + q] : 0xFF800000u;
-        } else {
-          const uint32_t a = at + 2 * q < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q] : 0xFF80u;
-          const uint32_t b = at + 2 * q + 1 < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q + 1] : 0xFF80u;
-          x[q] = a | b << 16;
-        }
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (F32) {
+        x[q] = at + q < V ? reinterpret_cast<const uint32_t *>(src)[at + q] : 0xFF800000u;
+      } else {
+        const uint32_t a = at + 2 * q < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q] : 0xFF80u;
+        const uint32_t b = at + 2 * q + 1 < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q + 1] : 0xFF80u;
+        x[q] = a | b << 16;
       }
-      w = make_uint4(x[0], x[1], x[2], x[3]);
     }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+  };
+  // NaN to -inf
+  auto without_nan = [&](uint4 w) {
     uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -336,18 +347,21 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
     }
     return make_uint4(x[0], x[1], x[2], x[3]);
   };
+  bool nan = false;  // (not held) this thread's block met a NaN
   auto vec = [&](int i) {
     if constexpr (HELD) return reinterpret_cast<const uint4 *>(data)[i];
-    else return fetch(i);
+    else return nan ? without_nan(fetch(i)) : fetch(i);
   };
-  // a vector's largest logit
+  // a vector's largest logit; NaN if it has one
   auto best_of = [&](const uint4 &w) {
+    float a, b;
     if constexpr (F32) {
-      return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+      a = max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), b = max_nan(__uint_as_float(w.z), __uint_as_float(w.w));
     } else {
-      const uint32_t m = bf16x2_max(bf16x2_max(w.x, w.y), bf16x2_max(w.z, w.w));
-      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+      const uint32_t m = bf16x2_max_nan(bf16x2_max_nan(w.x, w.y), bf16x2_max_nan(w.z, w.w));
+      a = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
     }
+    return max_nan(a, b);
   };
 
   // ---------------------------------------------------------------- the maximum
@@ -356,14 +370,31 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   constexpr int kAtOnce = 10;  // vectors a thread has in flight: a 40 KB slice at once
   for (int i0 = tid; i0 < vecs; i0 += kAtOnce * kThreads) {
     uint4 w[kAtOnce];
+    if (v0 + vecs * E <= V) {
 #pragma unroll
-    for (int q = 0; q < kAtOnce; ++q)
-      if (i0 + q * kThreads < vecs) w[q] = fetch(i0 + q * kThreads);
+      for (int q = 0; q < kAtOnce; ++q)
+        if (i0 + q * kThreads < vecs) w[q] = ld_stream_v4(src + (int64_t)(v0 + (i0 + q * kThreads) * E) * kSize);
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < kAtOnce; ++q)
+        if (i0 + q * kThreads < vecs) {
+          const uint4 x = fetch(i0 + q * kThreads);
+          if constexpr (HELD) reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] = x;
+        }
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q)
+        if (i0 + q * kThreads < vecs) w[q] = HELD ? reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] : fetch(i0 + q * kThreads);
+    }
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q) {
       if (i0 + q * kThreads >= vecs) continue;
+      float m = best_of(w[q]);
+      if (m != m) {
+        nan = true;
+        w[q] = without_nan(w[q]);
+        m = best_of(w[q]);
+      }
       if constexpr (HELD) reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] = w[q];
-      const float m = best_of(w[q]);
       mx = fmaxf(mx, m);
       low = fminf(low, m == -INFINITY ? INFINITY : m);
     }
@@ -383,7 +414,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
     s.listed = s.mine = 0;
     s.dmax = mp > 0.f ? __double2float_rd(fmax(0.0, -(double)t * log((double)fminf(mp, 1.f)))) : INFINITY;
   }
-  __syncthreads();
+  nan = __syncthreads_or(nan);
   for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s.redf[w]), low = fminf(low, __int_as_float(s.redi[w]));
   cluster_wait();  // every block of the cluster is there
   if (tid < blocks) {
@@ -440,23 +471,24 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   const bool by_list = small || (k < V && k <= kTopkMost);
   const bool by_mass = !by_list && k == V && tp < 1.f;
   const bool whole = k == V && tp >= 1.f && !small;    // min-p at most
-  bool general = !(by_list || by_mass || whole) || mx == INFINITY;
+  bool general = !(by_list || by_mass || whole) || mx == INFINITY || ts > 1e30f;
   // bins of d, 1.5 times the range down to the least vector maximum
   const float range = 1.5f * fmaxf(mx - low, 1e-6f), scale = (float)kBins / range;
   if (!small && !whole && !(range < 1e30f)) general = true;
   if (!general && (by_mass || (by_list && !small))) {
-    // histogram
+    // histogram: the bin is the integer below 2^23 + d scale, by the addition's own rounding
+    const float dtop = (float)(kBins - 1) / scale;
+    auto bin_of = [&](float x) { return __float_as_uint(fmaf(fminf(mx - x, dtop), scale, 8388608.f)) & (2 * kBins - 1); };
     for (int i = tid; i < vecs; i += kThreads) {
       const uint4 w = vec(i);
       if (by_list) {
         const float m = best_of(w);
-        if (m > -INFINITY) atomicAdd(&hist[min((int)((mx - m) * scale), kBins - 1)], 1u);
+        if (m > -INFINITY) atomicAdd(&hist[min(bin_of(m), (uint32_t)kBins - 1)], 1u);
       } else {
         float f[E];
         unpack<F32>(w, f);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (f[e] > -INFINITY) atomicAdd(&hist[(int)fminf((mx - f[e]) * scale, (float)(kBins - 1))], 1u);
+        for (int e = 0; e < E; ++e) atomicAdd(&hist[bin_of(f[e])], 1u);  // (-inf: the last bin)
       }
     }
     cluster_sync();
@@ -503,14 +535,14 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           if (tid == max(who, 0)) s.redi[0] = who < 0 ? kBins : bin + 1;
           __syncthreads();
           const int to = s.redi[0];
-          o = Orders{kCollect, 0.f, to >= kBins ? INFINITY : (float)to};
+          o = Orders{kCollect, 0.f, to >= kBins ? INFINITY : ((float)to + 0.5f) / scale};  // (half a bin to spare)
         } else {
           const float per_bin = range / (float)kBins * r.ch;
           // masses by the bins' middles; after a first try, from its exact masses on
           float m[kPer], mass = 0.f;
 #pragma unroll
           for (int q = 0; q < kPer; ++q) {
-            m[q] = n[q] ? (float)n[q] * ex2_approx(-((float)(tid * kPer + q) + 0.5f) * per_bin) : 0.f;
+            m[q] = n[q] ? (float)n[q] * ex2_approx(-(float)(tid * kPer + q) * per_bin) : 0.f;
             mass += m[q];
           }
           const float cum = block_scan(mass, s.redf);
@@ -536,10 +568,11 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           if (tid == max(who, 0)) s.redi[0] = who < 0 ? kBins - 1 : bin;
           __syncthreads();
           bin = s.redi[0];
-          // as many bins around it as three quarters of the list take: the
-          // counts before each bin go where the draw's sums will be
+          // as many bins around it as half of the list takes; the counts
+          // before each bin go where the candidates will be
           int upto = block_scan(sum, s.redi) - sum;
           uint32_t *cnt = reinterpret_cast<uint32_t *>(list);  // [kBins + 1] (the histogram is merged)
+          static_assert(kList * 8 >= (kBins + 1) * 4, "");
           __syncthreads();
 #pragma unroll
           for (int q = 0; q < kPer; ++q) {
@@ -550,14 +583,14 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           __syncthreads();
           int wide = 0;  // the widest 2^i - 1 bins to both sides that fit
           for (int x = 1; x < kBins; x = 2 * x + 1) {
-            if (cnt[min(kBins, bin + x + 1)] - cnt[max(0, bin - x)] > kList * 3 / 4) break;
+            if (cnt[min(kBins, bin + x + 1)] - cnt[max(0, bin - x)] > kList / 2) break;
             wide = x;
           }
           b1 = max(0, bin - wide), b2 = min(kBins, bin + wide + 1);
           const uint32_t inside = cnt[b2] - cnt[b1];
           __syncthreads();
           if (inside > kList || tries == 4) general = true;
-          else o = Orders{kWeigh, (float)b1, b2 >= kBins ? INFINITY : (float)b2};
+          else o = Orders{kWeigh, ((float)b1 - 0.5f) / scale, b2 >= kBins ? INFINITY : ((float)b2 - 0.5f) / scale};
         }
       }
       if (tid == 0) s.listed = 0;
@@ -593,19 +626,24 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       for (int i = tid; i < vecs; i += kThreads) {
         const uint4 w = vec(i);
         const float m = best_of(w);
-        if (m > -INFINITY && (mx - m) * scale < o.to) {
+        if (m > -INFINITY && mx - m < o.to) {
           float f[E];
           unpack<F32>(w, f);
           uint32_t bits = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) bits |= f[e] > -INFINITY && (mx - f[e]) * scale < o.to ? 1u << e : 0u;
+          for (int e = 0; e < E; ++e) bits |= f[e] > -INFINITY && mx - f[e] < o.to ? 1u << e : 0u;
           collect(i, bits);
         }
       }
     } else {
-      const float dfar = fminf(45.f / r.ch, 3e38f);  // beyond it a weight rounds to nothing
-      const float dkeep = fminf(r.dmax, dfar);
+      const float dfar = fminf(100.f / r.ch, 3e38f);  // a weight of 2^-100 stands for the lesser ones and for -inf
       const bool min_p = r.dmax < INFINITY;
+      u64 sure = 0, all = 0;
+      // weight of the logit at distance d
+      auto weight = [&](float d) {
+        const float zh = d * r.ch, zl = fmaf(d, r.cl, fmaf(d, r.ch, -zh)), w = ex2_approx(-zh);
+        return fmaf(-0.693147180559945f * w, zl, w);
+      };
       auto tree_sum = [](float(&w)[E]) {
 #pragma unroll
         for (int h = E / 2; h > 0; h >>= 1)
@@ -613,47 +651,62 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           for (int e = 0; e < h; ++e) w[e] += w[e + h];
         return w[0];
       };
-      u64 sure = 0, all = 0;
+      // a lane's sum (at most 16) in units of 2^-40, as 2^22 hi + lo
+      auto fixed = [](float x, uint32_t &hi, uint32_t &lo) {
+        const float y = x * 262144.f, f = floorf(y);
+        hi = (uint32_t)f;
+        lo = __float2uint_rn((y - f) * 4194304.f);
+      };
       for (int ch = warp; ch < nch; ch += kWarps) {
         float kept = 0.f, certain = 0.f, total = 0.f;  // of this lane's 16 tokens
 #pragma unroll 1
         for (int q = 0; q < kChunk / E / 32; ++q) {
           const int i = ch * (kChunk / E) + q * 32 + lane;
-          float f[E];
+          float f[E], w1[E];
           unpack<F32>(vec(i), f);
-          float w1[E], w3[E];
-          uint32_t bits = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float d = mx - f[e], zh = d * r.ch;
-            const float zl = fmaf(d, r.cl, fmaf(d, r.ch, -zh));
-            const float w0 = ex2_approx(-zh);
-            w3[e] = d < dfar ? fmaf(-0.693147180559945f * w0, zl, w0) : 0.f;
-            const float bin = d * scale;
-            w1[e] = bin < o.from ? w3[e] : 0.f;
-            bits |= bin >= o.from && bin < o.to ? 1u << e : 0u;  // (bin of -inf is infinite, or no number)
-          }
-          if (bits) collect(i, bits);
-          if (min_p) {  // the draw leaves out what min-p does; the border counts it
-            float w2[E];
+          for (int e = 0; e < E; ++e) f[e] = fminf(mx - f[e], dfar), w1[e] = weight(f[e]);
+          if (by_mass) {
+            float w3[E];
+            bool any = false;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-              w2[e] = w1[e];
-              w1[e] = mx - f[e] <= dkeep ? w1[e] : 0.f;
+              w3[e] = w1[e];
+              const bool before = f[e] < o.from;
+              w1[e] = before ? w1[e] : 0.f;
+              any |= !before && f[e] < o.to;
             }
-            certain += tree_sum(w2);
+            total += tree_sum(w3);
+            if (any) {
+              uint32_t bits = 0;
+              float x[E];
+              unpack<F32>(vec(i), x);
+#pragma unroll
+              for (int e = 0; e < E; ++e) bits |= f[e] >= o.from && f[e] < o.to && x[e] > -INFINITY ? 1u << e : 0u;
+              if (bits) collect(i, bits);
+            }
+            if (min_p) {  // the draw leaves out what min-p does; the border counts it
+              float w2[E];
+#pragma unroll
+              for (int e = 0; e < E; ++e) w2[e] = w1[e];
+              certain += tree_sum(w2);
+            }
+          }
+          if (min_p) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) w1[e] = f[e] <= r.dmax ? w1[e] : 0.f;
           }
           kept += tree_sum(w1);
-          if (by_mass) total += tree_sum(w3);
         }
-        if (!min_p) certain = kept;
-        u64 x = __float2ull_rn(kept * 1099511627776.f);
-#pragma unroll
-        for (int o2 = 16; o2 > 0; o2 >>= 1) x += __shfl_xor_sync(DC_FULL_MASK, x, o2);
+        uint32_t hi, lo;
+        fixed(kept, hi, lo);
+        const u64 x = ((u64)__reduce_add_sync(DC_FULL_MASK, hi) << 22) + __reduce_add_sync(DC_FULL_MASK, lo);
         if (lane == 0) put64(peer(&chunk_all[v0 / kChunk + ch], 0), x);
         if (by_mass) {
-          sure += __float2ull_rn(certain * 1099511627776.f);
-          all += __float2ull_rn(total * 1099511627776.f);
+          if (min_p) fixed(certain, hi, lo);
+          sure += ((u64)hi << 22) + lo;
+          fixed(total, hi, lo);
+          all += ((u64)hi << 22) + lo;
         }
       }
       if (by_mass) {
@@ -855,12 +908,12 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
 
 template <bool F32>
 cudaError_t launch(const SampleParams &p, cudaStream_t st) {
-  constexpr int kSize = F32 ? 4 : 2;
-  // blocks of a cluster: slices of about 40 KB, so that several clusters share
-  // the SMs and one's copies run under another's arithmetic
-  const int64_t bytes = (int64_t)p.V * kSize;
-  int blocks = 1;
-  while (blocks < kMostBlocks && bytes > blocks * (40 << 10)) blocks *= 2;
+  constexpr int kSize = F32 ? 4 : 2, kSms = 152;
+  // Blocks of a cluster: as many as keep the launch within four blocks an SM
+  // and a slice at 16 KB or more.  Many rows are fastest with a block each (a
+  // block's fixed steps cost as much as 10,000 tokens), few with all the SMs.
+  int blocks = kMostBlocks;
+  while (blocks > 1 && ((int64_t)p.rows * blocks > 4 * kSms || (int64_t)p.V * kSize < (int64_t)blocks << 14)) blocks /= 2;
   const int chunks = (p.V + kChunk - 1) / kChunk, slice = (chunks + blocks - 1) / blocks * kChunk;
   const bool held = (size_t)slice * kSize <= kMostSlice;
   const size_t smem = kList * 8 + (size_t)(chunks + 1) / 2 * 16 + kBins / blocks * 4 + (held ? (size_t)slice * kSize : 0);
