@@ -5,33 +5,82 @@
 // P = sum p:
 //   loss = T^2 sum_k p_k (log p_k - z_{id_k} + lse(z))
 //   d loss / d x_v = T (P q_v - sum_{k: id_k = v} p_k).
-// One block a row; the row is read once for the log-sum-exp (a running
-// maximum and sum a thread, joined at the end) and once for the gradient.
+//
+// Bound by the bytes of the rows: the loss reads each logit once, the gradient
+// reads and writes once, and the two in one step (k_step) still read once: a
+// cluster of blocks holds a whole row in registers between the sum and the
+// gradient.  The log-sum-exp is a running (maximum, sum) a thread, in a fixed
+// order of threads, warps and blocks, so that a row's result depends on
+// nothing but the row.
+//
+// A row's slices are the blocks': a block of k_loss and k_step takes up to
+// kHold 16-byte vectors a thread; the cluster's size follows from the row's
+// bytes alone.  The teacher's tokens belong to the slice they lie in: each
+// block sums its tokens' terms and writes their gradient after its slice's,
+// from the logit as it was read, so that the gradient may overwrite the logits.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 
 namespace dc {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxK = 1024;
+constexpr int kMostBlocks = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <bool F32>
 struct Row;
 template <>
 struct Row<false> {
+  static constexpr int kVec = 8;
   using T = uint16_t;
   __device__ static float get(const T *x, int v) { return bf16_bits_to_float(x[v]); }
   __device__ static void put(T *x, int v, float f) { x[v] = (uint16_t)bf16_rn_bits(f); }
+  __device__ static void unpack(const uint4 &w, float (&f)[8]) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(x[i] << 16), f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+  }
+  __device__ static uint4 pack(const float (&f)[8]) {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    return make_uint4(x[0], x[1], x[2], x[3]);
+  }
 };
 template <>
 struct Row<true> {
+  static constexpr int kVec = 4;
   using T = float;
   __device__ static float get(const T *x, int v) { return x[v]; }
   __device__ static void put(T *x, int v, float f) { x[v] = f; }
+  __device__ static void unpack(const uint4 &w, float (&f)[4]) {
+    f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
+  }
+  __device__ static uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
 };
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Puts v at `p` in block `rank` of the cluster.
+__device__ __forceinline__ void put_peer(const float *p, int rank, float v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+// s: kWarps entries; every thread gets the same value, warps in order.
 __device__ __forceinline__ float block_reduce(float v, float *s, bool maximum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   v = maximum ? warp_max(v) : warp_sum(v);
@@ -39,93 +88,250 @@ __device__ __forceinline__ float block_reduce(float v, float *s, bool maximum) {
   if (lane == 0) s[warp] = v;
   __syncthreads();
   float r = s[0];
+#pragma unroll
   for (int w = 1; w < kWarps; ++w) r = maximum ? fmaxf(r, s[w]) : r + s[w];
   return r;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kThreads) k_distill(const DistillParams p) {
-  using R = Row<F32>;
-  __shared__ float s_red[kWarps], s_p[kMaxK], s_fix[kMaxK];
-  __shared__ int s_id[kMaxK];
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const typename R::T *x = static_cast<const typename R::T *>(p.logits) + row * p.stride;
-  const float inv_t = 1.f / p.temperature;
-
-  // the teacher's shares
-  float tm = -INFINITY;
-  for (int k = tid; k < p.K; k += kThreads) {
-    const int id = p.ids[(int64_t)row * p.K + k];
-    const bool ok = id >= 0 && id < p.V;
-    s_id[k] = ok ? id : -1;
-    s_p[k] = ok ? p.teacher[(int64_t)row * p.K + k] * inv_t : -INFINITY;  // log p_k, not yet normalised
-    tm = fmaxf(tm, s_p[k]);
+struct Teacher {
+  float red[kWarps];
+  float logp[kMaxK];  // log p_k
+  float fix[kMaxK];   // gradient at the token
+  int4 id4[kMaxK / 4];  // tokens, -1: left out
+  __device__ int &id(int k) { return reinterpret_cast<int *>(id4)[k]; }
+  // sum of p_j over the k's with this token
+  __device__ float share(int token, int K) const {
+    float sum = 0.f;
+    for (int j = 0; j < (K + 3) / 4; ++j) {
+      const int4 t = id4[j];
+      if (t.x == token || t.y == token || t.z == token || t.w == token) {
+        const int ts[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (ts[q] == token && logp[4 * j + q] != -INFINITY) sum += expf(logp[4 * j + q]);
+      }
+    }
+    return sum;
   }
-  float t_lse;
-  if (p.teacher_lse) {
-    t_lse = p.teacher_lse[row];
-  } else {
-    tm = block_reduce(tm, s_red, true);
-    float s = 0.f;
-    if (tm != -INFINITY)
-      for (int k = tid; k < p.K; k += kThreads) s += expf(s_p[k] - tm);
-    s = block_reduce(s, s_red, false);
-    t_lse = tm == -INFINITY ? 0.f : tm + logf(s);
+};
+
+// The row's teacher into shared memory; returns P.
+__device__ __forceinline__ float load_teacher(const DistillParams &p, int64_t row, float inv_t, Teacher &s) {
+  const int tid = threadIdx.x;
+  float m = -INFINITY;
+  if (tid < 3 && p.K + tid < (p.K + 3) / 4 * 4) s.id(p.K + tid) = -1;
+  for (int k = tid; k < p.K; k += kThreads) {
+    const int id = p.ids[row * p.K + k];
+    const bool ok = id >= 0 && id < p.V;
+    const float t = ok ? p.teacher[row * p.K + k] * inv_t : -INFINITY;
+    s.id(k) = ok ? id : -1;
+    s.logp[k] = t;
+    m = fmaxf(m, t);
   }
   float lse;
-  if (p.loss) {
-    float m = -INFINITY;
-    for (int v = tid; v < p.V; v += kThreads) m = fmaxf(m, R::get(x, v));
-    m = block_reduce(m, s_red, true);
-    float s = 0.f;
-    for (int v = tid; v < p.V; v += kThreads) s += exp2f((R::get(x, v) - m) * inv_t * kLog2e);
-    s = block_reduce(s, s_red, false);
-    lse = m * inv_t + logf(s);
+  if (p.teacher_lse) {
+    lse = p.teacher_lse[row];
   } else {
-    lse = p.lse[row];
+    m = block_reduce(m, s.red, true);
+    float sum = 0.f;
+    if (m != -INFINITY)
+      for (int k = tid; k < p.K; k += kThreads) sum += expf(s.logp[k] - m);
+    sum = block_reduce(sum, s.red, false);
+    lse = m == -INFINITY ? 0.f : m + logf(sum);
   }
-  // loss and the corrections at the teacher's tokens
-  const float g = p.grad ? p.grad_loss[row] * p.temperature : 0.f;
-  float mass = 0.f, loss = 0.f;
+  float mass = 0.f;
   for (int k = tid; k < p.K; k += kThreads) {
-    const float logp = s_p[k] - t_lse;
-    const float pk = s_p[k] == -INFINITY ? 0.f : expf(logp);
-    mass += pk;
-    if (pk > 0.f) loss += pk * (logp - R::get(x, s_id[k]) * inv_t + lse);
-    s_p[k] = pk;
+    if (s.logp[k] != -INFINITY) s.logp[k] -= lse;
+    mass += s.logp[k] == -INFINITY ? 0.f : expf(s.logp[k]);
   }
-  mass = block_reduce(mass, s_red, false);
-  if (p.loss) {
-    loss = block_reduce(loss, s_red, false);
-    if (tid == 0) {
-      p.loss[row] = p.temperature * p.temperature * loss;
-      p.lse[row] = lse;
+  return block_reduce(mass, s.red, false);  // (its barriers also publish id and logp)
+}
+
+// Loss, and with GRAD the gradient in the same pass.  A cluster a row.
+template <bool F32, bool GRAD, int HOLD>
+__global__ void __launch_bounds__(kThreads)
+k_step(const DistillParams p, int blocks, int slice_vecs) {
+  using R = Row<F32>;
+  constexpr int E = R::kVec;
+  __shared__ Teacher s;
+  __shared__ float s_max[kMostBlocks], s_sum[kMostBlocks], s_loss[kMostBlocks];
+  const int tid = threadIdx.x, rank = blockIdx.z;
+  const int64_t row = blockIdx.x;
+  const typename R::T *x = static_cast<const typename R::T *>(p.logits) + row * p.stride;
+  const int v0 = rank * slice_vecs * E, v1 = min(p.V, v0 + slice_vecs * E);
+  const int nv = max(0, v1 - v0), full = nv / E;  // whole vectors; the rest singly
+  const uint4 *src = reinterpret_cast<const uint4 *>(x + v0);
+  const float inv_t = 1.f / p.temperature, c = inv_t * kLog2e;
+
+  // the slice: HOLD vectors a thread in flight and kept, what is beyond them read again
+  uint4 held[HOLD];
+#pragma unroll
+  for (int q = 0; q < HOLD; ++q)
+    if (tid + q * kThreads < full) held[q] = __ldcs(src + tid + q * kThreads);
+  const float mass = load_teacher(p, row, inv_t, s);  // (under the loads)
+
+  float m = -INFINITY, sum = 0.f;  // of 2^{c x}, relative to 2^{c m}
+  auto add = [&](const uint4 &w) {
+    float f[E];
+    R::unpack(w, f);
+    float top = f[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) top = fmaxf(top, f[e]);
+    if (top > m) sum *= ex2((m - top) * c), m = top;
+    const float b = m == -INFINITY ? 0.f : m;
+    float part = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) part += ex2((f[e] - b) * c);  // (the difference first: large z keep their accuracy)
+    sum += part;
+  };
+#pragma unroll
+  for (int q = 0; q < HOLD; ++q)
+    if (tid + q * kThreads < full) add(held[q]);
+#pragma unroll 4
+  for (int i = tid + HOLD * kThreads; i < full; i += kThreads) add(__ldcs(src + i));
+  if (tid < nv - full * E) {
+    const float f = R::get(x, v0 + full * E + tid);
+    if (f > m) sum *= ex2((m - f) * c), m = f;
+    if (f > -INFINITY) sum += ex2((f - m) * c);
+  }
+  const float bm = block_reduce(m, s.red, true);
+  const float bs = block_reduce(m == -INFINITY ? 0.f : sum * ex2((m - bm) * c), s.red, false);
+  if (tid == 0) {
+    for (int b = 0; b < blocks; ++b) {
+      put_peer(&s_max[rank], b, bm);
+      put_peer(&s_sum[rank], b, bs);
     }
   }
-  if (!p.grad) return;
+  cluster_sync();
+  float M = s_max[0], S = 0.f;
+  for (int b = 1; b < blocks; ++b) M = fmaxf(M, s_max[b]);
+  for (int b = 0; b < blocks; ++b) S += s_max[b] == -INFINITY ? 0.f : s_sum[b] * ex2((s_max[b] - M) * c);
+  const float lse = M * inv_t + logf(S);
+
+  // the teacher's tokens in this slice
+  const float g = GRAD ? p.grad_loss[row] * p.temperature : 0.f;
+  float loss = 0.f;
   for (int k = tid; k < p.K; k += kThreads) {
-    const int id = s_id[k];
-    if (id < 0) continue;
-    float sum = 0.f;
-    for (int j = 0; j < p.K; ++j)
-      if (s_id[j] == id) sum += s_p[j];
-    s_fix[k] = g == 0.f ? 0.f : g * (mass * expf(R::get(x, id) * inv_t - lse) - sum);
+    const int id = s.id(k);
+    if (id < v0 || id >= v1) continue;
+    const float lp = s.logp[k], xv = R::get(x, id);
+    const float pk = lp == -INFINITY ? 0.f : expf(lp);
+    if (pk > 0.f) loss += pk * (lp - xv * inv_t + lse);
+    if constexpr (GRAD) {
+      s.fix[k] = g == 0.f ? 0.f : g * (mass * expf(xv * inv_t - lse) - s.share(id, p.K));
+    }
   }
-  __syncthreads();
-  typename R::T *grad = static_cast<typename R::T *>(p.grad) + row * p.grad_stride;
-  for (int v = tid; v < p.V; v += kThreads)
-    R::put(grad, v, g == 0.f ? 0.f : g * mass * expf(R::get(x, v) * inv_t - lse));
+  loss = block_reduce(loss, s.red, false);
+  if (tid == 0) put_peer(&s_loss[rank], 0, loss);
+
+  if constexpr (GRAD) {
+    typename R::T *out = static_cast<typename R::T *>(p.grad) + row * p.grad_stride;
+    uint4 *dst = reinterpret_cast<uint4 *>(out + v0);
+    const float gm = g * mass;
+    auto gradient = [&](const uint4 &w) {
+      float f[E];
+      R::unpack(w, f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = gm == 0.f ? 0.f : gm * ex2(fmaf(f[e], inv_t, -lse) * kLog2e);
+      return R::pack(f);
+    };
+    // (what a block reads again it read itself before, and nobody else writes it)
+#pragma unroll
+    for (int q = 0; q < HOLD; ++q)
+      if (tid + q * kThreads < full) __stcs(dst + tid + q * kThreads, gradient(held[q]));
+#pragma unroll 4
+    for (int i = tid + HOLD * kThreads; i < full; i += kThreads) __stcs(dst + i, gradient(__ldcg(src + i)));
+    if (tid < nv - full * E) {
+      const int v = v0 + full * E + tid;
+      R::put(out, v, gm == 0.f ? 0.f : gm * ex2(fmaf(R::get(x, v), inv_t, -lse) * kLog2e));
+    }
+    __syncthreads();
+    for (int k = tid; k < p.K; k += kThreads)
+      if (s.id(k) >= v0 && s.id(k) < v1) R::put(out, s.id(k), s.fix[k]);
+  }
+  cluster_sync();  // the blocks' losses are in the first one's memory
+  if (rank == 0 && tid == 0) {
+    float l = 0.f;
+    for (int b2 = 0; b2 < blocks; ++b2) l += s_loss[b2];
+    p.loss[row] = p.temperature * p.temperature * l;
+    p.lse[row] = lse;
+  }
+}
+
+// The gradient alone, from the loss call's lse: blocks of a row need nothing
+// of each other.
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) k_grad(const DistillParams p, int slice_vecs) {
+  using R = Row<F32>;
+  constexpr int E = R::kVec, kAtOnce = 8;
+  __shared__ Teacher s;
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const typename R::T *x = static_cast<const typename R::T *>(p.logits) + row * p.stride;
+  typename R::T *out = static_cast<typename R::T *>(p.grad) + row * p.grad_stride;
+  const int v0 = blockIdx.z * slice_vecs * E, v1 = min(p.V, v0 + slice_vecs * E);
+  const int nv = max(0, v1 - v0), full = nv / E;
+  const uint4 *src = reinterpret_cast<const uint4 *>(x + v0);
+  uint4 *dst = reinterpret_cast<uint4 *>(out + v0);
+  const float inv_t = 1.f / p.temperature;
+  uint4 w[kAtOnce];
+#pragma unroll
+  for (int q = 0; q < kAtOnce; ++q)
+    if (tid + q * kThreads < full) w[q] = __ldcs(src + tid + q * kThreads);
+  const float lse = p.lse[row], g = p.grad_loss[row] * p.temperature;
+  const float mass = load_teacher(p, row, inv_t, s);  // (under the loads)
+  for (int k = tid; k < p.K; k += kThreads) {
+    const int id = s.id(k);
+    if (id < v0 || id >= v1) continue;
+    s.fix[k] = g == 0.f ? 0.f : g * (mass * expf(R::get(x, id) * inv_t - lse) - s.share(id, p.K));
+  }
+  const float gm = g * mass;
+  const float last = tid < nv - full * E ? R::get(x, v0 + full * E + tid) : 0.f;
+  __syncthreads();  // every logit that is read singly has been read
+  for (int i0 = tid; i0 < full; i0 += kAtOnce * kThreads) {
+    if (i0 != tid) {
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q)
+        if (i0 + q * kThreads < full) w[q] = __ldcs(src + i0 + q * kThreads);
+    }
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q) {
+      if (i0 + q * kThreads >= full) continue;
+      float f[E];
+      R::unpack(w[q], f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = gm == 0.f ? 0.f : gm * ex2(fmaf(f[e], inv_t, -lse) * kLog2e);
+      __stcs(dst + i0 + q * kThreads, R::pack(f));
+    }
+  }
+  if (tid < nv - full * E) R::put(out, v0 + full * E + tid, gm == 0.f ? 0.f : gm * ex2(fmaf(last, inv_t, -lse) * kLog2e));
   __syncthreads();
   for (int k = tid; k < p.K; k += kThreads)
-    if (s_id[k] >= 0) R::put(grad, s_id[k], s_fix[k]);
+    if (s.id(k) >= v0 && s.id(k) < v1) R::put(out, s.id(k), s.fix[k]);
+}
+
+template <bool F32>
+cudaError_t launch(const DistillParams &p, cudaStream_t st) {
+  constexpr int E = Row<F32>::kVec;
+  const int vecs = (p.V + E - 1) / E;
+  // blocks a row, by its length alone: slices of at most 8 vectors a thread
+  // (32 KB), up to eight of them; a longer slice's rest is read twice
+  int blocks = 1;
+  while (blocks < kMostBlocks && vecs > blocks * 8 * kThreads) blocks *= 2;
+  const int slice = (vecs + blocks - 1) / blocks;
+  const dim3 grid((unsigned)p.rows, 1, (unsigned)blocks), block(kThreads);
+  if (!p.loss) return launch_ex(k_grad<F32>, grid, block, 0, st, false, 0, p, slice);
+  const int hold = (slice + kThreads - 1) / kThreads;
+  if (!p.grad) return launch_ex(k_step<F32, false, 8>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
+  if (hold <= 8) return launch_ex(k_step<F32, true, 8>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
+  if (hold <= 12) return launch_ex(k_step<F32, true, 12>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
+  return launch_ex(k_step<F32, true, 20>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
 }
 
 }  // namespace
 
 cudaError_t launch_distill(const DistillParams &p, bool f32, cudaStream_t st) {
-  if (f32) k_distill<true><<<p.rows, kThreads, 0, st>>>(p);
-  else k_distill<false><<<p.rows, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return f32 ? launch<true>(p, st) : launch<false>(p, st);
 }
 
 }  // namespace dc

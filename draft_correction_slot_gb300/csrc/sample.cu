@@ -286,6 +286,38 @@ __device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The vector at `at` that reaches past the row's V logits: -inf there.
+template <bool F32>
+__device__ __noinline__ uint4 fetch_tail(const uint8_t *row, int at, int V) {
+  uint32_t x[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (F32) {
+      x[q] = at + q < V ? reinterpret_cast<const uint32_t *>(row)[at + q] : 0xFF800000u;
+    } else {
+      const uint32_t a = at + 2 * q < V ? reinterpret_cast<const uint16_t *>(row)[at + 2 * q] : 0xFF80u;
+      const uint32_t b = at + 2 * q + 1 < V ? reinterpret_cast<const uint16_t *>(row)[at + 2 * q + 1] : 0xFF80u;
+      x[q] = a | b << 16;
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+// NaN to -inf.
+template <bool F32>
+__device__ __noinline__ uint4 without_nan(uint4 w) {
+  uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (F32) {
+      if ((x[q] & 0x7FFFFFFFu) > 0x7F800000u) x[q] = 0xFF800000u;
+    } else {
+      if ((x[q] & 0x7FFFu) > 0x7F80u) x[q] = (x[q] & 0xFFFF0000u) | 0xFF80u;
+      if ((x[q] & 0x7FFF0000u) > 0x7F800000u) x[q] = (x[q] & 0xFFFFu) | 0xFF800000u;
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 // E logits of a 16-byte vector as floats.
 template <bool F32>
 __device__ __forceinline__ void unpack(const uint4 &w, float (&f)[F32 ? 4 : 8]) {
@@ -298,7 +330,7 @@ __device__ __forceinline__ void unpack(const uint4 &w, float (&f)[F32 ? 4 : 8]) 
 }
 
 template <bool F32, bool HELD>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
 k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   constexpr int E = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -316,41 +348,15 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   const int nch = (nv + kChunk - 1) / kChunk, vecs = nch * (kChunk / E);
   cluster_arrive();  // (this block is there)
 
+  bool nan = false;  // (not held) this thread's block met a NaN
   // A vector of the slice; past the vocabulary's end: -inf.
   auto fetch = [&](int i) {
     const int at = v0 + i * E;
-    if (at + E <= V) return ld_stream_v4(src + (int64_t)at * kSize);
-    uint32_t x[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if constexpr (F32) {
-        x[q] = at + q < V ? reinterpret_cast<const uint32_t *>(src)[at + q] : 0xFF800000u;
-      } else {
-        const uint32_t a = at + 2 * q < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q] : 0xFF80u;
-        const uint32_t b = at + 2 * q + 1 < V ? reinterpret_cast<const uint16_t *>(src)[at + 2 * q + 1] : 0xFF80u;
-        x[q] = a | b << 16;
-      }
-    }
-    return make_uint4(x[0], x[1], x[2], x[3]);
+    return at + E <= V ? ld_stream_v4(src + (int64_t)at * kSize) : fetch_tail<F32>(src, at, V);
   };
-  // NaN to -inf
-  auto without_nan = [&](uint4 w) {
-    uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if constexpr (F32) {
-        if ((x[q] & 0x7FFFFFFFu) > 0x7F800000u) x[q] = 0xFF800000u;
-      } else {
-        if ((x[q] & 0x7FFFu) > 0x7F80u) x[q] = (x[q] & 0xFFFF0000u) | 0xFF80u;
-        if ((x[q] & 0x7FFF0000u) > 0x7F800000u) x[q] = (x[q] & 0xFFFFu) | 0xFF800000u;
-      }
-    }
-    return make_uint4(x[0], x[1], x[2], x[3]);
-  };
-  bool nan = false;  // (not held) this thread's block met a NaN
   auto vec = [&](int i) {
     if constexpr (HELD) return reinterpret_cast<const uint4 *>(data)[i];
-    else return nan ? without_nan(fetch(i)) : fetch(i);
+    else return nan ? without_nan<F32>(fetch(i)) : fetch(i);
   };
   // a vector's largest logit; NaN if it has one
   auto best_of = [&](const uint4 &w) {
@@ -391,7 +397,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       float m = best_of(w[q]);
       if (m != m) {
         nan = true;
-        w[q] = without_nan(w[q]);
+        w[q] = without_nan<F32>(w[q]);
         m = best_of(w[q]);
       }
       if constexpr (HELD) reinterpret_cast<uint4 *>(data)[i0 + q * kThreads] = w[q];
@@ -479,8 +485,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
     // histogram: the bin is the integer below 2^23 + d scale, by the addition's own rounding
     const float dtop = (float)(kBins - 1) / scale;
     auto bin_of = [&](float x) { return __float_as_uint(fmaf(fminf(mx - x, dtop), scale, 8388608.f)) & (2 * kBins - 1); };
-    for (int i = tid; i < vecs; i += kThreads) {
-      const uint4 w = vec(i);
+    auto count = [&](const uint4 &w) {
       if (by_list) {
         const float m = best_of(w);
         if (m > -INFINITY) atomicAdd(&hist[min(bin_of(m), (uint32_t)kBins - 1)], 1u);
@@ -490,7 +495,18 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
 #pragma unroll
         for (int e = 0; e < E; ++e) atomicAdd(&hist[bin_of(f[e])], 1u);  // (-inf: the last bin)
       }
+    };
+    for (int i0 = tid; i0 < vecs; i0 += 4 * kThreads) {  // four loads in flight
+      uint4 w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i0 + q * kThreads < vecs) w[q] = vec(i0 + q * kThreads);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i0 + q * kThreads < vecs) count(w[q]);
     }
+  }
+  if (!general && (by_mass || (by_list && !small))) {
     cluster_sync();
     for (int i = tid; i < share; i += kThreads) {
       uint32_t n = 0;
@@ -623,16 +639,23 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       }
     };
     if (o.step == kCollect) {
-      for (int i = tid; i < vecs; i += kThreads) {
-        const uint4 w = vec(i);
-        const float m = best_of(w);
-        if (m > -INFINITY && mx - m < o.to) {
-          float f[E];
-          unpack<F32>(w, f);
-          uint32_t bits = 0;
+      for (int i0 = tid; i0 < vecs; i0 += 4 * kThreads) {
+        uint4 w[4];
 #pragma unroll
-          for (int e = 0; e < E; ++e) bits |= f[e] > -INFINITY && mx - f[e] < o.to ? 1u << e : 0u;
-          collect(i, bits);
+        for (int q = 0; q < 4; ++q)
+          if (i0 + q * kThreads < vecs) w[q] = vec(i0 + q * kThreads);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (i0 + q * kThreads >= vecs) continue;
+          const float m = best_of(w[q]);
+          if (m > -INFINITY && mx - m < o.to) {
+            float f[E];
+            unpack<F32>(w[q], f);
+            uint32_t bits = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) bits |= f[e] > -INFINITY && mx - f[e] < o.to ? 1u << e : 0u;
+            collect(i0 + q * kThreads, bits);
+          }
         }
       }
     } else {
@@ -657,13 +680,20 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
         hi = (uint32_t)f;
         lo = __float2uint_rn((y - f) * 4194304.f);
       };
+      constexpr int kVecs = kChunk / E / 32;  // of a lane in a chunk
+      uint4 ahead[kVecs];                     // the next chunk's
+      if (warp < nch) {
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) ahead[q] = vec(warp * (kChunk / E) + q * 32 + lane);
+      }
       for (int ch = warp; ch < nch; ch += kWarps) {
         float kept = 0.f, certain = 0.f, total = 0.f;  // of this lane's 16 tokens
-#pragma unroll 1
-        for (int q = 0; q < kChunk / E / 32; ++q) {
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
           const int i = ch * (kChunk / E) + q * 32 + lane;
           float f[E], w1[E];
-          unpack<F32>(vec(i), f);
+          unpack<F32>(ahead[q], f);
+          if (ch + kWarps < nch) ahead[q] = vec(i + kWarps * (kChunk / E));
 #pragma unroll
           for (int e = 0; e < E; ++e) f[e] = fminf(mx - f[e], dfar), w1[e] = weight(f[e]);
           if (by_mass) {
@@ -909,11 +939,15 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
 template <bool F32>
 cudaError_t launch(const SampleParams &p, cudaStream_t st) {
   constexpr int kSize = F32 ? 4 : 2, kSms = 152;
-  // Blocks of a cluster: as many as keep the launch within four blocks an SM
-  // and a slice at 16 KB or more.  Many rows are fastest with a block each (a
-  // block's fixed steps cost as much as 10,000 tokens), few with all the SMs.
+  // Blocks of a cluster: as many as keep the launch within the three blocks an
+  // SM holds and a slice at 16 KB or more, and two at least.  A block's fixed
+  // steps cost as much as some 10,000 tokens, so many rows want few blocks, but
+  // one block alone waits too long on its own loads.  512 rows of 151936 bf16
+  // logits: 208 / 180 / 260 us with 1 / 2 / 8 blocks; 100 rows: 59 / 66 us with
+  // 4 / 8; 16 rows: 90 / 51 / 30 us with 2 / 4 / 8.
   int blocks = kMostBlocks;
-  while (blocks > 1 && ((int64_t)p.rows * blocks > 4 * kSms || (int64_t)p.V * kSize < (int64_t)blocks << 14)) blocks /= 2;
+  while (blocks > 2 && (int64_t)p.rows * blocks > 3 * kSms) blocks /= 2;
+  while (blocks > 1 && (int64_t)p.V * kSize < (int64_t)blocks << 14) blocks /= 2;
   const int chunks = (p.V + kChunk - 1) / kChunk, slice = (chunks + blocks - 1) / blocks * kChunk;
   const bool held = (size_t)slice * kSize <= kMostSlice;
   const size_t smem = kList * 8 + (size_t)(chunks + 1) / 2 * 16 + kBins / blocks * 4 + (held ? (size_t)slice * kSize : 0);
