@@ -96,7 +96,7 @@ __device__ __forceinline__ float block_reduce(float v, float *s, bool maximum) {
 struct Teacher {
   float red[kWarps];
   float logp[kMaxK];  // log p_k
-  float fix[kMaxK];   // gradient at the token
+  float x[kMaxK];     // the logit of a token in this block's slice; then its gradient
   int4 id4[kMaxK / 4];  // tokens, -1: left out
   __device__ int &id(int k) { return reinterpret_cast<int *>(id4)[k]; }
   // sum of p_j over the k's with this token
@@ -115,8 +115,12 @@ struct Teacher {
   }
 };
 
-// The row's teacher into shared memory; returns P.
-__device__ __forceinline__ float load_teacher(const DistillParams &p, int64_t row, float inv_t, Teacher &s) {
+// The row's teacher into shared memory, and the logits of its tokens in [v0,
+// v1); returns P.
+template <bool F32>
+__device__ __forceinline__ float load_teacher(const DistillParams &p, int64_t row, float inv_t, int v0, int v1,
+                                              Teacher &s) {
+  const typename Row<F32>::T *x = static_cast<const typename Row<F32>::T *>(p.logits) + row * p.stride;
   const int tid = threadIdx.x;
   float m = -INFINITY;
   if (tid < 3 && p.K + tid < (p.K + 3) / 4 * 4) s.id(p.K + tid) = -1;
@@ -126,6 +130,7 @@ __device__ __forceinline__ float load_teacher(const DistillParams &p, int64_t ro
     const float t = ok ? p.teacher[row * p.K + k] * inv_t : -INFINITY;
     s.id(k) = ok ? id : -1;
     s.logp[k] = t;
+    if (id >= v0 && id < v1) s.x[k] = Row<F32>::get(x, id);
     m = fmaxf(m, t);
   }
   float lse;
@@ -147,14 +152,20 @@ __device__ __forceinline__ float load_teacher(const DistillParams &p, int64_t ro
   return block_reduce(mass, s.red, false);  // (its barriers also publish id and logp)
 }
 
+// What a block says of its slice: maximum, sum of e^{(x - max) / T}, and of
+// its teacher's tokens sum p_k (log p_k - (x_k - max) / T) and sum p_k.
+struct Part {
+  float max, sum, loss, mass;
+};
+
 // Loss, and with GRAD the gradient in the same pass.  A cluster a row.
 template <bool F32, bool GRAD, int HOLD>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, HOLD <= 10 ? 4 : 2)
 k_step(const DistillParams p, int blocks, int slice_vecs) {
   using R = Row<F32>;
   constexpr int E = R::kVec;
   __shared__ Teacher s;
-  __shared__ float s_max[kMostBlocks], s_sum[kMostBlocks], s_loss[kMostBlocks];
+  __shared__ Part s_part[kMostBlocks];
   const int tid = threadIdx.x, rank = blockIdx.z;
   const int64_t row = blockIdx.x;
   const typename R::T *x = static_cast<const typename R::T *>(p.logits) + row * p.stride;
@@ -168,7 +179,7 @@ k_step(const DistillParams p, int blocks, int slice_vecs) {
 #pragma unroll
   for (int q = 0; q < HOLD; ++q)
     if (tid + q * kThreads < full) held[q] = __ldcs(src + tid + q * kThreads);
-  const float mass = load_teacher(p, row, inv_t, s);  // (under the loads)
+  const float mass = load_teacher<F32>(p, row, inv_t, v0, v1, s);  // (under the loads)
 
   float m = -INFINITY, sum = 0.f;  // of 2^{c x}, relative to 2^{c m}
   auto add = [&](const uint4 &w) {
@@ -196,38 +207,51 @@ k_step(const DistillParams p, int blocks, int slice_vecs) {
   }
   const float bm = block_reduce(m, s.red, true);
   const float bs = block_reduce(m == -INFINITY ? 0.f : sum * ex2((m - bm) * c), s.red, false);
-  if (tid == 0) {
-    for (int b = 0; b < blocks; ++b) {
-      put_peer(&s_max[rank], b, bm);
-      put_peer(&s_sum[rank], b, bs);
-    }
-  }
-  cluster_sync();
-  float M = s_max[0], S = 0.f;
-  for (int b = 1; b < blocks; ++b) M = fmaxf(M, s_max[b]);
-  for (int b = 0; b < blocks; ++b) S += s_max[b] == -INFINITY ? 0.f : s_sum[b] * ex2((s_max[b] - M) * c);
-  const float lse = M * inv_t + logf(S);
-
-  // the teacher's tokens in this slice
-  const float g = GRAD ? p.grad_loss[row] * p.temperature : 0.f;
-  float loss = 0.f;
+  const float ref = bm == -INFINITY ? 0.f : bm;
+  float loss = 0.f, here = 0.f;
   for (int k = tid; k < p.K; k += kThreads) {
     const int id = s.id(k);
     if (id < v0 || id >= v1) continue;
-    const float lp = s.logp[k], xv = R::get(x, id);
-    const float pk = lp == -INFINITY ? 0.f : expf(lp);
-    if (pk > 0.f) loss += pk * (lp - xv * inv_t + lse);
-    if constexpr (GRAD) {
-      s.fix[k] = g == 0.f ? 0.f : g * (mass * expf(xv * inv_t - lse) - s.share(id, p.K));
-    }
+    const float lp = s.logp[k], pk = lp == -INFINITY ? 0.f : expf(lp);
+    here += pk;
+    if (pk > 0.f) loss += pk * (lp - (s.x[k] - ref) * inv_t);
   }
   loss = block_reduce(loss, s.red, false);
-  if (tid == 0) put_peer(&s_loss[rank], 0, loss);
+  here = block_reduce(here, s.red, false);
+  if (tid == 0) {
+    for (int b = GRAD ? 0 : blocks - 1; b < blocks; ++b) {
+      const int to = GRAD ? b : 0;  // the loss alone: the first block only
+      put_peer(&s_part[rank].max, to, bm);
+      put_peer(&s_part[rank].sum, to, bs);
+      put_peer(&s_part[rank].loss, to, loss);
+      put_peer(&s_part[rank].mass, to, here);
+    }
+  }
+  cluster_sync();
+  if (!GRAD && rank != 0) return;
+  float M = s_part[0].max, S = 0.f;
+  for (int b = 1; b < blocks; ++b) M = fmaxf(M, s_part[b].max);
+  for (int b = 0; b < blocks; ++b) S += s_part[b].max == -INFINITY ? 0.f : s_part[b].sum * ex2((s_part[b].max - M) * c);
+  const float lse = M * inv_t + logf(S);
+  if (rank == 0 && tid == 0) {
+    float l = 0.f;
+    for (int b = 0; b < blocks; ++b) {
+      const Part q = s_part[b];
+      // (log S on its own: the maxima's difference is exact where M / T + log S is rounded)
+      if (q.mass > 0.f) l += q.loss + q.mass * ((M - (q.max == -INFINITY ? 0.f : q.max)) * inv_t + logf(S));
+    }
+    p.loss[row] = p.temperature * p.temperature * l;
+    p.lse[row] = lse;
+  }
 
   if constexpr (GRAD) {
     typename R::T *out = static_cast<typename R::T *>(p.grad) + row * p.grad_stride;
     uint4 *dst = reinterpret_cast<uint4 *>(out + v0);
-    const float gm = g * mass;
+    const float g = p.grad_loss[row] * p.temperature, gm = g * mass;
+    for (int k = tid; k < p.K; k += kThreads) {
+      const int id = s.id(k);
+      if (id >= v0 && id < v1) s.x[k] = g == 0.f ? 0.f : g * (mass * expf(s.x[k] * inv_t - lse) - s.share(id, p.K));
+    }
     auto gradient = [&](const uint4 &w) {
       float f[E];
       R::unpack(w, f);
@@ -247,17 +271,9 @@ k_step(const DistillParams p, int blocks, int slice_vecs) {
     }
     __syncthreads();
     for (int k = tid; k < p.K; k += kThreads)
-      if (s.id(k) >= v0 && s.id(k) < v1) R::put(out, s.id(k), s.fix[k]);
-  }
-  cluster_sync();  // the blocks' losses are in the first one's memory
-  if (rank == 0 && tid == 0) {
-    float l = 0.f;
-    for (int b2 = 0; b2 < blocks; ++b2) l += s_loss[b2];
-    p.loss[row] = p.temperature * p.temperature * l;
-    p.lse[row] = lse;
+      if (s.id(k) >= v0 && s.id(k) < v1) R::put(out, s.id(k), s.x[k]);
   }
 }
-
 // The gradient alone, from the loss call's lse: blocks of a row need nothing
 // of each other.
 template <bool F32>
@@ -279,11 +295,10 @@ __global__ void __launch_bounds__(kThreads) k_grad(const DistillParams p, int sl
   for (int q = 0; q < kAtOnce; ++q)
     if (tid + q * kThreads < full) w[q] = __ldcs(src + tid + q * kThreads);
   const float lse = p.lse[row], g = p.grad_loss[row] * p.temperature;
-  const float mass = load_teacher(p, row, inv_t, s);  // (under the loads)
+  const float mass = load_teacher<F32>(p, row, inv_t, v0, v1, s);  // (under the loads)
   for (int k = tid; k < p.K; k += kThreads) {
     const int id = s.id(k);
-    if (id < v0 || id >= v1) continue;
-    s.fix[k] = g == 0.f ? 0.f : g * (mass * expf(R::get(x, id) * inv_t - lse) - s.share(id, p.K));
+    if (id >= v0 && id < v1) s.x[k] = g == 0.f ? 0.f : g * (mass * expf(s.x[k] * inv_t - lse) - s.share(id, p.K));
   }
   const float gm = g * mass;
   const float last = tid < nv - full * E ? R::get(x, v0 + full * E + tid) : 0.f;
@@ -307,25 +322,27 @@ __global__ void __launch_bounds__(kThreads) k_grad(const DistillParams p, int sl
   if (tid < nv - full * E) R::put(out, v0 + full * E + tid, gm == 0.f ? 0.f : gm * ex2(fmaf(last, inv_t, -lse) * kLog2e));
   __syncthreads();
   for (int k = tid; k < p.K; k += kThreads)
-    if (s.id(k) >= v0 && s.id(k) < v1) R::put(out, s.id(k), s.fix[k]);
+    if (s.id(k) >= v0 && s.id(k) < v1) R::put(out, s.id(k), s.x[k]);
 }
 
 template <bool F32>
 cudaError_t launch(const DistillParams &p, cudaStream_t st) {
   constexpr int E = Row<F32>::kVec;
   const int vecs = (p.V + E - 1) / E;
-  // blocks a row, by its length alone: slices of at most 8 vectors a thread
-  // (32 KB), up to eight of them; a longer slice's rest is read twice
+  // Blocks a row, by its length alone: slices of at most 8 vectors a thread
+  // (32 KB), up to eight of them.  A longer slice of the step takes up to 20
+  // vectors a thread (fewer blocks an SM), what is beyond them is read twice.
   int blocks = 1;
   while (blocks < kMostBlocks && vecs > blocks * 8 * kThreads) blocks *= 2;
   const int slice = (vecs + blocks - 1) / blocks;
   const dim3 grid((unsigned)p.rows, 1, (unsigned)blocks), block(kThreads);
   if (!p.loss) return launch_ex(k_grad<F32>, grid, block, 0, st, false, 0, p, slice);
   const int hold = (slice + kThreads - 1) / kThreads;
-  if (!p.grad) return launch_ex(k_step<F32, false, 8>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
-  if (hold <= 8) return launch_ex(k_step<F32, true, 8>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
-  if (hold <= 12) return launch_ex(k_step<F32, true, 12>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
-  return launch_ex(k_step<F32, true, 20>, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
+  const auto kernel = !p.grad      ? k_step<F32, false, 10>
+                      : hold <= 8  ? k_step<F32, true, 8>
+                      : hold <= 10 ? k_step<F32, true, 10>
+                                   : k_step<F32, true, 20>;
+  return launch_ex(kernel, grid, block, 0, st, false, (unsigned)blocks, p, blocks, slice);
 }
 
 }  // namespace
