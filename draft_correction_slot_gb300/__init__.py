@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -136,8 +137,8 @@ def _load():
     L.dcoco_stage_name.restype = C.c_char_p
     P, I, I64, F = C.c_void_p, C.c_int, C.c_int64, C.c_float
     L.dcoco_tree_create.argtypes = [C.POINTER(dcoco_tree_config), C.POINTER(P)]
-    L.dcoco_tree_attention.argtypes = [P, I, I, C.POINTER(dcoco_tree_attention_args), P, P, P]
-    L.dcoco_tree_commit.argtypes = [P, I, I, C.POINTER(dcoco_tree_commit_args), P, P, P, P, P]
+    L.dcoco_tree_attention.argtypes = [P, I, I, P, P, P, P]
+    L.dcoco_tree_commit.argtypes = [P, I, I, P, P, P, P, P, P]
     L.dcoco_tree_status.argtypes = [P]
     L.dcoco_tree_launches.argtypes = [P]
     L.dcoco_tree_launches.restype = C.c_longlong
@@ -337,28 +338,29 @@ def dcoco_stage_name(handle, s: int) -> str | None:
 
 
 # ------------------------------------------------------------------ the target's side of a drafted block
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
-def _dense(t, name: str, shape: tuple, dtype, none_ok: bool = False):
-    """A contiguous CUDA tensor of that shape and type (or None): its pointer."""
-    if t is None:
-        _need(none_ok, f"{name} is required")
-        return None
-    _need(t.dtype == dtype and t.is_cuda and t.shape == shape and t.is_contiguous(),
-          f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+def _dense(t, name: str, shape: tuple, dtype) -> int:
+    """The pointer of a contiguous CUDA tensor of that shape and type."""
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
-def _heads(t, name: str, shape: tuple, dtype):
-    """A CUDA tensor whose last axis (a head's elements) is dense: (pointer, the other axes' strides)."""
-    _need(t.dtype == dtype and t.is_cuda and t.shape == shape, f"{name} must be a CUDA {dtype} tensor of shape {shape}")
+def _dense_or_none(t, name: str, shape: tuple, dtype) -> int:
+    return 0 if t is None else _dense(t, name, shape, dtype)
+
+
+def _heads(t, name: str, shape: tuple, dtype) -> tuple:
+    """A CUDA tensor whose last axis (a head's elements) is dense: its pointer and the other axes' strides."""
     st = t.stride()
-    _need(st[-1] == 1, f"the elements of a head must be dense in {name}")
-    # the stride of an axis of one element says nothing: any value addresses it
-    return (t.data_ptr(), *(0 if n == 1 else x for n, x in zip(shape[:-1], st)))
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or st[-1] != 1:
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {shape} whose last axis is dense")
+    return (t.data_ptr(), *st[:-1])
+
+
+# the C structures as bytes (a ctypes structure takes several times as long to fill)
+_ATTENTION_ARGS = struct.Struct("@" + "P3q" * 5 + "PqPPPqif")
+_COMMIT_ARGS = struct.Struct("@6Pq" + "P4q" * 4 + "ii")
+assert _ATTENTION_ARGS.size == C.sizeof(dcoco_tree_attention_args) and _COMMIT_ARGS.size == C.sizeof(dcoco_tree_commit_args)
 
 
 class _TreeHandle(C.c_void_p):
@@ -377,11 +379,12 @@ def dcoco_tree_create(max_batch: int, max_tree: int, q_heads: int, kv_heads: int
     return h
 
 
-def _page_table(page_table, batch: int, max_pages: int):
-    _need(page_table.dtype == torch.int32 and page_table.is_cuda and page_table.dim() == 2
-          and page_table.shape[0] == batch and page_table.shape[1] >= max_pages and page_table.stride(1) == 1,
-          f"page_table must be a CUDA int32 tensor of shape ({batch}, >= {max_pages}) with dense rows")
-    return page_table.data_ptr(), (page_table.stride(0) if batch > 1 else max(page_table.stride(0), max_pages))
+def _page_table(page_table, batch: int, max_pages: int) -> tuple:
+    shape, st = page_table.shape, page_table.stride()
+    if page_table.dtype is not torch.int32 or not page_table.is_cuda or len(shape) != 2 or shape[0] != batch \
+            or shape[1] < max_pages or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"page_table must be a CUDA int32 tensor of shape ({batch}, >= {max_pages}) with dense rows")
+    return page_table.data_ptr(), (st[0] if batch > 1 else max_pages)
 
 
 def dcoco_tree_attention(handle, batch: int, q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, *, out,
@@ -395,21 +398,21 @@ def dcoco_tree_attention(handle, batch: int, q, k_new, v_new, k_cache, v_cache, 
     out [batch, nodes, q_heads, D] and lse fp32 [batch, nodes, q_heads] are written.  scale: 1/sqrt(D)."""
     hq, hkv, d, page, max_pages, dt = handle.sizes
     nodes, pages = q.shape[1], k_cache.shape[0]
-    new, pool = (batch, nodes, hkv, d), (pages, page, hkv, d)
-    mask_ptr, mask_stride = None, 0
+    new, pool, one, i32 = (batch, nodes, hkv, d), (pages, page, hkv, d), (batch,), torch.int32
+    mask_ptr = mask_stride = 0
     if tree_mask is not None:
         words = (nodes + 31) // 32
-        n = batch if tree_mask.dim() == 3 and tree_mask.shape[0] == batch else 1
-        mask_ptr = _dense(tree_mask, "tree_mask", (n, nodes, words), torch.int32)
-        mask_stride = nodes * words if n == batch else 0
-    args = dcoco_tree_attention_args(
+        shared = tree_mask.shape[0] == 1 and batch != 1
+        mask_ptr = _dense(tree_mask, "tree_mask", (1 if shared else batch, nodes, words), i32)
+        mask_stride = 0 if shared else nodes * words
+    args = _ATTENTION_ARGS.pack(
         *_heads(q, "q", (batch, nodes, hq, d), dt), *_heads(k_new, "k_new", new, dt),
         *_heads(v_new, "v_new", new, dt), *_heads(k_cache, "k_cache", pool, dt),
         *_heads(v_cache, "v_cache", pool, dt), *_page_table(page_table, batch, max_pages),
-        _dense(ctx_len, "ctx_len", (batch,), torch.int32), _dense(tree_len, "tree_len", (batch,), torch.int32, True),
+        _dense(ctx_len, "ctx_len", one, i32), _dense_or_none(tree_len, "tree_len", one, i32),
         mask_ptr, mask_stride, pages, d ** -0.5 if scale is None else scale)
-    _check(_lib.dcoco_tree_attention(handle, batch, nodes, C.byref(args), _dense(out, "out", (batch, nodes, hq, d), dt),
-                                     _dense(lse, "lse", (batch, nodes, hq), torch.float32, True), _stream(stream)),
+    _check(_lib.dcoco_tree_attention(handle, batch, nodes, args, _dense(out, "out", (batch, nodes, hq, d), dt),
+                                     _dense_or_none(lse, "lse", (batch, nodes, hq), torch.float32), _stream(stream)),
            "dcoco_tree_attention")
 
 
@@ -423,13 +426,13 @@ def dcoco_tree_commit(handle, batch: int, tokens, parents, sampled, k_new, v_new
     nodes, layers, pages = tokens.shape[1], k_cache.shape[0], k_cache.shape[1]
     i32, tree, one = torch.int32, (batch, nodes), (batch,)
     new, pool = (layers, batch, nodes, hkv, d), (layers, pages, page, hkv, d)
-    args = dcoco_tree_commit_args(
+    args = _COMMIT_ARGS.pack(
         _dense(tokens, "tokens", tree, i32), _dense(parents, "parents", tree, i32),
-        _dense(sampled, "sampled", tree, i32), _dense(tree_len, "tree_len", one, i32, True),
+        _dense(sampled, "sampled", tree, i32), _dense_or_none(tree_len, "tree_len", one, i32),
         _dense(ctx_len, "ctx_len", one, i32), *_page_table(page_table, batch, max_pages),
         *_heads(k_new, "k_new", new, dt), *_heads(v_new, "v_new", new, dt),
         *_heads(k_cache, "k_cache", pool, dt), *_heads(v_cache, "v_cache", pool, dt), pages, layers)
-    _check(_lib.dcoco_tree_commit(handle, batch, nodes, C.byref(args), _dense(path, "path", tree, i32),
+    _check(_lib.dcoco_tree_commit(handle, batch, nodes, args, _dense(path, "path", tree, i32),
                                   _dense(accept_len, "accept_len", one, i32),
                                   _dense(next_token, "next_token", one, i32), _dense(new_len, "new_len", one, i32),
                                   _stream(stream)), "dcoco_tree_commit")
@@ -447,13 +450,15 @@ def dcoco_tree_destroy(handle) -> None:
     _lib.dcoco_tree_destroy(handle)
 
 
-def _logit_rows(logits, name: str = "logits"):
+def _logit_rows(logits, name: str = "logits") -> tuple:
     """[rows, vocab] with dense rows: (rows, vocab, pointer, dtype code, row stride)."""
-    _need(logits.dim() == 2 and logits.is_cuda and logits.dtype in (torch.bfloat16, torch.float32)
-          and logits.stride(1) == 1, f"{name} must be a CUDA bf16 or fp32 [rows, vocab] tensor with dense rows")
-    rows, vocab = logits.shape
-    stride = logits.stride(0) if rows > 1 else max(logits.stride(0), (vocab + 7) // 8 * 8)
-    return rows, vocab, logits.data_ptr(), _DTYPE[logits.dtype], stride
+    dt, shape, st = logits.dtype, logits.shape, logits.stride()
+    if len(shape) != 2 or not logits.is_cuda or (dt is not torch.bfloat16 and dt is not torch.float32) \
+            or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be a CUDA bf16 or fp32 [rows, vocab] tensor with dense rows")
+    rows, vocab = shape
+    # (one row's stride is never used: any that passes)
+    return rows, vocab, logits.data_ptr(), _DTYPE[dt], st[0] if rows > 1 else (vocab + 7) // 8 * 8
 
 
 def dcoco_sample(logits, u, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
@@ -462,24 +467,26 @@ def dcoco_sample(logits, u, tokens, *, temperature=None, top_k=None, top_p=None,
     [rows]; temperature, top_p, min_p fp32 and top_k int32 [rows] or None; tokens int32, logprob fp32 [rows]."""
     rows, vocab, ptr, dt, stride = _logit_rows(logits)
     one, f32 = (rows,), torch.float32
-    _check(_lib.dcoco_sample(rows, vocab, ptr, dt, stride, _dense(temperature, "temperature", one, f32, True),
-                             _dense(top_k, "top_k", one, torch.int32, True), _dense(top_p, "top_p", one, f32, True),
-                             _dense(min_p, "min_p", one, f32, True), _dense(u, "u", one, f32),
-                             _dense(tokens, "tokens", one, torch.int32), _dense(logprob, "logprob", one, f32, True),
+    _check(_lib.dcoco_sample(rows, vocab, ptr, dt, stride, _dense_or_none(temperature, "temperature", one, f32),
+                             _dense_or_none(top_k, "top_k", one, torch.int32), _dense_or_none(top_p, "top_p", one, f32),
+                             _dense_or_none(min_p, "min_p", one, f32), _dense(u, "u", one, f32),
+                             _dense(tokens, "tokens", one, torch.int32), _dense_or_none(logprob, "logprob", one, f32),
                              _stream(stream)), "dcoco_sample")
 
 
 def _teacher(logits, teacher_ids, teacher_logits, teacher_lse, temperature):
     rows, vocab, ptr, dt, stride = _logit_rows(logits)
-    _need(teacher_ids.dim() == 2, "teacher_ids must be [rows, topk]")
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must be [rows, topk]")
     k, f32 = teacher_ids.shape[1], torch.float32
     return (rows, vocab, ptr, dt, stride, k, _dense(teacher_ids, "teacher_ids", (rows, k), torch.int32),
             _dense(teacher_logits, "teacher_logits", (rows, k), f32),
-            _dense(teacher_lse, "teacher_lse", (rows,), f32, True), float(temperature))
+            _dense_or_none(teacher_lse, "teacher_lse", (rows,), f32), float(temperature))
 
 
 def _grad_rows(grad, logits):
-    _need(grad.shape == logits.shape and grad.dtype == logits.dtype, "grad must have the logits' shape and type")
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype:
+        raise ValueError("grad must have the logits' shape and type")
     rows = _logit_rows(grad, "grad")
     return rows[2], rows[4]
 
