@@ -606,3 +606,71 @@ def test_distill_gradient_by_differences(env):
             d.append(loss.double().clone())
         # losses of order 10 in fp32 (error 2^-20 each), and the third derivative (below 1 / T) times h^2 / 6
         assert ((d[0] - d[1]) / (2 * h) - grad[:, v].double()).abs().max() <= 2.0 ** -20 / h + h * h / 6
+
+
+# ------------------------------------------------------------------ largest rows, graphs
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("what", ["top_k", "all"])
+def test_sample_largest_vocabulary(env, what, f32):
+    test_sample(env, 1 << 20, f32, what)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_distill_largest_vocabulary(env, f32):
+    test_distill(env, 3, (1 << 20) - 3, 16, True, f32)
+
+
+def test_calls_in_a_graph(env):
+    """Sampling, commit and distillation recorded once, replayed over changed inputs, equal the eager calls."""
+    torch, dc = env
+    N, T, V, K, H, D, page = 3, 5, 5003, 8, 2, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(8)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.empty(N * T, (V + 7) // 8 * 8, device="cuda")[:, :V]
+    u, lp = torch.empty(N * T, device="cuda"), torch.empty(N * T, device="cuda")
+    tok, picked = torch.empty(N, T, **i32), torch.empty(N * T, **i32)
+    par = torch.tensor([-1, 0, 0, 1, 2], **i32).repeat(N, 1).contiguous()
+    new = torch.empty(2, N, T, H, D, device="cuda").bfloat16()
+    cache, other = (torch.empty(2, 6, page, H, D, device="cuda").bfloat16() for _ in range(2))
+    table, ctx = torch.arange(6, **i32).view(3, 2), torch.tensor([0, 7, 15], **i32)
+    v = dc.TreeVerifier(H, H, D, page, 2, max_batch=N, max_tree=T)
+    outs = dict(path=torch.empty(N, T, **i32), **{k: torch.empty(N, **i32) for k in ("accept_len", "next_token", "new_len")})
+    ids, teacher, one = torch.empty(N * T, K, **i32), torch.empty(N * T, K, device="cuda"), torch.ones(N * T, device="cuda")
+    loss, lse = torch.empty(N * T, device="cuda"), torch.empty(N * T, device="cuda")
+    grad = torch.empty(N * T, (V + 7) // 8 * 8, device="cuda")[:, :V]
+
+    def fill():
+        x.copy_(3 * torch.randn(N * T, V, generator=g, device="cuda"))
+        x[:, 1::3] = -math.inf
+        u.uniform_(generator=g)
+        new.normal_(generator=g), cache.normal_(generator=g), other.normal_(generator=g)
+        ids.copy_(torch.randint(0, V, (N * T, K), generator=g, device="cuda") // 3 * 3)
+        teacher.normal_(generator=g)
+        picked.random_(0, 3, generator=g)
+        tok.random_(0, 3, generator=g)
+
+    def calls():
+        dc.dcoco_sample(x, u, picked, logprob=lp)
+        dc.dcoco_tree_commit(v.handle, N, tok, par, picked.view(N, T) % 3, new, new, cache, other, table, ctx, **outs)
+        dc.dcoco_distill_step(x, ids, teacher, one, loss=loss, lse=lse, grad=grad)
+        return [t.clone() for t in (picked, lp, cache, other, *outs.values(), loss, lse, grad)]
+
+    fill()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls()
+    for _ in range(3):
+        fill()
+        before = cache.clone(), other.clone()
+        graph.replay()
+        again = [t.clone() for t in got]
+        cache.copy_(before[0]), other.copy_(before[1])
+        for a, b in zip(again, calls()):
+            assert torch.equal(a, b)
+    assert v.status() == dc.DCOCO_OK
