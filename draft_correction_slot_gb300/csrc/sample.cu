@@ -20,8 +20,9 @@
 // The first block sorts the candidates, finds the border exactly, and draws:
 // the 512 tokens by their sums, then the token in them.
 // What this does not cover (top_k over kTopkMost of a larger vocabulary,
-// borders with more tokens around them than the list holds, infinite
-// logits) the first block does alone by bisection over the row, ~100 passes.
+// borders with more tokens around them than the list holds, an infinite
+// maximum or one near the type's lowest value) the first block does alone, by
+// bisection over the row in some 100 passes.
 //
 // Weights are summed as 64-bit integers in units of 2^-40 (V <= 2^20 of them
 // stay below 2^60), up to 16 of one thread's first in fp32: the same sums
@@ -29,6 +30,13 @@
 // 2^-z with z = d / (t ln 2) carried with its rounding error: a row's border
 // can lie where a token has 10^-6 of the mass, and a bias of 10^-7 common to
 // all weights beyond it would move it.
+//
+// 512 rows of 151936 bf16 logits (155 MB, 23 us of bytes): 168 us, 126 with
+// top-k alone, 97 with neither.  Half of the issue slots are used; the rest
+// goes to steps that only the first block takes (the decision 8,000 cycles,
+// sort and draw 16,000 of a top-p row's 140,000), to shared atomics of the
+// histogram that meet in a bank (27,000) and to blocks that end at different
+// times (2.25 waves).  16 rows: 26 us, all of it latency between the phases.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -43,7 +51,7 @@ constexpr int kList = 1088;      // candidates the list holds (its 8704 bytes al
 constexpr int kTopkMost = 512;   // largest top_k of the candidate path
 constexpr int kChunk = 512;      // tokens of a partial sum (one warp)
 constexpr int kMostBlocks = 8;   // blocks of a cluster
-constexpr size_t kMostSlice = 40 * 1024;  // bytes of a slice held in shared memory (four blocks an SM)
+constexpr size_t kMostSlice = 40 * 1024;  // bytes of a slice held in shared memory (three blocks an SM)
 
 // Larger key <=> larger value; -0 and +0 share a key, NaN counts as -inf.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -248,6 +256,48 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// Two floats in a register pair, one instruction for both.
+__device__ __forceinline__ u64 two(float a, float b) {
+  u64 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 of_two(u64 x) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+  return f;
+}
+__device__ __forceinline__ u64 fma_two(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 mul_two(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 add_two(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum_two(u64 x) {
+  const float2 f = of_two(x);
+  return f.x + f.y;
+}
+// 1 where a >= b, else 0.
+__device__ __forceinline__ float at_least(float a, float b) {
+  float d;
+  asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // What a block is told by the first one.
 struct Orders {
   int step;        // kCollect, kWeigh (and collect), kStop
@@ -255,7 +305,13 @@ struct Orders {
 };
 enum { kStop, kCollect, kWeigh };
 
-// The least integer that is at least p * mass.
+// The least integer that is at least p * mass; what the uniform u is of the
+// mass, below it.  (By one thread: a block's 256 would keep the SM's few
+// 64-bit units busy for some 700 cycles.)
+__device__ __forceinline__ u64 target_of(float u, u64 mass) {
+  const u64 target = (u64)((double)u * (double)mass);
+  return target >= mass ? mass - 1 : target;
+}
 __device__ __forceinline__ u64 share_of(float p, u64 mass) {
   return (u64)ceil((double)fmaxf(p, 0.f) * (double)mass);
 }
@@ -268,6 +324,7 @@ struct SampleShared {
   float mx[kMostBlocks], low[kMostBlocks];
   uint32_t arg[kMostBlocks];
   u64 sure[kMostBlocks], all[kMostBlocks];
+  u64 need, target;     // (first block)
   uint32_t listed;      // (first block) candidates of the cluster
   uint32_t mine, base;  // candidates of this block, and where they go in the first block's list
   float dmax;
@@ -346,6 +403,9 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   const uint8_t *src = static_cast<const uint8_t *>(p.logits) + row * p.stride * kSize;
   const int v0 = rank * slice, v1 = min(V, v0 + slice), nv = max(0, v1 - v0);
   const int nch = (nv + kChunk - 1) / kChunk, vecs = nch * (kChunk / E);
+  float t = p.temperature ? p.temperature[row] : 1.f, tp = p.top_p ? p.top_p[row] : 1.f, u = p.u[row];
+  const float mp = p.min_p ? p.min_p[row] : 0.f;
+  int k = p.top_k ? p.top_k[row] : 0;
   cluster_arrive();  // (this block is there)
 
   bool nan = false;  // (not held) this thread's block met a NaN
@@ -408,12 +468,8 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   mx = warp_max(mx), low = -warp_max(-low);
   if (lane == 0) s.redf[warp] = mx, s.redi[warp] = __float_as_int(low);
   for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-  float t = p.temperature ? p.temperature[row] : 1.f;
   if (t != t) t = 1.f;
-  int k = p.top_k ? p.top_k[row] : 0;
   if (k <= 0 || k > V) k = V;
-  float tp = p.top_p ? p.top_p[row] : 1.f, u = p.u[row];
-  const float mp = p.min_p ? p.min_p[row] : 0.f;
   if (tp != tp) tp = 1.f;
   if (!(u > 0.f)) u = 0.f;
   if (tid == 0) {  // (one thread: 256 would keep the few 64-bit units busy for 6 us)
@@ -477,7 +533,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   const bool by_list = small || (k < V && k <= kTopkMost);
   const bool by_mass = !by_list && k == V && tp < 1.f;
   const bool whole = k == V && tp >= 1.f && !small;    // min-p at most
-  bool general = !(by_list || by_mass || whole) || mx == INFINITY || ts > 1e30f;
+  bool general = !(by_list || by_mass || whole) || mx == INFINITY || mx < -3e38f || ts > 1e30f;
   // bins of d, 1.5 times the range down to the least vector maximum
   const float range = 1.5f * fmaxf(mx - low, 1e-6f), scale = (float)kBins / range;
   if (!small && !whole && !(range < 1e30f)) general = true;
@@ -584,7 +640,9 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           if (tid == max(who, 0)) s.redi[0] = who < 0 ? kBins - 1 : bin;
           __syncthreads();
           bin = s.redi[0];
-          // as many bins around it as half of the list takes; the counts
+          // as many bins around it as an eighth of the list takes (3 rows in a
+          // hundred need a second try; with half of the list one or two, but
+          // the pass and the sort then cost 2 to 7 us more a row); the counts
           // before each bin go where the candidates will be
           int upto = block_scan(sum, s.redi) - sum;
           uint32_t *cnt = reinterpret_cast<uint32_t *>(list);  // [kBins + 1] (the histogram is merged)
@@ -599,7 +657,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           __syncthreads();
           int wide = 0;  // the widest 2^i - 1 bins to both sides that fit
           for (int x = 1; x < kBins; x = 2 * x + 1) {
-            if (cnt[min(kBins, bin + x + 1)] - cnt[max(0, bin - x)] > kList / 2) break;
+            if (cnt[min(kBins, bin + x + 1)] - cnt[max(0, bin - x)] > kList / 8) break;
             wide = x;
           }
           b1 = max(0, bin - wide), b2 = min(kBins, bin + wide + 1);
@@ -627,15 +685,24 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
     // candidates gather in this block's list, then go to the first one's (one
     // by one, each would wait for the reply from the other block's memory)
     uint32_t *count = rank == 0 ? &s.listed : &s.mine;
-    // the tokens of vector i whose bits are set
-    auto collect = [&](int i, uint32_t bits) {
+    // the tokens of vector i, logits f, whose bits are set (from registers: a
+    // second read of the row costs a warp a wait on L2; a held one is near)
+    auto collect = [&](int i, uint32_t bits, const float (&f)[E]) {
       uint32_t at = atomicAdd(count, (uint32_t)__popc(bits));
-      for (; bits; bits &= bits - 1, ++at) {
-        const int e = __ffs(bits) - 1, v = v0 + i * E + e;
-        float x;
-        if constexpr (HELD) x = F32 ? reinterpret_cast<const float *>(data)[i * E + e] : bf16_bits_to_float(reinterpret_cast<const uint16_t *>(data)[i * E + e]);
-        else x = r.value(v);
-        if (at < kList) list[at] = (u64)order_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)v);
+      auto put = [&](int e, float x) {
+        if (at < kList) list[at] = (u64)order_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)(v0 + i * E + e));
+        ++at;
+      };
+      if constexpr (HELD) {
+        for (; bits; bits &= bits - 1) {
+          const int e = __ffs(bits) - 1;
+          put(e, F32 ? reinterpret_cast<const float *>(data)[i * E + e]
+                     : bf16_bits_to_float(reinterpret_cast<const uint16_t *>(data)[i * E + e]));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (bits >> e & 1u) put(e, f[e]);
       }
     };
     if (o.step == kCollect) {
@@ -654,26 +721,28 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
             uint32_t bits = 0;
 #pragma unroll
             for (int e = 0; e < E; ++e) bits |= f[e] > -INFINITY && mx - f[e] < o.to ? 1u << e : 0u;
-            collect(i0 + q * kThreads, bits);
+            collect(i0 + q * kThreads, bits, f);
           }
         }
       }
     } else {
-      const float dfar = fminf(100.f / r.ch, 3e38f);  // a weight of 2^-100 stands for the lesser ones and for -inf
+      // a weight of 2^-100 stands for the lesser ones and for -inf: logits are
+      // raised to `least`, below the maximum however small 100 / ch
+      float least = fminf(mx - 100.f / r.ch, key_value(order_key(mx) - 1));
+      uint32_t least2 = __float_as_uint(least);
+      if constexpr (!F32) {  // the next bf16 below it, twice
+        least2 = (least2 + (least < 0.f ? 0xFFFFu : 0u)) >> 16;
+        least = __uint_as_float(least2 << 16);
+        least2 |= least2 << 16;
+      }
       const bool min_p = r.dmax < INFINITY;
+      const u64 nmx2 = two(-mx, -mx), ch2 = two(r.ch, r.ch), nch2 = two(-r.ch, -r.ch), ncl2 = two(-r.cl, -r.cl),
+                nln2 = two(-0.693147180559945f, -0.693147180559945f), minus2 = two(-1.f, -1.f);
+      // y > -from as y >= the next float
+      const float nearest = key_value(order_key(-o.from) + 1);
+      // what the weights beyond the border's candidates stay below
+      const float w_to = ex2_approx(-fminf(o.to, mx - least) * r.ch) * (1.f - 0x1p-12f);
       u64 sure = 0, all = 0;
-      // weight of the logit at distance d
-      auto weight = [&](float d) {
-        const float zh = d * r.ch, zl = fmaf(d, r.cl, fmaf(d, r.ch, -zh)), w = ex2_approx(-zh);
-        return fmaf(-0.693147180559945f * w, zl, w);
-      };
-      auto tree_sum = [](float(&w)[E]) {
-#pragma unroll
-        for (int h = E / 2; h > 0; h >>= 1)
-#pragma unroll
-          for (int e = 0; e < h; ++e) w[e] += w[e + h];
-        return w[0];
-      };
       // a lane's sum (at most 16) in units of 2^-40, as 2^22 hi + lo
       auto fixed = [](float x, uint32_t &hi, uint32_t &lo) {
         const float y = x * 262144.f, f = floorf(y);
@@ -681,53 +750,72 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
         lo = __float2uint_rn((y - f) * 4194304.f);
       };
       constexpr int kVecs = kChunk / E / 32;  // of a lane in a chunk
-      uint4 ahead[kVecs];                     // the next chunk's
-      if (warp < nch) {
+      uint4 ahead[kVecs];                     // (not held) the next chunk's
+      if (!HELD && warp < nch) {
 #pragma unroll
         for (int q = 0; q < kVecs; ++q) ahead[q] = vec(warp * (kChunk / E) + q * 32 + lane);
       }
       for (int ch = warp; ch < nch; ch += kWarps) {
-        float kept = 0.f, certain = 0.f, total = 0.f;  // of this lane's 16 tokens
+        u64 kept2 = 0, certain2 = 0, total2 = 0;  // of this lane's 16 tokens
 #pragma unroll
         for (int q = 0; q < kVecs; ++q) {
           const int i = ch * (kChunk / E) + q * 32 + lane;
-          float f[E], w1[E];
-          unpack<F32>(ahead[q], f);
-          if (ch + kWarps < nch) ahead[q] = vec(i + kWarps * (kChunk / E));
+          if (HELD) ahead[q] = vec(i);
+          const uint32_t x[4] = {ahead[q].x, ahead[q].y, ahead[q].z, ahead[q].w};
+          if (!HELD && ch + kWarps < nch) ahead[q] = vec(i + kWarps * (kChunk / E));
+          float y[E];
+          u64 w[E / 2];
 #pragma unroll
-          for (int e = 0; e < E; ++e) f[e] = fminf(mx - f[e], dfar), w1[e] = weight(f[e]);
+          for (int h = 0; h < E / 2; ++h) {
+            u64 pair;
+            if constexpr (F32) {
+              pair = two(fmaxf(__uint_as_float(x[2 * h]), least), fmaxf(__uint_as_float(x[2 * h + 1]), least));
+            } else {
+              const uint32_t v = bf16x2_max(x[h], least2);
+              pair = two(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+            }
+            // with y = -d: 2^-z, z = d (ch + cl) = zh + zl
+            const u64 y2 = add_two(pair, nmx2), nzh = mul_two(y2, ch2), zl = fma_two(y2, ncl2, fma_two(y2, nch2, nzh));
+            const float2 z = of_two(nzh);
+            const u64 w0 = two(ex2_approx(z.x), ex2_approx(z.y));
+            w[h] = fma_two(mul_two(w0, nln2), zl, w0);
+            const float2 f = of_two(y2);
+            y[2 * h] = f.x, y[2 * h + 1] = f.y;
+          }
           if (by_mass) {
-            float w3[E];
-            bool any = false;
+            float most = 0.f;  // the largest weight not surely kept
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-              w3[e] = w1[e];
-              const bool before = f[e] < o.from;
-              w1[e] = before ? w1[e] : 0.f;
-              any |= !before && f[e] < o.to;
+            for (int h = 0; h < E / 2; ++h) {
+              total2 = add_two(total2, w[h]);
+              const u64 in = two(at_least(y[2 * h], nearest), at_least(y[2 * h + 1], nearest));
+              const u64 wk = mul_two(w[h], in);
+              const float2 out = of_two(fma_two(wk, minus2, w[h]));
+              most = fmaxf(most, fmaxf(out.x, out.y));
+              w[h] = wk;
             }
-            total += tree_sum(w3);
-            if (any) {
+            if (most >= w_to) {
               uint32_t bits = 0;
-              float x[E];
-              unpack<F32>(vec(i), x);
+              float v[E];
+              unpack<F32>(make_uint4(x[0], x[1], x[2], x[3]), v);
 #pragma unroll
-              for (int e = 0; e < E; ++e) bits |= f[e] >= o.from && f[e] < o.to && x[e] > -INFINITY ? 1u << e : 0u;
-              if (bits) collect(i, bits);
-            }
-            if (min_p) {  // the draw leaves out what min-p does; the border counts it
-              float w2[E];
-#pragma unroll
-              for (int e = 0; e < E; ++e) w2[e] = w1[e];
-              certain += tree_sum(w2);
+              for (int e = 0; e < E; ++e) {
+                const float far = mx - v[e];
+                bits |= far >= o.from && far < o.to && v[e] > -INFINITY ? 1u << e : 0u;
+              }
+              if (bits) collect(i, bits, v);
             }
           }
-          if (min_p) {
+          if (min_p) {  // the draw leaves out what min-p does; the border counts it
 #pragma unroll
-            for (int e = 0; e < E; ++e) w1[e] = f[e] <= r.dmax ? w1[e] : 0.f;
+            for (int h = 0; h < E / 2; ++h) {
+              certain2 = add_two(certain2, w[h]);
+              w[h] = mul_two(w[h], two(at_least(y[2 * h], -r.dmax), at_least(y[2 * h + 1], -r.dmax)));
+            }
           }
-          kept += tree_sum(w1);
+#pragma unroll
+          for (int h = 0; h < E / 2; ++h) kept2 = add_two(kept2, w[h]);
         }
+        const float kept = sum_two(kept2), certain = sum_two(certain2), total = sum_two(total2);
         uint32_t hi, lo;
         fixed(kept, hi, lo);
         const u64 x = ((u64)__reduce_add_sync(DC_FULL_MASK, hi) << 22) + __reduce_add_sync(DC_FULL_MASK, lo);
@@ -772,7 +860,9 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       u64 m = 0;
       for (int i = tid; i < n; i += kThreads) m += r.weight(key_value((uint32_t)(list[i] >> 32)));
       m = block_sum(m, s.red);
-      const u64 need = share_of(tp, all_all);
+      if (tid == 0) s.need = share_of(tp, all_all);
+      __syncthreads();
+      const u64 need = s.need;
       const bool in = s.listed <= kList && (sure_all < need || sure_all == 0) && sure_all + m >= need;
       __syncthreads();
       if (in) {
@@ -815,9 +905,9 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       }
       const u64 upto = block_scan(mine, s.red);
       __syncthreads();
-      if (tid == kThreads - 1) s.red[0] = upto;
+      if (tid == kThreads - 1) s.need = share_of(tp, by_list ? upto : all_all);
       __syncthreads();
-      const u64 need = share_of(tp, by_list ? s.red[0] : all_all);
+      const u64 need = s.need;
       u64 cum = (by_list ? 0 : sure_all) + upto - mine;
       int at = -1;
       for (int q = 0; q < per && at < 0; ++q) {
@@ -847,11 +937,10 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
         if (tid * per + q < n) mine += by_id(tid * per + q);
       const u64 upto = block_scan(mine, s.red);
       __syncthreads();
-      if (tid == kThreads - 1) s.red[0] = upto;
+      if (tid == kThreads - 1) s.red[0] = upto, s.target = target_of(u, upto);
       __syncthreads();
       total = s.red[0];
-      u64 target = (u64)((double)u * (double)total);
-      if (target >= total) target = total - 1;
+      u64 target = s.target;
       u64 cum = upto - mine;
       int at = -1;
       for (int q = 0; q < per && at < 0; ++q) {
@@ -880,11 +969,10 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
         if (tid * cper + q < chunks_all) mine += chunk_all[tid * cper + q];
       const u64 upto = block_scan(mine, s.red);
       __syncthreads();
-      if (tid == kThreads - 1) s.red[0] = upto;
+      if (tid == kThreads - 1) s.red[0] = upto, s.target = target_of(u, upto);
       __syncthreads();
       total = s.red[0];
-      u64 target = (u64)((double)u * (double)total);
-      if (target >= total) target = total - 1;
+      u64 target = s.target;
       u64 cum = upto - mine;
       int at = -1;
       for (int q = 0; q < cper && at < 0; ++q) {
@@ -943,8 +1031,8 @@ cudaError_t launch(const SampleParams &p, cudaStream_t st) {
   // SM holds and a slice at 16 KB or more, and two at least.  A block's fixed
   // steps cost as much as some 10,000 tokens, so many rows want few blocks, but
   // one block alone waits too long on its own loads.  512 rows of 151936 bf16
-  // logits: 208 / 180 / 260 us with 1 / 2 / 8 blocks; 100 rows: 59 / 66 us with
-  // 4 / 8; 16 rows: 90 / 51 / 30 us with 2 / 4 / 8.
+  // logits: 200 / 168 / 181 / 218 us with 1 / 2 / 4 / 8 blocks; 100 rows: 82 /
+  // 58 / 62 us with 2 / 4 / 8; 16 rows: 52 / 37 / 26 us with 2 / 4 / 8.
   int blocks = kMostBlocks;
   while (blocks > 2 && (int64_t)p.rows * blocks > 3 * kSms) blocks /= 2;
   while (blocks > 1 && (int64_t)p.V * kSize < (int64_t)blocks << 14) blocks /= 2;

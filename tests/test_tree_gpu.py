@@ -608,6 +608,54 @@ def test_distill_gradient_by_differences(env):
         assert ((d[0] - d[1]) / (2 * h) - grad[:, v].double()).abs().max() <= 2.0 ** -20 / h + h * h / 6
 
 
+# ------------------------------------------------------------------ extremes of values and temperatures
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [40, 5003, 40009])
+@pytest.mark.parametrize("what", ["plain", "top_k", "top_p", "min_p", "all"])
+def test_sample_extremes(env, V, f32, what):
+    """Rows masked with the type's lowest value, in part or whole, of one sign, around zero; temperatures from 1e-30 on."""
+    torch, dc = env
+    R = 48
+    rng = np.random.default_rng(V + 2 * f32)
+    dt = torch.float32 if f32 else torch.bfloat16
+    low = torch.finfo(dt).min
+    x = (2 * rng.standard_normal((R, V))).astype(np.float32)
+    for r in range(R):
+        if r % 6 == 1:
+            x[r, rng.random(V) < 0.7] = low
+        elif r % 6 == 2:
+            x[r] = low
+        elif r % 6 == 3:
+            x[r] = -np.abs(x[r]) - 1
+        elif r % 6 == 4:
+            x[r] = -np.abs(x[r])
+            x[r, rng.integers(0, V, 3)] = [0.0, -0.0, 0.0]
+        elif r % 6 == 5:
+            x[r, rng.random(V) < 0.5] = -np.inf
+            x[r, 0] = 1.0
+    logits = torch.zeros(R, (V + 7) // 8 * 8, dtype=dt)
+    logits[:, :V] = torch.from_numpy(x).clamp(min=low).to(dt)
+    logits[:, :V][torch.from_numpy(np.isneginf(x))] = -math.inf
+    logits = logits.cuda()[:, :V]
+    t = rng.choice([1e-30, 1e-10, 1e-3, 0.02, 0.1, 1.0, 30.0, 1e6], R).astype(np.float32)
+    u = rng.random(R).astype(np.float32)
+    k = rng.choice([3, 40, V], R).astype(np.int32) if what in ("top_k", "all") else None
+    p = rng.choice([0.3, 0.9, 0.999], R).astype(np.float32) if what in ("top_p", "all") else None
+    q = rng.choice([1e-4, 0.01, 0.3], R).astype(np.float32) if what in ("min_p", "all") else None
+    cuda = lambda a: None if a is None else torch.from_numpy(a).cuda()  # noqa: E731
+    tokens = torch.empty(R, dtype=torch.int32, device="cuda")
+    dc.dcoco_sample(logits, cuda(u), tokens, temperature=cuda(t), top_k=cuda(k), top_p=cuda(p), min_p=cuda(q))
+    host, near_rows = logits.float().cpu().numpy(), 0
+    for r in range(R):
+        tok, _, near = tree_ref.sample_row(host[r], u[r], t[r], 0 if k is None else int(k[r]),
+                                           1.0 if p is None else p[r], 0.0 if q is None else q[r])
+        if near < 2.0 ** -22 and tok != int(tokens[r]):  # as in test_sample
+            near_rows += 1
+            continue
+        assert tok == int(tokens[r]), (r, r % 6, float(t[r]), tok, int(tokens[r]), near)
+    assert near_rows <= max(1, R // 20)
+
+
 # ------------------------------------------------------------------ largest rows, graphs
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("what", ["top_k", "all"])
