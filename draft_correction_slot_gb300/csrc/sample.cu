@@ -21,8 +21,8 @@
 // the 512 tokens by their sums, then the token in them.
 // What this does not cover (top_k over kTopkMost of a larger vocabulary,
 // borders with more tokens around them than the list holds, an infinite
-// maximum or one near the type's lowest value) the first block does alone, by
-// bisection over the row in some 100 passes.
+// maximum or one near the type's lowest value) the first block does alone, in
+// about eight passes over the row.
 //
 // Weights are summed as 64-bit integers in units of 2^-40 (V <= 2^20 of them
 // stay below 2^60), up to 16 of one thread's first in fp32: the same sums
@@ -31,12 +31,13 @@
 // can lie where a token has 10^-6 of the mass, and a bias of 10^-7 common to
 // all weights beyond it would move it.
 //
-// 512 rows of 151936 bf16 logits (155 MB, 23 us of bytes): 168 us, 126 with
+// 512 rows of 151936 bf16 logits (155 MB, 23 us of bytes): 169 us, 126 with
 // top-k alone, 97 with neither.  Half of the issue slots are used; the rest
 // goes to steps that only the first block takes (the decision 8,000 cycles,
 // sort and draw 16,000 of a top-p row's 140,000), to shared atomics of the
 // histogram that meet in a bank (27,000) and to blocks that end at different
-// times (2.25 waves).  16 rows: 26 us, all of it latency between the phases.
+// times (2.25 waves).  16 rows: 27 us, all of it latency between the phases.
+// The first block alone: 1.4 ms for 16 rows with top_k 1000, 4.3 ms for 512.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -99,80 +100,6 @@ struct SampleRow {
     return (k > key || (k == key && i <= last)) && (v == mx || mx - v <= dmax);
   }
 };
-
-
-// The general path: the border's value by bisection on the key, its id by
-// bisection on the id, a pass over the row each step.  One block.
-template <bool F32>
-__device__ __noinline__ int sample_general(SampleRow<F32> r, int V, int k, float tp, float u, u64 *s_red, u64 *kept) {
-  const int tid = threadIdx.x;
-  // The shortest prefix of the order for which `over` (monotone in the
-  // prefix) of its count and mass holds: its last value by bisection on the
-  // key, then its last id.
-  auto shortest = [&](auto over) {
-    const uint32_t key0 = r.key;
-    const int last0 = r.last;
-    auto measure = [&](uint32_t key, int last) {
-      u64 n = 0, m = 0;
-      for (int v = tid; v < V; v += kThreads) {
-        const float f = r.value(v);
-        const uint32_t q = order_key(f);
-        if ((q > key || (q == key && v <= last)) && (q > key0 || (q == key0 && v <= last0))) ++n, m += r.weight(f);
-      }
-      n = block_sum(n, s_red);
-      m = block_sum(m, s_red);
-      return over(n, m);
-    };
-    uint32_t lo = 0, hi = order_key(r.mx);  // largest key in [lo, hi] whose whole prefix is over
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2 + 1;
-      if (measure(mid, V)) lo = mid;
-      else hi = mid - 1;
-    }
-    int a = 0, b = V - 1;  // smallest id
-    while (a < b) {
-      const int mid = a + (b - a) / 2;
-      if (measure(lo, mid)) b = mid;
-      else a = mid + 1;
-    }
-    r.key = lo, r.last = a;
-  };
-  if (k < V) shortest([&](u64 n, u64) { return n >= (u64)k; });
-  auto mass_of = [&]() {
-    u64 m = 0;
-    for (int v = tid; v < V; v += kThreads) {
-      const float f = r.value(v);
-      const uint32_t q = order_key(f);
-      if (q > r.key || (q == r.key && v <= r.last)) m += r.weight(f);
-    }
-    return block_sum(m, s_red);
-  };
-  if (tp < 1.f) {
-    const double need = fmax((double)tp, 0.0) * (double)mass_of();
-    shortest([&](u64 n, u64 m) { return n > 0 && (double)m >= need; });
-  }
-  u64 total = 0;
-  for (int v = tid; v < V; v += kThreads) {
-    const float f = r.value(v);
-    if (r.kept(f, v)) total += r.weight(f);
-  }
-  total = block_sum(total, s_red);
-  u64 target = (u64)((double)u * (double)total);  // below `total`
-  if (target >= total) target = total - 1;
-  int a = 0, b = V - 1;
-  while (a < b) {
-    const int mid = a + (b - a) / 2;
-    u64 m = 0;
-    for (int v = tid; v <= mid; v += kThreads) {
-      const float f = r.value(v);
-      if (r.kept(f, v)) m += r.weight(f);
-    }
-    if (block_sum(m, s_red) > target) b = mid;
-    else a = mid + 1;
-  }
-  *kept = total;
-  return a;
-}
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -341,6 +268,163 @@ __device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+
+// The general path, one block, for what the candidate list does not hold: the
+// border's key a byte at a time by histograms (of counts for top-k, of masses
+// for top-p), its id and the drawn token by sums of kChunk tokens.  The
+// tokens of a key have one weight, so how many of them are kept follows by a
+// division.  About eight passes over the row.
+template <bool F32>
+struct General {
+  SampleRow<F32> r;
+  int V;
+  u64 *hist;       // [2][256]
+  u64 *chunk_all;  // [chunks]
+  SampleShared &s;
+
+  // f(value, id, there) of this thread's tokens, eight loads in flight; all threads together
+  template <typename F>
+  __device__ void pass(F f) const {
+    for (int v0 = 0; v0 < V; v0 += 8 * kThreads) {
+      float x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = r.value(min(v0 + q * kThreads + (int)threadIdx.x, V - 1));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int v = v0 + q * kThreads + (int)threadIdx.x;
+        f(x[q], v, v < V);
+      }
+    }
+  }
+  // The largest key whose tokens and those of larger keys reach `need` (> 0)
+  // together; `of` a token's share.  before: the share of larger keys.
+  template <typename F>
+  __device__ uint32_t border(u64 need, F of, u64 &before) const {
+    const int tid = threadIdx.x;
+    u64 *h = hist + (tid >> 5 & 1) * 256;  // two copies: half as many warps meet in a bin
+    uint32_t key = 0;
+    before = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      __syncthreads();
+      hist[tid] = hist[256 + tid] = 0;
+      __syncthreads();
+      pass([&](float x, int v, bool there) {
+        const uint32_t q = order_key(x), digit = q >> shift & 255u;
+        const u64 n = there && (shift == 24 || q >> (shift + 8) == key) ? of(x, v) : 0;
+        const uint32_t some = __ballot_sync(DC_FULL_MASK, n != 0);
+        if (n) {  // a warp's tokens of a bin together: most share their first byte (n <= 2^40)
+          const uint32_t peers = __match_any_sync(some, digit);
+          const uint32_t hi = __reduce_add_sync(peers, (uint32_t)(n >> 20)), lo = __reduce_add_sync(peers, (uint32_t)n & 0xFFFFFu);
+          if ((tid & 31) == __ffs(peers) - 1) atomicAdd(&h[digit], ((u64)hi << 20) + lo);
+        }
+        __syncwarp();
+      });
+      __syncthreads();
+      const u64 n = hist[255 - tid] + hist[511 - tid], upto = block_scan(n, s.red);
+      const int who = block_first(before + upto >= need, &s.first);
+      if (tid == max(who, 0)) s.target = upto - n;
+      __syncthreads();
+      before += s.target;
+      key = key << 8 | (uint32_t)(255 - max(who, 0));
+    }
+    return key;
+  }
+  // The smallest id up to which the tokens' shares are more than aim(total).
+  template <typename F, typename A>
+  __device__ int find(F of, A aim, u64 &total) const {
+    const int tid = threadIdx.x, lane = tid & 31, chunks = (V + kChunk - 1) / kChunk;
+    __syncthreads();
+    for (int ch = tid >> 5; ch < chunks; ch += kWarps) {
+      float x[kChunk / 32];
+      u64 n = 0;
+#pragma unroll
+      for (int q = 0; q < kChunk / 32; ++q) x[q] = r.value(min(ch * kChunk + q * 32 + lane, V - 1));
+#pragma unroll
+      for (int q = 0; q < kChunk / 32; ++q) {
+        const int v = ch * kChunk + q * 32 + lane;
+        if (v < V) n += of(x[q], v);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(DC_FULL_MASK, n, o);
+      if (lane == 0) chunk_all[ch] = n;
+    }
+    __syncthreads();
+    const int per = (chunks + kThreads - 1) / kThreads;
+    u64 mine = 0;
+    for (int i = tid * per; i < min(chunks, (tid + 1) * per); ++i) mine += chunk_all[i];
+    const u64 upto = block_scan(mine, s.red);
+    __syncthreads();
+    if (tid == kThreads - 1) s.red[0] = upto, s.target = aim(upto);
+    __syncthreads();
+    total = s.red[0];
+    u64 target = s.target, cum = upto - mine;
+    int at = -1;
+    for (int i = tid * per; i < min(chunks, (tid + 1) * per) && at < 0; ++i) {
+      if (cum + chunk_all[i] > target) at = i;
+      else cum += chunk_all[i];
+    }
+    int who = block_first(at >= 0, &s.first);
+    if (tid == max(who, 0)) s.redi[0] = max(at, 0), s.target = target - cum;
+    __syncthreads();
+    const int v = s.redi[0] * kChunk + tid * (kChunk / kThreads);
+    target = s.target;
+    u64 n[kChunk / kThreads], sum = 0;
+#pragma unroll
+    for (int q = 0; q < kChunk / kThreads; ++q) {
+      n[q] = v + q < V ? of(r.value(v + q), v + q) : 0;
+      sum += n[q];
+    }
+    u64 before = block_scan(sum, s.red) - sum;
+    at = -1;
+#pragma unroll
+    for (int q = 0; q < kChunk / kThreads; ++q) {
+      before += n[q];
+      if (at < 0 && before > target) at = v + q;
+    }
+    who = block_first(at >= 0, &s.first);
+    if (tid == max(who, 0)) s.redi[0] = max(at, 0);
+    __syncthreads();
+    return s.redi[0];
+  }
+  __device__ int operator()(int k, float tp, float u, u64 &total) {
+    u64 before, n;
+    auto count = [](float, int) -> u64 { return 1; };
+    if (k < V) {
+      const uint32_t key = border((u64)k, count, before);
+      r.last = find([&](float x, int) -> u64 { return order_key(x) == key; }, [&](u64) { return (u64)k - before - 1; }, n);
+      r.key = key;
+    }
+    if (tp < 1.f) {
+      const SampleRow<F32> top = r;  // what top-k left
+      auto in = [&](float x, int v) { return order_key(x) > top.key || (order_key(x) == top.key && v <= top.last); };
+      auto mass = [&](float x, int v) -> u64 { return in(x, v) ? top.weight(x) : 0; };
+      u64 all = 0;
+      pass([&](float x, int v, bool there) { all += there ? mass(x, v) : 0; });
+      all = block_sum(all, s.red);
+      __syncthreads();
+      if (threadIdx.x == 0) s.need = max(share_of(tp, all), (u64)1);
+      __syncthreads();
+      const u64 need = s.need;
+      const uint32_t key = border(need, mass, before);
+      const u64 w = top.weight(key_value(key));
+      const u64 more = (need - before + w - 1) / w;  // tokens of the border's key; w > 0, its mass is
+      r.last = find([&](float x, int v) -> u64 { return order_key(x) == key && in(x, v); }, [&](u64) { return more - 1; }, n);
+      r.key = key;
+    }
+    return find([&](float x, int v) -> u64 { return r.kept(x, v) ? r.weight(x) : 0; },
+                [&](u64 all) { return target_of(u, all); }, total);
+  }
+};
+// (s.need: the kept total)
+template <bool F32>
+__device__ __noinline__ int sample_general(SampleRow<F32> r, int V, int k, float tp, float u, u64 *hist,
+                                           u64 *chunk_all, SampleShared &s) {
+  General<F32> g{r, V, hist, chunk_all, s};
+  u64 total;
+  const int token = g(k, tp, u, total);
+  if (threadIdx.x == 0) s.need = total;
+  return token;
 }
 
 // The vector at `at` that reaches past the row's V logits: -inf there.
@@ -577,6 +661,8 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   u64 sure_all = 0, all_all = 0;  // (first block) weight surely kept, and of all tokens
   int tries = 0;
   int b1 = 0, b2 = kBins;         // (first block) bins collected: [b1, b2)
+  int edge = 0;                   // (first block) after a try: the end of [b1, b2) that the border lies beyond,
+  u64 edge_mass = 0;              // and the exact mass before it
   while (true) {
     if (rank == 0) {
       Orders o{kStop, 0.f, 0.f};
@@ -620,10 +706,10 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           const float cum = block_scan(mass, s.redf);
           __syncthreads();
           if (tid == kThreads - 1) s.redf[0] = cum;
-          if (tries && tid == b1 / kPer) {  // what an exact mass says the middles' are off by, at bin b1
+          if (tries && tid == edge / kPer) {  // what the exact mass says the middles' are off by
             float before = cum - mass;
-            for (int q = 0; q < b1 % kPer; ++q) before += m[q];
-            s.redf[1] = __ull2float_rn(sure_all) * 0x1p-40f - before;
+            for (int q = 0; q < edge % kPer; ++q) before += m[q];
+            s.redf[1] = __ull2float_rn(edge_mass) * 0x1p-40f - before;
           }
           __syncthreads();
           const float need = fmaxf(tp, 0.f) * (tries ? __ull2float_rn(all_all) * 0x1p-40f : s.redf[0]);
@@ -640,10 +726,11 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           if (tid == max(who, 0)) s.redi[0] = who < 0 ? kBins - 1 : bin;
           __syncthreads();
           bin = s.redi[0];
-          // as many bins around it as an eighth of the list takes (3 rows in a
-          // hundred need a second try; with half of the list one or two, but
-          // the pass and the sort then cost 2 to 7 us more a row); the counts
-          // before each bin go where the candidates will be
+          // as many bins around it as an eighth of the list takes (the first
+          // try then finds the border in all but 2 rows of a hundred; with
+          // half of the list in one more, but the pass and the sort take 2 to
+          // 7 us longer); the counts before each bin go where the candidates
+          // will be
           int upto = block_scan(sum, s.redi) - sum;
           uint32_t *cnt = reinterpret_cast<uint32_t *>(list);  // [kBins + 1] (the histogram is merged)
           static_assert(kList * 8 >= (kBins + 1) * 4, "");
@@ -663,7 +750,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
           b1 = max(0, bin - wide), b2 = min(kBins, bin + wide + 1);
           const uint32_t inside = cnt[b2] - cnt[b1];
           __syncthreads();
-          if (inside > kList || tries == 4) general = true;
+          if (inside > kList || tries == 4 || edge >= kBins) general = true;
           else o = Orders{kWeigh, ((float)b1 - 0.5f) / scale, b2 >= kBins ? INFINITY : ((float)b2 - 0.5f) / scale};
         }
       }
@@ -864,6 +951,8 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       __syncthreads();
       const u64 need = s.need;
       const bool in = s.listed <= kList && (sure_all < need || sure_all == 0) && sure_all + m >= need;
+      if (sure_all >= need) edge = b1, edge_mass = sure_all;
+      else edge = b2, edge_mass = sure_all + m;
       __syncthreads();
       if (in) {
         // it is: the others are done
@@ -885,7 +974,8 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   u64 total = 0;
   if (!general && by_list && s.listed > kList) general = true;
   if (general) {
-    token = sample_general<F32>(r, V, k, tp, u, s.red, &total);
+    token = sample_general<F32>(r, V, k, tp, u, list, chunk_all, s);
+    total = s.need;  // (thread 0 uses it)
   } else {
     // candidates in order
     int n = whole ? 0 : (int)s.listed, pad = 1;
