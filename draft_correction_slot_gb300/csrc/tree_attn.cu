@@ -76,6 +76,14 @@ static_assert(sizeof(Small) <= 3072, "");
 
 __device__ __forceinline__ void both_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 
+// 32 bytes at once: a warp's lanes write rows of their own, so that a store
+// takes a cycle a lane whatever its width.
+__device__ __forceinline__ void store_sector(float *at, const float *x) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
@@ -343,8 +351,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
         }
         if (used && ok) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            reinterpret_cast<float4 *>(part)[q * 8 + k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          for (int k = 0; k < 4; ++k) store_sector(part + q * 32 + k * 8, &x[k * 8]);
         }
         __syncwarp();
       }
