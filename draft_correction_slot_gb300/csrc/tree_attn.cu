@@ -397,9 +397,10 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(256) k_tree_join(const TreeAttnParams p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, heads = p.kv_heads * p.group;
-  const int64_t orow = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (orow >= (int64_t)p.N * p.T * heads) return;
-  const int hq = (int)(orow % heads), node = (int)(orow / heads % p.T), n = (int)(orow / heads / p.T);
+  const int n = blockIdx.x, of_n = blockIdx.y * 8 + (threadIdx.x >> 5);  // request, row of it
+  if (of_n >= p.T * heads) return;
+  const int node = of_n / heads, hq = of_n - node * heads;
+  const int64_t orow = (int64_t)n * p.T * heads + of_n;
   int ctx, len;
   const int nchunks = request_chunks(p, n, ctx, len);
   const int h = hq / p.group, mt = node / p.tile_nodes;
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(256) k_tree_join(const TreeAttnParams p) {
 
 template <int D, bool F16>
 cudaError_t launch_join(const TreeAttnParams &p, cudaStream_t st) {
-  const int64_t rows = (int64_t)p.N * p.T * p.kv_heads * p.group;
-  return launch_ex(k_tree_join<D, F16>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, true, 0, p);
+  const int rows = p.T * p.kv_heads * p.group;  // at most 256 x 1024 a request
+  return launch_ex(k_tree_join<D, F16>, dim3((unsigned)p.N, (unsigned)((rows + 7) / 8)), dim3(256), 0, st, true, 0, p);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
