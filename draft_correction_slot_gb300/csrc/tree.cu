@@ -68,9 +68,11 @@ struct RowTiles {
 // the SMs.  Several differ in length, and small chunks balance them, but each
 // costs its block a unit border and leaves a partial result.  Measured: 32
 // requests x 16 nodes, 64 rows, to 8000 tokens: 136 / 133 / 133 us at 8 / 16 /
-// 32 tiles; 24 x 1, 4 rows, to 16001: 114 / 103 / 105 us; 8 x 64, three tiles
-// of 125 rows, to 32000: 490 / 359 / 304 us.
-int chunk_cap(const dcoco_tree_config &c, bool few) { return c.max_batch == 1 ? 1 << 30 : few ? 16 : 32; }
+// 32 tiles; 24 x 1, 4 rows, to 16001: 114 / 103 / 105 us.  The kernel for many
+// rows, whose borders cost more, at 32 / 48 / 64 / 96 tiles: 8 x 64, three
+// tiles of 125 rows, to 32000: 310 / 305 / 314 / 308 us; 32 x 64 to 8000: 369 /
+// 352 / 341 / 342 us; 16 x 128 to 16000: 641 / 605 / 583 / 560 us.
+int chunk_cap(const dcoco_tree_config &c, bool few) { return c.max_batch == 1 ? 1 << 30 : few ? 16 : 64; }
 
 int check_distill(int rows, int vocab, const void *logits, int dtype, int64_t row_stride, int topk,
                   const int32_t *ids, const float *teacher, float temperature) {

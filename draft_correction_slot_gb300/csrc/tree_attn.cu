@@ -394,7 +394,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
 // an item, took that block 7 us for 64 rows and four chunks, and some blocks
 // had four items to join.)
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) k_tree_join(const TreeAttnParams p) {
+__global__ void __launch_bounds__(256, 5) k_tree_join(const TreeAttnParams p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, heads = p.kv_heads * p.group;
   const int n = blockIdx.x, of_n = blockIdx.y * 8 + (threadIdx.x >> 5);  // request, row of it
