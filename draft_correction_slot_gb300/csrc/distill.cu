@@ -13,11 +13,17 @@
 // order of threads, warps and blocks, so that a row's result depends on
 // nothing but the row.
 //
-// A row's slices are the blocks': a block of k_loss and k_step takes up to
-// kHold 16-byte vectors a thread; the cluster's size follows from the row's
-// bytes alone.  The teacher's tokens belong to the slice they lie in: each
-// block sums its tokens' terms and writes their gradient after its slice's,
-// from the logit as it was read, so that the gradient may overwrite the logits.
+// A row's slices are the blocks': a block of k_step (the loss alone is k_step
+// without its gradient) takes up to HOLD 16-byte vectors a thread; the cluster's
+// size follows from the row's bytes alone.  The teacher's tokens belong to the
+// slice they lie in: each block sums its tokens' terms and writes their gradient
+// after its slice's, from the logit as it was read, so that the gradient may
+// overwrite the logits.
+//
+// 480 rows of 151936 bf16 logits: loss 41 us (146 MB, floor 22), gradient 58 us
+// (292 MB, 43), both in one step 89 us (43); 2000 rows of 32001 fp32: step 127 us
+// (512 MB, 76).  A block's loads, barriers and stores follow one another, and
+// the registers that hold the row allow four blocks an SM to fill the gaps.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"

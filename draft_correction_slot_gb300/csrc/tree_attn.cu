@@ -29,6 +29,13 @@
 // unnormalised output with their references and sums, and a second kernel
 // joins the chunks.
 //
+// 8 requests of up to 32000 tokens, 64 nodes x 5 heads: 310 us (floor
+// 108, operations).  A pair of tiles takes 3700 cycles, of which the
+// exponentials need 2050 (16 a cycle) and the products 2080; from "weights
+// stored" to "next scores there" pass 2500, and a unit's border costs some 10,000.
+// Half tiles with two S buffers a group took 417 us: a product of 64 columns
+// takes as long as one of 128.
+//
 // Roles: warps 0-7 softmax and output (thread = row = TMEM lane), warp 8 the
 // tensor core, warps 9-10 TMA.  After an expired wait the softmax warps run
 // their loops to the end without waiting or storing, so that their block
@@ -392,9 +399,11 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
 // tree's length and for one that saw nothing.  One warp a row, its elements
 // over the lanes.  (Joining inside the attention kernel, by the last block of
 // an item, took that block 7 us for 64 rows and four chunks, and some blocks
-// had four items to join.)
+// had four items to join.)  Bound by the latency of its loads: six blocks an
+// SM with four chunks in flight a warp; four with eight took 3 us longer for
+// 16,384 rows of up to 16 chunks, eight with four 2 us.
 template <int D, bool F16>
-__global__ void __launch_bounds__(256, 5) k_tree_join(const TreeAttnParams p) {
+__global__ void __launch_bounds__(256, 6) k_tree_join(const TreeAttnParams p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, heads = p.kv_heads * p.group;
   const int n = blockIdx.x, of_n = blockIdx.y * 8 + (threadIdx.x >> 5);  // request, row of it
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(256, 5) k_tree_join(const TreeAttnParams p) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int k1 = min(live, q * 32 + 32);
-#pragma unroll 8
+#pragma unroll 4
     for (int k = q * 32; k < k1; ++k) {
       const float f = __shfl_sync(DC_FULL_MASK, w[q], k & 31);
       const float *src = po + (int64_t)k * R * D;

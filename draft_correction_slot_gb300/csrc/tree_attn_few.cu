@@ -18,7 +18,9 @@
 // by 2^8, and only then the references are taken anew (the maxima across the
 // group) and the rows' O^T is rescaled.
 //
-// Every unit leaves its result to the join kernel (tree_attn.cu).
+// Every unit leaves its result to the join kernel (tree_attn.cu).  32 requests
+// of up to 8000 tokens, 16 nodes x 4 heads: 132 us with it, 614 MB (floor 91);
+// inside a unit a 64 KB tile takes 2865 cycles, HBM's rate.
 //
 // Roles: warps 0-7 softmax (thread = token = TMEM lane) and output (thread =
 // element), warp 8 the tensor core, warps 9-10 TMA.  After an expired wait the
