@@ -37,7 +37,8 @@
 // sort and draw 16,000 of a top-p row's 140,000), to shared atomics of the
 // histogram that meet in a bank (27,000) and to blocks that end at different
 // times (2.25 waves).  16 rows: 27 us, all of it latency between the phases.
-// The first block alone: 1.4 ms for 16 rows with top_k 1000, 4.3 ms for 512.
+// The first block alone: 0.32 ms for 16 rows with top_k 1000, 1.0 ms for 512;
+// 0.95 ms for 16 rows whose top-p border more than kList tokens share.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -270,6 +271,49 @@ __device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The vector at `at` that reaches past the row's V logits: -inf there.
+template <bool F32>
+__device__ __noinline__ uint4 fetch_tail(const uint8_t *row, int at, int V) {
+  uint32_t x[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (F32) {
+      x[q] = at + q < V ? reinterpret_cast<const uint32_t *>(row)[at + q] : 0xFF800000u;
+    } else {
+      const uint32_t a = at + 2 * q < V ? reinterpret_cast<const uint16_t *>(row)[at + 2 * q] : 0xFF80u;
+      const uint32_t b = at + 2 * q + 1 < V ? reinterpret_cast<const uint16_t *>(row)[at + 2 * q + 1] : 0xFF80u;
+      x[q] = a | b << 16;
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+// NaN to -inf.
+template <bool F32>
+__device__ __noinline__ uint4 without_nan(uint4 w) {
+  uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (F32) {
+      if ((x[q] & 0x7FFFFFFFu) > 0x7F800000u) x[q] = 0xFF800000u;
+    } else {
+      if ((x[q] & 0x7FFFu) > 0x7F80u) x[q] = (x[q] & 0xFFFF0000u) | 0xFF80u;
+      if ((x[q] & 0x7FFF0000u) > 0x7F800000u) x[q] = (x[q] & 0xFFFFu) | 0xFF800000u;
+    }
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// E logits of a 16-byte vector as floats.
+template <bool F32>
+__device__ __forceinline__ void unpack(const uint4 &w, float (&f)[F32 ? 4 : 8]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) f[i] = __uint_as_float(x[i]);
+    else f[2 * i] = __uint_as_float(x[i] << 16), f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+  }
+}
+
 // The general path, one block, for what the candidate list does not hold: the
 // border's key a byte at a time by histograms (of counts for top-k, of masses
 // for top-p), its id and the drawn token by sums of kChunk tokens.  The
@@ -279,49 +323,71 @@ template <bool F32>
 struct General {
   SampleRow<F32> r;
   int V;
-  u64 *hist;       // [2][256]
+  uint32_t *hist;  // [2][4][256]
   u64 *chunk_all;  // [chunks]
   SampleShared &s;
 
-  // f(value, id, there) of this thread's tokens, eight loads in flight; all threads together
+  static constexpr int E = F32 ? 4 : 8;
+  __device__ uint4 load(int i) const {  // vector i of the row; -inf past its end
+    const uint8_t *row = static_cast<const uint8_t *>(r.x);
+    return (i + 1) * E <= V ? __ldg(reinterpret_cast<const uint4 *>(row) + i) : fetch_tail<F32>(row, i * E, V);
+  }
+  __device__ void values(const uint4 &w, float (&f)[E]) const {
+    unpack<F32>(w, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = f[e] != f[e] ? -INFINITY : f[e];
+  }
+  // f(value, id) of this thread's tokens, four vectors in flight
   template <typename F>
   __device__ void pass(F f) const {
-    for (int v0 = 0; v0 < V; v0 += 8 * kThreads) {
-      float x[8];
+    const int vecs = (V + E - 1) / E;
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += 4 * kThreads) {
+      uint4 w[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = r.value(min(v0 + q * kThreads + (int)threadIdx.x, V - 1));
+      for (int q = 0; q < 4; ++q) w[q] = load(min(i0 + q * kThreads, vecs - 1));
+#pragma unroll 1
+      for (int q = 0; q < 4 && i0 + q * kThreads < vecs; ++q) {
+        float x[E];
+        values(q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3], x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int v = v0 + q * kThreads + (int)threadIdx.x;
-        f(x[q], v, v < V);
+        for (int e = 0; e < E; ++e) {
+          const int v = (i0 + q * kThreads) * E + e;
+          if (v < V) f(x[e], v);
+        }
       }
     }
   }
   // The largest key whose tokens and those of larger keys reach `need` (> 0)
-  // together; `of` a token's share.  before: the share of larger keys.
-  template <typename F>
+  // together; `of` a token's share (LIMBS: 1 if below 2^11, 4 if below 2^44).
+  // before: the share of larger keys.  A bin is summed in limbs of 11 bits (2^20
+  // tokens of one stay below 2^31): 32-bit atomics on shared memory are the fast ones.
+  template <int LIMBS, typename F>
   __device__ uint32_t border(u64 need, F of, u64 &before) const {
     const int tid = threadIdx.x;
-    u64 *h = hist + (tid >> 5 & 1) * 256;  // two copies: half as many warps meet in a bin
+    uint32_t *h = hist + (tid >> 5 & 1) * 1024;  // two copies: half as many warps meet in a bin
     uint32_t key = 0;
     before = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
       __syncthreads();
-      hist[tid] = hist[256 + tid] = 0;
+      for (int i = tid; i < 2048; i += kThreads) hist[i] = 0;
       __syncthreads();
-      pass([&](float x, int v, bool there) {
-        const uint32_t q = order_key(x), digit = q >> shift & 255u;
-        const u64 n = there && (shift == 24 || q >> (shift + 8) == key) ? of(x, v) : 0;
-        const uint32_t some = __ballot_sync(DC_FULL_MASK, n != 0);
-        if (n) {  // a warp's tokens of a bin together: most share their first byte (n <= 2^40)
-          const uint32_t peers = __match_any_sync(some, digit);
-          const uint32_t hi = __reduce_add_sync(peers, (uint32_t)(n >> 20)), lo = __reduce_add_sync(peers, (uint32_t)n & 0xFFFFFu);
-          if ((tid & 31) == __ffs(peers) - 1) atomicAdd(&h[digit], ((u64)hi << 20) + lo);
+      pass([&](float x, int v) {
+        const uint32_t q = order_key(x);
+        if (shift == 24 || q >> (shift + 8) == key) {
+          const u64 n = of(x, v);
+#pragma unroll
+          for (int l = 0; l < LIMBS; ++l) {
+            const uint32_t part = (uint32_t)(n >> (11 * l)) & 2047u;
+            if (part) atomicAdd(&h[l * 256 + (q >> shift & 255u)], part);
+          }
         }
-        __syncwarp();
       });
       __syncthreads();
-      const u64 n = hist[255 - tid] + hist[511 - tid], upto = block_scan(n, s.red);
+      u64 n = 0;
+#pragma unroll
+      for (int l = 0; l < LIMBS; ++l)
+        n += ((u64)hist[l * 256 + 255 - tid] + hist[1024 + l * 256 + 255 - tid]) << (11 * l);
+      const u64 upto = block_scan(n, s.red);
       const int who = block_first(before + upto >= need, &s.first);
       if (tid == max(who, 0)) s.target = upto - n;
       __syncthreads();
@@ -336,14 +402,19 @@ struct General {
     const int tid = threadIdx.x, lane = tid & 31, chunks = (V + kChunk - 1) / kChunk;
     __syncthreads();
     for (int ch = tid >> 5; ch < chunks; ch += kWarps) {
-      float x[kChunk / 32];
+      constexpr int kVecs = kChunk / E / 32;
+      const int i = ch * (kChunk / E) + lane, last = (V - 1) / E;
+      uint4 w[kVecs];
       u64 n = 0;
 #pragma unroll
-      for (int q = 0; q < kChunk / 32; ++q) x[q] = r.value(min(ch * kChunk + q * 32 + lane, V - 1));
+      for (int q = 0; q < kVecs; ++q) w[q] = load(min(i + q * 32, last));
 #pragma unroll
-      for (int q = 0; q < kChunk / 32; ++q) {
-        const int v = ch * kChunk + q * 32 + lane;
-        if (v < V) n += of(x[q], v);
+      for (int q = 0; q < kVecs; ++q) {
+        float x[E];
+        values(w[q], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((i + q * 32) * E + e < V) n += of(x[e], (i + q * 32) * E + e);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(DC_FULL_MASK, n, o);
@@ -391,7 +462,7 @@ struct General {
     u64 before, n;
     auto count = [](float, int) -> u64 { return 1; };
     if (k < V) {
-      const uint32_t key = border((u64)k, count, before);
+      const uint32_t key = border<1>((u64)k, count, before);
       r.last = find([&](float x, int) -> u64 { return order_key(x) == key; }, [&](u64) { return (u64)k - before - 1; }, n);
       r.key = key;
     }
@@ -400,13 +471,13 @@ struct General {
       auto in = [&](float x, int v) { return order_key(x) > top.key || (order_key(x) == top.key && v <= top.last); };
       auto mass = [&](float x, int v) -> u64 { return in(x, v) ? top.weight(x) : 0; };
       u64 all = 0;
-      pass([&](float x, int v, bool there) { all += there ? mass(x, v) : 0; });
+      pass([&](float x, int v) { all += mass(x, v); });
       all = block_sum(all, s.red);
       __syncthreads();
       if (threadIdx.x == 0) s.need = max(share_of(tp, all), (u64)1);
       __syncthreads();
       const u64 need = s.need;
-      const uint32_t key = border(need, mass, before);
+      const uint32_t key = border<4>(need, mass, before);
       const u64 w = top.weight(key_value(key));
       const u64 more = (need - before + w - 1) / w;  // tokens of the border's key; w > 0, its mass is
       r.last = find([&](float x, int v) -> u64 { return order_key(x) == key && in(x, v); }, [&](u64) { return more - 1; }, n);
@@ -418,56 +489,13 @@ struct General {
 };
 // (s.need: the kept total)
 template <bool F32>
-__device__ __noinline__ int sample_general(SampleRow<F32> r, int V, int k, float tp, float u, u64 *hist,
+__device__ __noinline__ int sample_general(SampleRow<F32> r, int V, int k, float tp, float u, uint32_t *hist,
                                            u64 *chunk_all, SampleShared &s) {
   General<F32> g{r, V, hist, chunk_all, s};
   u64 total;
   const int token = g(k, tp, u, total);
   if (threadIdx.x == 0) s.need = total;
   return token;
-}
-
-// The vector at `at` that reaches past the row's V logits: -inf there.
-template <bool F32>
-__device__ __noinline__ uint4 fetch_tail(const uint8_t *row, int at, int V) {
-  uint32_t x[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if constexpr (F32) {
-      x[q] = at + q < V ? reinterpret_cast<const uint32_t *>(row)[at + q] : 0xFF800000u;
-    } else {
-      const uint32_t a = at + 2 * q < V ? reinterpret_cast<const uint16_t *>(row)[at + 2 * q] : 0xFF80u;
-      const uint32_t b = at + 2 * q + 1 < V ? reinterpret_cast<const uint16_t *>(row)[at + 2 * q + 1] : 0xFF80u;
-      x[q] = a | b << 16;
-    }
-  }
-  return make_uint4(x[0], x[1], x[2], x[3]);
-}
-// NaN to -inf.
-template <bool F32>
-__device__ __noinline__ uint4 without_nan(uint4 w) {
-  uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if constexpr (F32) {
-      if ((x[q] & 0x7FFFFFFFu) > 0x7F800000u) x[q] = 0xFF800000u;
-    } else {
-      if ((x[q] & 0x7FFFu) > 0x7F80u) x[q] = (x[q] & 0xFFFF0000u) | 0xFF80u;
-      if ((x[q] & 0x7FFF0000u) > 0x7F800000u) x[q] = (x[q] & 0xFFFFu) | 0xFF800000u;
-    }
-  }
-  return make_uint4(x[0], x[1], x[2], x[3]);
-}
-
-// E logits of a 16-byte vector as floats.
-template <bool F32>
-__device__ __forceinline__ void unpack(const uint4 &w, float (&f)[F32 ? 4 : 8]) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (F32) f[i] = __uint_as_float(x[i]);
-    else f[2 * i] = __uint_as_float(x[i] << 16), f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-  }
 }
 
 template <bool F32, bool HELD>
@@ -974,7 +1002,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   u64 total = 0;
   if (!general && by_list && s.listed > kList) general = true;
   if (general) {
-    token = sample_general<F32>(r, V, k, tp, u, list, chunk_all, s);
+    token = sample_general<F32>(r, V, k, tp, u, hist, chunk_all, s);
     total = s.need;  // (thread 0 uses it)
   } else {
     // candidates in order

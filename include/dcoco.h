@@ -469,7 +469,8 @@ void dcoco_tree_destroy(dcoco_tree_handle *h);
  * (u: as 0).
  * The order and the sums do not depend on rows or timing.  A top_k above 512
  * (and below the vocabulary), a border of top_p that more than 1088 tokens share
- * and a row with +inf are served by a slower form (16 rows of 151936: 1.4 ms).
+ * and a row with +inf are served by a slower form (16 rows of
+ * 151936: 0.3 to 1 ms).
  * One launch, no workspace.  rows == 0 is a no-op.  Errors: EINVAL (null or
  * misaligned pointers, vocab outside 1..2^20, stride, dtype, rows < 0), ECUDA. */
 int dcoco_sample(int rows, int vocab, const void *logits, int dtype, int64_t row_stride,
