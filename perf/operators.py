@@ -201,12 +201,11 @@ def _prepare_commit(c, g):
     parents, anc = _tree(g, N, T)
     tokens = torch.randint(0, VOCAB, (N, T), generator=g, device="cuda", dtype=torch.int32)
     sampled = torch.randint(0, VOCAB, (N, T), generator=g, device="cuda", dtype=torch.int32)
-    # the target agrees with one child of most nodes: the latest of those that it may agree with
-    agree = (_rand(g, N, T) < 0.8) & (parents >= 0)
-    node = torch.arange(T, device="cuda").expand(N, T)
-    child = torch.zeros(N, T, dtype=torch.long, device="cuda").scatter_reduce(
-        1, parents.clamp(min=0).long(), torch.where(agree, node, 0), "amax")
-    sampled = torch.where(child > 0, tokens.gather(1, child), sampled)
+    # the target agrees with one child of most nodes: the last writer among the children of a node
+    agree = _rand(g, N, T) < 0.8
+    up = torch.where(agree & (parents >= 0), parents, T).long()
+    wide = torch.cat([sampled, sampled[:, :1]], 1)
+    sampled = wide.scatter(1, up, tokens)[:, :T].contiguous()
     s = dict(c=c, k_new=new[0], v_new=new[1], k_cache=cache[0], v_cache=cache[1], table=table, ctx=ctx,
              parents=parents, anc=anc, tokens=tokens, sampled=sampled)
     for name, shape in (("path", (N, T)), ("accept_len", (N,)), ("next_token", (N,)), ("new_len", (N,))):
