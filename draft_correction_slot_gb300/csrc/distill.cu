@@ -76,9 +76,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Puts v at `p` in block `rank` of the cluster.
 __device__ __forceinline__ void put_peer(const float *p, int rank, float v) {
   uint32_t at;
@@ -179,6 +178,7 @@ k_step(const DistillParams p, int blocks, int slice_vecs) {
   const int nv = max(0, v1 - v0), full = nv / E;  // whole vectors; the rest singly
   const uint4 *src = reinterpret_cast<const uint4 *>(x + v0);
   const float inv_t = 1.f / p.temperature, c = inv_t * kLog2e;
+  cluster_arrive();  // (this block is there)
 
   // the slice: HOLD vectors a thread in flight and kept, what is beyond them read again
   uint4 held[HOLD];
@@ -224,6 +224,7 @@ k_step(const DistillParams p, int blocks, int slice_vecs) {
   }
   loss = block_reduce(loss, s.red, false);
   here = block_reduce(here, s.red, false);
+  cluster_wait();  // every block of the cluster is there: its shared memory may be written
   if (tid == 0) {
     for (int b = GRAD ? 0 : blocks - 1; b < blocks; ++b) {
       const int to = GRAD ? b : 0;  // the loss alone: the first block only
@@ -233,7 +234,8 @@ k_step(const DistillParams p, int blocks, int slice_vecs) {
       put_peer(&s_part[rank].mass, to, here);
     }
   }
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
   if (!GRAD && rank != 0) return;
   float M = s_part[0].max, S = 0.f;
   for (int b = 1; b < blocks; ++b) M = fmaxf(M, s_part[b].max);

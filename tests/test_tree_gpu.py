@@ -722,3 +722,37 @@ def test_calls_in_a_graph(env):
         for a, b in zip(again, calls()):
             assert torch.equal(a, b)
     assert v.status() == dc.DCOCO_OK
+
+
+# ------------------------------------------------------------------ blocks that start or end at different times
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [16392, 40000, 151936])
+def test_distill_beside_other_work(env, V, f32):
+    """Clusters of 2 to 8 blocks a row, whose sums meet in shared memory, under work of another stream: the same bits."""
+    torch, dc = env
+    R, K = 300, 16
+    g = torch.Generator(device="cuda").manual_seed(V + f32)
+    x = (3 * torch.randn(R, V, generator=g, device="cuda")).to(torch.float32 if f32 else torch.bfloat16)
+    top = x.float().topk(K, dim=1)
+    ids, teacher = top.indices.int(), top.values.contiguous()
+    weight = torch.rand(R, generator=g, device="cuda")
+
+    def calls():
+        loss, lse, loss2, lse2 = (torch.empty(R, device="cuda") for _ in range(4))
+        grad = torch.empty_like(x)
+        dc.dcoco_distill_loss(x, ids, teacher, loss=loss, lse=lse)
+        dc.dcoco_distill_step(x, ids, teacher, weight, loss=loss2, lse=lse2, grad=grad)
+        return loss, lse, loss2, lse2, grad
+
+    quiet = calls()
+    assert torch.equal(quiet[0], quiet[2]) and torch.equal(quiet[1], quiet[3])
+    torch.cuda.synchronize()
+    side, big = torch.cuda.Stream(), torch.randn(4096, 4096, generator=g, device="cuda").bfloat16()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                big @ big
+        for a, b in zip(calls(), quiet):
+            assert torch.equal(a, b)
+    torch.cuda.current_stream().wait_stream(side)
