@@ -333,9 +333,11 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
       const int last = g - 1, g0 = g - w.ntiles;  // the unit's last and first tile
       const bool lone = w.ntiles == 1;            // only group g0 & 1 had a tile
       if (!lone || group == (g0 & 1)) {
-        sm.ml[group][row] = make_float2(ref, l);
         const int mine = (last & 1) == group ? last : last - 1;
         wait(&b.pv_done[group], mine >> 1);
+        // after the wait: this unit's first products waited for o_free, where
+        // the other group arrives when it has read the last unit's ml
+        sm.ml[group][row] = make_float2(ref, l);
       }
       both_sync();
       tc_fence_after();

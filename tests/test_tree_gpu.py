@@ -756,3 +756,27 @@ def test_distill_beside_other_work(env, V, f32):
         for a, b in zip(calls(), quiet):
             assert torch.equal(a, b)
     torch.cuda.current_stream().wait_stream(side)
+
+
+@pytest.mark.parametrize("T,H,g,D,page,dtype", [(65, 4, 1, 128, 64, "bfloat16"), (70, 3, 2, 64, 32, "float16"),
+                                                (130, 2, 2, 128, 16, "float16"), (256, 2, 3, 64, 128, "bfloat16")])
+def test_attention_short_units_in_a_row(env, T, H, g, D, page, dtype):
+    """More than 64 rows a K/V head, units of one to three tiles, many a block: what the two halves of a block tell
+    each other of a unit is not the next one's."""
+    torch, dc = env
+    rng = np.random.default_rng(T + D)
+    ctx = [int(rng.choice([0, 1, 100, 128, 129, 250])) for _ in range(90)]
+    a = Attn(torch, T, ctx, T, H, g, D, page, getattr(torch, dtype), tree_len=[int(rng.choice([1, T // 2, T])) for _ in ctx])
+    v = a.verifier(dc)
+    out, lse = a.run(v)
+    for _ in range(20):
+        again, lse2 = a.run(v)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    for n in rng.choice(90, 6, replace=False):
+        one = slice(n, n + 1)
+        b = Attn.__new__(Attn)
+        b.__dict__.update(a.__dict__)
+        b.q, b.k_new, b.v_new = a.q[one], a.k_new[one], a.v_new[one]
+        b.table, b.ctx, b.sees, b.len = a.table[one], a.ctx[one], a.sees[one], a.len[one]
+        b.check(out[one], lse[one])
+    assert v.status() == dc.DCOCO_OK
