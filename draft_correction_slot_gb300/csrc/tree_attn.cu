@@ -341,8 +341,11 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
       }
       both_sync();
       tc_fence_after();
-      const float2 other = sm.ml[group ^ 1][row];
-      const float M = fmaxf(ref, other.x), f = ex2(ref - M), fo = ex2(other.x - M);
+      // In the order of the tiles, not of the groups: which group has a unit's
+      // first tile depends on the units before it, and the result must not.
+      const int ga = g0 & 1;  // has the unit's first tile (and third, ...)
+      const float2 a = sm.ml[ga][row], z = lone ? make_float2(kNone, 0.f) : sm.ml[ga ^ 1][row];
+      const float M = fmaxf(a.x, z.x), fa = ex2(a.x - M), fz = ex2(z.x - M);
       const int64_t item = ((int64_t)w.n * p.kv_heads + w.h) * p.mtiles + w.mt;
       const int64_t slot = (item * p.max_chunks + w.chunk) * p.part_rows + row;
       float *part = reinterpret_cast<float *>(p.part_o) + slot * D + group * (D / 2);
@@ -350,13 +353,11 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
       for (int q = 0; q < D / 64; ++q) {
         const uint32_t col = trow + kO + group * (D / 2) + q * 32;
         float x[32], y[32];
-        if (lone) {
-          tmem_ld32(col + (g0 & 1) * 128, x);
-        } else {
-          tmem_ld32(col + group * 128, x);
-          tmem_ld32(col + (group ^ 1) * 128, y);
+        tmem_ld32(col + ga * 128, x);
+        if (!lone) {
+          tmem_ld32(col + (ga ^ 1) * 128, y);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = fmaf(y[k], fo, x[k] * f);
+          for (int k = 0; k < 32; ++k) x[k] = fmaf(y[k], fz, x[k] * fa);
         }
         if (used && ok) {
 #pragma unroll
@@ -368,7 +369,7 @@ k_tree_attn(const TreeAttnParams p, const __grid_constant__ TreeAttnMaps maps) {
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free));
       if (group == 0 && used && ok)
-        p.part_ml[slot] = lone ? ((g0 & 1) ? other : make_float2(ref, l)) : make_float2(M, fmaf(other.y, fo, l * f));
+        p.part_ml[slot] = lone ? a : make_float2(M, fmaf(z.y, fz, a.y * fa));
       if (seen_tree && live_row && ok) {
         // infinities and NaN of the nodes that the row sees
 #pragma unroll 1

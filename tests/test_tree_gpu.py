@@ -780,3 +780,22 @@ def test_attention_short_units_in_a_row(env, T, H, g, D, page, dtype):
         b.table, b.ctx, b.sees, b.len = a.table[one], a.ctx[one], a.sees[one], a.len[one]
         b.check(out[one], lse[one])
     assert v.status() == dc.DCOCO_OK
+
+
+@pytest.mark.parametrize("T,H,g,D,page,dtype", [(65, 4, 1, 128, 64, "bfloat16"), (70, 3, 2, 64, 32, "float16"),
+                                                (130, 2, 2, 128, 16, "float16"), (20, 4, 4, 64, 64, "bfloat16"),
+                                                (16, 4, 4, 128, 16, "bfloat16"), (1, 8, 4, 64, 32, "float16")])
+def test_attention_alone_and_among_others(env, T, H, g, D, page, dtype):
+    """Odd and even numbers of tiles and units in a block before a request's own: the same bits alone."""
+    torch, dc = env
+    rng = np.random.default_rng(T + D + 1)
+    ctx = [int(rng.choice([0, 1, 100, 128, 129, 250, 500, 1500])) for _ in range(90)]
+    a = Attn(torch, T, ctx, T, H, g, D, page, getattr(torch, dtype), tree_len=[int(rng.choice([1, T // 2, T])) for _ in ctx])
+    v = a.verifier(dc)
+    out, lse = a.run(v)
+    for n in range(90):
+        one = slice(n, n + 1)
+        o, l = v.attention(a.q[one], a.k_new[one], a.v_new[one], a.k_cache, a.v_cache, a.t_table[one], a.t_ctx[one],
+                           tree_mask=a.mask[one], tree_len=a.t_len[one])
+        assert torch.equal(o[0], out[n]), n
+        assert torch.equal(l[0], lse[n]), n
