@@ -257,6 +257,7 @@ struct SampleShared {
   uint32_t mine, base;  // candidates of this block, and where they go in the first block's list
   float dmax;
   Orders orders;
+  int again;            // by mass, after a try: the border was not among the candidates
 };
 
 // Maxima that a NaN goes through.
@@ -982,15 +983,12 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       if (sure_all >= need) edge = b1, edge_mass = sure_all;
       else edge = b2, edge_mass = sure_all + m;
       __syncthreads();
-      if (in) {
-        // it is: the others are done
-        if (tid < blocks) put32(peer(&s.orders.step, tid), kStop);
-      } else if (tid < blocks) {
-        put32(peer(&s.orders.step, tid), kWeigh);
-      }
+      // (not in `orders`: the next ones may be written while a block still reads this,
+      // and a block that took their kStop for this one would leave under the writes)
+      if (tid < blocks) put32(peer(&s.again, tid), in ? 0u : 1u);
     }
     cluster_sync();
-    if (s.orders.step == kStop) {
+    if (!s.again) {  // the others are done
       if (rank != 0) return;
       break;
     }

@@ -799,3 +799,25 @@ def test_attention_alone_and_among_others(env, T, H, g, D, page, dtype):
                            tree_mask=a.mask[one], tree_len=a.t_len[one])
         assert torch.equal(o[0], out[n]), n
         assert torch.equal(l[0], lse[n]), n
+
+
+@pytest.mark.parametrize("R", [40, 200])
+@pytest.mark.parametrize("V", [40001, 70001, 200003])
+def test_sample_borders_past_the_first_window(env, V, R):
+    """Evenly spread fp32 logits, a histogram bin a fair share of the mass: the first window round top-p's border
+    misses some rows' borders, and the blocks go over the tokens again."""
+    torch, dc = env
+    rng = np.random.default_rng(V + R)
+    x = np.zeros((R, (V + 7) // 8 * 8), np.float32)
+    x[:, :V] = rng.random((R, V), dtype=np.float32)
+    t = (1.5 / 2048 / rng.uniform(0.2, 3.0, R)).astype(np.float32)  # a bin is 0.2 to 3 temperatures wide
+    p, u = rng.uniform(0.05, 0.97, R).astype(np.float32), rng.random(R).astype(np.float32)
+    cuda = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    tokens, logprob = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, device="cuda")
+    dc.dcoco_sample(cuda(x)[:, :V], cuda(u), tokens, temperature=cuda(t), top_p=cuda(p), logprob=logprob)
+    for r in range(R):
+        tok, lp, near = tree_ref.sample_row(x[r, :V], u[r], t[r], 0, p[r])
+        if near < 2.0 ** -22 and tok != int(tokens[r]):  # as in test_sample
+            continue
+        assert tok == int(tokens[r]), (r, float(t[r]), tok, int(tokens[r]), near)
+        assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp) + (2.0 ** -12 if near < 2.0 ** -22 else 0)
