@@ -157,17 +157,23 @@ __device__ __forceinline__ int block_first(bool hit, int *s) {
   return *s == kThreads ? -1 : *s;
 }
 
-// Sorts list[0, n) descending (n a power of two), the whole block.  Pairs
-// closer than 64 stay within a warp's 64 entries: those steps need no block
-// barrier.
+// Sorts list[0, n) descending, the whole block.  A bitonic network whose
+// merges begin with mirrored pairs, so that every exchange puts the larger
+// entry first: what a power of two above n would add are least entries that
+// never move, and pairs that reach past n are left out.  Pairs closer than 64
+// stay within a warp's 64 entries: those steps need no block barrier.
 __device__ __forceinline__ void sort_desc(u64 *list, int n) {
   __syncthreads();
-  for (int k = 2; k <= n; k <<= 1)
+  int pairs = 1;
+  while (2 * pairs < n) pairs <<= 1;
+  for (int k = 2; k <= 2 * pairs; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int a = ((i & ~(j - 1)) << 1) | (i & (j - 1)), b = a + j;
+      const bool mirrored = 2 * j == k;
+      for (int i = threadIdx.x; i < pairs; i += kThreads) {
+        const int a = ((i & ~(j - 1)) << 1) | (i & (j - 1)), b = mirrored ? a ^ (k - 1) : a + j;
+        if (b >= n) continue;
         const u64 x = list[a], y = list[b];
-        if ((x < y) == ((a & k) == 0)) list[a] = y, list[b] = x;
+        if (x < y) list[a] = y, list[b] = x;
       }
       if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
       else __syncwarp();
@@ -1004,10 +1010,8 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
     total = s.need;  // (thread 0 uses it)
   } else {
     // candidates in order
-    int n = whole ? 0 : (int)s.listed, pad = 1;
-    while (pad < n) pad <<= 1;
-    for (int i = n + tid; i < pad; i += kThreads) list[i] = 0;
-    if (n > 0) sort_desc(list, pad);
+    const int n = whole ? 0 : (int)s.listed;
+    if (n > 0) sort_desc(list, n);
     const auto weight_at = [&](int i) { return r.weight(key_value((uint32_t)(list[i] >> 32))); };
     // the first `m` of them stay: the shortest prefix with mass `need`
     int m = n;
@@ -1040,13 +1044,13 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
     }
     if (by_list) {
       // the kept ones, by id, and the draw among them
-      for (int i = tid; i < pad; i += kThreads) {
+      for (int i = tid; i < n; i += kThreads) {
         const u64 e = list[i];
         const float x = key_value((uint32_t)(e >> 32));
         const bool keep = i < m && (x == mx || mx - x <= r.dmax);
         list[i] = keep ? (e & 0xFFFFFFFFull) << 32 | (e >> 32) : 0;  // ids are stored complemented: descending is by id
       }
-      sort_desc(list, pad);
+      sort_desc(list, n);
       const auto by_id = [&](int i) { return list[i] ? r.weight(key_value((uint32_t)list[i])) : 0; };
       u64 mine = 0;
       for (int q = 0; q < per; ++q)

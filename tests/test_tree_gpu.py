@@ -821,3 +821,31 @@ def test_sample_borders_past_the_first_window(env, V, R):
             continue
         assert tok == int(tokens[r]), (r, float(t[r]), tok, int(tokens[r]), near)
         assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp) + (2.0 ** -12 if near < 2.0 ** -22 else 0)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [4099, 40000, 200003])
+@pytest.mark.parametrize("what", ["top_p", "top_k", "both"])
+def test_sample_many_tokens_share_the_border(env, V, f32, what):
+    """A border that 1022 to 1090 tokens share: as many candidates as the list of one row holds, a few less, and more."""
+    torch, dc = env
+    counts = [1022, 1023, 1024, 1025, 1050, 1087, 1088, 1089, 1090]
+    R = 3 * len(counts)
+    rng = np.random.default_rng(V + f32)
+    x = np.full((R, (V + 7) // 8 * 8), -20, np.float32)
+    for r in range(R):
+        at = rng.choice(V, counts[r % len(counts)] + 1, replace=False)
+        x[r, at] = 0
+        x[r, at[0]] = 5
+    p = rng.uniform(0.2, 0.95, R).astype(np.float32) if what != "top_k" else None
+    k = rng.integers(2, 512, R).astype(np.int32) if what != "top_p" else None
+    u = rng.random(R).astype(np.float32)
+    logits = torch.from_numpy(x).to(torch.float32 if f32 else torch.bfloat16).cuda()[:, :V]
+    cuda = lambda a: None if a is None else torch.from_numpy(a).cuda()  # noqa: E731
+    tokens, logprob = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, device="cuda")
+    dc.dcoco_sample(logits, cuda(u), tokens, top_k=cuda(k), top_p=cuda(p), logprob=logprob)
+    for r in range(R):
+        tok, lp, near = tree_ref.sample_row(x[r, :V], u[r], None, 0 if k is None else int(k[r]), 1.0 if p is None else p[r])
+        assert near > 2.0 ** -22, (r, near)  # as in test_sample (no border and no draw of these rows is near another outcome)
+        assert tok == int(tokens[r]), (r, counts[r % len(counts)], tok, int(tokens[r]))
+        assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp)
