@@ -85,17 +85,20 @@ struct SampleRow {
                         : bf16_bits_to_float(static_cast<const uint16_t *>(x)[v]);
     return f != f ? -INFINITY : f;
   }
-  // e^{-d / t} in units of 2^-40.  d / (t ln 2) as a product with its
-  // rounding error, so that weights of large d keep fp32's relative
-  // accuracy and carry no common bias.
-  __device__ u64 weight(float v) const {
+  // e^{-d / t}; 0 below 2^-64.  d / (t ln 2) as a product with its rounding
+  // error, so that weights of large d keep fp32's relative accuracy and carry
+  // no common bias.
+  __device__ float share(float v) const {
     const float d = v == mx ? 0.f : mx - v;
     const float zh = d * ch;
-    if (!(zh < 64.f)) return 0;
+    if (!(zh < 64.f)) return 0.f;
     const float zl = fmaf(d, cl, fmaf(d, ch, -zh));
     const float w = exp2f(-zh);
-    return __float2ull_rn(fmaf(-w * 0.693147180559945f, zl, w) * 1099511627776.f);
+    return fmaf(-w * 0.693147180559945f, zl, w);
   }
+  // In units of 2^-40, and of 2^-54 (512 of these stay below 2^64).
+  __device__ u64 weight(float v) const { return __float2ull_rn(share(v) * 1099511627776.f); }
+  __device__ u64 fine_weight(float v) const { return __float2ull_rn(share(v) * 18014398509481984.f); }
   __device__ bool kept(float v, int i) const {
     const uint32_t k = order_key(v);
     return (k > key || (k == key && i <= last)) && (v == mx || mx - v <= dmax);
@@ -1105,13 +1108,14 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       if (tid == who) s.redi[0] = at, s.red[0] = target - cum;
       __syncthreads();
       const int v = s.redi[0] * kChunk + tid * (kChunk / kThreads);
-      target = s.red[0];
-      // in the chunk
+      target = s.red[0] << 14;
+      // in the chunk: in finer units, since the chunk's sum, rounded 16 tokens
+      // at a time, may have mass where each token alone rounds to none
       u64 w[kChunk / kThreads], sum = 0;
 #pragma unroll
       for (int q = 0; q < kChunk / kThreads; ++q) {
         const float x = v + q < V ? r.value(v + q) : -INFINITY;
-        w[q] = v + q < V && x > -INFINITY && r.kept(x, v + q) ? r.weight(x) : 0;
+        w[q] = v + q < V && x > -INFINITY && r.kept(x, v + q) ? r.fine_weight(x) : 0;
         sum += w[q];
       }
       u64 before = block_scan(sum, s.red) - sum;
@@ -1128,7 +1132,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
       if (got >= 0) {
         if (tid == got) s.redi[0] = found;
       } else {
-        // the chunk's sum, rounded 16 tokens at a time, was above its tokens': the last one
+        // the chunk's sum was above its tokens': the last one
         if (tid == 0) s.redi[0] = -1;
         __syncthreads();
         if (last >= 0) atomicMax(&s.redi[0], last);

@@ -849,3 +849,35 @@ def test_sample_many_tokens_share_the_border(env, V, f32, what):
         assert near > 2.0 ** -22, (r, near)  # as in test_sample (no border and no draw of these rows is near another outcome)
         assert tok == int(tokens[r]), (r, counts[r % len(counts)], tok, int(tokens[r]))
         assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [1500, 4099, 40000, 200003])
+def test_sample_far_below_one_peak(env, V, f32):
+    """One token, and all others 28.5 to 31 temperatures below it: no one of them has half a unit of the sums, 16
+    together do.  A row with finite logits gives a token, and the first one for u = 0 (or NaN)."""
+    torch, dc = env
+    rows = [(gap, at, u) for gap in (28.5, 29, 30, 31) for at in (5, 700, V // 2, V - 1)
+            for u in (0.0, math.nan, 2.0 ** -30, 0.5, 1 - 2.0 ** -23, 1 - 2.0 ** -24)]
+    R = len(rows)
+    x = np.zeros((R, (V + 7) // 8 * 8), np.float32)
+    for r, (gap, at, _) in enumerate(rows):
+        x[r, :V] = -gap
+        x[r, at] = 0
+    u = np.array([w for _, _, w in rows], np.float32)
+    logits = torch.from_numpy(x).to(torch.float32 if f32 else torch.bfloat16).cuda()[:, :V]
+    tokens, logprob = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, device="cuda")
+    dc.dcoco_sample(logits, torch.from_numpy(u).cuda(), tokens, logprob=logprob)
+    for r, (gap, at, _) in enumerate(rows):
+        got, low = int(tokens[r]), math.exp(-gap)
+        assert 0 <= got < V, (rows[r], got)
+        total = 1 + (V - 1) * low
+        before = got * low + (1 - low if at < got else 0)  # mass before the token
+        mass = 1 if got == at else low
+        target = 0.0 if np.isnan(u[r]) else float(u[r]) * total
+        if target == 0:
+            assert got == 0, rows[r]
+        # sums of weights with fp32 relative errors, as in test_sample
+        assert before <= target + 2.0 ** -22 * total and before + mass > target - 2.0 ** -22 * total, (rows[r], got)
+        lp = (0 if got == at else -gap) - math.log(total)
+        assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp)
