@@ -659,6 +659,9 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   // bins of d, 1.5 times the range down to the least vector maximum
   const float range = 1.5f * fmaxf(mx - low, 1e-6f), scale = (float)kBins / range;
   if (!small && !whole && !(range < 1e30f)) general = true;
+  // (the weighing pass takes distances of up to a step of the logits' type below
+  // the maximum: over t they have to stay finite)
+  if (!by_list && !(r.ch * fabsf(mx) < 1e38f)) general = true;
   if (!general && (by_mass || (by_list && !small))) {
     // histogram: the bin is the integer below 2^23 + d scale, by the addition's own rounding
     const float dtop = (float)(kBins - 1) / scale;

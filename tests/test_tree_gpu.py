@@ -881,3 +881,36 @@ def test_sample_far_below_one_peak(env, V, f32):
         assert before <= target + 2.0 ** -22 * total and before + mass > target - 2.0 ** -22 * total, (rows[r], got)
         lp = (0 if got == at else -gap) - math.log(total)
         assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("V", [1500, 40000, 200003])
+@pytest.mark.parametrize("what", ["plain", "top_k", "top_p", "min_p"])
+def test_sample_large_logits_over_small_temperatures(env, V, f32, what):
+    """A step of the logits' type, over the temperature, is past fp32's range: the best tokens share the mass."""
+    torch, dc = env
+    rng = np.random.default_rng(V + f32)
+    rows = [(top, t) for top in (1e38, -1e38, 1e30, -1e30, 3e12, -3e12, 1e9, 1.0) for t in (1e-30, 1e-18, 1e-9, 1e-4, 1e-2)]
+    R = len(rows)
+    x = np.zeros((R, (V + 7) // 8 * 8), np.float32)
+    for r, (top, _) in enumerate(rows):
+        x[r, :V] = top - abs(top) * rng.choice([0.02, 0.5, 1.0], V)  # (0.02: some steps of bf16)
+        x[r, rng.choice(V, 5, replace=False)] = top
+        x[r, rng.choice(V, 5, replace=False)] = -math.inf
+    logits = torch.from_numpy(x).to(torch.float32 if f32 else torch.bfloat16).cuda()[:, :V]
+    host = logits.float().cpu().numpy()
+    u, t = rng.random(R).astype(np.float32), np.array([t for _, t in rows], np.float32)
+    k = np.full(R, 40, np.int32) if what == "top_k" else None
+    p = rng.uniform(0.1, 0.95, R).astype(np.float32) if what == "top_p" else None
+    q = np.full(R, 0.1, np.float32) if what == "min_p" else None
+    cuda = lambda a: None if a is None else torch.from_numpy(a).cuda()  # noqa: E731
+    tokens, logprob = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, device="cuda")
+    dc.dcoco_sample(logits, cuda(u), tokens, temperature=cuda(t), top_k=cuda(k), top_p=cuda(p), min_p=cuda(q),
+                    logprob=logprob)
+    for r in range(R):
+        tok, lp, near = tree_ref.sample_row(host[r], u[r], t[r], 0 if k is None else int(k[r]),
+                                            1.0 if p is None else p[r], 0.0 if q is None else q[r])
+        if near < 2.0 ** -22 and tok != int(tokens[r]):  # as in test_sample
+            continue
+        assert tok == int(tokens[r]), (r, rows[r], tok, int(tokens[r]), near)
+        assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp) + (2.0 ** -12 if near < 2.0 ** -22 else 0)
