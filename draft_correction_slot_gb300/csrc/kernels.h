@@ -216,7 +216,8 @@ struct TreeAttnParams {
   // group <= 128 rows); tree_box: nodes of a K/V copy
   int mtiles, tile_nodes, tile_rows, tree_box;
   // chunks (see tree_chunk_tiles): (request, head, row tile) items of a full
-  // batch, SMs, the largest chunk, the most chunks of a request
+  // batch, SMs, the largest chunk, the most chunks of a request (for this call's
+  // kernel and row tiles)
   int items, sms, chunk_cap, max_chunks;
   int part_rows;    // tile_rows as the partial results are laid out: padded by the kernel for few rows
   float4 *part_o;   // [item][max_chunks][part_rows][head_dim], fp32

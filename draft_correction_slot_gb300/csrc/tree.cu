@@ -14,7 +14,10 @@ struct dcoco_tree_handle {
   dcoco_tree_config cfg;
   int device = 0;
   int page_shift = 0, sms = 1;
-  int max_chunks = 1;     // see TreeAttnParams
+  // the most chunks of a request (see TreeAttnParams): of the kernel for few
+  // rows, and of the other by the number of row tiles
+  int few_chunks = 0;
+  uint8_t many_chunks[257] = {};
   void *block = nullptr;              // one device allocation: status word, partial results
   int *err = nullptr;
   float2 *part_ml = nullptr;
@@ -74,6 +77,19 @@ struct RowTiles {
 // 352 / 341 / 342 us; 16 x 128 to 16000: 641 / 605 / 583 / 560 us.
 int chunk_cap(const dcoco_tree_config &c, bool few) { return c.max_batch == 1 ? 1 << 30 : few ? 16 : 64; }
 
+// The most chunks that a request of up to max_tiles tiles is cut into, with
+// `items` (request, head, row tile) items in a full batch.
+int most_chunks(int64_t max_tiles, int items, int sms, int cap) {
+  // (from 64 tiles a chunk on, the largest cap, the rule's other limit holds: kTreeMaxChunks)
+  const int64_t scan = max_tiles < 64 * dc::kTreeMaxChunks ? max_tiles : 64 * dc::kTreeMaxChunks;
+  int most = max_tiles > scan ? dc::kTreeMaxChunks : 1;
+  for (int nt = 1; nt <= scan; ++nt) {
+    const int per = dc::tree_chunk_tiles(nt, items, sms, cap), n = (nt + per - 1) / per;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
 int check_distill(int rows, int vocab, const void *logits, int dtype, int64_t row_stride, int topk,
                   const int32_t *ids, const float *teacher, float temperature) {
   if (rows < 0 || vocab < 1 || vocab > (1 << 20) || topk < 1 || topk > 1024) return DCOCO_EINVAL;
@@ -103,17 +119,24 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
   }
   const int64_t max_tiles = ((int64_t)cfg->page_size * cfg->max_pages + dc::kTreeTile - 1) / dc::kTreeTile +
                             (cfg->max_tree + dc::kTreeTile - 1) / dc::kTreeTile;
-  const RowTiles rt(*cfg, cfg->max_tree);
-  const int64_t scan = max_tiles < 2048 ? max_tiles : 2048;
-  for (int nt = 1; nt <= scan; ++nt) {
-    const int per = dc::tree_chunk_tiles(nt, cfg->max_batch * cfg->kv_heads, h->sms, chunk_cap(*cfg, true));
-    const int n = (nt + per - 1) / per;
-    if (n > h->max_chunks) h->max_chunks = n;
-  }
-  if (max_tiles > scan) h->max_chunks = dc::kTreeMaxChunks;
-  const size_t items = (size_t)cfg->max_batch * cfg->kv_heads * rt.mtiles;
-  // (a call on fewer nodes has no more rows than this: at most 64 where it has one tile of them)
-  const size_t rows = items * h->max_chunks * rt.part_rows;
+  // Partial results of the largest call, over the numbers of nodes up to max_tree:
+  // of either kernel its own chunks and rows (the most nodes that a number of row
+  // tiles stands for have the most rows)
+  const int group = cfg->q_heads / cfg->kv_heads, pairs = cfg->max_batch * cfg->kv_heads;
+  size_t rows = 0;
+  const auto reach = [&](int nodes) {
+    const RowTiles rt(*cfg, nodes);
+    const int n = most_chunks(max_tiles, pairs * rt.mtiles, h->sms, chunk_cap(*cfg, rt.few));
+    if (rt.few) h->few_chunks = n;
+    else h->many_chunks[rt.mtiles] = (uint8_t)n;
+    const size_t r = (size_t)pairs * rt.mtiles * n * rt.part_rows;
+    if (r > rows) rows = r;
+  };
+  const int few_nodes = 64 / group, tile_nodes = 128 / group;
+  if (few_nodes >= 1) reach(few_nodes < cfg->max_tree ? few_nodes : cfg->max_tree);
+  for (int nodes = tile_nodes; nodes - tile_nodes < cfg->max_tree; nodes += tile_nodes)
+    if (!RowTiles(*cfg, nodes < cfg->max_tree ? nodes : cfg->max_tree).few)
+      reach(nodes < cfg->max_tree ? nodes : cfg->max_tree);
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t at_ml = 256, at_o = at_ml + up(rows * sizeof(float2));
   const size_t bytes = at_o + rows * cfg->head_dim * sizeof(float);
@@ -176,7 +199,7 @@ int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco
   p.part_rows = rt.part_rows, p.few = rt.few;
   p.tree_box = nodes < dc::kTreeTile ? (nodes + 7) / 8 * 8 : dc::kTreeTile;
   p.items = c.max_batch * c.kv_heads * rt.mtiles, p.sms = h->sms;
-  p.chunk_cap = chunk_cap(c, rt.few), p.max_chunks = h->max_chunks;
+  p.chunk_cap = chunk_cap(c, rt.few), p.max_chunks = rt.few ? h->few_chunks : h->many_chunks[rt.mtiles];
   p.part_o = h->part_o, p.part_ml = h->part_ml;
   h->last_stream = static_cast<cudaStream_t>(stream);
   h->launches += 2;

@@ -377,7 +377,14 @@ typedef struct {
 
 /* Validate `cfg` and allocate the workspace on the current device.  Errors:
  * EINVAL, EUNSUPPORTED (head_dim, dtype, group or page size outside the set
- * above), ENOMEM, ECUDA.  Validation happens before any CUDA call. */
+ * above), ENOMEM, ECUDA.  Validation happens before any CUDA call.
+ * The workspace holds the partial results of the largest call: for every
+ * request, K/V head and chunk of tokens 4 head_dim + 8 bytes a row, the rows
+ * being nodes x (q_heads / kv_heads).  A request has up to 64 chunks, of 16
+ * tiles of 128 tokens (up to 64 rows) or 64 tiles (more rows), longer ones past
+ * 1024 or 4096 tiles, shorter ones where a full batch would not fill the GPU.
+ * With 32 query and 8 K/V heads of 128: 43 MB for 32 requests of 16 nodes up to
+ * 8192 tokens, 170 MB for 32 of 64 nodes up to 32768, 580 MB up to 131072. */
 int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out);
 
 /* Attention of `batch` trees of up to `nodes` nodes:

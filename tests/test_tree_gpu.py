@@ -914,3 +914,49 @@ def test_sample_large_logits_over_small_temperatures(env, V, f32, what):
             continue
         assert tok == int(tokens[r]), (r, rows[r], tok, int(tokens[r]), near)
         assert abs(lp - float(logprob[r])) <= 2.0 ** -20 + 2.0 ** -22 * abs(lp) + (2.0 ** -12 if near < 2.0 ** -22 else 0)
+
+
+# ------------------------------------------------------------------ handles larger than the call
+@pytest.mark.parametrize("kw,most_mb", [
+    (dict(max_batch=8, max_tree=64, q_heads=40, kv_heads=8, head_dim=128, page_size=64, max_pages=501), 64),
+    (dict(max_batch=32, max_tree=64, q_heads=32, kv_heads=8, head_dim=128, page_size=16, max_pages=2048), 192),
+    (dict(max_batch=32, max_tree=16, q_heads=32, kv_heads=8, head_dim=128, page_size=16, max_pages=512), 48),
+])
+def test_tree_workspace(env, kw, most_mb):
+    """A handle's memory: the chunks that a call can have times the rows of the kernel that has them, 4 D + 8 bytes each."""
+    torch, dc = env
+    one = dc.dcoco_tree_create(1, 1, 1, 1, 64, 16, 1)  # what the first handle of a process loads is not counted
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    h = dc.dcoco_tree_create(**kw)
+    taken = before - torch.cuda.mem_get_info()[0]
+    dc.dcoco_tree_destroy(h)
+    dc.dcoco_tree_destroy(one)
+    assert taken <= most_mb << 20
+
+
+@pytest.mark.parametrize("Hkv,g,D,page,tree", [(2, 4, 128, 16, 70), (2, 5, 64, 64, 64), (1, 1, 128, 32, 256),
+                                               (2, 71, 64, 16, 5), (1, 33, 128, 64, 9)])
+def test_attention_on_a_larger_handle(env, Hkv, g, D, page, tree):
+    """Calls of 1 to max_tree nodes on one handle, full batch and longest contexts among them: the same bits as on a
+    handle for just that many nodes, and as the 64-bit reference says."""
+    torch, dc = env
+    rng = np.random.default_rng(tree + g)
+    N, top = 6, 40 * 128
+    v = dc.TreeVerifier(Hkv * g, Hkv, D, page, top // page, max_batch=N, max_tree=tree)
+    edges = [1, tree, 16 // g, 64 // g, 64 // g + 1, 128 // g, 128 // g + 1, 2 * (128 // g) + 1]
+    for T in sorted({min(max(e, 1), tree) for e in edges}):
+        ctx = [top] * (N - 2) + [int(rng.integers(0, top)), 129]
+        a = Attn(torch, T, ctx, T, Hkv, g, D, page, torch.bfloat16)
+        out, lse = a.run(v)
+        fit = dc.TreeVerifier(Hkv * g, Hkv, D, page, top // page, max_batch=N, max_tree=T)
+        o, l = a.run(fit)
+        assert torch.equal(out, o) and torch.equal(lse, l)
+        fit.close()
+        one = slice(N - 1, N)
+        b = Attn.__new__(Attn)
+        b.__dict__.update(a.__dict__)
+        b.q, b.k_new, b.v_new = a.q[one], a.k_new[one], a.v_new[one]
+        b.table, b.ctx, b.sees, b.len = a.table[one], a.ctx[one], a.sees[one], a.len[one]
+        b.check(out[one], lse[one])
+    assert v.status() == dc.DCOCO_OK
