@@ -76,6 +76,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// (relaxed: there is nothing to publish; a release at entry cost a step of 2000 rows of 32001 fp32 logits 7 us of 129)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Puts v at `p` in block `rank` of the cluster.
@@ -178,7 +180,7 @@ k_step(const DistillParams p, int blocks, int slice_vecs) {
   const int nv = max(0, v1 - v0), full = nv / E;  // whole vectors; the rest singly
   const uint4 *src = reinterpret_cast<const uint4 *>(x + v0);
   const float inv_t = 1.f / p.temperature, c = inv_t * kLog2e;
-  cluster_arrive();  // (this block is there)
+  cluster_arrive_relaxed();  // this block is there
 
   // the slice: HOLD vectors a thread in flight and kept, what is beyond them read again
   uint4 held[HOLD];
