@@ -106,6 +106,8 @@ struct SampleRow {
 };
 
 // ---------------------------------------------------------------- clusters
+// (relaxed: publishes nothing)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
@@ -171,9 +173,9 @@ __device__ __forceinline__ void sort_desc(u64 *list, int n) {
   while (2 * pairs < n) pairs <<= 1;
   for (int k = 2; k <= 2 * pairs; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
-      const bool mirrored = 2 * j == k;
+      const int to = 2 * j == k ? k - 1 : j;  // the partner's distance, in bits: mirrored or plain
       for (int i = threadIdx.x; i < pairs; i += kThreads) {
-        const int a = ((i & ~(j - 1)) << 1) | (i & (j - 1)), b = mirrored ? a ^ (k - 1) : a + j;
+        const int a = ((i & ~(j - 1)) << 1) | (i & (j - 1)), b = a ^ to;
         if (b >= n) continue;
         const u64 x = list[a], y = list[b];
         if (x < y) list[a] = y, list[b] = x;
@@ -528,7 +530,7 @@ k_sample(const SampleParams p, int blocks, int slice, int chunks_all) {
   float t = p.temperature ? p.temperature[row] : 1.f, tp = p.top_p ? p.top_p[row] : 1.f, u = p.u[row];
   const float mp = p.min_p ? p.min_p[row] : 0.f;
   int k = p.top_k ? p.top_k[row] : 0;
-  cluster_arrive();  // (this block is there)
+  cluster_arrive_relaxed();  // this block is there
 
   bool nan = false;  // (not held) this thread's block met a NaN
   // A vector of the slice; past the vocabulary's end: -inf.
