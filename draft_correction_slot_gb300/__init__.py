@@ -544,7 +544,8 @@ def tree_mask(parents) -> torch.Tensor:
 
 class TreeVerifier:
     """Owns a tree handle; allocates output tensors per call.  One step of the target on a drafted tree:
-    attention() in every layer, sample() on the nodes' logits, commit() for all layers at once."""
+    attention() in every layer, sample() on the nodes' logits, commit() for all layers at once.  max_batch is best
+    near the batches that are run: the attention cuts requests for a full one (see include/dcoco.h)."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, max_pages: int, max_batch: int = 32,
                  max_tree: int = 64, dtype: torch.dtype = torch.bfloat16):

@@ -20,9 +20,10 @@
 // after its slice's, from the logit as it was read, so that the gradient may
 // overwrite the logits.
 //
-// 480 rows of 151936 bf16 logits: loss 41 us (146 MB, floor 22), gradient 58 us
-// (292 MB, 43), both in one step 89 us (43); 2000 rows of 32001 fp32: step 127 us
-// (512 MB, 76).  A block's loads, barriers and stores follow one another, and
+// 480 rows of 151936 bf16 logits: loss 43 us (146 MB, floor 22), gradient 58 us
+// (292 MB, 43), both in one step 89 us (43); 2000 rows of 32001 fp32: step 128 us
+// (512 MB, 76).  Longer rows keep fewer blocks an SM: 480 rows of 200008 take a
+// step 142 us (57), of 262144 156 us (74).  A block's loads, barriers and stores follow one another, and
 // the registers that hold the row allow four blocks an SM to fill the gaps.
 #include "common.cuh"
 #include "kernels.h"

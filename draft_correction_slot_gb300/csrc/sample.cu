@@ -19,26 +19,32 @@
 //     over those surely kept, and per 512 tokens for the draw.
 // The first block sorts the candidates, finds the border exactly, and draws:
 // the 512 tokens by their sums, then the token in them.
-// What this does not cover (top_k over kTopkMost of a larger vocabulary,
-// borders with more tokens around them than the list holds, an infinite
-// maximum or one near the type's lowest value) the first block does alone, in
-// about eight passes over the row.
+// What this does not cover the first block does alone, in about eight passes
+// over the row: top_k over kTopkMost, or over the row's 16-byte vectors, of a
+// larger vocabulary; borders with more tokens around them than the list holds;
+// an infinite maximum, one near the type's lowest value, or one that over the
+// temperature is past 10^38.  The bins follow the least vector maximum, so a
+// vector of tokens masked with a finite value far below the others leaves the
+// live ones in a few bins, and such rows go there too (-inf does not count).
 //
 // Weights are summed as 64-bit integers in units of 2^-40 (V <= 2^20 of them
 // stay below 2^60), up to 16 of one thread's first in fp32: the same sums
-// whatever the cluster's size and the blocks' timing.  e^{-d / t} is taken as
+// whatever the cluster's size and the blocks' timing.  A token below half a
+// unit counts as far as its thread's 16 reach one.  e^{-d / t} is taken as
 // 2^-z with z = d / (t ln 2) carried with its rounding error: a row's border
 // can lie where a token has 10^-6 of the mass, and a bias of 10^-7 common to
 // all weights beyond it would move it.
 //
-// 512 rows of 151936 bf16 logits (155 MB, 23 us of bytes): 169 us, 126 with
-// top-k alone, 97 with neither.  Half of the issue slots are used; the rest
+// 512 rows of 151936 bf16 logits (155 MB, 23 us of bytes), in a graph: 172 us
+// with rows of all kinds, 200 with top-p alone, 135 with top-k alone, 97 with neither.  Half of the issue slots are used; the rest
 // goes to steps that only the first block takes (the decision 8,000 cycles,
 // sort and draw 16,000 of a top-p row's 140,000), to shared atomics of the
 // histogram that meet in a bank (27,000) and to blocks that end at different
 // times (2.25 waves).  16 rows: 27 us, all of it latency between the phases.
 // The first block alone: 0.32 ms for 16 rows with top_k 1000, 1.0 ms for 512;
-// 0.95 ms for 16 rows whose top-p border more than kList tokens share.
+// 0.95 ms for 16 rows whose top-p border more than kList tokens share.  With
+// 272 tokens masked at -1e4, 16 rows of top_p 0.9 take 0.69 ms (30 us without),
+// 512 rows 2.3 ms (0.23).
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -53,7 +59,11 @@ constexpr int kList = 1088;      // candidates the list holds (its 8704 bytes al
 constexpr int kTopkMost = 512;   // largest top_k of the candidate path
 constexpr int kChunk = 512;      // tokens of a partial sum (one warp)
 constexpr int kMostBlocks = 8;   // blocks of a cluster
-constexpr size_t kMostSlice = 40 * 1024;  // bytes of a slice held in shared memory (three blocks an SM)
+// Bytes of a slice held in shared memory.  Three blocks an SM leave about 62 KB
+// beside the list; 40 KB is what a thread loads at once (kAtOnce vectors).  An
+// eighth of 151936 bf16 logits fits, of 200008 not: 16 rows with top_p 0.9 take
+// 30 and 50 us.
+constexpr size_t kMostSlice = 40 * 1024;
 
 // Larger key <=> larger value; -0 and +0 share a key, NaN counts as -inf.
 __device__ __forceinline__ uint32_t order_key(float x) {

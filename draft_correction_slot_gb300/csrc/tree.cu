@@ -74,7 +74,14 @@ struct RowTiles {
 // 32 tiles; 24 x 1, 4 rows, to 16001: 114 / 103 / 105 us.  The kernel for many
 // rows, whose borders cost more, at 32 / 48 / 64 / 96 tiles: 8 x 64, three
 // tiles of 125 rows, to 32000: 310 / 305 / 314 / 308 us; 32 x 64 to 8000: 369 /
-// 352 / 341 / 342 us; 16 x 128 to 16000: 641 / 605 / 583 / 560 us.
+// 352 / 341 / 342 us; 16 x 128 to 16000: 641 / 605 / 583 / 560 us.  (96 was as
+// good or better in these and is not taken yet.)
+//
+// The handle's batch, not the call's, so that a request's result has the same
+// bits whatever runs beside it.  Its price: one request on a handle for 32, 8
+// K/V heads of 128, in a graph, against a handle for one: 16 nodes x 4 heads at
+// 1000 tokens 20 us (13), at 8000 28 (20); 64 nodes x 5 at 4000 50 (25), at 8000
+// 83 (31).  Four requests: 21 (16), 30 (27), 55 (42), 91 (60).
 int chunk_cap(const dcoco_tree_config &c, bool few) { return c.max_batch == 1 ? 1 << 30 : few ? 16 : 64; }
 
 // The most chunks that a request of up to max_tiles tiles is cut into, with

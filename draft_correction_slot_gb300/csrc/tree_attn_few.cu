@@ -19,7 +19,7 @@
 // group) and the rows' O^T is rescaled.
 //
 // Every unit leaves its result to the join kernel (tree_attn.cu).  32 requests
-// of up to 8000 tokens, 16 nodes x 4 heads: 132 us with it, 614 MB (floor 91);
+// of up to 8000 tokens, 16 nodes x 4 heads: 132 us with it, 613 MB (floor 91);
 // inside a unit a 64 KB tile takes 2865 cycles, HBM's rate.
 //
 // Roles: warps 0-7 softmax (thread = token = TMEM lane) and output (thread =

@@ -336,7 +336,11 @@ void dcoco_destroy(dcoco_handle *h);
 typedef struct dcoco_tree_handle dcoco_tree_handle; /* sizes + device workspace */
 
 typedef struct {
-  int max_batch; /* largest batch of any call, 1..4096                         */
+  int max_batch; /* largest batch of any call, 1..4096.  It also says how finely a
+                    request is cut for the attention, whatever the call's batch
+                    (results do not depend on it): one request on a handle for 32
+                    takes 1.4 to 2.7 times as long as on a handle for one, four
+                    1.1 to 1.5 times as long as on a handle for four         */
   int max_tree;  /* most nodes of a tree, 1..256                               */
   int q_heads;   /* query heads, a multiple of kv_heads, <= 1024; q_heads / kv_heads <= 128 */
   int kv_heads;  /* K/V heads, >= 1                                            */
@@ -474,10 +478,18 @@ void dcoco_tree_destroy(dcoco_tree_handle *h);
  * mass; +inf takes the whole mass (shared by all +inf).  A row with nothing
  * above -inf gives token -1 and logprob -inf.  A NaN parameter counts as off
  * (u: as 0).
- * The order and the sums do not depend on rows or timing.  A top_k above 512
- * (and below the vocabulary), a border of top_p that more than 1088 tokens share
- * and a row with +inf are served by a slower form (16 rows of
- * 151936: 0.3 to 1 ms).
+ * The order and the sums do not depend on rows or timing.  Masses are sums in
+ * units of 2^-40 of the largest token's: what lies below half a unit may count
+ * as none.  A temperature in (0, 1e-30) counts as 1e-30.
+ * Some rows are served by a slower form (16 rows of 151936: 0.3 to 1 ms in place
+ * of 0.03):
+ *   a top_k below the vocabulary and above 512, or above the row's 16-byte
+ *     vectors with a finite logit (vocabularies above 1088);
+ *   a border of top_p that more than 1088 tokens share, or one of top_k with more
+ *     than 1088 tokens above and at it;
+ *   with either, tokens masked with a finite value far below the others (-1e4,
+ *     the type's lowest): mask with -inf;
+ *   +inf, or without top_k a largest logit past 1e38 temperatures.
  * One launch, no workspace.  rows == 0 is a no-op.  Errors: EINVAL (null or
  * misaligned pointers, vocab outside 1..2^20, stride, dtype, rows < 0), ECUDA. */
 int dcoco_sample(int rows, int vocab, const void *logits, int dtype, int64_t row_stride,
