@@ -68,7 +68,10 @@ EXPORTED = ("dcoco_version", "dcoco_status_string", "dcoco_create", "dcoco_weigh
             "dcoco_topk_noalloc_plan", "dcoco_verify_stochastic", "dcoco_host_range_covers",
             "dcoco_tree_create", "dcoco_tree_attention", "dcoco_tree_commit", "dcoco_tree_status",
             "dcoco_tree_launches", "dcoco_tree_destroy", "dcoco_sample", "dcoco_distill_loss",
-            "dcoco_distill_grad", "dcoco_distill_step")
+            "dcoco_distill_grad", "dcoco_distill_step", "dcoco_tree_create_quant", "dcoco_tree_attention_quant",
+            "dcoco_tree_commit_quant", "dcoco_tree_append_quant", "dcoco_pages_create", "dcoco_pages_reserve",
+            "dcoco_pages_fork", "dcoco_pages_free", "dcoco_pages_compact", "dcoco_pages_status",
+            "dcoco_pages_launches", "dcoco_pages_destroy")
 
 DCOCO_BF16, DCOCO_FP16, DCOCO_FP32 = 0, 1, 2
 _DTYPE = {torch.bfloat16: DCOCO_BF16, torch.float16: DCOCO_FP16, torch.float32: DCOCO_FP32}
@@ -97,6 +100,31 @@ class dcoco_tree_commit_args(C.Structure):
                 + _strided("k_new", "l", "n", "t", "h") + _strided("v_new", "l", "n", "t", "h")
                 + _strided("k_cache", "l", "page", "token", "h") + _strided("v_cache", "l", "page", "token", "h")
                 + [("num_pages", C.c_int), ("layers", C.c_int)])
+
+
+class dcoco_quant_scales(C.Structure):
+    _fields_ = _strided("k_scale", "l", "page", "block", "h") + _strided("v_scale", "l", "page", "block", "h")
+
+
+class dcoco_tree_append_args(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("first", "ctx_len", "page_table")] + [("page_table_stride", C.c_int64)]
+                + _strided("k_new", "l", "t", "h") + _strided("v_new", "l", "t", "h")
+                + _strided("k_cache", "l", "page", "token", "h") + _strided("v_cache", "l", "page", "token", "h")
+                + [("num_pages", C.c_int), ("layers", C.c_int), ("tokens", C.c_int)])
+
+
+class dcoco_pages_config(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("num_pages", "page_size", "max_pages", "max_rows")]
+
+
+class dcoco_pages_state(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("page_table_stride", C.c_int64), ("held", C.c_void_p),
+                ("len", C.c_void_p), ("refs", C.c_void_p)]
+
+
+class dcoco_page_plane(C.Structure):
+    _fields_ = [("base", C.c_void_p), ("layer_stride", C.c_int64), ("page_stride", C.c_int64),
+                ("page_bytes", C.c_int64), ("layers", C.c_int)]
 
 
 def _load():
@@ -144,6 +172,20 @@ def _load():
     L.dcoco_tree_launches.restype = C.c_longlong
     L.dcoco_tree_destroy.argtypes = [P]
     L.dcoco_tree_destroy.restype = None
+    L.dcoco_tree_create_quant.argtypes = [C.POINTER(dcoco_tree_config), I, C.POINTER(P)]
+    L.dcoco_tree_attention_quant.argtypes = [P, I, I, P, P, P, P, P]
+    L.dcoco_tree_commit_quant.argtypes = [P, I, I, P, P, P, P, P, P, P]
+    L.dcoco_tree_append_quant.argtypes = [P, I, P, P, P, P]
+    L.dcoco_pages_create.argtypes = [C.POINTER(dcoco_pages_config), C.POINTER(P)]
+    L.dcoco_pages_reserve.argtypes = [P, P, I, P, P, P, P]
+    L.dcoco_pages_fork.argtypes = [P, P, I, P, I, P, P, P, P]
+    L.dcoco_pages_free.argtypes = [P, P, I, P, P]
+    L.dcoco_pages_compact.argtypes = [P, P, I, P, P, I64, P, P, P]
+    L.dcoco_pages_status.argtypes = [P]
+    L.dcoco_pages_launches.argtypes = [P]
+    L.dcoco_pages_launches.restype = C.c_longlong
+    L.dcoco_pages_destroy.argtypes = [P]
+    L.dcoco_pages_destroy.restype = None
     L.dcoco_sample.argtypes = [I, I, P, I, I64, P, P, P, P, P, P, P, P]
     teacher = [I, I, P, I, I64, I, P, P, P, F]
     L.dcoco_distill_loss.argtypes = teacher + [P, P, P]
@@ -372,6 +414,7 @@ assert _ATTENTION_ARGS.size == C.sizeof(dcoco_tree_attention_args) and _COMMIT_A
 class _TreeHandle(C.c_void_p):
     """A dcoco_tree_handle and the sizes it was made for."""
     sizes: tuple = ()
+    scale_tokens: int = 0  # of a cache in 8 bits; 0: in 16
 
 
 def dcoco_tree_create(max_batch: int, max_tree: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
@@ -444,6 +487,109 @@ def dcoco_tree_commit(handle, batch: int, tokens, parents, sampled, k_new, v_new
                                   _stream(stream)), "dcoco_tree_commit")
 
 
+# the same on a cache in 8 bits
+_E4M3 = torch.float8_e4m3fn
+_SCALES = struct.Struct("@" + "P4q" * 2)
+_APPEND_ARGS = struct.Struct("@3Pq" + "P3q" * 2 + "P4q" * 2 + "iii0q")
+assert _SCALES.size == C.sizeof(dcoco_quant_scales) and _APPEND_ARGS.size == C.sizeof(dcoco_tree_append_args)
+
+
+def dcoco_tree_create_quant(max_batch: int, max_tree: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
+                            max_pages: int, scale_tokens: int, dtype: torch.dtype = torch.bfloat16) -> _TreeHandle:
+    """As dcoco_tree_create, for a cache of torch.float8_e4m3fn with an fp32 scale for each block of scale_tokens
+    tokens and K/V head; dtype is that of q, the nodes' K/V and the outputs."""
+    cfg = dcoco_tree_config(max_batch, max_tree, q_heads, kv_heads, head_dim, page_size, max_pages,
+                            _DTYPE.get(dtype, -1))
+    h = _TreeHandle()
+    _check(_lib.dcoco_tree_create_quant(C.byref(cfg), scale_tokens, C.byref(h)), "dcoco_tree_create_quant")
+    h.sizes, h.scale_tokens = (q_heads, kv_heads, head_dim, page_size, max_pages, dtype), scale_tokens
+    return h
+
+
+def _blocks(handle, what: str) -> int:
+    """Scales of a page; refuses a handle for a cache in 16 bits."""
+    if not handle.scale_tokens:
+        raise DcocoError(DCOCO_EUNSUPPORTED, what)
+    return handle.sizes[3] // handle.scale_tokens
+
+
+def _scales(k_scale, v_scale, shape: tuple) -> bytes:
+    """k_scale and v_scale of that shape ([layers,] pages, blocks, kv_heads), any positive strides."""
+    packed = []
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype is not torch.float32 or not t.is_cuda or t.shape != shape:
+            raise ValueError(f"{name} must be a CUDA fp32 tensor of shape {tuple(shape)}")
+        packed += [t.data_ptr(), *((0,) if len(shape) == 3 else ()), *t.stride()]
+    return _SCALES.pack(*packed)
+
+
+def dcoco_tree_attention_quant(handle, batch: int, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, page_table,
+                               ctx_len, *, out, tree_mask=None, tree_len=None, lse=None, scale: float | None = None,
+                               stream=None) -> None:
+    """dcoco_tree_attention on k_cache and v_cache of torch.float8_e4m3fn (strides multiples of 16) with k_scale and
+    v_scale fp32 [pages, page_size / scale_tokens, kv_heads]."""
+    blocks = _blocks(handle, "dcoco_tree_attention_quant")
+    hq, hkv, d, page, max_pages, dt = handle.sizes
+    nodes, pages = q.shape[1], k_cache.shape[0]
+    new, pool, one, i32 = (batch, nodes, hkv, d), (pages, page, hkv, d), (batch,), torch.int32
+    mask_ptr = mask_stride = 0
+    if tree_mask is not None:
+        words = (nodes + 31) // 32
+        shared = tree_mask.shape[0] == 1 and batch != 1
+        mask_ptr = _dense(tree_mask, "tree_mask", (1 if shared else batch, nodes, words), i32)
+        mask_stride = 0 if shared else nodes * words
+    args = _ATTENTION_ARGS.pack(
+        *_heads(q, "q", (batch, nodes, hq, d), dt), *_heads(k_new, "k_new", new, dt),
+        *_heads(v_new, "v_new", new, dt), *_heads(k_cache, "k_cache", pool, _E4M3),
+        *_heads(v_cache, "v_cache", pool, _E4M3), *_page_table(page_table, batch, max_pages),
+        _dense(ctx_len, "ctx_len", one, i32), _dense_or_none(tree_len, "tree_len", one, i32),
+        mask_ptr, mask_stride, pages, d ** -0.5 if scale is None else scale)
+    _check(_lib.dcoco_tree_attention_quant(
+        handle, batch, nodes, args, _scales(k_scale, v_scale, (pages, blocks, hkv)),
+        _dense(out, "out", (batch, nodes, hq, d), dt), _dense_or_none(lse, "lse", (batch, nodes, hq), torch.float32),
+        _stream(stream)), "dcoco_tree_attention_quant")
+
+
+def dcoco_tree_commit_quant(handle, batch: int, tokens, parents, sampled, k_new, v_new, k_cache, v_cache, k_scale,
+                            v_scale, page_table, ctx_len, *, path, accept_len, next_token, new_len, tree_len=None,
+                            stream=None) -> None:
+    """dcoco_tree_commit into k_cache and v_cache of torch.float8_e4m3fn with k_scale and v_scale fp32
+    [layers, pages, page_size / scale_tokens, kv_heads], both written."""
+    blocks = _blocks(handle, "dcoco_tree_commit_quant")
+    _, hkv, d, page, max_pages, dt = handle.sizes
+    nodes, layers, pages = tokens.shape[1], k_cache.shape[0], k_cache.shape[1]
+    i32, tree, one = torch.int32, (batch, nodes), (batch,)
+    new, pool = (layers, batch, nodes, hkv, d), (layers, pages, page, hkv, d)
+    args = _COMMIT_ARGS.pack(
+        _dense(tokens, "tokens", tree, i32), _dense(parents, "parents", tree, i32),
+        _dense(sampled, "sampled", tree, i32), _dense_or_none(tree_len, "tree_len", one, i32),
+        _dense(ctx_len, "ctx_len", one, i32), *_page_table(page_table, batch, max_pages),
+        *_heads(k_new, "k_new", new, dt), *_heads(v_new, "v_new", new, dt),
+        *_heads(k_cache, "k_cache", pool, _E4M3), *_heads(v_cache, "v_cache", pool, _E4M3), pages, layers)
+    _check(_lib.dcoco_tree_commit_quant(
+        handle, batch, nodes, args, _scales(k_scale, v_scale, (layers, pages, blocks, hkv)),
+        _dense(path, "path", tree, i32), _dense(accept_len, "accept_len", one, i32),
+        _dense(next_token, "next_token", one, i32), _dense(new_len, "new_len", one, i32), _stream(stream)),
+        "dcoco_tree_commit_quant")
+
+
+def dcoco_tree_append_quant(handle, batch: int, first, k_new, v_new, k_cache, v_cache, k_scale, v_scale, page_table,
+                            ctx_len, *, new_len, stream=None) -> None:
+    """Append ragged prompts: request n's tokens are rows first[n] .. first[n + 1] - 1 of k_new and v_new
+    [layers, rows, kv_heads, D]; first int32 [batch + 1], ctx_len and new_len int32 [batch], the rest as above."""
+    blocks = _blocks(handle, "dcoco_tree_append_quant")
+    _, hkv, d, page, max_pages, dt = handle.sizes
+    layers, pages, rows = k_cache.shape[0], k_cache.shape[1], k_new.shape[1]
+    i32, one, new, pool = torch.int32, (batch,), (layers, rows, hkv, d), (layers, pages, page, hkv, d)
+    args = _APPEND_ARGS.pack(
+        _dense(first, "first", (batch + 1,), i32), _dense(ctx_len, "ctx_len", one, i32),
+        *_page_table(page_table, batch, max_pages), *_heads(k_new, "k_new", new, dt), *_heads(v_new, "v_new", new, dt),
+        *_heads(k_cache, "k_cache", pool, _E4M3), *_heads(v_cache, "v_cache", pool, _E4M3), pages, layers, rows)
+    _check(_lib.dcoco_tree_append_quant(handle, batch, args, _scales(k_scale, v_scale, (layers, pages, blocks, hkv)),
+                                        _dense(new_len, "new_len", one, i32), _stream(stream)),
+           "dcoco_tree_append_quant")
+
+
 def dcoco_tree_status(handle) -> int:
     return _lib.dcoco_tree_status(handle)
 
@@ -454,6 +600,108 @@ def dcoco_tree_launches(handle) -> int:
 
 def dcoco_tree_destroy(handle) -> None:
     _lib.dcoco_tree_destroy(handle)
+
+
+# ------------------------------------------------------------------ a cache's pages
+_POOL_STATE = struct.Struct("@PqPPP")
+_PLANE = struct.Struct("@PqqqiI")
+assert _POOL_STATE.size == C.sizeof(dcoco_pages_state) and _PLANE.size == C.sizeof(dcoco_page_plane)
+
+
+class _PagesHandle(C.c_void_p):
+    """A dcoco_pages_handle and the sizes it was made for."""
+    sizes: tuple = ()
+
+
+def dcoco_pages_create(num_pages: int, page_size: int, max_pages: int, max_rows: int) -> _PagesHandle:
+    """Handle of the page calls for one pool; see include/dcoco.h."""
+    cfg = dcoco_pages_config(num_pages, page_size, max_pages, max_rows)
+    h = _PagesHandle()
+    _check(_lib.dcoco_pages_create(C.byref(cfg), C.byref(h)), "dcoco_pages_create")
+    h.sizes = (num_pages, max_pages, max_rows)
+    return h
+
+
+class page_planes:
+    """The tensors whose pages are copied with the pool's: [layers, pages, ...] each, what one page has of a layer
+    contiguous in any order of its axes.  Keeps the tensors; make it once for a cache."""
+
+    def __init__(self, tensors):
+        self.tensors, self.pages, packed = tuple(tensors), set(), []
+        for t in self.tensors:
+            if not t.is_cuda or t.dim() < 3:
+                raise ValueError("a plane must be a CUDA tensor [layers, pages, ...]")
+            inner, dense = sorted(zip(t.stride()[2:], t.shape[2:])), 1
+            for stride, n in inner:
+                if n > 1 and stride != dense:
+                    raise ValueError("what a page has of a layer must be contiguous")
+                dense *= n
+            size = t.element_size()
+            self.pages.add(t.shape[1])
+            packed.append(_PLANE.pack(t.data_ptr(), t.stride(0) * size, t.stride(1) * size, dense * size, t.shape[0], 0))
+        if len(self.pages) > 1:
+            raise ValueError("the planes must have the same number of pages")
+        self.count, self.packed = len(packed), b"".join(packed)
+
+
+def _pool_state(handle, page_table, held, lens, refs) -> bytes:
+    pages, max_pages, rows = handle.sizes
+    i32 = torch.int32
+    return _POOL_STATE.pack(*_page_table(page_table, rows, max_pages), _dense(held, "held", (rows,), i32),
+                            _dense_or_none(lens, "lens", (rows,), i32), _dense(refs, "refs", (pages,), i32))
+
+
+def _planes_for(handle, planes) -> tuple:
+    if planes.count and planes.pages != {handle.sizes[0]}:
+        raise ValueError(f"the planes must have {handle.sizes[0]} pages")
+    return planes.count, planes.packed
+
+
+def dcoco_pages_reserve(handle, rows, tokens, page_table, held, refs, *, done=None, stream=None) -> None:
+    """Give each listed row pages for so many tokens.  rows, tokens and done int32 [count]; the pool's state:
+    page_table int32 [max_rows, >= max_pages], held int32 [max_rows], refs int32 [num_pages]."""
+    n, i32 = rows.shape, torch.int32
+    _check(_lib.dcoco_pages_reserve(handle, _pool_state(handle, page_table, held, None, refs), n[0],
+                                    _dense(rows, "rows", n, i32), _dense(tokens, "tokens", n, i32),
+                                    _dense_or_none(done, "done", n, i32), _stream(stream)), "dcoco_pages_reserve")
+
+
+def dcoco_pages_fork(handle, planes, src, dst, page_table, held, lens, refs, *, done=None, stream=None) -> None:
+    """Rows dst become copies of rows src (int32 [count]): full pages shared, the partly filled one copied in all
+    planes.  lens int32 [max_rows]: the rows' tokens."""
+    n, i32 = src.shape, torch.int32
+    _check(_lib.dcoco_pages_fork(handle, _pool_state(handle, page_table, held, lens, refs), *_planes_for(handle, planes),
+                                 n[0], _dense(src, "src", n, i32), _dense(dst, "dst", n, i32),
+                                 _dense_or_none(done, "done", n, i32), _stream(stream)), "dcoco_pages_fork")
+
+
+def dcoco_pages_free(handle, rows, page_table, held, lens, refs, *, stream=None) -> None:
+    """The listed rows (int32 [count]) hold nothing any more."""
+    _check(_lib.dcoco_pages_free(handle, _pool_state(handle, page_table, held, lens, refs), rows.shape[0],
+                                 _dense(rows, "rows", rows.shape, torch.int32), _stream(stream)), "dcoco_pages_free")
+
+
+def dcoco_pages_compact(handle, planes, page_table, held, refs, *, live, page_table_out=None, refs_out=None,
+                        stream=None) -> None:
+    """Move the pages in use to the front.  live int32 [1]; page_table_out and refs_out: the state's own where None."""
+    table_out, refs_to = page_table if page_table_out is None else page_table_out, refs if refs_out is None else refs_out
+    pages, max_pages, rows = handle.sizes
+    _check(_lib.dcoco_pages_compact(handle, _pool_state(handle, page_table, held, None, refs),
+                                    *_planes_for(handle, planes), *_page_table(table_out, rows, max_pages),
+                                    _dense(refs_to, "refs_out", (pages,), torch.int32),
+                                    _dense(live, "live", (1,), torch.int32), _stream(stream)), "dcoco_pages_compact")
+
+
+def dcoco_pages_status(handle) -> int:
+    return _lib.dcoco_pages_status(handle)
+
+
+def dcoco_pages_launches(handle) -> int:
+    return int(_lib.dcoco_pages_launches(handle))
+
+
+def dcoco_pages_destroy(handle) -> None:
+    _lib.dcoco_pages_destroy(handle)
 
 
 def _logit_rows(logits, name: str = "logits") -> tuple:
@@ -594,6 +842,93 @@ class TreeVerifier:
 
     def status(self) -> int:
         return dcoco_tree_status(self.handle)
+
+
+class QuantTreeVerifier(TreeVerifier):
+    """A TreeVerifier on a cache in 8 bits: torch.float8_e4m3fn with an fp32 scale for each block of scale_tokens
+    tokens and K/V head, [layers, pages, page_size / scale_tokens, kv_heads].  append() takes prompts."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, max_pages: int, max_batch: int = 32,
+                 max_tree: int = 64, dtype: torch.dtype = torch.bfloat16, scale_tokens: int = 16):
+        self.handle = dcoco_tree_create_quant(max_batch, max_tree, q_heads, kv_heads, head_dim, page_size, max_pages,
+                                              scale_tokens, dtype)
+
+    def attention(self, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, page_table, ctx_len, tree_mask=None,
+                  tree_len=None, scale=None, stream=None):
+        """-> (out [N, T, q_heads, D], lse [N, T, q_heads]); the cache and scales of one layer."""
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        dcoco_tree_attention_quant(self.handle, q.shape[0], q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                   page_table, ctx_len, out=out, tree_mask=tree_mask, tree_len=tree_len, lse=lse,
+                                   scale=scale, stream=stream)
+        return out, lse
+
+    def commit(self, tokens, parents, sampled, k_new, v_new, k_cache, v_cache, k_scale, v_scale, page_table, ctx_len,
+               tree_len=None, stream=None):
+        """-> dict(path [N, T], accept_len [N], next_token [N], new_len [N]); the caches and scales are written."""
+        n, t = tokens.shape
+        out = {"path": torch.empty(n, t, dtype=torch.int32, device=tokens.device)}
+        for name in ("accept_len", "next_token", "new_len"):
+            out[name] = torch.empty(n, dtype=torch.int32, device=tokens.device)
+        dcoco_tree_commit_quant(self.handle, n, tokens, parents, sampled, k_new, v_new, k_cache, v_cache, k_scale,
+                                v_scale, page_table, ctx_len, tree_len=tree_len, stream=stream, **out)
+        return out
+
+    def append(self, first, k_new, v_new, k_cache, v_cache, k_scale, v_scale, page_table, ctx_len, stream=None):
+        """Rows first[n] .. first[n + 1] - 1 of k_new and v_new [layers, rows, kv_heads, D] onto request n. -> new_len [N]"""
+        new_len = torch.empty_like(ctx_len)
+        dcoco_tree_append_quant(self.handle, ctx_len.shape[0], first, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                page_table, ctx_len, new_len=new_len, stream=stream)
+        return new_len
+
+
+class PagePool:
+    """A pool of pages for max_rows sequences: owns a handle and the state (table [max_rows, max_pages], held, lens
+    [max_rows], refs [num_pages], all int32), and copies the pages of `planes` (tensors [layers, pages, ...])."""
+
+    def __init__(self, planes, page_size: int, max_pages: int, max_rows: int):
+        self.planes = page_planes(planes)
+        first = self.planes.tensors[0]
+        i32 = dict(dtype=torch.int32, device=first.device)
+        self.handle = dcoco_pages_create(first.shape[1], page_size, max_pages, max_rows)
+        self.table = torch.zeros(max_rows, max_pages, **i32)
+        self.held, self.lens = torch.zeros(max_rows, **i32), torch.zeros(max_rows, **i32)
+        self.refs, self.live = torch.zeros(first.shape[1], **i32), torch.zeros(1, **i32)
+
+    def close(self):
+        if getattr(self, "handle", None) is not None:
+            dcoco_pages_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def reserve(self, rows, tokens, stream=None):
+        """-> done [count]: 1 where the row has pages for so many tokens."""
+        done = torch.empty_like(rows)
+        dcoco_pages_reserve(self.handle, rows, tokens, self.table, self.held, self.refs, done=done, stream=stream)
+        return done
+
+    def fork(self, src, dst, stream=None):
+        """-> done [count]: 1 where row dst is a copy of row src."""
+        done = torch.empty_like(src)
+        dcoco_pages_fork(self.handle, self.planes, src, dst, self.table, self.held, self.lens, self.refs, done=done,
+                         stream=stream)
+        return done
+
+    def free(self, rows, stream=None):
+        dcoco_pages_free(self.handle, rows, self.table, self.held, self.lens, self.refs, stream=stream)
+
+    def compact(self, stream=None):
+        """-> live [1], the pages in use: 0 .. live - 1 from then on."""
+        dcoco_pages_compact(self.handle, self.planes, self.table, self.held, self.refs, live=self.live, stream=stream)
+        return self.live
+
+    def status(self) -> int:
+        return dcoco_pages_status(self.handle)
 
 
 # ------------------------------------------------------------------ convenience wrapper

@@ -15,6 +15,8 @@ enum : int {
   kErrTimeout = 2,          // a bounded wait inside a kernel expired
   kErrBadLength = 4,        // a context or tree length was out of range
   kErrBadPage = 8,          // a page number was outside the pool, or a position past the page table
+  kErrBadRow = 16,          // a pool's row was out of range, named twice, or not in the state the call needs
+  kErrNoPages = 32,         // a pool had too few free pages
 };
 
 // ---- bf16 bit helpers ------------------------------------------------------

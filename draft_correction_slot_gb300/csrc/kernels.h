@@ -260,6 +260,45 @@ struct TreeCommitParams {
 };
 cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t st);
 
+// ---------------------------------------------------------------- K/V in 8 bits
+// Attention over a cache of e4m3 payloads with fp32 scales.  The cache and
+// workspace fields of `t` are not used.
+struct QuantAttnParams {
+  TreeAttnParams t;
+  const uint8_t *k_cache, *v_cache;
+  int64_t kc_sp, kc_st, kc_sh, vc_sp, vc_st, vc_sh;
+  const float *k_scale, *v_scale;  // [page][block][kv head]
+  int64_t ks_sp, ks_sb, ks_sh, vs_sp, vs_sb, vs_sh;
+  int scale_shift;                 // tokens of a block: 1 << scale_shift
+};
+cudaError_t launch_quant_attention(const QuantAttnParams &p, cudaStream_t st);
+
+// Tokens' K/V into such a cache: a tree's accepted path, or ragged prompts.
+struct QuantWriteParams {
+  const uint16_t *k_new, *v_new;
+  int64_t kn_sl, kn_sn, kn_st, kn_sh, vn_sl, vn_sn, vn_st, vn_sh;
+  uint8_t *k_cache, *v_cache;
+  int64_t kc_sl, kc_sp, kc_st, kc_sh, vc_sl, vc_sp, vc_st, vc_sh;
+  float *k_scale, *v_scale;
+  int64_t ks_sl, ks_sp, ks_sb, ks_sh, vs_sl, vs_sp, vs_sb, vs_sh;
+  const int32_t *ctx_len, *page_table;
+  int64_t pt_stride;
+  int num_pages, max_pages, page_shift, scale_shift, layers;
+  int N, kv_heads, head_dim;
+  bool f16;
+  int *err;
+  int32_t *new_len;
+  // the tree's path
+  const int32_t *tokens, *parents, *sampled, *tree_len;
+  int T;
+  int32_t *path, *accept_len, *next_token;
+  // prompts: rows first[n] .. first[n + 1] - 1 of `total`
+  const int32_t *first;
+  int total;
+};
+cudaError_t launch_quant_commit(const QuantWriteParams &p, cudaStream_t st);
+cudaError_t launch_quant_append(const QuantWriteParams &p, cudaStream_t st);
+
 // ---------------------------------------------------------------- sampling
 // See dcoco_sample.  `f32`: fp32 logits, else bf16.
 struct SampleParams {

@@ -1,6 +1,6 @@
 // tree.cu -- C ABI of the tree calls (declared in include/dcoco.h): handle,
-// argument checks and launches of tree attention and tree commit, and the
-// handle-free sampling and distillation entries.
+// argument checks and launches of tree attention and tree commit, over a cache
+// in 16 or in 8 bits, and the handle-free sampling and distillation entries.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -18,6 +18,7 @@ struct dcoco_tree_handle {
   // rows, and of the other by the number of row tiles
   int few_chunks = 0;
   uint8_t many_chunks[257] = {};
+  int scale_shift = -1;               // cache in 8 bits: tokens of a scale's block; -1: cache in 16 bits
   void *block = nullptr;              // one device allocation: status word, partial results
   int *err = nullptr;
   float2 *part_ml = nullptr;
@@ -32,11 +33,14 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool good(const void *p) { return p && aligned16(p); }
 // Strides of axes with these extents: multiples of 8 elements (16 bytes), and
 // positive where the axis has more than one entry.
-bool steps8(std::initializer_list<int64_t> strides, std::initializer_list<int> extents) {
+bool steps(int unit, std::initializer_list<int64_t> strides, std::initializer_list<int> extents) {
   const int *n = extents.begin();
   for (int64_t s : strides)
-    if (*n++ > 1 && (s <= 0 || s % 8 != 0 || s >= (1ll << 39))) return false;
+    if (*n++ > 1 && (s <= 0 || s % unit != 0 || s >= (1ll << 39))) return false;
   return true;
+}
+bool steps8(std::initializer_list<int64_t> strides, std::initializer_list<int> extents) {
+  return steps(8, strides, extents);
 }
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? DCOCO_OK : DCOCO_ECUDA; }
 
@@ -107,17 +111,116 @@ int check_distill(int rows, int vocab, const void *logits, int dtype, int64_t ro
   return DCOCO_OK;
 }
 
+// The arguments of either attention call; `unit`: what the cache's strides are
+// multiples of (16 bytes).
+int check_attention(const dcoco_tree_config &c, int batch, int nodes, const dcoco_tree_attention_args *a, const void *out,
+                    int unit) {
+  if (batch < 0 || batch > c.max_batch) return DCOCO_EBATCH;
+  if (nodes < 0 || nodes > c.max_tree) return DCOCO_EINVAL;
+  if (batch == 0 || nodes == 0) return DCOCO_OK;
+  if (!good(a->q) || !good(a->k_new) || !good(a->v_new) || !good(a->k_cache) || !good(a->v_cache) || !good(out) ||
+      !a->page_table || !a->ctx_len)
+    return DCOCO_EINVAL;
+  if (!steps8({a->q_stride_n, a->q_stride_t, a->q_stride_h}, {batch, nodes, c.q_heads}) ||
+      !steps8({a->k_new_stride_n, a->k_new_stride_t, a->k_new_stride_h}, {batch, nodes, c.kv_heads}) ||
+      !steps8({a->v_new_stride_n, a->v_new_stride_t, a->v_new_stride_h}, {batch, nodes, c.kv_heads}) ||
+      !steps(unit, {a->k_cache_stride_page, a->k_cache_stride_token, a->k_cache_stride_h},
+             {a->num_pages, c.page_size, c.kv_heads}) ||
+      !steps(unit, {a->v_cache_stride_page, a->v_cache_stride_token, a->v_cache_stride_h},
+             {a->num_pages, c.page_size, c.kv_heads}))
+    return DCOCO_EINVAL;
+  if (a->num_pages < 1 || a->page_table_stride < c.max_pages || a->tree_mask_stride_n < 0 || !std::isfinite(a->scale))
+    return DCOCO_EINVAL;
+  return DCOCO_OK;
+}
+
+// What both attention calls take from their arguments: all but the cache, the
+// row tiles, chunks and workspace.
+void fill_attention(const dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_attention_args *a, void *out,
+                    float *lse, dc::TreeAttnParams *to) {
+  const dcoco_tree_config &c = h->cfg;
+  dc::TreeAttnParams &p = *to;
+  p.q = (const uint16_t *)a->q, p.k_new = (const uint16_t *)a->k_new, p.v_new = (const uint16_t *)a->v_new;
+  p.q_sn = a->q_stride_n, p.q_st = a->q_stride_t, p.q_sh = a->q_stride_h;
+  p.kn_sn = a->k_new_stride_n, p.kn_st = a->k_new_stride_t, p.kn_sh = a->k_new_stride_h;
+  p.vn_sn = a->v_new_stride_n, p.vn_st = a->v_new_stride_t, p.vn_sh = a->v_new_stride_h;
+  p.page_table = a->page_table, p.pt_stride = a->page_table_stride;
+  p.ctx_len = a->ctx_len, p.tree_len = a->tree_len, p.tree_mask = a->tree_mask, p.mask_sn = a->tree_mask_stride_n;
+  p.num_pages = a->num_pages, p.max_pages = c.max_pages, p.page_shift = h->page_shift;
+  p.N = batch, p.T = nodes, p.kv_heads = c.kv_heads, p.group = c.q_heads / c.kv_heads, p.head_dim = c.head_dim;
+  p.f16 = c.dtype == DCOCO_FP16;
+  p.scale = a->scale;
+  p.out = (uint16_t *)out, p.lse = lse, p.err = h->err;
+}
+
+// The arguments of either commit call.
+int check_commit(const dcoco_tree_config &c, int batch, int nodes, const dcoco_tree_commit_args *a, const int32_t *path,
+                 const int32_t *accept_len, const int32_t *next_token, const int32_t *new_len, int unit) {
+  if (batch < 0 || batch > c.max_batch) return DCOCO_EBATCH;
+  if (nodes < 0 || nodes > c.max_tree) return DCOCO_EINVAL;
+  if (batch == 0 || nodes == 0) return DCOCO_OK;
+  if (!a->tokens || !a->parents || !a->sampled || !a->ctx_len || !a->page_table || !path || !accept_len ||
+      !next_token || !new_len || !good(a->k_new) || !good(a->v_new) || !good(a->k_cache) || !good(a->v_cache))
+    return DCOCO_EINVAL;
+  if (!steps8({a->k_new_stride_l, a->k_new_stride_n, a->k_new_stride_t, a->k_new_stride_h},
+              {a->layers, batch, nodes, c.kv_heads}) ||
+      !steps8({a->v_new_stride_l, a->v_new_stride_n, a->v_new_stride_t, a->v_new_stride_h},
+              {a->layers, batch, nodes, c.kv_heads}) ||
+      !steps(unit, {a->k_cache_stride_l, a->k_cache_stride_page, a->k_cache_stride_token, a->k_cache_stride_h},
+             {a->layers, a->num_pages, c.page_size, c.kv_heads}) ||
+      !steps(unit, {a->v_cache_stride_l, a->v_cache_stride_page, a->v_cache_stride_token, a->v_cache_stride_h},
+             {a->layers, a->num_pages, c.page_size, c.kv_heads}))
+    return DCOCO_EINVAL;
+  if (a->num_pages < 1 || a->layers < 1 || a->layers > 65535 || a->page_table_stride < c.max_pages ||
+      new_len == a->ctx_len)
+    return DCOCO_EINVAL;
+  return DCOCO_OK;
+}
+
+// The scales of a cache held in 8 bits: any order of strides.
+bool good_scales(const dcoco_quant_scales *s, int layers, int pages, int blocks, int heads) {
+  return s && s->k_scale && s->v_scale &&
+         steps(1, {s->k_scale_stride_l, s->k_scale_stride_page, s->k_scale_stride_block, s->k_scale_stride_h},
+               {layers, pages, blocks, heads}) &&
+         steps(1, {s->v_scale_stride_l, s->v_scale_stride_page, s->v_scale_stride_block, s->v_scale_stride_h},
+               {layers, pages, blocks, heads});
+}
+
+// What commit and append take alike from their arguments.
+template <class Args>
+void fill_quant_write(const dcoco_tree_handle *h, int batch, const Args *a, const dcoco_quant_scales *s, int32_t *new_len,
+                      dc::QuantWriteParams *to) {
+  const dcoco_tree_config &c = h->cfg;
+  dc::QuantWriteParams &p = *to;
+  p.k_new = (const uint16_t *)a->k_new, p.v_new = (const uint16_t *)a->v_new;
+  p.kn_sl = a->k_new_stride_l, p.kn_st = a->k_new_stride_t, p.kn_sh = a->k_new_stride_h;
+  p.vn_sl = a->v_new_stride_l, p.vn_st = a->v_new_stride_t, p.vn_sh = a->v_new_stride_h;
+  p.k_cache = (uint8_t *)a->k_cache, p.v_cache = (uint8_t *)a->v_cache;
+  p.kc_sl = a->k_cache_stride_l, p.kc_sp = a->k_cache_stride_page;
+  p.kc_st = a->k_cache_stride_token, p.kc_sh = a->k_cache_stride_h;
+  p.vc_sl = a->v_cache_stride_l, p.vc_sp = a->v_cache_stride_page;
+  p.vc_st = a->v_cache_stride_token, p.vc_sh = a->v_cache_stride_h;
+  p.k_scale = s->k_scale, p.v_scale = s->v_scale;
+  p.ks_sl = s->k_scale_stride_l, p.ks_sp = s->k_scale_stride_page;
+  p.ks_sb = s->k_scale_stride_block, p.ks_sh = s->k_scale_stride_h;
+  p.vs_sl = s->v_scale_stride_l, p.vs_sp = s->v_scale_stride_page;
+  p.vs_sb = s->v_scale_stride_block, p.vs_sh = s->v_scale_stride_h;
+  p.ctx_len = a->ctx_len, p.page_table = a->page_table, p.pt_stride = a->page_table_stride;
+  p.num_pages = a->num_pages, p.max_pages = c.max_pages, p.page_shift = h->page_shift, p.scale_shift = h->scale_shift;
+  p.layers = a->layers, p.N = batch, p.kv_heads = c.kv_heads, p.head_dim = c.head_dim;
+  p.f16 = c.dtype == DCOCO_FP16;
+  p.err = h->err, p.new_len = new_len;
+}
+
 }  // namespace
 
 extern "C" {
 
-int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
-  if (!out) return DCOCO_EINVAL;
-  const int rc = validate_tree_config(cfg);
-  if (rc != DCOCO_OK) return rc;
+static int create(const dcoco_tree_config *cfg, int scale_shift, dcoco_tree_handle **out) {
   dcoco_tree_handle *h = new (std::nothrow) dcoco_tree_handle();
   if (!h) return DCOCO_ENOMEM;
   h->cfg = *cfg;
+  h->scale_shift = scale_shift;
   while ((1 << h->page_shift) < cfg->page_size) ++h->page_shift;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
@@ -166,41 +269,36 @@ int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
   return DCOCO_OK;
 }
 
+int dcoco_tree_create(const dcoco_tree_config *cfg, dcoco_tree_handle **out) {
+  if (!out) return DCOCO_EINVAL;
+  const int rc = validate_tree_config(cfg);
+  return rc != DCOCO_OK ? rc : create(cfg, -1, out);
+}
+
+int dcoco_tree_create_quant(const dcoco_tree_config *cfg, int scale_tokens, dcoco_tree_handle **out) {
+  if (!out) return DCOCO_EINVAL;
+  const int rc = validate_tree_config(cfg);
+  if (rc != DCOCO_OK) return rc;
+  if (scale_tokens < 16 || scale_tokens > cfg->page_size || (scale_tokens & (scale_tokens - 1)) != 0)
+    return DCOCO_EUNSUPPORTED;
+  int shift = 0;
+  while ((1 << shift) < scale_tokens) ++shift;
+  return create(cfg, shift, out);
+}
+
 int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_attention_args *a,
                          void *out, float *lse, void *stream) {
   if (!h || !a) return DCOCO_EINVAL;
+  if (h->scale_shift >= 0) return DCOCO_EUNSUPPORTED;
   const dcoco_tree_config &c = h->cfg;
-  if (batch < 0 || batch > c.max_batch) return DCOCO_EBATCH;
-  if (nodes < 0 || nodes > c.max_tree) return DCOCO_EINVAL;
+  const int rc = check_attention(c, batch, nodes, a, out, 8);
+  if (rc != DCOCO_OK) return rc;
   if (batch == 0 || nodes == 0) return DCOCO_OK;
-  if (!good(a->q) || !good(a->k_new) || !good(a->v_new) || !good(a->k_cache) || !good(a->v_cache) || !good(out) ||
-      !a->page_table || !a->ctx_len)
-    return DCOCO_EINVAL;
-  if (!steps8({a->q_stride_n, a->q_stride_t, a->q_stride_h}, {batch, nodes, c.q_heads}) ||
-      !steps8({a->k_new_stride_n, a->k_new_stride_t, a->k_new_stride_h}, {batch, nodes, c.kv_heads}) ||
-      !steps8({a->v_new_stride_n, a->v_new_stride_t, a->v_new_stride_h}, {batch, nodes, c.kv_heads}) ||
-      !steps8({a->k_cache_stride_page, a->k_cache_stride_token, a->k_cache_stride_h},
-              {a->num_pages, c.page_size, c.kv_heads}) ||
-      !steps8({a->v_cache_stride_page, a->v_cache_stride_token, a->v_cache_stride_h},
-              {a->num_pages, c.page_size, c.kv_heads}))
-    return DCOCO_EINVAL;
-  if (a->num_pages < 1 || a->page_table_stride < c.max_pages || a->tree_mask_stride_n < 0 || !std::isfinite(a->scale))
-    return DCOCO_EINVAL;
   dc::TreeAttnParams p;
-  p.q = (const uint16_t *)a->q, p.k_new = (const uint16_t *)a->k_new, p.v_new = (const uint16_t *)a->v_new;
+  fill_attention(h, batch, nodes, a, out, lse, &p);
   p.k_cache = (const uint16_t *)a->k_cache, p.v_cache = (const uint16_t *)a->v_cache;
-  p.q_sn = a->q_stride_n, p.q_st = a->q_stride_t, p.q_sh = a->q_stride_h;
-  p.kn_sn = a->k_new_stride_n, p.kn_st = a->k_new_stride_t, p.kn_sh = a->k_new_stride_h;
-  p.vn_sn = a->v_new_stride_n, p.vn_st = a->v_new_stride_t, p.vn_sh = a->v_new_stride_h;
   p.kc_sp = a->k_cache_stride_page, p.kc_st = a->k_cache_stride_token, p.kc_sh = a->k_cache_stride_h;
   p.vc_sp = a->v_cache_stride_page, p.vc_st = a->v_cache_stride_token, p.vc_sh = a->v_cache_stride_h;
-  p.page_table = a->page_table, p.pt_stride = a->page_table_stride;
-  p.ctx_len = a->ctx_len, p.tree_len = a->tree_len, p.tree_mask = a->tree_mask, p.mask_sn = a->tree_mask_stride_n;
-  p.num_pages = a->num_pages, p.max_pages = c.max_pages, p.page_shift = h->page_shift;
-  p.N = batch, p.T = nodes, p.kv_heads = c.kv_heads, p.group = c.q_heads / c.kv_heads, p.head_dim = c.head_dim;
-  p.f16 = c.dtype == DCOCO_FP16;
-  p.scale = a->scale;
-  p.out = (uint16_t *)out, p.lse = lse, p.err = h->err;
   const RowTiles rt(c, nodes);
   p.mtiles = rt.mtiles, p.tile_nodes = rt.tile_nodes, p.tile_rows = rt.tile_rows;
   p.part_rows = rt.part_rows, p.few = rt.few;
@@ -216,25 +314,11 @@ int dcoco_tree_attention(dcoco_tree_handle *h, int batch, int nodes, const dcoco
 int dcoco_tree_commit(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_commit_args *a, int32_t *path,
                       int32_t *accept_len, int32_t *next_token, int32_t *new_len, void *stream) {
   if (!h || !a) return DCOCO_EINVAL;
+  if (h->scale_shift >= 0) return DCOCO_EUNSUPPORTED;
   const dcoco_tree_config &c = h->cfg;
-  if (batch < 0 || batch > c.max_batch) return DCOCO_EBATCH;
-  if (nodes < 0 || nodes > c.max_tree) return DCOCO_EINVAL;
+  const int rc = check_commit(c, batch, nodes, a, path, accept_len, next_token, new_len, 8);
+  if (rc != DCOCO_OK) return rc;
   if (batch == 0 || nodes == 0) return DCOCO_OK;
-  if (!a->tokens || !a->parents || !a->sampled || !a->ctx_len || !a->page_table || !path || !accept_len ||
-      !next_token || !new_len || !good(a->k_new) || !good(a->v_new) || !good(a->k_cache) || !good(a->v_cache))
-    return DCOCO_EINVAL;
-  if (!steps8({a->k_new_stride_l, a->k_new_stride_n, a->k_new_stride_t, a->k_new_stride_h},
-              {a->layers, batch, nodes, c.kv_heads}) ||
-      !steps8({a->v_new_stride_l, a->v_new_stride_n, a->v_new_stride_t, a->v_new_stride_h},
-              {a->layers, batch, nodes, c.kv_heads}) ||
-      !steps8({a->k_cache_stride_l, a->k_cache_stride_page, a->k_cache_stride_token, a->k_cache_stride_h},
-              {a->layers, a->num_pages, c.page_size, c.kv_heads}) ||
-      !steps8({a->v_cache_stride_l, a->v_cache_stride_page, a->v_cache_stride_token, a->v_cache_stride_h},
-              {a->layers, a->num_pages, c.page_size, c.kv_heads}))
-    return DCOCO_EINVAL;
-  if (a->num_pages < 1 || a->layers < 1 || a->layers > 65535 || a->page_table_stride < c.max_pages ||
-      new_len == a->ctx_len)
-    return DCOCO_EINVAL;
   dc::TreeCommitParams p;
   p.tokens = a->tokens, p.parents = a->parents, p.sampled = a->sampled, p.tree_len = a->tree_len;
   p.ctx_len = a->ctx_len, p.page_table = a->page_table, p.pt_stride = a->page_table_stride;
@@ -252,6 +336,79 @@ int dcoco_tree_commit(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tr
   h->last_stream = static_cast<cudaStream_t>(stream);
   ++h->launches;
   return cuda_status(dc::launch_tree_commit(p, h->last_stream));
+}
+
+int dcoco_tree_attention_quant(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_attention_args *a,
+                               const dcoco_quant_scales *s, void *out, float *lse, void *stream) {
+  if (!h || !a) return DCOCO_EINVAL;
+  if (h->scale_shift < 0) return DCOCO_EUNSUPPORTED;
+  const dcoco_tree_config &c = h->cfg;
+  const int rc = check_attention(c, batch, nodes, a, out, 16);
+  if (rc != DCOCO_OK) return rc;
+  if (batch == 0 || nodes == 0) return DCOCO_OK;
+  if (!good_scales(s, 1, a->num_pages, c.page_size >> h->scale_shift, c.kv_heads)) return DCOCO_EINVAL;
+  dc::QuantAttnParams p;
+  fill_attention(h, batch, nodes, a, out, lse, &p.t);
+  p.k_cache = (const uint8_t *)a->k_cache, p.v_cache = (const uint8_t *)a->v_cache;
+  p.kc_sp = a->k_cache_stride_page, p.kc_st = a->k_cache_stride_token, p.kc_sh = a->k_cache_stride_h;
+  p.vc_sp = a->v_cache_stride_page, p.vc_st = a->v_cache_stride_token, p.vc_sh = a->v_cache_stride_h;
+  p.k_scale = s->k_scale, p.v_scale = s->v_scale;
+  p.ks_sp = s->k_scale_stride_page, p.ks_sb = s->k_scale_stride_block, p.ks_sh = s->k_scale_stride_h;
+  p.vs_sp = s->v_scale_stride_page, p.vs_sb = s->v_scale_stride_block, p.vs_sh = s->v_scale_stride_h;
+  p.scale_shift = h->scale_shift;
+  h->last_stream = static_cast<cudaStream_t>(stream);
+  ++h->launches;
+  return cuda_status(dc::launch_quant_attention(p, h->last_stream));
+}
+
+int dcoco_tree_commit_quant(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_commit_args *a,
+                            const dcoco_quant_scales *s, int32_t *path, int32_t *accept_len, int32_t *next_token,
+                            int32_t *new_len, void *stream) {
+  if (!h || !a) return DCOCO_EINVAL;
+  if (h->scale_shift < 0) return DCOCO_EUNSUPPORTED;
+  const dcoco_tree_config &c = h->cfg;
+  const int rc = check_commit(c, batch, nodes, a, path, accept_len, next_token, new_len, 16);
+  if (rc != DCOCO_OK) return rc;
+  if (batch == 0 || nodes == 0) return DCOCO_OK;
+  if (!good_scales(s, a->layers, a->num_pages, c.page_size >> h->scale_shift, c.kv_heads)) return DCOCO_EINVAL;
+  dc::QuantWriteParams p = {};
+  fill_quant_write(h, batch, a, s, new_len, &p);
+  p.kn_sn = a->k_new_stride_n, p.vn_sn = a->v_new_stride_n;
+  p.tokens = a->tokens, p.parents = a->parents, p.sampled = a->sampled, p.tree_len = a->tree_len;
+  p.T = nodes, p.path = path, p.accept_len = accept_len, p.next_token = next_token;
+  h->last_stream = static_cast<cudaStream_t>(stream);
+  ++h->launches;
+  return cuda_status(dc::launch_quant_commit(p, h->last_stream));
+}
+
+int dcoco_tree_append_quant(dcoco_tree_handle *h, int batch, const dcoco_tree_append_args *a, const dcoco_quant_scales *s,
+                            int32_t *new_len, void *stream) {
+  if (!h || !a) return DCOCO_EINVAL;
+  if (h->scale_shift < 0) return DCOCO_EUNSUPPORTED;
+  const dcoco_tree_config &c = h->cfg;
+  if (batch < 0 || batch > c.max_batch) return DCOCO_EBATCH;
+  if (a->tokens < 0) return DCOCO_EINVAL;
+  if (batch == 0) return DCOCO_OK;
+  if (!a->first || !a->ctx_len || !a->page_table || !new_len || !good(a->k_cache) || !good(a->v_cache) ||
+      (a->tokens > 0 && (!good(a->k_new) || !good(a->v_new))))
+    return DCOCO_EINVAL;
+  if (!steps8({a->k_new_stride_l, a->k_new_stride_t, a->k_new_stride_h}, {a->layers, a->tokens, c.kv_heads}) ||
+      !steps8({a->v_new_stride_l, a->v_new_stride_t, a->v_new_stride_h}, {a->layers, a->tokens, c.kv_heads}) ||
+      !steps(16, {a->k_cache_stride_l, a->k_cache_stride_page, a->k_cache_stride_token, a->k_cache_stride_h},
+             {a->layers, a->num_pages, c.page_size, c.kv_heads}) ||
+      !steps(16, {a->v_cache_stride_l, a->v_cache_stride_page, a->v_cache_stride_token, a->v_cache_stride_h},
+             {a->layers, a->num_pages, c.page_size, c.kv_heads}))
+    return DCOCO_EINVAL;
+  if (a->num_pages < 1 || a->layers < 1 || a->layers > 32767 || a->page_table_stride < c.max_pages ||
+      new_len == a->ctx_len)
+    return DCOCO_EINVAL;
+  if (!good_scales(s, a->layers, a->num_pages, c.page_size >> h->scale_shift, c.kv_heads)) return DCOCO_EINVAL;
+  dc::QuantWriteParams p = {};
+  fill_quant_write(h, batch, a, s, new_len, &p);
+  p.first = a->first, p.total = a->tokens;
+  h->last_stream = static_cast<cudaStream_t>(stream);
+  ++h->launches;
+  return cuda_status(dc::launch_quant_append(p, h->last_stream));
 }
 
 int dcoco_tree_status(dcoco_tree_handle *h) {

@@ -460,6 +460,164 @@ long long dcoco_tree_launches(const dcoco_tree_handle *h);
 /* NULL is allowed.  Synchronises the device before freeing. */
 void dcoco_tree_destroy(dcoco_tree_handle *h);
 
+/* ====================================================================
+ * The same on a cache in 8 bits: K and V as e4m3 (sign, 4 bits of exponent, 3
+ * of mantissa; largest 448; no infinities, 0x7F and 0xFF are NaN), with one fp32
+ * scale for each block of tokens and K/V head: value = payload x scale.
+ * q, the nodes' own K/V and the outputs keep the handle's 16-bit type.
+ * ==================================================================== */
+
+/* Scales of K and V (device pointers), [layer][page][block][kv head], block b of a
+ * page being its tokens b * scale_tokens .. ; strides in elements, positive (any
+ * value where the axis has one entry).  Positive and finite.  The attention
+ * takes one layer's (the stride of layers is not used). */
+typedef struct {
+  float *k_scale;
+  int64_t k_scale_stride_l, k_scale_stride_page, k_scale_stride_block, k_scale_stride_h;
+  float *v_scale;
+  int64_t v_scale_stride_l, v_scale_stride_page, v_scale_stride_block, v_scale_stride_h;
+} dcoco_quant_scales;
+
+/* As dcoco_tree_create, for a cache in 8 bits whose scales cover scale_tokens
+ * tokens: a power of two, 16..page_size (else EUNSUPPORTED).  On such a handle
+ * dcoco_tree_attention and _commit answer EUNSUPPORTED, and the _quant calls do so on
+ * a handle for 16 bits; status, launches and destroy are the same calls. */
+int dcoco_tree_create_quant(const dcoco_tree_config *cfg, int scale_tokens, dcoco_tree_handle **out);
+
+/* dcoco_tree_attention with k_cache and v_cache in 8 bits; their strides are
+ * multiples of 16 (elements, one byte each).  All else as there. */
+int dcoco_tree_attention_quant(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_attention_args *in,
+                               const dcoco_quant_scales *scales, void *out, float *lse, void *stream);
+
+/* How tokens enter the cache (commit and append).  Of a block's new tokens let a
+ * be the largest finite magnitude of K (or V) in the head, and need the least power of
+ * two with a <= 448 need, within 2^-64 .. 2^64 (2^-64 for a = 0).
+ *   scale = need if the block holds no committed token, else the larger of need
+ *   and the block's scale; a payload is x / scale rounded to nearest even, the
+ *   committed tokens' are rounded anew where the scale has grown (a power of two
+ *   from these calls grows by powers of two: only what falls below e4m3's least
+ *   step, 2^-9, is lost then).  Infinities and NaN become NaN and do not count for a.
+ * Committed are the positions below ctx_len: what a page holds past them has no
+ * part in this and is left as it is. */
+
+/* dcoco_tree_commit into a cache in 8 bits; the caches' strides are multiples of 16. */
+int dcoco_tree_commit_quant(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_commit_args *in,
+                            const dcoco_quant_scales *scales, int32_t *path, int32_t *accept_len, int32_t *next_token,
+                            int32_t *new_len, void *stream);
+
+/* Inputs of dcoco_tree_append_quant (device pointers; strides as above). */
+typedef struct {
+  const int32_t *first;   /* [n + 1] request n's tokens are rows first[n] .. first[n + 1] - 1 */
+  const int32_t *ctx_len; /* [n] tokens committed before */
+  const int32_t *page_table;
+  int64_t page_table_stride;
+  const void *k_new; /* [layer][row][kv head] */
+  int64_t k_new_stride_l, k_new_stride_t, k_new_stride_h;
+  const void *v_new;
+  int64_t v_new_stride_l, v_new_stride_t, v_new_stride_h;
+  void *k_cache; /* [layer][page][token][kv head] */
+  int64_t k_cache_stride_l, k_cache_stride_page, k_cache_stride_token, k_cache_stride_h;
+  void *v_cache;
+  int64_t v_cache_stride_l, v_cache_stride_page, v_cache_stride_token, v_cache_stride_h;
+  int num_pages;
+  int layers;
+  int tokens; /* rows of k_new and v_new */
+} dcoco_tree_append_args;
+
+/* Append prompts, or pieces of them: request n's rows go to cache positions
+ * ctx_len[n] .. of every layer.  Any number of tokens (max_tree does not matter).
+ *   new_len: int32 [batch], ctx_len + the request's rows; not ctx_len itself (EINVAL)
+ * The rows follow from one another: first does not decrease and stays within
+ * 0..tokens.  A request whose rows or lengths do not (or would not fit its page
+ * table) is left out, new_len = ctx_len (clamped), and recorded in the status word, as is a
+ * page outside the pool, whose tokens are not written.  No page may belong to
+ * two requests.  One launch.  Errors: as dcoco_tree_commit; tokens < 0: EINVAL;
+ * layers outside 1..32767: EINVAL. */
+int dcoco_tree_append_quant(dcoco_tree_handle *h, int batch, const dcoco_tree_append_args *in,
+                            const dcoco_quant_scales *scales, int32_t *new_len, void *stream);
+
+/* ====================================================================
+ * The pages of a cache, in 16 or 8 bits.  A pool's state is in the caller's device
+ * arrays; the handle has sizes and a workspace.  A page is free when nobody holds
+ * it (count 0), and free pages are given out lowest first, so that results depend
+ * on the state and the call alone.  Stream-ordered, no allocation, no
+ * synchronisation; one handle's calls are ordered as a tree handle's.
+ * ==================================================================== */
+
+typedef struct dcoco_pages_handle dcoco_pages_handle;
+
+typedef struct {
+  int num_pages; /* 1..2^20 */
+  int page_size; /* tokens, >= 1 */
+  int max_pages; /* page-table entries of a row, >= 1; max_pages * page_size at most 2^30 */
+  int max_rows;  /* rows (sequences), 1..2^20; also the most rows of a call's lists */
+} dcoco_pages_config;
+
+/* Device pointers. */
+typedef struct {
+  int32_t *page_table;       /* [max_rows][max_pages] */
+  int64_t page_table_stride; /* entries, >= max_pages */
+  int32_t *held;             /* [max_rows] entries that the row holds: pages page_table[row][0 .. held - 1] */
+  int32_t *len;              /* [max_rows] tokens of the row (reserve and compact do not use it) */
+  int32_t *refs;             /* [num_pages] holders of each page */
+} dcoco_pages_state;
+
+/* A tensor whose pages are copied with the pool's (K, V, their scales): `layers`
+ * times num_pages pages of page_bytes contiguous bytes.  All in bytes and multiples of 4
+ * (of 16: copied in wider steps); pages do not overlap. */
+#define DCOCO_MAX_PLANES 64
+typedef struct {
+  void *base;
+  int64_t layer_stride, page_stride; /* any value where there is one layer, or one page */
+  int64_t page_bytes;                /* 4..2^30 */
+  int layers;                        /* 1..65536 */
+} dcoco_page_plane;
+
+/* Errors: EINVAL (sizes), ENOMEM, ECUDA.  Workspace: some 24 bytes a page, 28 a row. */
+int dcoco_pages_create(const dcoco_pages_config *cfg, dcoco_pages_handle **out);
+
+/* Give rows[i] pages for tokens[i] tokens (no fewer than it holds: nothing is given
+ * back), in the list's order.  A row gets all that it lacks or nothing: where the free
+ * pages run out it gets nothing, nor does any row after it that lacks some.
+ *   done: int32 [count], 1 where the row now has its pages, else 0; NULL = not wanted
+ * A row out of range, named before in the list, or asked for more than max_pages gets
+ * nothing.  Such rows and missing pages are recorded in the status word.
+ * Errors (of all calls below): EINVAL (null pointers, strides, planes), EBATCH (count
+ * outside 0..max_rows), ECUDA.  count == 0 is a no-op. */
+int dcoco_pages_reserve(dcoco_pages_handle *h, const dcoco_pages_state *s, int count, const int32_t *rows,
+                        const int32_t *tokens, int32_t *done, void *stream);
+
+/* Row dst[i] becomes a copy of row src[i]: it holds the pages that src's tokens fill
+ * (their counts grow), and a page of its own with a copy of the one that they
+ * fill in part.  Pages that src holds past its tokens are its own.  dst rows hold
+ * nothing before (free them first); a row may be the source of many.
+ *   done: as above
+ * A fork gets nothing where dst[i] holds pages, is named before or is a source in
+ * the same call, where a row is out of range, and where free pages run out (in
+ * the list's order); recorded in the status word. */
+int dcoco_pages_fork(dcoco_pages_handle *h, const dcoco_pages_state *s, int planes_count, const dcoco_page_plane *planes,
+                     int count, const int32_t *src, const int32_t *dst, int32_t *done, void *stream);
+
+/* The rows hold nothing any more (held = len = 0, counts go down); a row named twice
+ * is freed once.  Their table entries are left as they are. */
+int dcoco_pages_free(dcoco_pages_handle *h, const dcoco_pages_state *s, int count, const int32_t *rows, void *stream);
+
+/* Move the pages in use to the front: with `live` of them, those from page live on go,
+ * in order, to the free pages below it, in order.  table_out gets the held entries
+ * renumbered (others are not written), refs_out the counts; both may be the state's own
+ * arrays (the same stride) or overlap them nowhere.  live: int32 [1].  Page numbers kept
+ * elsewhere than in held entries are not renumbered. */
+int dcoco_pages_compact(dcoco_pages_handle *h, const dcoco_pages_state *s, int planes_count,
+                        const dcoco_page_plane *planes, int32_t *table_out, int64_t table_out_stride, int32_t *refs_out,
+                        int32_t *live, void *stream);
+
+/* As dcoco_tree_status, _launches and _destroy.  DCOCO_EDEVICE: a call named rows
+ * that it could not serve, a table entry outside the pool or to a page that
+ * nobody holds, or free pages ran out. */
+int dcoco_pages_status(dcoco_pages_handle *h);
+long long dcoco_pages_launches(const dcoco_pages_handle *h);
+void dcoco_pages_destroy(dcoco_pages_handle *h);
+
 /* One token per row from the target's logits, with random numbers that the
  * caller draws.  logits: [rows][row_stride] of dtype DCOCO_BF16 or DCOCO_FP32,
  * the first `vocab` of each row; 16-byte aligned, row_stride >= vocab a

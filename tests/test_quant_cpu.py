@@ -1,0 +1,102 @@
+"""CPU checks of the calls on a cache in 8 bits and of its pages: refusals before
+any CUDA call, and the references against what defines them."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+import quant_ref
+
+
+@pytest.fixture(scope="module")
+def dc():
+    import __graft_entry__
+    __graft_entry__.build()
+    import draft_correction_slot_gb300 as dc
+    return dc
+
+
+GOOD = dict(max_batch=4, max_tree=16, q_heads=8, kv_heads=2, head_dim=128, page_size=64, max_pages=8, scale_tokens=32)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(max_batch=0), -1), (dict(max_tree=257), -1), (dict(q_heads=9), -1), (dict(max_pages=1 << 25), -1),
+    (dict(head_dim=96), -2), (dict(page_size=24), -2), (dict(dtype=None), -2), (dict(scale_tokens=0), -2),
+    (dict(scale_tokens=8), -2), (dict(scale_tokens=24), -2), (dict(scale_tokens=128), -2), (dict(scale_tokens=-32), -2),
+])
+def test_create_refuses_without_cuda(dc, kw, status):
+    with pytest.raises(dc.DcocoError) as e:
+        dc.dcoco_tree_create_quant(**{**GOOD, **kw})
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("kw", [dict(num_pages=0), dict(num_pages=(1 << 20) + 1), dict(page_size=0), dict(max_pages=0),
+                                dict(max_rows=0), dict(max_rows=(1 << 20) + 1), dict(page_size=1 << 20, max_pages=1 << 11)])
+def test_pages_create_refuses_without_cuda(dc, kw):
+    with pytest.raises(dc.DcocoError) as e:
+        dc.dcoco_pages_create(**{**dict(num_pages=8, page_size=16, max_pages=4, max_rows=2), **kw})
+    assert e.value.status == -1
+
+
+def test_null_handles(dc):
+    lib = dc.lib()
+    assert lib.dcoco_tree_create_quant(None, 16, None) == -1
+    assert lib.dcoco_tree_attention_quant(None, 1, 1, None, None, None, None, None) == -1
+    assert lib.dcoco_tree_commit_quant(None, 1, 1, None, None, None, None, None, None, None) == -1
+    assert lib.dcoco_tree_append_quant(None, 1, None, None, None, None) == -1
+    assert lib.dcoco_pages_create(None, None) == -1
+    assert lib.dcoco_pages_reserve(None, None, 1, None, None, None, None) == -1
+    assert lib.dcoco_pages_fork(None, None, 0, None, 1, None, None, None, None) == -1
+    assert lib.dcoco_pages_free(None, None, 1, None, None) == -1
+    assert lib.dcoco_pages_compact(None, None, 0, None, None, 8, None, None, None) == -1
+    assert lib.dcoco_pages_status(None) == -1
+    assert lib.dcoco_pages_launches(None) == -1
+    lib.dcoco_pages_destroy(None)
+
+
+def test_exported_names(dc):
+    lib = C.CDLL(dc.LIB_PATH)
+    for n in dc.EXPORTED:
+        assert hasattr(lib, n) and callable(getattr(dc, n))
+
+
+def test_python_checks(dc):
+    import torch
+    with pytest.raises(ValueError):
+        dc.page_planes([torch.zeros(2, 4, 8)])  # not on the GPU
+    h = dc._TreeHandle()
+    h.sizes = (1, 1, 64, 16, 1, torch.bfloat16)  # a handle for a cache in 16 bits
+    x = torch.zeros(1, 1, 1, 64)
+    for call in (lambda: dc.dcoco_tree_attention_quant(h, 1, x, x, x, x, x, x, x, x, x, out=x),
+                 lambda: dc.dcoco_tree_append_quant(h, 1, x, x, x, x, x, x, x, x, x, new_len=x)):
+        with pytest.raises(dc.DcocoError) as e:
+            call()
+        assert e.value.status == -2
+
+
+def test_reference_rounding():
+    """Every e4m3 value is its own nearest, midpoints go to the even one, as torch's conversion has it."""
+    import torch
+    codes = torch.arange(256, dtype=torch.uint8)
+    vals = codes.view(torch.float8_e4m3fn).double().numpy()
+    ok = np.isfinite(vals)
+    assert (quant_ref.e4m3(vals[ok]) == vals[ok]).all()
+    rng = np.random.default_rng(1)
+    x = np.concatenate([rng.standard_normal(20000) * np.exp2(rng.integers(-12, 8, 20000)), (vals[ok][1:] + vals[ok][:-1]) / 2])
+    x = np.clip(x, -448, 448).astype(np.float32)
+    assert (quant_ref.e4m3(x) == torch.from_numpy(x).to(torch.float8_e4m3fn).double().numpy()).all()
+    assert np.isnan(quant_ref.e4m3([np.inf, -np.inf, np.nan])).all()
+    assert quant_ref.need(448.0) == 1 and quant_ref.need(448.5) == 2 and quant_ref.need(0.0) == 2.0 ** -64
+    assert quant_ref.need(3e38) == 2.0 ** 64 and quant_ref.need(1e-30) == 2.0 ** -64
+
+
+def test_reference_pool():
+    p = quant_ref.Pool(6, 4, 3, 4)
+    assert p.reserve([1, 0, 1, 9], [9, 4, 4, 1]) == [1, 1, 0, 0] and p.table[1] == [0, 1, 2] and p.table[0] == [3]
+    p.lens[:2] = [4, 9]
+    p.cache = list("abcdef")
+    assert p.fork([1, 0, 1], [2, 3, 2]) == [1, 1, 0]
+    assert p.table[2] == [0, 1, 4] and p.cache[4] == "c" and p.table[3] == [3] and p.refs == [2, 2, 1, 2, 1, 0]
+    p.free([1, 0, 1])
+    assert p.refs == [1, 1, 0, 1, 1, 0]
+    assert p.compact() == 4 and p.table[2] == [0, 1, 2] and p.cache[2] == "c" and p.refs == [1, 1, 1, 1, 0, 0]
