@@ -261,8 +261,12 @@ struct TreeCommitParams {
 cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t st);
 
 // ---------------------------------------------------------------- K/V in 8 bits
-// Attention over a cache of e4m3 payloads with fp32 scales.  The cache and
-// workspace fields of `t` are not used.
+// Attention over a cache of e4m3 payloads with fp32 scales.  Of `t` the cache,
+// the row tiles and the workspace are not used: rows here are (node, query head
+// of the K/V head) in one sequence, in tiles of kQuantRows (one tile, padded to
+// quant_rows, where they are fewer).
+constexpr int kQuantRows = 64;
+inline int quant_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kQuantRows; }
 struct QuantAttnParams {
   TreeAttnParams t;
   const uint8_t *k_cache, *v_cache;
@@ -270,7 +274,22 @@ struct QuantAttnParams {
   const float *k_scale, *v_scale;  // [page][block][kv head]
   int64_t ks_sp, ks_sb, ks_sh, vs_sp, vs_sb, vs_sh;
   int scale_shift;                 // tokens of a block: 1 << scale_shift
+  int mtiles, R;                   // row tiles of a K/V head, rows of a tile
+  // chunks of the context (see quant_chunk_tiles), and the most partial results of a
+  // request: its chunks and one for the tree
+  int items, sms, chunk_cap, slots;
+  float *part_o;   // [(n, K/V head, row tile)][slots][R][head_dim]
+  float2 *part_ml; // [...][slots][R] (log2 reference, sum)
 };
+// Tiles of a chunk for a context of nt tiles: as tree_chunk_tiles, but at most
+// kTreeMaxChunks - 1 chunks, so that with the tree's there are kTreeMaxChunks.
+__host__ __device__ inline int quant_chunk_tiles(int nt, int items, int sms, int cap) {
+  const long long want = ((long long)nt * items + sms - 1) / sms;
+  int c = want < cap ? (int)want : cap;
+  const int least = (nt + kTreeMaxChunks - 2) / (kTreeMaxChunks - 1);
+  if (c < least) c = least;
+  return c < 1 ? 1 : c;
+}
 cudaError_t launch_quant_attention(const QuantAttnParams &p, cudaStream_t st);
 
 // Tokens' K/V into such a cache: a tree's accepted path, or ragged prompts.

@@ -18,6 +18,7 @@ struct dcoco_tree_handle {
   // rows, and of the other by the number of row tiles
   int few_chunks = 0;
   uint8_t many_chunks[257] = {};
+  uint8_t quant_slots[513] = {};      // cache in 8 bits: partial results of a request, by row tiles
   int scale_shift = -1;               // cache in 8 bits: tokens of a scale's block; -1: cache in 16 bits
   void *block = nullptr;              // one device allocation: status word, partial results
   int *err = nullptr;
@@ -96,6 +97,18 @@ int most_chunks(int64_t max_tiles, int items, int sms, int cap) {
   int most = max_tiles > scan ? dc::kTreeMaxChunks : 1;
   for (int nt = 1; nt <= scan; ++nt) {
     const int per = dc::tree_chunk_tiles(nt, items, sms, cap), n = (nt + per - 1) / per;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
+// The same for the attention on a cache in 8 bits, whose tiles take half the time.
+int quant_chunk_cap(const dcoco_tree_config &c) { return c.max_batch == 1 ? 1 << 30 : 16; }
+int most_quant_chunks(int64_t max_tiles, int items, int sms, int cap) {
+  const int64_t scan = max_tiles < 64 * dc::kTreeMaxChunks ? max_tiles : 64 * dc::kTreeMaxChunks;
+  int most = max_tiles > scan ? dc::kTreeMaxChunks - 1 : 1;
+  for (int nt = 1; nt <= scan; ++nt) {
+    const int per = dc::quant_chunk_tiles(nt, items, sms, cap), n = (nt + per - 1) / per;
     if (n > most) most = n;
   }
   return most;
@@ -243,10 +256,21 @@ static int create(const dcoco_tree_config *cfg, int scale_shift, dcoco_tree_hand
     if (r > rows) rows = r;
   };
   const int few_nodes = 64 / group, tile_nodes = 128 / group;
-  if (few_nodes >= 1) reach(few_nodes < cfg->max_tree ? few_nodes : cfg->max_tree);
-  for (int nodes = tile_nodes; nodes - tile_nodes < cfg->max_tree; nodes += tile_nodes)
-    if (!RowTiles(*cfg, nodes < cfg->max_tree ? nodes : cfg->max_tree).few)
-      reach(nodes < cfg->max_tree ? nodes : cfg->max_tree);
+  if (scale_shift >= 0) {
+    const int64_t ctx_tiles = ((int64_t)cfg->page_size * cfg->max_pages + dc::kTreeTile - 1) / dc::kTreeTile;
+    const int most_rows = cfg->max_tree * group, most_tiles = (most_rows + dc::kQuantRows - 1) / dc::kQuantRows;
+    for (int m = 1; m <= most_tiles; ++m) {
+      const int n = most_quant_chunks(ctx_tiles, pairs * m, h->sms, quant_chunk_cap(*cfg)) + 1;
+      h->quant_slots[m] = (uint8_t)n;
+      const size_t r = (size_t)pairs * m * n * (m > 1 ? dc::kQuantRows : dc::quant_rows(most_rows));
+      if (r > rows) rows = r;
+    }
+  } else {
+    if (few_nodes >= 1) reach(few_nodes < cfg->max_tree ? few_nodes : cfg->max_tree);
+    for (int nodes = tile_nodes; nodes - tile_nodes < cfg->max_tree; nodes += tile_nodes)
+      if (!RowTiles(*cfg, nodes < cfg->max_tree ? nodes : cfg->max_tree).few)
+        reach(nodes < cfg->max_tree ? nodes : cfg->max_tree);
+  }
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t at_ml = 256, at_o = at_ml + up(rows * sizeof(float2));
   const size_t bytes = at_o + rows * cfg->head_dim * sizeof(float);
@@ -356,8 +380,13 @@ int dcoco_tree_attention_quant(dcoco_tree_handle *h, int batch, int nodes, const
   p.ks_sp = s->k_scale_stride_page, p.ks_sb = s->k_scale_stride_block, p.ks_sh = s->k_scale_stride_h;
   p.vs_sp = s->v_scale_stride_page, p.vs_sb = s->v_scale_stride_block, p.vs_sh = s->v_scale_stride_h;
   p.scale_shift = h->scale_shift;
+  const int rows = nodes * p.t.group;
+  p.mtiles = (rows + dc::kQuantRows - 1) / dc::kQuantRows, p.R = dc::quant_rows(rows);
+  p.items = c.max_batch * c.kv_heads * p.mtiles, p.sms = h->sms, p.chunk_cap = quant_chunk_cap(c);
+  p.slots = h->quant_slots[p.mtiles];
+  p.part_o = reinterpret_cast<float *>(h->part_o), p.part_ml = h->part_ml;
   h->last_stream = static_cast<cudaStream_t>(stream);
-  ++h->launches;
+  h->launches += 2;
   return cuda_status(dc::launch_quant_attention(p, h->last_stream));
 }
 

@@ -41,6 +41,7 @@
 // their loops to the end without waiting or storing, so that their block
 // barriers stay complete.
 #include "launch.h"
+#include "tma_map.h"
 #include "tree_attn.cuh"
 
 namespace dc {
@@ -457,24 +458,6 @@ template <int D, bool F16>
 cudaError_t launch_join(const TreeAttnParams &p, cudaStream_t st) {
   const int rows = p.T * p.kv_heads * p.group;  // at most 256 x 1024 a request
   return launch_ex(k_tree_join<D, F16>, dim3((unsigned)p.N, (unsigned)((rows + 7) / 8)), dim3(256), 0, st, true, 0, p);
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
 }
 
 // A 4D map (column, a, b, c) with element strides of a, b, c and a box of 64
