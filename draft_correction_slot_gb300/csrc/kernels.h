@@ -262,10 +262,10 @@ cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t st);
 
 // ---------------------------------------------------------------- K/V in 8 bits
 // Attention over a cache of e4m3 payloads with fp32 scales.  Of `t` the cache,
-// the row tiles and the workspace are not used: rows here are (node, query head
+// the row tiles (but tree_box) and the workspace are not used: rows here are (node, query head
 // of the K/V head) in one sequence, in tiles of kQuantRows (one tile, padded to
 // quant_rows, where they are fewer).
-constexpr int kQuantRows = 64;
+constexpr int kQuantRows = 64, kQuantNodes = 64;  // (nodes of a tile of the tree)
 inline int quant_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kQuantRows; }
 struct QuantAttnParams {
   TreeAttnParams t;
@@ -275,11 +275,11 @@ struct QuantAttnParams {
   int64_t ks_sp, ks_sb, ks_sh, vs_sp, vs_sb, vs_sh;
   int scale_shift;                 // tokens of a block: 1 << scale_shift
   int mtiles, R;                   // row tiles of a K/V head, rows of a tile
-  // chunks of the context (see quant_chunk_tiles), and the most partial results of a
-  // request: its chunks and one for the tree
+  // chunks of the context (see quant_chunk_tiles), and the most units of a
+  // request: its chunks and the tree; a unit leaves kQuantRows / R partial results
   int items, sms, chunk_cap, slots;
-  float *part_o;   // [(n, K/V head, row tile)][slots][R][head_dim]
-  float2 *part_ml; // [...][slots][R] (log2 reference, sum)
+  float *part_o;   // [(n, K/V head, row tile)][slots][kQuantRows / R][R][head_dim]
+  float2 *part_ml; // the same without head_dim (log2 reference, sum)
 };
 // Tiles of a chunk for a context of nt tiles: as tree_chunk_tiles, but at most
 // kTreeMaxChunks - 1 chunks, so that with the tree's there are kTreeMaxChunks.

@@ -262,7 +262,7 @@ static int create(const dcoco_tree_config *cfg, int scale_shift, dcoco_tree_hand
     for (int m = 1; m <= most_tiles; ++m) {
       const int n = most_quant_chunks(ctx_tiles, pairs * m, h->sms, quant_chunk_cap(*cfg)) + 1;
       h->quant_slots[m] = (uint8_t)n;
-      const size_t r = (size_t)pairs * m * n * (m > 1 ? dc::kQuantRows : dc::quant_rows(most_rows));
+      const size_t r = (size_t)pairs * m * n * dc::kQuantRows;  // (few rows have as many partial results more)
       if (r > rows) rows = r;
     }
   } else {
@@ -382,6 +382,7 @@ int dcoco_tree_attention_quant(dcoco_tree_handle *h, int batch, int nodes, const
   p.scale_shift = h->scale_shift;
   const int rows = nodes * p.t.group;
   p.mtiles = (rows + dc::kQuantRows - 1) / dc::kQuantRows, p.R = dc::quant_rows(rows);
+  p.t.tree_box = nodes < dc::kQuantNodes ? (nodes + 7) / 8 * 8 : dc::kQuantNodes;
   p.items = c.max_batch * c.kv_heads * p.mtiles, p.sms = h->sms, p.chunk_cap = quant_chunk_cap(c);
   p.slots = h->quant_slots[p.mtiles];
   p.part_o = reinterpret_cast<float *>(h->part_o), p.part_ml = h->part_ml;

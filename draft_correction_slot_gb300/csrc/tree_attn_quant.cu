@@ -39,24 +39,29 @@
 namespace dc {
 namespace {
 
-constexpr int kGroup = 128, kSoft = 2 * kGroup;  // softmax threads of a group, of both
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kPrepWarp = 12;
-constexpr int kThreads = 512;  // four warpgroups; warp 11 only completes the third
-// Registers a thread: 128 at launch (65,536 / 512), then 2 x 168 + 2 x 88 = 4 x 128.
-constexpr int kSoftRegs = 168, kOtherRegs = 88;
-constexpr int kTreeNodes = 64;  // nodes of a tree tile
-constexpr int kAhead = 8;       // units whose row factors and odd nodes are kept
+constexpr int kGroup = 128, kGroups = 4;  // softmax threads of a group, groups
+constexpr int kCols = 16;                 // rows of a group
+constexpr int kScoreWarp = 16, kOutWarp = 17, kLoadWarp = 18, kPrepWarp = 19;
+constexpr int kThreads = 640;  // five warpgroups
+// Registers a thread: 96 at launch (65,536 / 640 in steps of 8), then 4 x 104 + 64 = 5 x 96.
+constexpr int kSoftRegs = 104, kOtherRegs = 64;
+constexpr int kTreeNodes = kQuantNodes;  // nodes of a tree tile
+constexpr int kAhead = 16, kUnits = 32;  // units whose row factors and odd nodes are kept; whose description is
 constexpr float kTop = 7.f;     // log2 of a weight at its row's reference
 constexpr float kGrow = kTop + kRescale;  // log2 of the largest weight: 2^15 fits fp16 and e5m2
 
 struct QuantMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v, k_new, v_new;
 };
 
 template <int D, int R, int NP>
 struct Geom8 {
+  // The four softmax groups are teams that take the tiles in turn, R rows of a tile each
+  static constexpr int kTeams = kGroups * kCols / R, kParts = R / kCols;  // teams, groups of a team
+  static constexpr int kNS = 2 * kTeams, kNP = kTeams > 2 ? kTeams : 2;   // buffers of S and of P
   static constexpr uint32_t kTileBytes = kTile * D;        // a context tile of K or V; a tree tile takes the same
-  static constexpr int kNK = D == 64 ? 6 : NP == 3 ? 3 : 4, kNV = D == 64 ? 6 : 4;
+  // K's products run ahead of V's, and a tile's V stays until its weights are there: V's ring is the longer one
+  static constexpr int kNK = D == 64 ? 5 : R == 64 && NP == 3 ? 2 : 3, kNV = D == 64 ? 8 : R == 64 ? 5 : 7;
   static constexpr uint32_t kQPart = R * D, kQBytes = NP * kQPart;
   static constexpr int kPAtoms = (3 * R + 63) / 64;        // 64-byte column blocks of P
   static constexpr uint32_t kPAtom = kTile * 64, kPBytes = kPAtoms * kPAtom;
@@ -64,20 +69,20 @@ struct Geom8 {
   // which have to be shared memory of ours (their results are not used); so do the
   // tree's products over 64 nodes past a K stage
   static constexpr uint32_t kK = 0, kV = kK + kNK * kTileBytes, kP = kV + kNV * kTileBytes;
-  static constexpr uint32_t kQ = kP + 2 * kPBytes, kSmem = kQ + 2 * kQBytes;
-  static constexpr uint32_t kTmem = 8 * R;                 // columns: S^T of even and odd tiles, O^T of even and odd units
-  static constexpr uint32_t kS = 0, kO = 2 * R;
+  static constexpr uint32_t kQ = kP + kNP * kPBytes, kSmem = kQ + 2 * kQBytes;
+  // TMEM columns, all 512: S^T of kNS tiles, O^T of each team's even and odd units
+  static constexpr uint32_t kTmem = 512, kS = 0, kO = kNS * R;
+  static_assert(kO + kTeams * 6 * R == kTmem, "");
+  static_assert(kSmem + 1024 + 9216 <= 232448, "");
   // descriptors' high words: D-byte swizzle for K8, V8, Q8, 64 for P8
   static constexpr uint32_t kHi = D == 128 ? (1024 >> 4) | 1u << 14 | 2u << 29 : (512 >> 4) | 1u << 14 | 4u << 29;
   static constexpr uint32_t kHiP = (512 >> 4) | 1u << 14 | 4u << 29;
 };
 
 struct Bars8 {
-  unsigned long long q_full[2], q_empty[2], k_full[8], k_empty[8], v_full[8], v_empty[8];
-  unsigned long long s_full[2], p_full[2], pv_done[2], o_free[2], factors[kAhead], done;
+  unsigned long long q_empty[2], k_full[8], k_empty[8], v_full[8], v_empty[8];
+  unsigned long long s_full[8], s_free[8], p_full[4], pv_done[4], o_free[kGroups][2], units[kUnits], factors[kAhead], done[2];
 };
-
-constexpr int kVFull = 33;  // arrivals that fill a V stage: TMA's and each lane's scales
 
 // D[tmem] (+)= A[smem] B[smem], 8-bit operands
 template <uint32_t kHiA, uint32_t kHiB>
@@ -102,7 +107,6 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[C]) {
   tmem_st_wait();
 }
 __device__ __forceinline__ void soft_sync(int group) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); }
-__device__ __forceinline__ void prep_sync() { asm volatile("barrier.cta.sync 3, 128;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(int group, bool x) {
   uint32_t r;
   asm volatile(
@@ -145,6 +149,81 @@ __device__ __forceinline__ void warp_col_sums(float (&v)[N], float *dst) {
   for (int k = 0; k < kLeft; ++k) dst[col + k] = v[k];
 }
 
+__device__ __forceinline__ float rcp(float x) {  // within an ulp
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A value that all lanes have alike, in a uniform register: what loops, addresses and descriptors
+// are made of then stays out of the vector registers (a product or copy whose operands come
+// from those took 60 to 140 cycles to issue).
+__device__ __forceinline__ int uni(int x) { return __reduce_max_sync(DC_FULL_MASK, x); }
+// Two fp32 values in one register pair.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 both(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 apart(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// A load of C columns in flight: the registers are the caller's after tmem_wait.
+template <int C>
+__device__ __forceinline__ void tmem_start(uint32_t addr, uint32_t (&r)[C]) {
+#pragma unroll
+  for (int i = 0; i < C; i += 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]),
+                   "=r"(r[i + 6]), "=r"(r[i + 7])
+                 : "r"(addr + i)
+                 : "memory");
+}
+template <int C>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[C]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < C; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
+}
+// bar_wait for up to three barriers at once: their tries overlap.
+__device__ __forceinline__ bool bar_wait3(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc,
+                                          volatile int *abort, int *err) {
+  unsigned long long t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    const bool x = mbar_try(a, pa), y = mbar_try(b, pb), z = mbar_try(c, pc);
+    if (x & y & z) return true;
+    if ((it & 255u) == 0u) {
+      if (*abort) return false;
+      const unsigned long long t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitNs) {
+        *abort = 1;
+        atomicOr(err, kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -166,14 +245,14 @@ __device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32
     h[i] = top_bytes(p);
     const uint32_t r = hsub2(p, h[i]);
     m[i] = top_bytes(r);
-    l[i] = top_bytes(hmul2(hsub2(r, m[i]), 0x58005800u));  // 2^7
+    l[i] = hmul2(hsub2(r, m[i]), 0x58005800u) + 0x00800080u;  // 2^7
   }
   hi = __byte_perm(h[0], h[1], 0x7531), mid = __byte_perm(m[0], m[1], 0x7531), lo = __byte_perm(l[0], l[1], 0x7531);
 }
 
 // ---------------------------------------------------------------- units
 struct QuantUnit {
-  int n, h, mt, slot;        // request, K/V head, row tile, place among the partial results
+  int n, h, mt, slot;        // request, K/V head, row tile, chunk (the tree comes last)
   int ctx, len;              // clamped lengths
   int tile0, ntiles;         // tiles of 128 context tokens, or of 64 nodes (0: no live rows)
   bool tree;
@@ -274,6 +353,35 @@ struct QuantUnits {
   }
 };
 
+// A node's row of V before the product reads it: zeros past the tree's end; a
+// node's infinities and NaN stay out of the product (they would reach nodes that do
+// not see it) and are added to the output of those that do.  Returns whether it had any.
+template <int D, bool F16>
+__device__ __forceinline__ bool clean_node(uint8_t *row, bool there) {
+  bool bad = false;
+#pragma unroll 2
+  for (int e = 0; e < D / 8; ++e) {
+    uint4 *v = reinterpret_cast<uint4 *>(row + (e >> 3) * (kTreeNodes * 128) + (e & 7) * 16);
+    if (!there) {
+      *v = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 x = *v;
+    uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (nonfinite2<F16>(xs[k])) {
+        const bool lo = nonfinite2<F16>(xs[k] & 0xFFFFu), hi = nonfinite2<F16>(xs[k] >> 16);
+        xs[k] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+        any = true;
+      }
+    if (any) *v = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+    bad |= any;
+  }
+  return bad;
+}
+
 template <int D, int R, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
@@ -286,554 +394,652 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(16) float s_factor[kAhead][R];      // score per unit of S, log2 (the row's power of two and p.scale)
+  __shared__ QuantUnit s_unit[kUnits];                     // the block's units in turn; ntiles 0: the end
   __shared__ uint32_t s_odd[kAhead][8];                    // tree units: nodes whose V holds an infinity or NaN
   __shared__ float s_scale[G::kNV][2][8];                  // a V stage's tile: K and V scales of its blocks
-  __shared__ __align__(16) float s_mb[R], s_f[R];          // the rows' references less kTop, and rescale factors
-  __shared__ __align__(16) float s_part[4][R];
-  uint32_t(*const s_word)[R] = reinterpret_cast<uint32_t(*)[R]>(s_part);  // mask words (a tile's step between uses of s_part)
+  // of each group: its rows' references less kTop, rescale factors, and what its warps put together
+  __shared__ __align__(16) float s_mb[kGroups][kCols], s_f[kGroups][kCols], s_part[kGroups][4][kCols];
   const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&b.q_full[i]), 4), mbar_init(smem_u32(&b.q_empty[i]), 1);
-      mbar_init(smem_u32(&b.s_full[i]), 1), mbar_init(smem_u32(&b.p_full[i]), kSoft / 32);
-      mbar_init(smem_u32(&b.pv_done[i]), 1), mbar_init(smem_u32(&b.o_free[i]), kSoft / 32);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&b.q_empty[i]), 1);
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&b.k_full[i]), 1), mbar_init(smem_u32(&b.k_empty[i]), 1);
-      mbar_init(smem_u32(&b.v_full[i]), kVFull), mbar_init(smem_u32(&b.v_empty[i]), 1);
-      mbar_init(smem_u32(&b.factors[i]), 4);
+      mbar_init(smem_u32(&b.v_full[i]), 33), mbar_init(smem_u32(&b.v_empty[i]), 1);
+      mbar_init(smem_u32(&b.s_full[i]), 1), mbar_init(smem_u32(&b.s_free[i]), G::kParts * 4);
     }
-    mbar_init(smem_u32(&b.done), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&b.p_full[i]), G::kParts * 4), mbar_init(smem_u32(&b.pv_done[i]), 1);
+      for (int j = 0; j < 2; ++j) mbar_init(smem_u32(&b.o_free[i][j]), G::kParts * 4);
+    }
+    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&b.factors[i]), 1);
+    for (int i = 0; i < kUnits; ++i) mbar_init(smem_u32(&b.units[i]), 1);
+    mbar_init(smem_u32(&b.done[0]), 1), mbar_init(smem_u32(&b.done[1]), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kLoadWarp && lane == 0) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
-  }
-  if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), G::kTmem);
+  if (tid < kGroups * kCols) s_mb[tid / kCols][tid % kCols] = kNone;
+  if (warp == kLoadWarp && lane < 4)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k + lane)) : "memory");
+  if (warp == kScoreWarp) tmem_alloc(smem_u32(&s_tmem), G::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(DC_FULL_MASK, s_tmem, 0);
-  int g = 0, live = 0;  // tiles and units with tiles that this role has begun
-
   pdl_trigger();
 
-  QuantUnit w;
-  if (warp >= kMmaWarp) {
+  int g = 0;  // tiles that this role has begun
+  // Unit number `unit` as the preparing warp has published it.
+  const auto unit_at = [&](int unit) -> const QuantUnit & { return s_unit[unit & (kUnits - 1)]; };
+  const auto units_bar = [&](int unit) { return smem_u32(&b.units[unit & (kUnits - 1)]); };
+  const auto factors_bar = [&](int unit) { return smem_u32(&b.factors[unit & (kAhead - 1)]); };
+  if (warp >= kScoreWarp) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp >= kPrepWarp) {
-    // ------------------------------------------------------------ Q parts, the tree's K and V
-    QuantUnits it(p, false);
-    const int pt = tid - kPrepWarp * 32;
-    constexpr int kPer = 128 / R;              // threads of a row
-    constexpr int kVecs = D / kPer / 8;        // 16-byte vectors of a thread
-    const int row = pt / kPer, e0 = (pt % kPer) * (D / kPer);
-    const float c = t.scale * kLog2e;
-    bool ok = true;
-    auto wait = [&](unsigned long long *bar, int phase) {
-      if (ok) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(bar), phase & 1, &s_abort, t.err));
-    };
-    while (it.next(w)) {
-      if (w.ntiles == 0) continue;
-      const int qb = live & 1, r = w.mt * R + row, node = r / t.group;
-      const bool there = node < w.len;
-      const uint4 *q = reinterpret_cast<const uint4 *>(t.q + w.n * t.q_sn + (there ? node : 0) * t.q_st +
-                                                       (w.h * t.group + r - node * t.group) * t.q_sh + e0);
-      float most = 0.f;
-      if (!w.tree && there) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          const uint4 x = __ldg(q + i);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            most = fmaxf(most, fmaxf(fabsf(unpack_lo<F16>(u[j])), fabsf(unpack_lo<F16>(u[j] >> 16))));
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < kPer; o <<= 1) most = fmaxf(most, __shfl_xor_sync(DC_FULL_MASK, most, o));
-      // the power of two that brings the row's largest to 128..256 (rows below 2^-100 count as of that size)
-      const int e = max((int)(__float_as_uint(most) >> 23), 27);
-      const float mul = __uint_as_float((uint32_t)(261 - e) << 23);
-      const float factor = w.tree ? c : c * __uint_as_float((uint32_t)min(e - 7, 254) << 23);
-      if (live >= 2) wait(&b.q_empty[qb], (live >> 1) - 1);
-      uint8_t *dst = smem + G::kQ + qb * G::kQBytes;
-#pragma unroll 1
-      for (int i = 0; i < kVecs; ++i) {  // (one at a time: the elements are at hand in L1, registers are not)
-        const uint4 x = there ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-        const int at = e0 + i * 8;
-        if (w.tree) {
-          if (ok)
-            *reinterpret_cast<uint4 *>(dst + (at >> 6) * (R * 128) + row * 128 + ((((at & 63) >> 3) ^ (row & 7)) << 4)) = x;
-          continue;
-        }
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[2 * j] = unpack_lo<F16>(u[j]) * mul, f[2 * j + 1] = unpack_lo<F16>(u[j] >> 16) * mul;
-        uint8_t *d = dst + row * D + (((at >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4) + (at & 8);
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[j] = to_e4m3x2(f[2 * j], f[2 * j + 1]);
-            const float2 y = from_e4m3x2(h[j]);
-            f[2 * j] -= y.x, f[2 * j + 1] -= y.y;
-          }
-          if (ok) *reinterpret_cast<uint2 *>(d + k * G::kQPart) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-        }
-      }
-      if (pt % kPer == 0 && ok) s_factor[live & (kAhead - 1)][row] = factor;
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0 && ok) {
-        mbar_arrive(smem_u32(&b.q_full[qb]));
-        mbar_arrive(smem_u32(&b.factors[live & (kAhead - 1)]));
-      }
-      for (int i = 0; w.tree && i < w.ntiles; ++i) {
-        const int gt = g + i, ks = gt % G::kNK, vs = gt % G::kNV;
-        const int nd = i * kTreeNodes + (pt >> 1), k0 = (pt & 1) * (D / 2);  // a node's half a thread
-        const bool in = nd < w.len;
-        const uint16_t *src[2] = {t.k_new + w.n * t.kn_sn + nd * t.kn_st + w.h * t.kn_sh + k0,
-                                  t.v_new + w.n * t.vn_sn + nd * t.vn_st + w.h * t.vn_sh + k0};
-        uint8_t *dst[2] = {smem + G::kK + ks * G::kTileBytes + (pt >> 1) * 128, smem + G::kV + vs * G::kTileBytes + (pt >> 1) * 128};
-        bool bad = false;
-        if (in) asm volatile("prefetch.global.L2 [%0];" ::"l"(src[1]) : "memory");  // (V's first sectors, under the wait for K)
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          uint4 x[D / 16];
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j)
-            x[j] = in ? __ldg(reinterpret_cast<const uint4 *>(kv ? src[1] : src[0]) + j) : make_uint4(0, 0, 0, 0);
-          // A stage is free when its last tile's product is done.  The products of the unit before come
-          // first: past them the stage's barrier is at most one phase behind, and a parity tells.
-          if (kv == 0 && i == 0 && live > 0) wait(&b.q_empty[(live - 1) & 1], (live - 1) >> 1);
-          if (kv == 0 && gt >= G::kNK) wait(&b.k_empty[ks], gt / G::kNK - 1);
-          if (kv == 1 && gt >= G::kNV) wait(&b.v_empty[vs], gt / G::kNV - 1);
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-            // a node's infinities and NaN in V stay out of the product (they would reach
-            // nodes that do not see it) and are added to the output of those that do
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (kv == 1 && nonfinite2<F16>(xs[k])) {
-                const bool lo = nonfinite2<F16>(xs[k] & 0xFFFFu), hi = nonfinite2<F16>(xs[k] >> 16);
-                xs[k] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
-                bad = true;
-              }
-            const int e = k0 + j * 8;
-            if (ok)
-              *reinterpret_cast<uint4 *>((kv ? dst[1] : dst[0]) + (e >> 6) * (kTreeNodes * 128) +
-                                         ((((e & 63) >> 3) ^ ((pt >> 1) & 7)) << 4)) = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-          }
-        }
-        // (__ballot: two bits a node, gathered to one)
-        uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
-        bits = (bits | bits >> 1) & 0x55555555u;
-        bits = (bits | bits >> 1) & 0x33333333u, bits = (bits | bits >> 2) & 0x0F0F0F0Fu;
-        bits = (bits | bits >> 4) & 0x00FF00FFu, bits = (bits | bits >> 8) & 0xFFFFu;
-        if (lane == 0 && ok) reinterpret_cast<uint16_t *>(s_odd[live & (kAhead - 1)])[i * 4 + (pt >> 5)] = (uint16_t)bits;
-        fence_proxy_async();
-        prep_sync();
-        if (pt == 0 && ok) {
-          mbar_arrive(smem_u32(&b.k_full[ks]));
-          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&b.v_full[vs])), "n"(kVFull) : "memory");
-        }
-      }
-      g += w.ntiles;
-      ++live;
-    }
-  } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    // ------------------------------------------------------------ TMA: the context's K; V and the scales
-    const bool is_v = warp != kLoadWarp, flag = !is_v && blockIdx.x == 0;
-    const int stages = is_v ? G::kNV : G::kNK;
-    unsigned long long *full = is_v ? b.v_full : b.k_full, *empty = is_v ? b.v_empty : b.k_empty;
-    const uint32_t ring = sbase + (is_v ? G::kV : G::kK);
-    const CUtensorMap *map = is_v ? &maps.v : &maps.k;
-    const int page_size = 1 << t.page_shift, box = min(page_size, kTile), boxes = kTile / box, per = 32 / boxes;
-    // lanes 0-7 fetch K's scales of a tile, 8-15 V's; block j of the tile
-    const int j = lane & 7, tok_j = j << p.scale_shift;
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ TMA for K and V, the scales
+    const int page_size = 1 << t.page_shift, box = min(page_size, kTile), boxes = kTile / box;
+    const uint32_t box_bytes = box * D;
+    // lanes 0-7 fetch K's scales of a tile, 8-15 V's: block j of the tile, in box box_j; its place in its
+    // page is its place in the box where a box is a page
+    const int j = lane & 7, tok_j = j << p.scale_shift, box_j = min(tok_j, kTile - 1) / box;
     const float *scale = lane < 8 ? p.k_scale : p.v_scale;
     const int64_t sp = lane < 8 ? p.ks_sp : p.vs_sp, sb = lane < 8 ? p.ks_sb : p.vs_sb, ss = lane < 8 ? p.ks_sh : p.vs_sh;
-    QuantUnits it(p, flag);
+    scale += ((tok_j & (box - 1)) >> p.scale_shift) * sb;
     bool ok = true;
-    while (ok && it.next(w, flag)) {
-      if (w.tree) {
-        g += w.ntiles;
-        continue;
-      }
-      int page = 0;  // lane l: page of box l of the tiles at hand
-      for (int i = 0; ok && i < w.ntiles; ++i, ++g) {
-        const int tok0 = (w.tile0 + i) * kTile, at = i % per * boxes, stage = g % stages;
-        if (at == 0) {
-          const int tok = tok0 + lane * box;
-          page = 0;
-          if (tok < w.ctx && lane < (w.ntiles - i) * boxes) {
-            page = __ldg(t.page_table + w.n * t.pt_stride + (tok >> t.page_shift));
-            if (page < 0 || page >= t.num_pages) {
-              atomicOr(t.err, kErrBadPage);
-              page = 0;
-            }
-          }
+    int ks = 0, k_phase = 1, vs = 0, v_phase = 1;  // (a wait for phase 1 of a new barrier is over at once)
+    for (int unit = 0; ok; ++unit) {
+      ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
+      if (!ok) break;
+      const QuantUnit &u = unit_at(unit);
+      const int ntiles = uni(u.ntiles), n = uni(u.n), h = uni(u.h), tile0 = uni(u.tile0), ctx = uni(u.ctx);
+      const bool tree = uni(u.tree);
+      if (ntiles == 0) break;
+      const float *scale_h = scale + h * ss;
+      const int32_t *table = t.page_table + n * t.pt_stride;
+      const int end = tree ? 0 : min(ctx, (tile0 + ntiles) * kTile);
+      auto pages_from = [&](int tok) {  // lane l: page of the l-th box from token `tok` on
+        tok += lane * box;
+        int page = 0;
+        if (tok < end) page = __ldg(table + (tok >> t.page_shift));
+        return page;
+      };
+      int tok0 = tile0 * kTile, at = 0;
+      int page = pages_from(tok0), page_next = pages_from(tok0 + 32 * box);
+      for (int i = 0; i < ntiles; ++i, ++g, tok0 += kTile) {
+        if (at == 32) {
+          at = 0, page = page_next;
+          page_next = pages_from(tok0 + 32 * box);
         }
-        if (g >= stages) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&empty[stage]), (g / stages - 1) & 1, &s_abort, t.err));
+        if (at == 0 && (page < 0 || page >= t.num_pages)) {
+          atomicOr(t.err, kErrBadPage);
+          page = 0;
+        }
+        const uint32_t k_bar = smem_u32(&b.k_full[ks]), v_bar = smem_u32(&b.v_full[vs]);
+        const uint32_t k_empty = smem_u32(&b.k_empty[ks]);
+        ok = __all_sync(DC_FULL_MASK, bar_wait3(k_empty, k_phase, smem_u32(&b.v_empty[vs]), v_phase, k_empty, k_phase,
+                                                &s_abort, t.err));
         if (!ok) break;
-        const int used = min(boxes, (w.ctx - tok0 + box - 1) / box);  // copies of the tile
-        const uint32_t dst = ring + stage * G::kTileBytes, bar = smem_u32(&full[stage]);
-        if (is_v) {
-          const int pg = __shfl_sync(DC_FULL_MASK, page, at + min(tok_j, kTile - 1) / box);
-          if (lane < 16 && tok_j < kTile && tok0 + tok_j < w.ctx) {
-            const float *src = scale + pg * sp + (((tok0 + tok_j) & (page_size - 1)) >> p.scale_shift) * sb + w.h * ss;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[stage][lane >> 3][j])), "l"(src)
+        const uint32_t k_dst = sbase + G::kK + ks * G::kTileBytes, v_dst = sbase + G::kV + vs * G::kTileBytes;
+        if (tree) {
+          const int bytes = (D / 64) * 128 * t.tree_box;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(k_bar, bytes);
+            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(v_bar), "r"(bytes) : "memory");
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_4d(k_dst + c * kTreeNodes * 128, &maps.k_new, c * 64, i * kTreeNodes, h, n, k_bar);
+              tma_load_4d(v_dst + c * kTreeNodes * 128, &maps.v_new, c * 64, i * kTreeNodes, h, n, v_bar);
+            }
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 33;" ::"r"(v_bar) : "memory");
+          }
+          __syncwarp();
+        } else {
+          const int used = min(boxes, (end - tok0 + box - 1) / box);  // copies of the tile
+          // (the pages first, then all copies by one lane: a shuffle and an election between copies cost 130 cycles each)
+          int pg[kTile / 16];
+#pragma unroll
+          for (int r = 0; r < kTile / 16; ++r)
+            if (r < boxes) pg[r] = uni(lane == at + r ? page : 0);
+          const int slot = tok0 & (page_size - 1);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(k_bar, used * box_bytes);
+            mbar_arrive_expect_tx(v_bar, used * box_bytes);
+#pragma unroll
+            for (int r = 0; r < kTile / 16; ++r)
+              if (r < used) {  // (used <= boxes)
+                tma_load_4d(k_dst + r * box_bytes, &maps.k, 0, slot, h, pg[r], k_bar);
+                tma_load_4d(v_dst + r * box_bytes, &maps.v, 0, slot, h, pg[r], v_bar);
+              }
+          }
+          __syncwarp();
+          const int pg_j = __shfl_sync(DC_FULL_MASK, page, at + box_j);
+          if (lane < 16 && tok_j < kTile && tok0 + tok_j < end) {
+            const float *src = scale_h + pg_j * sp;
+            if (page_size > kTile) src += (slot >> p.scale_shift) * sb;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[vs][lane >> 3][j])), "l"(src)
                          : "memory");
           }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_bar) : "memory");
+          at += boxes;
         }
-        if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(used * box * D));
-        __syncwarp();
-        for (int r = 0; r < used; ++r) {
-          const int pg = __shfl_sync(DC_FULL_MASK, page, at + r);
-          if (elect_one()) tma_load_4d(dst + r * box * D, map, 0, tok0 & (page_size - 1), w.h, pg, bar);
-          __syncwarp();
-        }
+        if (++ks == G::kNK) ks = 0, k_phase ^= 1;
+        if (++vs == G::kNV) vs = 0, v_phase ^= 1;
       }
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ tensor core
-    constexpr uint32_t kId8 = (1u << 4) | (8u << 24);                              // fp32 += e4m3 e4m3, M = 128
-    constexpr uint32_t kIdS = kId8 | (uint32_t)(R >> 3) << 17;
-    constexpr uint32_t kIdO = kId8 | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t)(3 * R >> 3) << 17;  // B e5m2; both M- and N-major
-    constexpr uint32_t kIdS16 = F16 ? idesc_f16(128, R) : idesc_bf16(128, R);
-    constexpr uint32_t kIdO16 = kIdS16 | (1u << 15) | (1u << 16);
-    QuantUnits it(p, false);
-    bool ok = true;
-    // O^T (+)= V^T P^T of tile x, the first of the block's unit number `unit` if `first`
-    auto pv = [&](int x, bool first, int unit, bool tree) {
-      const int vs = x % G::kNV;
-      const bool go = bar_wait(smem_u32(&b.v_full[vs]), (x / G::kNV) & 1, &s_abort, t.err) &&
-                      (!first || unit < 2 || bar_wait(smem_u32(&b.o_free[unit & 1]), ((unit >> 1) - 1) & 1, &s_abort, t.err)) &&
-                      bar_wait(smem_u32(&b.p_full[x & 1]), (x >> 1) & 1, &s_abort, t.err);
-      if (!__all_sync(DC_FULL_MASK, go)) return false;
-      tc_fence_after();
-      const uint32_t to = tmem + G::kO + (unit & 1) * 3 * R;
-      const uint32_t sv = sbase + G::kV + vs * G::kTileBytes, sp = sbase + G::kP + (x & 1) * G::kPBytes;
-      if (tree) {
-        const uint32_t a = desc_lo(sv, kTreeNodes * 128), pb = desc_lo(sp);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kTreeNodes / 16; ++k)
-            mma_ss(to, a + k * (2048 >> 4), pb + k * (2048 >> 4), kIdO16, (!first || k > 0) ? 1u : 0u);
-          mma_commit(smem_u32(&b.v_empty[vs]));
-          mma_commit(smem_u32(&b.pv_done[x & 1]));
+  } else if (warp == kPrepWarp) {
+    // ------------------------------------------------------------ units, Q parts
+    constexpr int kPer = D / 16, kRows = 32 / kPer;  // lanes of a row (16 elements each), rows a step
+    const int sub = lane / kPer, e0 = (lane % kPer) * 16;
+    const float c = t.scale * kLog2e;
+    const bool flag = blockIdx.x == 0;
+    QuantUnits it(p, flag);
+    bool ok = true, more = true;
+    int made = 0;
+    for (int unit = 0; ok; ++unit) {
+      const int qb = unit & 1, slot = unit & (kAhead - 1);
+      // Units are published ahead of their Q, up to nine: the loads of short ones run that far ahead.
+      for (int k = 0; k < 2 && more && made <= unit + 8; ++k) {
+        QuantUnit w;
+        do more = it.next(w, flag);
+        while (more && w.ntiles == 0);
+        if (!more) w.ntiles = 0;
+        if (lane == 0) {
+          s_unit[made & (kUnits - 1)] = w;
+          mbar_arrive(units_bar(made));
         }
-      } else {
-        const uint32_t a = desc_lo(sv, G::kTileBytes), pb = desc_lo(sp, G::kPAtom);
-        if (elect_one()) {
+        ++made;
+        __syncwarp();
+      }
+      if (unit >= 2) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_empty[qb]), ((unit >> 1) - 1) & 1, &s_abort, t.err));
+      if (!ok) break;
+      const QuantUnit &u = unit_at(unit);
+      const int ntiles = uni(u.ntiles), len = uni(u.len), r0 = uni(u.mt) * R;
+      const bool tree = uni(u.tree);
+      if (ntiles > 0) {
+        uint8_t *dst = smem + G::kQ + qb * G::kQBytes;
+        const uint16_t *q0 = t.q + u.n * t.q_sn + (int64_t)u.h * t.group * t.q_sh + e0;
+        // kFlight steps' loads in flight (one at a time a unit's Q took 16,000 cycles, more than its tiles)
+        constexpr int kSteps = R / kRows, kFlight = kSteps < 4 ? kSteps : 4;
+#pragma unroll 1
+        for (int s0 = 0; s0 < kSteps; s0 += kFlight) {
+          uint4 x[kFlight][2];
 #pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            mma8<G::kHi, G::kHiP>(to, a + k * (32 * D >> 4), pb + k * (2048 >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
-          mma_commit(smem_u32(&b.v_empty[vs]));
-          mma_commit(smem_u32(&b.pv_done[x & 1]));
+          for (int y = 0; y < kFlight; ++y) {
+            const int r = r0 + (s0 + y) * kRows + sub, node = r / t.group;
+            x[y][0] = x[y][1] = make_uint4(0, 0, 0, 0);
+            if (node < len) {
+              const uint4 *q = reinterpret_cast<const uint4 *>(q0 + node * t.q_st + (r - node * t.group) * t.q_sh);
+              x[y][0] = __ldg(q), x[y][1] = __ldg(q + 1);
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < kFlight; ++y) {
+            const int row = (s0 + y) * kRows + sub;
+            const uint32_t u8[8] = {x[y][0].x, x[y][0].y, x[y][0].z, x[y][0].w, x[y][1].x, x[y][1].y, x[y][1].z, x[y][1].w};
+            if (tree) {
+              uint8_t *d = dst + (e0 >> 6) * (R * 128) + row * 128;
+              const int chunk = (e0 & 63) >> 3;
+              *reinterpret_cast<uint4 *>(d + ((chunk ^ (row & 7)) << 4)) = x[y][0];
+              *reinterpret_cast<uint4 *>(d + (((chunk + 1) ^ (row & 7)) << 4)) = x[y][1];
+              if (lane % kPer == 0) s_factor[slot][row] = c;
+              continue;
+            }
+            float most = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              most = fmaxf(most, fmaxf(fabsf(unpack_lo<F16>(u8[j])), fabsf(unpack_lo<F16>(u8[j] >> 16))));
+#pragma unroll
+            for (int o = 1; o < kPer; o <<= 1) most = fmaxf(most, __shfl_xor_sync(DC_FULL_MASK, most, o));
+            // the power of two that brings the row's largest to 128..256 (rows below 2^-100 count as of that
+            // size; a row with an infinity becomes NaN)
+            const int e = max((int)(__float_as_uint(most) >> 23), 27);
+            const float mul = __uint_as_float(e < 255 ? (uint32_t)(261 - e) << 23 : 0x7FC00000u);
+            if (lane % kPer == 0) s_factor[slot][row] = c * __uint_as_float((uint32_t)min(e - 7, 254) << 23);
+            uint8_t *d = dst + row * D + (((e0 >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
+            uint32_t h[NP][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              // (fp16 holds either type's elements of that size but for what lies below 2^-24)
+              uint32_t f = pack2<true>(unpack_lo<F16>(u8[j]) * mul, unpack_lo<F16>(u8[j] >> 16) * mul);
+#pragma unroll
+              for (int k = 0; k < NP; ++k) {
+                uint16_t y;
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(y) : "r"(f));
+                if (k + 1 < NP) {
+                  uint32_t back;
+                  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(y));
+                  f = hsub2(f, back);
+                }
+                h[k][j >> 1] = j & 1 ? h[k][j >> 1] | (uint32_t)y << 16 : y;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+              *reinterpret_cast<uint4 *>(d + k * G::kQPart) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+          }
         }
+        fence_proxy_async();
       }
       __syncwarp();
-      return true;
-    };
-    bool prev_first = false, prev_tree = false;
-    int prev_unit = 0;
-    while (ok && it.next(w)) {
-      if (w.ntiles == 0) continue;
-      const int qb = live & 1;
-      ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (live >> 1) & 1, &s_abort, t.err));
-      for (int i = 0; ok && i < w.ntiles; ++i, ++g) {
-        const int ks = g % G::kNK;
-        ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.k_full[ks]), (g / G::kNK) & 1, &s_abort, t.err));
+      if (lane == 0) mbar_arrive(factors_bar(unit));
+      if (ntiles == 0) break;
+    }
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------------ tensor core: S^T = K Q^T
+    constexpr uint32_t kId = (1u << 4) | (8u << 24) | (uint32_t)(R >> 3) << 17;  // fp32 += e4m3 e4m3, M = 128, N = R
+    constexpr uint32_t kId16 = F16 ? idesc_f16(128, R) : idesc_bf16(128, R);
+    bool ok = true;
+    int ks = 0, k_phase = 0;
+    for (int unit = 0; ok; ++unit) {
+      const int qb = unit & 1;
+      ok = __all_sync(DC_FULL_MASK, bar_wait(factors_bar(unit), (unit / kAhead) & 1, &s_abort, t.err));
+      if (!ok) break;
+      const int ntiles = uni(unit_at(unit).ntiles);
+      const bool tree = uni(unit_at(unit).tree);
+      if (ntiles == 0) break;
+      const uint32_t sq = desc_lo(sbase + G::kQ + qb * G::kQBytes);
+      for (int i = 0; i < ntiles; ++i, ++g) {
+        const int sb = g % G::kNS;
+        const uint32_t k_bar = smem_u32(&b.k_full[ks]);
+        ok = __all_sync(DC_FULL_MASK, bar_wait3(k_bar, k_phase, k_bar, k_phase, g >= G::kNS ? smem_u32(&b.s_free[sb]) : k_bar,
+                                                g >= G::kNS ? (g / G::kNS - 1) & 1 : k_phase, &s_abort, t.err));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sq = desc_lo(sbase + G::kQ + qb * G::kQBytes), sk = desc_lo(sbase + G::kK + ks * G::kTileBytes);
-        const uint32_t to = tmem + G::kS + (g & 1) * R;
+        const uint32_t sk = desc_lo(sbase + G::kK + ks * G::kTileBytes), to = tmem + G::kS + sb * R;
         if (elect_one()) {
-          if (w.tree) {
+          if (tree) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
               mma_ss(to, sk + (((k >> 2) * (kTreeNodes * 128) + (k & 3) * 32) >> 4),
-                     sq + (((k >> 2) * (R * 128) + (k & 3) * 32) >> 4), kIdS16, k > 0 ? 1u : 0u);
+                     sq + (((k >> 2) * (R * 128) + (k & 3) * 32) >> 4), kId16, k > 0 ? 1u : 0u);
           } else {
 #pragma unroll
             for (int x = 0; x < NP; ++x)
 #pragma unroll
               for (int k = 0; k < D / 32; ++k)
-                mma8<G::kHi, G::kHi>(to, sk + k * 2, sq + ((x * G::kQPart) >> 4) + k * 2, kIdS, (x > 0 || k > 0) ? 1u : 0u);
+                mma8<G::kHi, G::kHi>(to, sk + k * 2, sq + ((x * G::kQPart) >> 4) + k * 2, kId, (x > 0 || k > 0) ? 1u : 0u);
           }
-          mma_commit(smem_u32(&b.s_full[g & 1]));
+          mma_commit(smem_u32(&b.s_full[sb]));
           mma_commit(smem_u32(&b.k_empty[ks]));
-          if (i == w.ntiles - 1) mma_commit(smem_u32(&b.q_empty[qb]));
+          if (i == ntiles - 1) mma_commit(smem_u32(&b.q_empty[qb]));
         }
         __syncwarp();
-        if (g > 0) ok = pv(g - 1, prev_first, prev_unit, prev_tree);
-        prev_first = i == 0, prev_unit = live, prev_tree = w.tree;
+        if (++ks == G::kNK) ks = 0, k_phase ^= 1;
       }
-      ++live;
     }
-    if (ok && g > 0) pv(g - 1, prev_first, prev_unit, prev_tree);
     if (elect_one()) {  // the lane that issued: nothing is in flight when the block frees its TMEM
-      mma_commit(smem_u32(&b.done));
-      mbar_drain(smem_u32(&b.done), 0);
+      mma_commit(smem_u32(&b.done[0]));
+      mbar_drain(smem_u32(&b.done[0]), 0);
+    }
+    __syncwarp();
+  } else if (warp == kOutWarp) {
+    // ------------------------------------------------------------ tensor core: O^T += V^T P^T
+    constexpr uint32_t kId =  // B e5m2; both M- and N-major
+        (1u << 4) | (8u << 24) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t)(3 * R >> 3) << 17;
+    constexpr uint32_t kId16 = (F16 ? idesc_f16(128, R) : idesc_bf16(128, R)) | (1u << 15) | (1u << 16);
+    bool ok = true;
+    int vs = 0, v_phase = 0;
+    int begun[G::kTeams] = {};  // units that each team has begun
+    for (int unit = 0; ok; ++unit) {
+      ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
+      if (!ok) break;
+      const int ntiles = uni(unit_at(unit).ntiles);
+      const bool tree = uni(unit_at(unit).tree);
+      if (ntiles == 0) break;
+      for (int i = 0; i < ntiles; ++i, ++g) {
+        const int team = g % G::kTeams, pb = g % G::kNP;
+        const bool first = i < G::kTeams;
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < G::kTeams; ++k)
+          if (k == team) mine = (begun[k] += first) - 1;
+        const uint32_t v_bar = smem_u32(&b.v_full[vs]);
+        const bool wait_o = first && mine >= 2;
+        ok = __all_sync(DC_FULL_MASK, bar_wait3(v_bar, v_phase, smem_u32(&b.p_full[pb]), (g / G::kNP) & 1,
+                                                wait_o ? smem_u32(&b.o_free[team][mine & 1]) : v_bar,
+                                                wait_o ? ((mine >> 1) - 1) & 1 : v_phase, &s_abort, t.err));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t to = tmem + G::kO + (team * 2 + (mine & 1)) * 3 * R;
+        const uint32_t sv = sbase + G::kV + vs * G::kTileBytes, sp = sbase + G::kP + pb * G::kPBytes;
+        const uint32_t a = desc_lo(sv, tree ? kTreeNodes * 128 : G::kTileBytes), bd = desc_lo(sp, tree ? 16 : G::kPAtom);
+        if (elect_one()) {
+          if (tree) {
+#pragma unroll
+            for (int k = 0; k < kTreeNodes / 16; ++k)
+              mma_ss(to, a + k * (2048 >> 4), bd + k * (2048 >> 4), kId16, (!first || k > 0) ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              mma8<G::kHi, G::kHiP>(to, a + k * (32 * D >> 4), bd + k * (2048 >> 4), kId, (!first || k > 0) ? 1u : 0u);
+          }
+          mma_commit(smem_u32(&b.v_empty[vs]));
+          mma_commit(smem_u32(&b.pv_done[pb]));
+        }
+        __syncwarp();
+        if (++vs == G::kNV) vs = 0, v_phase ^= 1;
+      }
+    }
+    if (elect_one()) {
+      mma_commit(smem_u32(&b.done[1]));
+      mbar_drain(smem_u32(&b.done[1]), 0);
     }
     __syncwarp();
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ------------------------------------------------------------ softmax, output
-    QuantUnits it(p, false);
-    constexpr int C = R / 2;  // this group's rows: columns col0 .. col0 + C - 1
-    const int group = warp >> 2, quad = warp & 3, tok = tid & (kGroup - 1), col0 = group * C;
+    // Each team of groups takes every kTeams-th tile, with references, sums and O of its own; a unit's
+    // tiles i, i + kTeams, ... make a partial result of their own, whichever team has them.
+    constexpr int C = kCols;
+    const int group = warp >> 2, quad = warp & 3, tok = tid & (kGroup - 1);
+    const int team = group / G::kParts, col0 = group % G::kParts * C;  // this group's rows: columns col0 .. col0 + C - 1
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + col0;
+    float *const mb_of = s_mb[group], *const f_of = s_f[group];
+    uint32_t(*const s_word)[C] = reinterpret_cast<uint32_t(*)[C]>(s_part[group]);  // mask words (a tile's step between uses of s_part)
     bool ok = true;
     auto wait = [&](unsigned long long *bar, int phase) {
       if (ok) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(bar), phase & 1, &s_abort, t.err));
     };
-    // A unit's output, unnormalised, leaves for the join after the first tile of
-    // the unit that follows, whose products go to the other half of O, so that the
-    // tensor core and the copies go on meanwhile.
-    QuantUnit done = {};
-    int done_g = -1, done_unit = 0;  // that unit's last tile (-1: none), its number
-    auto slot_of = [&](const QuantUnit &u) {  // the unit's rows among the partial results
-      return ((((int64_t)u.n * t.kv_heads + u.h) * p.mtiles + u.mt) * p.slots + u.slot) * R;
+    // rows of partial result j of a unit
+    auto slot_of = [&](const QuantUnit &u, int j) {
+      return (((((int64_t)u.n * t.kv_heads + u.h) * p.mtiles + u.mt) * p.slots + u.slot) * G::kTeams + j) * R + col0;
     };
-    auto finish = [&] {
-      const int par = done_unit & 1;
-      wait(&b.pv_done[done_g & 1], done_g >> 1);
+    // A unit's output, unnormalised, leaves for the join after the team's first tile of
+    // the unit that follows, whose products go to the other half of its O, so that the
+    // tensor core and the copies go on meanwhile.
+    int done_g = -1, done_unit = 0, done_i = 0;  // that unit's last tile of this team (-1: none), its number, the team's first tile of it
+    int begun = 0;                               // units that this team has begun
+    auto finish = [&](int par) {
+      // (with a P buffer a team the tile after it has waited for that product already)
+      if (G::kNP > G::kTeams) wait(&b.pv_done[done_g % G::kNP], done_g / G::kNP);
       tc_fence_after();
-      const uint32_t from = trow + G::kO + par * 3 * R;
-      float o[C];
-      tmem_ld<C>(from, o);
-      if (!done.tree) {
-        float x[C];
-        tmem_ld<C>(from + R, x);
+      const QuantUnit &u = unit_at(done_unit);
+      const uint32_t from = trow + G::kO + (team * 2 + par) * 3 * R;
+      float *part = p.part_o + slot_of(u, done_i) * D + tok;  // [row][D]
+      const bool tree = u.tree;
+#pragma unroll 1
+      for (int k0 = 0; k0 < C; k0 += 8) {
+        uint32_t x[8], y[8], z[8];
+        tmem_start<8>(from + k0, x);
+        if (!tree) tmem_start<8>(from + R + k0, y), tmem_start<8>(from + 2 * R + k0, z);
+        tmem_wait<8>(x);
+        if (!tree) {
+          tmem_wait<8>(y), tmem_wait<8>(z);
 #pragma unroll
-        for (int k = 0; k < C; ++k) o[k] += x[k];
-        tmem_ld<C>(from + 2 * R, x);
+          for (int k = 0; k < 8; ++k)
+            x[k] = __float_as_uint(fmaf(__uint_as_float(z[k]), 0.0078125f, __uint_as_float(x[k]) + __uint_as_float(y[k])));
+        }
+        if (tok < D && ok) {
 #pragma unroll
-        for (int k = 0; k < C; ++k) o[k] = fmaf(x[k], 0.0078125f, o[k]);
+          for (int k = 0; k < 8; ++k) part[(k0 + k) * D] = __uint_as_float(x[k]);
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free[par]));
-      float *part = p.part_o + (slot_of(done) + col0) * D + tok;  // [row][D]
-      if (tok < D && ok) {
-#pragma unroll
-        for (int k = 0; k < C; ++k) part[k * D] = o[k];
-        if (done.tree) {
-          // infinities and NaN of the nodes that a row sees
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&b.o_free[team][par]));
+      if (tok < D && ok && tree) {
+        // infinities and NaN of this team's nodes that a row sees
 #pragma unroll 1
-          for (int q = 0; q < (done.len + 31) / 32; ++q)
+        for (int q = done_i * 2; q < (u.len + 31) / 32; q += (q & 1) ? 2 * G::kTeams - 1 : 1)
 #pragma unroll 1
-            for (uint32_t r = s_odd[done_unit & (kAhead - 1)][q]; r; r &= r - 1) {
-              const int x = __ffs(r) - 1;
-              const uint32_t e = t.v_new[done.n * t.vn_sn + (q * 32 + x) * t.vn_st + done.h * t.vn_sh + tok];
+          for (uint32_t r = s_odd[done_unit & (kAhead - 1)][q]; r; r &= r - 1) {
+              const int nd = __ffs(r) - 1;
+              const uint32_t e = t.v_new[u.n * t.vn_sn + (q * 32 + nd) * t.vn_st + u.h * t.vn_sh + tok];
               if (!nonfinite2<F16>(e)) continue;
 #pragma unroll 1
               for (int k = 0; k < C; ++k)
-                if ((tree_sees(t, done.n, done.len, (done.mt * R + col0 + k) / t.group, q) >> x) & 1u)
-                  part[k * D] += unpack_lo<F16>(e);
+                if ((tree_sees(t, u.n, u.len, (u.mt * R + col0 + k) / t.group, q) >> nd) & 1u) part[k * D] += unpack_lo<F16>(e);
             }
-        }
       }
       __syncwarp();
       done_g = -1;
     };
-    while (it.next(w)) {
-      if (w.ntiles == 0) continue;
-      const float *factor = s_factor[live & (kAhead - 1)] + col0;
-      wait(&b.factors[live & (kAhead - 1)], live / kAhead);
-      ++live;
-      float l[C];  // the rows' sums over this thread's tokens
+    for (int unit = 0;; ++unit) {
+      if (ok) ok = __all_sync(DC_FULL_MASK, bar_wait(factors_bar(unit), (unit / kAhead) & 1, &s_abort, t.err));
+      // the group's warps leave together when a wait has expired
+      if (soft_any(group, !ok)) {
+        ok = false;
+        break;
+      }
+      const QuantUnit &u = unit_at(unit);
+      const int ntiles = uni(u.ntiles), tile0 = uni(u.tile0);
+      const bool tree = uni(u.tree);
+      const int end = uni(tree ? u.len : u.ctx);
+      if (ntiles == 0) break;
+      const int first = (team + G::kTeams - g % G::kTeams) % G::kTeams;  // the team's first tile of the unit
+      if (first >= ntiles) {  // none: an empty partial result
+        if (tok < C) p.part_ml[slot_of(u, first) + tok] = make_float2(kNone, 0.f);
+        g += ntiles;
+        continue;
+      }
+      const float *factor = s_factor[unit & (kAhead - 1)] + col0;
+      const uint32_t to_o = trow + G::kO + (team * 2 + (begun & 1)) * 3 * R;
+      f32x2 l[C / 2];  // the rows' sums over this thread's tokens
 #pragma unroll
-      for (int k = 0; k < C; ++k) l[k] = 0.f;
-      for (int i = 0; i < w.ntiles; ++i, ++g) {
-        const int tok0 = (w.tile0 + i) * (w.tree ? kTreeNodes : kTile), vs = g % G::kNV;
-        const int valid = w.tree ? min(kTreeNodes, w.len - tok0) : min(kTile, w.ctx - tok0);
-        wait(&b.v_full[vs], g / G::kNV);  // the scales, and the tree's odd nodes
-        float ks = 1.f, lvs = 0.f, inv = 1.f;
-        if (!w.tree && tok < valid) {
-          const int blk = tok >> p.scale_shift;
-          ks = s_scale[vs][0][blk];
-          const float x = s_scale[vs][1][blk];
-          lvs = __log2f(x), inv = __frcp_rn(x);
+      for (int k = 0; k < C / 2; ++k) l[k] = 0ull;
+      bool leave = false;
+      int x_g = 0;  // this tile
+      for (int i = first; i < ntiles; i += G::kTeams) {
+        x_g = g + i;
+        const int vs = x_g % G::kNV, sb = x_g % G::kNS, pb = x_g % G::kNP;
+        const int width = tree ? kTreeNodes : kTile, tok0 = (tile0 + i) * width, valid = min(width, end - tok0);
+        {
+          // S; V with its scales (and the tree's odd nodes); P's buffer is free
+          const uint32_t s_bar = smem_u32(&b.s_full[sb]), s_phase = (x_g / G::kNS) & 1;
+          const bool used = x_g >= G::kNP;
+          if (ok)
+            ok = __all_sync(DC_FULL_MASK,
+                            bar_wait3(s_bar, s_phase, smem_u32(&b.v_full[vs]), (x_g / G::kNV) & 1,
+                                      used ? smem_u32(&b.pv_done[pb]) : s_bar, used ? (x_g / G::kNP - 1) & 1 : s_phase,
+                                      &s_abort, t.err));
         }
-        if (!w.tree && valid < kTile && group == 0) {
-          // past the end lies what a page or a copy left: zeros in its place, since a zero weight does not cancel NaN
-          if (ok && tok >= valid) {
+        tc_fence_after();
+        uint32_t raw[C];
+        tmem_start<C>(trow + G::kS + sb * R, raw);  // in flight under the scales
+        float ks = 1.f, lvs = 0.f, inv = 1.f;
+        if (!tree) {
+          if (tok < valid) {
+            const int blk = tok >> p.scale_shift;
+            ks = s_scale[vs][0][blk];
+            const float f = s_scale[vs][1][blk];
+            lvs = __log2f(f), inv = rcp(f);
+          } else if (col0 == 0 && ok) {
+            // past the end lies what a page or a copy left: zeros in its place, since a zero weight does not cancel NaN
             uint4 *row = reinterpret_cast<uint4 *>(smem + G::kV + vs * G::kTileBytes + tok * D);
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) row[e] = make_uint4(0, 0, 0, 0);
           }
+        } else {
+          if (col0 == 0 && quad < kTreeNodes / 32) {
+            bool bad = false;
+            if (ok) bad = clean_node<D, F16>(smem + G::kV + vs * G::kTileBytes + tok * 128, tok < valid);
+            const uint32_t bits = __ballot_sync(DC_FULL_MASK, bad);
+            if (lane == 0) s_odd[unit & (kAhead - 1)][i * 2 + quad] = bits;
+          }
+          // this warp's 32 nodes are one word of each row's mask: lane k fetches row k's
+          if (lane < C)
+            s_word[quad][lane] = quad < kTreeNodes / 32 ? tree_sees(t, u.n, u.len, (u.mt * R + col0 + lane) / t.group, tok0 / 32 + quad) : 0u;
+          __syncwarp();
         }
-        wait(&b.s_full[g & 1], g >> 1);
-        if (g >= 2) wait(&b.pv_done[g & 1], (g >> 1) - 1);  // P's buffer is free
-        tc_fence_after();
-        float v[C];
-        // once, or once more when a score has outgrown its row's reference
-        for (bool renew = false;;) {
-          // log2 of weight x vs
-          tmem_ld<C>(trow + G::kS + (g & 1) * R, v);
+        const bool mask = tree || valid < kTile;
+        const f32x2 ks2 = both(ks, ks), lvs2 = both(lvs, lvs);
+        f32x2 x[C / 2];
+        // log2 of weight x vs
+        auto scaled = [&] {
 #pragma unroll
           for (int k = 0; k < C; k += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(factor + k);
-            v[k] = fmaf(v[k] * ks, f.x, lvs), v[k + 1] = fmaf(v[k + 1] * ks, f.y, lvs);
-            v[k + 2] = fmaf(v[k + 2] * ks, f.z, lvs), v[k + 3] = fmaf(v[k + 3] * ks, f.w, lvs);
+            x[k / 2] = fma2(mul2(both(__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])), ks2), both(f.x, f.y), lvs2);
+            x[k / 2 + 1] = fma2(mul2(both(__uint_as_float(raw[k + 2]), __uint_as_float(raw[k + 3])), ks2), both(f.z, f.w), lvs2);
           }
-          if (w.tree) {
-            // this warp's 32 nodes are one word of each row's mask: lane k fetches row k's
-            if (lane < C)
-              s_word[quad][col0 + lane] =
-                  quad < kTreeNodes / 32 ? tree_sees(t, w.n, w.len, (w.mt * R + col0 + lane) / t.group, tok0 / 32 + quad) : 0u;
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < C; k += 4) {
-              const uint4 word = *reinterpret_cast<const uint4 *>(&s_word[quad][col0 + k]);
-              v[k] = (word.x >> lane) & 1u ? v[k] : -INFINITY;
-              v[k + 1] = (word.y >> lane) & 1u ? v[k + 1] : -INFINITY;
-              v[k + 2] = (word.z >> lane) & 1u ? v[k + 2] : -INFINITY;
-              v[k + 3] = (word.w >> lane) & 1u ? v[k + 3] : -INFINITY;
-            }
-            __syncwarp();
-          } else if (tok >= valid) {
-#pragma unroll
-            for (int k = 0; k < C; ++k) v[k] = -INFINITY;
-          }
-          if (renew) {
-            // references from the rows' maxima over the tile; l and O^T follow
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-              const float m = warp_fmax(v[k]);
-              if (lane == k) s_part[quad][col0 + k] = m;
-            }
-            soft_sync(group);
-            if (tok < C) {
-              const int k = col0 + tok;
-              const float m = fmaxf(fmaxf(s_part[0][k], s_part[1][k]), fmaxf(s_part[2][k], s_part[3][k]));
-              const float old = s_mb[k];
-              const bool grown = m - old > kGrow;  // (the others stay: a row's result hangs on its own scores)
-              s_mb[k] = grown ? m - kTop : old;
-              s_f[k] = grown ? ex2(old - m + kTop) : 1.f;
-            }
-            soft_sync(group);
-#pragma unroll
-            for (int k = 0; k < C; ++k) l[k] *= s_f[col0 + k];
-            if (i > 0) {
-              wait(&b.pv_done[(g - 1) & 1], (g - 1) >> 1);
-              tc_fence_after();
-              const uint32_t to = trow + G::kO + ((live - 1) & 1) * 3 * R;
-#pragma unroll 1
-              for (int x = 0; x < (w.tree ? 1 : 3); ++x) {
-                float o[C];
-                tmem_ld<C>(to + x * R, o);
-#pragma unroll
-                for (int k = 0; k < C; ++k) o[k] *= s_f[col0 + k];
-                tmem_st<C>(to + x * R, o);
-              }
-            }
-          } else if (i == 0) {
-            // a unit begins with the best of four tokens' scores as the references
-            if (lane == 0) {
-#pragma unroll
-              for (int k = 0; k < C; k += 4)
-                *reinterpret_cast<float4 *>(&s_part[quad][col0 + k]) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-            }
-            soft_sync(group);
-            if (tok < C) {
-              const int k = col0 + tok;
-              const float m = fmaxf(fmaxf(s_part[0][k], s_part[1][k]), fmaxf(s_part[2][k], s_part[3][k])) - kTop;
-              s_mb[k] = fabsf(m) < INFINITY ? m : kNone;
-            }
-            soft_sync(group);
-          }
-          // exponents against the references, in v's place
-          float grow[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (!mask) return;
 #pragma unroll
           for (int k = 0; k < C; k += 4) {
-            const float4 mb = *reinterpret_cast<const float4 *>(&s_mb[col0 + k]);
-            v[k] -= mb.x, v[k + 1] -= mb.y, v[k + 2] -= mb.z, v[k + 3] -= mb.w;
-            grow[0] = fmaxf(grow[0], v[k]), grow[1] = fmaxf(grow[1], v[k + 1]);
-            grow[2] = fmaxf(grow[2], v[k + 2]), grow[3] = fmaxf(grow[3], v[k + 3]);
+            const uint4 word = *reinterpret_cast<const uint4 *>(&s_word[quad][k]);
+            const bool in = tree || tok < valid;  // (the words are of the tree alone)
+            const float2 a = apart(x[k / 2]), c = apart(x[k / 2 + 1]);
+            auto sees = [&](uint32_t m) { return tree ? (m >> lane) & 1u : (uint32_t)in; };
+            x[k / 2] = both(sees(word.x) ? a.x : -INFINITY, sees(word.y) ? a.y : -INFINITY);
+            x[k / 2 + 1] = both(sees(word.z) ? c.x : -INFINITY, sees(word.w) ? c.y : -INFINITY);
           }
-          if (renew || !soft_any(group, fmaxf(fmaxf(grow[0], grow[1]), fmaxf(grow[2], grow[3])) > kGrow)) break;
-          renew = true;
+        };
+        float grow;
+        auto against = [&] {  // the exponents against the references, in x's place
+          float g0 = -INFINITY, g1 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < C; k += 4) {
+            const float4 mb = *reinterpret_cast<const float4 *>(mb_of + k);
+            x[k / 2] = add2(x[k / 2], both(-mb.x, -mb.y)), x[k / 2 + 1] = add2(x[k / 2 + 1], both(-mb.z, -mb.w));
+            const float2 a = apart(x[k / 2]), c = apart(x[k / 2 + 1]);
+            g0 = fmaxf(g0, fmaxf(a.x, a.y)), g1 = fmaxf(g1, fmaxf(c.x, c.y));
+          }
+          grow = fmaxf(g0, g1);
+        };
+        tmem_wait<C>(raw);
+        scaled();
+        // The group's warps vote on every tile but a unit's first, which gives the references: whether a
+        // score has outgrown its row's reference, or a wait has expired, when all leave together.
+        bool renew = i == first;
+        if (!renew) {
+          against();
+          if (soft_any(group, grow > kGrow || !ok)) {
+            if (soft_any(group, !ok)) {
+              leave = true, ok = false;
+              break;
+            }
+            renew = true;
+            tmem_start<C>(trow + G::kS + sb * R, raw);
+            tmem_wait<C>(raw);
+            scaled();
+          }
         }
-        uint8_t *pbuf = smem + G::kP + (g & 1) * G::kPBytes;
-        if (w.tree) {
+        if (renew) {
+          // references from the rows' maxima over the tile; l and O^T follow
+          __syncwarp();  // (the mask's words have been read)
+#pragma unroll
+          for (int k = 0; k < C; k += 4) {
+            const float2 a = apart(x[k / 2]), c = apart(x[k / 2 + 1]);
+            const float m0 = warp_fmax(a.x), m1 = warp_fmax(a.y), m2 = warp_fmax(c.x), m3 = warp_fmax(c.y);
+            if (lane == 0) *reinterpret_cast<float4 *>(&s_part[group][quad][k]) = make_float4(m0, m1, m2, m3);
+          }
+          soft_sync(group);
+          if (tok < C) {
+            const float m = fmaxf(fmaxf(s_part[group][0][tok], s_part[group][1][tok]),
+                                  fmaxf(s_part[group][2][tok], s_part[group][3][tok]));
+            const float old = mb_of[tok];
+            const bool grown = m - old > kGrow;  // (the others stay: a row's result hangs on its own scores)
+            mb_of[tok] = grown ? m - kTop : old;
+            f_of[tok] = grown ? ex2(old - m + kTop) : 1.f;
+          }
+          soft_sync(group);
+          if (i > first) {
+#pragma unroll
+            for (int k = 0; k < C / 2; ++k) l[k] = mul2(l[k], both(f_of[2 * k], f_of[2 * k + 1]));
+            // this team's last product
+            wait(&b.pv_done[(x_g - G::kTeams) % G::kNP], (x_g - G::kTeams) / G::kNP);
+            tc_fence_after();
+#pragma unroll 1
+            for (int part = 0; part < (tree ? 1 : 3); ++part)
+#pragma unroll 1
+              for (int k0 = 0; k0 < C; k0 += 8) {
+                float o[8];
+                tmem_ld<8>(to_o + part * R + k0, o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] *= f_of[k0 + k];
+                tmem_st<8>(to_o + part * R + k0, o);
+              }
+          }
+          // (the words anew: s_part took their place)
+#pragma unroll
+          for (int k = 0; k < C; k += 4) {
+            const float4 mb = *reinterpret_cast<const float4 *>(mb_of + k);
+            x[k / 2] = add2(x[k / 2], both(-mb.x, -mb.y)), x[k / 2 + 1] = add2(x[k / 2 + 1], both(-mb.z, -mb.w));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&b.s_free[sb]));
+        uint8_t *pbuf = smem + G::kP + pb * G::kPBytes;
+        const f32x2 inv2 = both(inv, inv);
+        if (tree) {
 #pragma unroll
           for (int k = 0; k < C; k += 8) {
-            float e[8];
+            uint32_t pk[4];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              e[x] = ex2(v[k + x]);
-              l[k + x] += e[x];
+            for (int y = 0; y < 8; y += 2) {
+              const float2 v = apart(x[(k + y) / 2]);
+              const float e0 = ex2(v.x), e1 = ex2(v.y);
+              l[(k + y) / 2] = add2(l[(k + y) / 2], both(e0, e1));
+              pk[y / 2] = pack2<F16>(e0, e1);
             }
             if (tok < kTreeNodes)
               *reinterpret_cast<uint4 *>(pbuf + tok * 128 + ((((col0 + k) >> 3) ^ (tok & 7)) << 4)) =
-                  make_uint4(pack2<F16>(e[0], e[1]), pack2<F16>(e[2], e[3]), pack2<F16>(e[4], e[5]), pack2<F16>(e[6], e[7]));
+                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         } else {
-          constexpr int kStep = C < 16 ? C : 16;  // rows of a store
+          uint32_t parts[3][C / 4];
 #pragma unroll
-          for (int k = 0; k < C; k += kStep) {
-            uint32_t parts[3][kStep / 4];
+          for (int k = 0; k < C; k += 4) {
+            float e[4];
 #pragma unroll
-            for (int x = 0; x < kStep; x += 4) {
-              float e[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                e[y] = ex2(v[k + x + y]);
-                l[k + x + y] = fmaf(e[y], inv, l[k + x + y]);
-              }
-              split4(e, parts[0][x / 4], parts[1][x / 4], parts[2][x / 4]);
+            for (int z = 0; z < 4; z += 2) {
+              const int at = (k + z) / 2;
+              const float2 v = apart(x[at]);
+              e[z] = ex2(v.x), e[z + 1] = ex2(v.y);
+              l[at] = fma2(both(e[z], e[z + 1]), inv2, l[at]);
             }
+            split4(e, parts[0][k / 4], parts[1][k / 4], parts[2][k / 4]);
+          }
 #pragma unroll
-            for (int x = 0; x < 3; ++x) {
-              const int col = x * R + col0 + k;  // of the parts side by side
-              uint8_t *d = pbuf + (col >> 6) * G::kPAtom + tok * 64 + ((((col & 63) >> 4) ^ ((tok >> 1) & 3)) << 4) + (col & 15);
-              if constexpr (kStep == 16) *reinterpret_cast<uint4 *>(d) = make_uint4(parts[x][0], parts[x][1], parts[x][2], parts[x][3]);
-              else *reinterpret_cast<uint2 *>(d) = make_uint2(parts[x][0], parts[x][1]);
-            }
+          for (int y = 0; y < 3; ++y) {
+            const int col = y * R + col0;  // of the parts side by side
+            *reinterpret_cast<uint4 *>(pbuf + (col >> 6) * G::kPAtom + tok * 64 + ((((col & 63) >> 4) ^ ((tok >> 1) & 3)) << 4)) =
+                make_uint4(parts[y][0], parts[y][1], parts[y][2], parts[y][3]);
           }
         }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(smem_u32(&b.p_full[g & 1]));
-        if (i == 0 && done_g >= 0) finish();
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&b.p_full[pb]));
+        if (i == first && done_g >= 0) finish((begun - 1) & 1);
       }
-      warp_col_sums<C>(l, s_part[quad] + col0);
+      if (leave) break;
+      float sum[C];
+#pragma unroll
+      for (int k = 0; k < C / 2; ++k) {
+        const float2 v = apart(l[k]);
+        sum[2 * k] = v.x, sum[2 * k + 1] = v.y;
+      }
+      warp_col_sums<C>(sum, s_part[group][quad]);
       soft_sync(group);
-      if (tok < C && ok) {
-        const int k = col0 + tok;
-        p.part_ml[slot_of(w) + k] = make_float2(s_mb[k], (s_part[0][k] + s_part[1][k]) + (s_part[2][k] + s_part[3][k]));
+      if (tok < C) {
+        const float *s4 = s_part[group][0] + tok;
+        if (ok) p.part_ml[slot_of(u, first) + tok] = make_float2(mb_of[tok], (s4[0] + s4[C]) + (s4[2 * C] + s4[3 * C]));
+        mb_of[tok] = kNone;  // no reference yet: any score outgrows it
       }
       soft_sync(group);
-      done = w, done_g = g - 1, done_unit = live - 1;
+      done_g = x_g, done_unit = unit, done_i = first, ++begun;
+      g += ntiles;
     }
-    if (done_g >= 0) finish();
+    if (done_g >= 0 && ok) {  // (after an expired wait there is no output)
+      // (nothing has waited for this product yet)
+      wait(&b.pv_done[done_g % G::kNP], done_g / G::kNP);
+      if (ok) finish((begun - 1) & 1);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kLoadWarp + 1) asm volatile("cp.async.wait_all;" ::: "memory");
-  if (s_abort && lane == 0 && (warp == kLoadWarp || warp == kLoadWarp + 1)) {
+  if (warp == kLoadWarp) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (s_abort && warp == kLoadWarp && lane == 0) {
     // after an expired wait: copies in flight land before the block gives its memory back
-    const int stages = warp == kLoadWarp ? G::kNK : G::kNV;
-    unsigned long long *full = warp == kLoadWarp ? b.k_full : b.v_full;
-    for (int x = max(0, g - stages); x < g; ++x) mbar_drain(smem_u32(&full[x % stages]), (x / stages) & 1);
+    for (int x = max(0, g - G::kNK); x < g; ++x) mbar_drain(smem_u32(&b.k_full[x % G::kNK]), (x / G::kNK) & 1);
+    for (int x = max(0, g - G::kNV); x < g; ++x) mbar_drain(smem_u32(&b.v_full[x % G::kNV]), (x / G::kNV) & 1);
   }
-  if (warp == kMmaWarp) tmem_dealloc(tmem, G::kTmem);
+  if (warp == kScoreWarp) tmem_dealloc(tmem, G::kTmem);
 }
 
 // The output of each row from its units: sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M)
@@ -851,24 +1057,26 @@ __global__ void __launch_bounds__(256, 6) k_quant_join(const QuantAttnParams p) 
   int ctx, len;
   const int nc = context_chunks(p, n, ctx, len);
   const int h = hq / t.group, r = node * t.group + hq - h * t.group, mt = r / p.R, row = r - mt * p.R;
-  const int64_t first = (((int64_t)n * t.kv_heads + h) * p.mtiles + mt) * p.slots * p.R + row;
+  const int teams = kGroups * kCols / p.R;  // partial results of a unit
+  const int64_t first = (((int64_t)n * t.kv_heads + h) * p.mtiles + mt) * p.slots * teams * p.R + row;
   const float *po = p.part_o + first * D + lane * E;
   const float2 *ml = p.part_ml + first;
   pdl_wait();
-  float2 a[2];  // partial results lane and 32 + lane (at most kTreeMaxChunks)
-  const int live = node < len ? nc + 1 : 0;
-  for (int q = 0; q < 2; ++q) a[q] = q * 32 + lane < live ? __ldcg(&ml[(q * 32 + lane) * p.R]) : make_float2(kNone, 0.f);
-  const float M = warp_max(fmaxf(a[0].x, a[1].x));
-  const float w[2] = {ex2(a[0].x - M), ex2(a[1].x - M)};
-  const float L = warp_sum(w[0] * a[0].y + w[1] * a[1].y);
-  float acc[E] = {};
+  const int live = node < len ? (nc + 1) * teams : 0;
+  float M = kNone, L = 0.f, acc[E] = {};
+  // 32 partial results at a time, one a lane
+  for (int k0 = 0; k0 < live; k0 += 32) {
+    const float2 a = k0 + lane < live ? __ldcg(&ml[(int64_t)(k0 + lane) * p.R]) : make_float2(kNone, 0.f);
+    const float top = fmaxf(M, warp_max(a.x)), f0 = ex2(M - top), wk = a.y != 0.f ? ex2(a.x - top) : 0.f;
+    M = top, L = fmaf(L, f0, warp_sum(wk * a.y));
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int k1 = min(live, q * 32 + 32);
+    for (int e = 0; e < E; ++e) acc[e] *= f0;
+    const int k1 = min(live - k0, 32);
 #pragma unroll 4
-    for (int k = q * 32; k < k1; ++k) {
-      const float f = __shfl_sync(DC_FULL_MASK, w[q], k & 31);
-      const float *src = po + (int64_t)k * p.R * D;
+    for (int k = 0; k < k1; ++k) {
+      const float f = __shfl_sync(DC_FULL_MASK, wk, k);
+      if (f == 0.f) continue;  // (an empty one holds nothing; NaN goes on)
+      const float *src = po + (int64_t)(k0 + k) * p.R * D;
       if constexpr (E == 4) {
         const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
         acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
@@ -903,6 +1111,20 @@ bool encode_cache(CUtensorMap *map, const QuantAttnParams &p, const void *base, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same of the tree's own K or V: (64 elements, nodes, head, request) of a 16-bit type.
+bool encode_nodes(CUtensorMap *map, const TreeAttnParams &t, const void *base, int64_t st, int64_t sh, int64_t sn) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const auto bytes = [&](int n, int64_t s) { return (cuuint64_t)(n > 1 ? s * 2 : t.head_dim * 2); };
+  const cuuint64_t dims[4] = {(cuuint64_t)t.head_dim, (cuuint64_t)t.T, (cuuint64_t)t.kv_heads, (cuuint64_t)t.N};
+  const cuuint64_t strides[3] = {bytes(t.T, st), bytes(t.kv_heads, sh), bytes(t.N, sn)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)t.tree_box, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, t.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int R, bool F16>
 cudaError_t launch(const QuantAttnParams &p, const QuantMaps &maps, unsigned grid, cudaStream_t st) {
   const size_t smem = Geom8<D, R, F16 ? 3 : 2>::kSmem + 1024;
@@ -928,7 +1150,9 @@ cudaError_t launch_all(const QuantAttnParams &p, const QuantMaps &maps, unsigned
 cudaError_t launch_quant_attention(const QuantAttnParams &p, cudaStream_t st) {
   QuantMaps maps;
   if (!encode_cache(&maps.k, p, p.k_cache, p.kc_st, p.kc_sh, p.kc_sp) ||
-      !encode_cache(&maps.v, p, p.v_cache, p.vc_st, p.vc_sh, p.vc_sp))
+      !encode_cache(&maps.v, p, p.v_cache, p.vc_st, p.vc_sh, p.vc_sp) ||
+      !encode_nodes(&maps.k_new, p.t, p.t.k_new, p.t.kn_st, p.t.kn_sh, p.t.kn_sn) ||
+      !encode_nodes(&maps.v_new, p.t, p.t.v_new, p.t.vn_st, p.t.vn_sh, p.t.vn_sn))
     return cudaErrorInvalidValue;
   const int64_t most = (int64_t)p.t.N * p.t.kv_heads * p.mtiles * p.slots;
   const unsigned grid = (unsigned)(most < p.sms ? most : p.sms);
