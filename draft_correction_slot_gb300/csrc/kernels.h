@@ -278,6 +278,7 @@ struct QuantAttnParams {
   // chunks of the context (see quant_chunk_tiles), and the most units of a
   // request: its chunks and the tree; a unit leaves kQuantRows / R partial results
   int items, sms, chunk_cap, slots;
+  uint8_t *q_parts; // [(n, K/V head, row tile)], quant_q_bytes each
   float *part_o;   // [(n, K/V head, row tile)][slots][kQuantRows / R][R][head_dim]
   float2 *part_ml; // the same without head_dim (log2 reference, sum)
 };
@@ -290,6 +291,8 @@ __host__ __device__ inline int quant_chunk_tiles(int nt, int items, int sms, int
   if (c < least) c = least;
   return c < 1 ? 1 : c;
 }
+// Bytes of a row tile's Q: `parts` of 8 bits and one form of 16, and two factors a row.
+__host__ __device__ inline int64_t quant_q_bytes(int parts, int R, int D) { return (int64_t)(parts + 2) * R * D + 8 * R; }
 cudaError_t launch_quant_attention(const QuantAttnParams &p, cudaStream_t st);
 
 // Tokens' K/V into such a cache: a tree's accepted path, or ragged prompts.

@@ -24,6 +24,7 @@ struct dcoco_tree_handle {
   int *err = nullptr;
   float2 *part_ml = nullptr;
   float4 *part_o = nullptr;
+  uint8_t *q_parts = nullptr;         // cache in 8 bits: Q as the products take it
   cudaStream_t last_stream = nullptr;
   long long launches = 0;
 };
@@ -246,7 +247,7 @@ static int create(const dcoco_tree_config *cfg, int scale_shift, dcoco_tree_hand
   // of either kernel its own chunks and rows (the most nodes that a number of row
   // tiles stands for have the most rows)
   const int group = cfg->q_heads / cfg->kv_heads, pairs = cfg->max_batch * cfg->kv_heads;
-  size_t rows = 0;
+  size_t rows = 0, q_bytes = 0;
   const auto reach = [&](int nodes) {
     const RowTiles rt(*cfg, nodes);
     const int n = most_chunks(max_tiles, pairs * rt.mtiles, h->sms, chunk_cap(*cfg, rt.few));
@@ -265,6 +266,7 @@ static int create(const dcoco_tree_config *cfg, int scale_shift, dcoco_tree_hand
       const size_t r = (size_t)pairs * m * n * dc::kQuantRows;  // (few rows have as many partial results more)
       if (r > rows) rows = r;
     }
+    q_bytes = (size_t)pairs * most_tiles * dc::quant_q_bytes(3, dc::quant_rows(most_rows), cfg->head_dim);
   } else {
     if (few_nodes >= 1) reach(few_nodes < cfg->max_tree ? few_nodes : cfg->max_tree);
     for (int nodes = tile_nodes; nodes - tile_nodes < cfg->max_tree; nodes += tile_nodes)
@@ -273,7 +275,7 @@ static int create(const dcoco_tree_config *cfg, int scale_shift, dcoco_tree_hand
   }
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t at_ml = 256, at_o = at_ml + up(rows * sizeof(float2));
-  const size_t bytes = at_o + rows * cfg->head_dim * sizeof(float);
+  const size_t at_q = at_o + up(rows * cfg->head_dim * sizeof(float)), bytes = at_q + q_bytes;
   if (cudaMalloc(&h->block, bytes) != cudaSuccess) {
     cudaGetLastError();
     delete h;
@@ -283,6 +285,7 @@ static int create(const dcoco_tree_config *cfg, int scale_shift, dcoco_tree_hand
   h->err = reinterpret_cast<int *>(base);
   h->part_ml = reinterpret_cast<float2 *>(base + at_ml);
   h->part_o = reinterpret_cast<float4 *>(base + at_o);
+  h->q_parts = reinterpret_cast<uint8_t *>(base + at_q);
   if (cudaMemset(base, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     cudaFree(h->block);
@@ -385,9 +388,9 @@ int dcoco_tree_attention_quant(dcoco_tree_handle *h, int batch, int nodes, const
   p.t.tree_box = nodes < dc::kQuantNodes ? (nodes + 7) / 8 * 8 : dc::kQuantNodes;
   p.items = c.max_batch * c.kv_heads * p.mtiles, p.sms = h->sms, p.chunk_cap = quant_chunk_cap(c);
   p.slots = h->quant_slots[p.mtiles];
-  p.part_o = reinterpret_cast<float *>(h->part_o), p.part_ml = h->part_ml;
+  p.part_o = reinterpret_cast<float *>(h->part_o), p.part_ml = h->part_ml, p.q_parts = h->q_parts;
   h->last_stream = static_cast<cudaStream_t>(stream);
-  h->launches += 2;
+  h->launches += 3;
   return cuda_status(dc::launch_quant_attention(p, h->last_stream));
 }
 

@@ -39,12 +39,7 @@
 namespace dc {
 namespace {
 
-constexpr int kGroup = 128, kGroups = 4;  // softmax threads of a group, groups
-constexpr int kCols = 16;                 // rows of a group
-constexpr int kScoreWarp = 16, kOutWarp = 17, kLoadWarp = 18, kPrepWarp = 19;
-constexpr int kThreads = 640;  // five warpgroups
-// Registers a thread: 96 at launch (65,536 / 640 in steps of 8), then 4 x 104 + 64 = 5 x 96.
-constexpr int kSoftRegs = 104, kOtherRegs = 64;
+constexpr int kGroup = 128;    // softmax threads of a group
 constexpr int kTreeNodes = kQuantNodes;  // nodes of a tree tile
 constexpr int kAhead = 16, kUnits = 32;  // units whose row factors and odd nodes are kept; whose description is
 constexpr float kTop = 7.f;     // log2 of a weight at its row's reference
@@ -56,13 +51,18 @@ struct QuantMaps {
 
 template <int D, int R, int NP>
 struct Geom8 {
-  // The four softmax groups are teams that take the tiles in turn, R rows of a tile each
-  static constexpr int kTeams = kGroups * kCols / R, kParts = R / kCols;  // teams, groups of a team
+  // Softmax groups and rows of one.  The groups are teams that take the tiles in turn, R rows of a tile each.
+  static constexpr int kGroups = 4, kCols = 64 / kGroups;
+  static constexpr int kTeams = 64 / R, kParts = R / kCols;  // teams, groups of a team
+  static constexpr int kScoreWarp = 4 * kGroups, kOutWarp = kScoreWarp + 1, kLoadWarp = kScoreWarp + 2,
+                       kPrepWarp = kScoreWarp + 3, kThreads = 32 * (kScoreWarp + 4);
+  // Registers a thread: 96 at launch (65,536 / 640 in steps of 8), then 4 x 104 + 64 = 5 x 96.
+  static constexpr int kSoftRegs = 104, kOtherRegs = 64;
   static constexpr int kNS = 2 * kTeams, kNP = kTeams > 2 ? kTeams : 2;   // buffers of S and of P
   static constexpr uint32_t kTileBytes = kTile * D;        // a context tile of K or V; a tree tile takes the same
   // K's products run ahead of V's, and a tile's V stays until its weights are there: V's ring is the longer one
   static constexpr int kNK = D == 64 ? 5 : R == 64 && NP == 3 ? 2 : 3, kNV = D == 64 ? 8 : R == 64 ? 5 : 7;
-  static constexpr uint32_t kQPart = R * D, kQBytes = NP * kQPart;
+  static constexpr uint32_t kQPart = R * D, kQBytes = NP * kQPart, kQTree = 2 * kQPart;  // a unit's Q in parts, in 16 bits
   static constexpr int kPAtoms = (3 * R + 63) / 64;        // 64-byte column blocks of P
   static constexpr uint32_t kPAtom = kTile * 64, kPBytes = kPAtoms * kPAtom;
   // V before P: products over 64 elements read as many rows of M past a V stage,
@@ -80,8 +80,8 @@ struct Geom8 {
 };
 
 struct Bars8 {
-  unsigned long long q_empty[2], k_full[8], k_empty[8], v_full[8], v_empty[8];
-  unsigned long long s_full[8], s_free[8], p_full[4], pv_done[4], o_free[kGroups][2], units[kUnits], factors[kAhead], done[2];
+  unsigned long long q_full[2], q_empty[2], k_full[8], k_empty[8], v_full[8], v_empty[8];
+  unsigned long long s_full[8], s_free[8], p_full[4], pv_done[4], o_free[4][2], units[kUnits], factors[kAhead], done[2];
 };
 
 // D[tmem] (+)= A[smem] B[smem], 8-bit operands
@@ -97,6 +97,12 @@ __device__ __forceinline__ void mma8(uint32_t tmem_d, uint32_t a_lo, uint32_t b_
 }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead = 16) { return ((saddr & 0x3FFFFu) >> 4) | (lead >> 4) << 16; }
 
+// Contiguous bytes (16 at a time) from global to shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
 template <int C>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[C]) {
 #pragma unroll
@@ -383,7 +389,7 @@ __device__ __forceinline__ bool clean_node(uint8_t *row, bool there) {
 }
 
 template <int D, int R, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Geom8<D, R, F16 ? 3 : 2>::kThreads, 1)
 k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   constexpr int NP = F16 ? 3 : 2;
   using G = Geom8<D, R, NP>;
@@ -398,12 +404,12 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   __shared__ uint32_t s_odd[kAhead][8];                    // tree units: nodes whose V holds an infinity or NaN
   __shared__ float s_scale[G::kNV][2][8];                  // a V stage's tile: K and V scales of its blocks
   // of each group: its rows' references less kTop, rescale factors, and what its warps put together
-  __shared__ __align__(16) float s_mb[kGroups][kCols], s_f[kGroups][kCols], s_part[kGroups][4][kCols];
+  __shared__ __align__(16) float s_mb[G::kGroups][G::kCols], s_f[G::kGroups][G::kCols], s_part[G::kGroups][4][G::kCols];
   const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&b.q_empty[i]), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&b.q_full[i]), 1), mbar_init(smem_u32(&b.q_empty[i]), 1);
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&b.k_full[i]), 1), mbar_init(smem_u32(&b.k_empty[i]), 1);
       mbar_init(smem_u32(&b.v_full[i]), 33), mbar_init(smem_u32(&b.v_empty[i]), 1);
@@ -419,10 +425,10 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < kGroups * kCols) s_mb[tid / kCols][tid % kCols] = kNone;
-  if (warp == kLoadWarp && lane < 4)
+  if (tid < 64) s_mb[tid / G::kCols][tid % G::kCols] = kNone;
+  if (warp == G::kLoadWarp && lane < 4)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k + lane)) : "memory");
-  if (warp == kScoreWarp) tmem_alloc(smem_u32(&s_tmem), G::kTmem);
+  if (warp == G::kScoreWarp) tmem_alloc(smem_u32(&s_tmem), G::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -434,15 +440,15 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   const auto unit_at = [&](int unit) -> const QuantUnit & { return s_unit[unit & (kUnits - 1)]; };
   const auto units_bar = [&](int unit) { return smem_u32(&b.units[unit & (kUnits - 1)]); };
   const auto factors_bar = [&](int unit) { return smem_u32(&b.factors[unit & (kAhead - 1)]); };
-  if (warp >= kScoreWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kLoadWarp) {
+  if (warp >= G::kScoreWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+  if (warp == G::kLoadWarp) {
     // ------------------------------------------------------------ TMA for K and V, the scales
-    const int page_size = 1 << t.page_shift, box = min(page_size, kTile), boxes = kTile / box;
+    const int page_size = 1 << t.page_shift, box_shift = min(t.page_shift, 7), box = 1 << box_shift, boxes = kTile >> box_shift;
     const uint32_t box_bytes = box * D;
     // lanes 0-7 fetch K's scales of a tile, 8-15 V's: block j of the tile, in box box_j; its place in its
     // page is its place in the box where a box is a page
-    const int j = lane & 7, tok_j = j << p.scale_shift, box_j = min(tok_j, kTile - 1) / box;
+    const int j = lane & 7, tok_j = j << p.scale_shift, box_j = min(tok_j, kTile - 1) >> box_shift;
     const float *scale = lane < 8 ? p.k_scale : p.v_scale;
     const int64_t sp = lane < 8 ? p.ks_sp : p.vs_sp, sb = lane < 8 ? p.ks_sb : p.vs_sb, ss = lane < 8 ? p.ks_sh : p.vs_sh;
     scale += ((tok_j & (box - 1)) >> p.scale_shift) * sb;
@@ -495,7 +501,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
           }
           __syncwarp();
         } else {
-          const int used = min(boxes, (end - tok0 + box - 1) / box);  // copies of the tile
+          const int used = min(boxes, (end - tok0 + box - 1) >> box_shift);  // copies of the tile
           // (the pages first, then all copies by one lane: a shuffle and an election between copies cost 130 cycles each)
           int pg[kTile / 16];
 #pragma unroll
@@ -527,20 +533,19 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
         if (++vs == G::kNV) vs = 0, v_phase ^= 1;
       }
     }
-  } else if (warp == kPrepWarp) {
-    // ------------------------------------------------------------ units, Q parts
-    constexpr int kPer = D / 16, kRows = 32 / kPer;  // lanes of a row (16 elements each), rows a step
-    const int sub = lane / kPer, e0 = (lane % kPer) * 16;
-    const float c = t.scale * kLog2e;
+  } else if (warp == G::kPrepWarp) {
+    // ------------------------------------------------------------ units, their Q
     const bool flag = blockIdx.x == 0;
     QuantUnits it(p, flag);
+    QuantUnit w;
     bool ok = true, more = true;
     int made = 0;
+    pdl_wait();  // k_quant_q's Q
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     for (int unit = 0; ok; ++unit) {
       const int qb = unit & 1, slot = unit & (kAhead - 1);
       // Units are published ahead of their Q, up to nine: the loads of short ones run that far ahead.
       for (int k = 0; k < 2 && more && made <= unit + 8; ++k) {
-        QuantUnit w;
         do more = it.next(w, flag);
         while (more && w.ntiles == 0);
         if (!more) w.ntiles = 0;
@@ -554,78 +559,21 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
       if (unit >= 2) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_empty[qb]), ((unit >> 1) - 1) & 1, &s_abort, t.err));
       if (!ok) break;
       const QuantUnit &u = unit_at(unit);
-      const int ntiles = uni(u.ntiles), len = uni(u.len), r0 = uni(u.mt) * R;
-      const bool tree = uni(u.tree);
-      if (ntiles > 0) {
-        uint8_t *dst = smem + G::kQ + qb * G::kQBytes;
-        const uint16_t *q0 = t.q + u.n * t.q_sn + (int64_t)u.h * t.group * t.q_sh + e0;
-        // kFlight steps' loads in flight (one at a time a unit's Q took 16,000 cycles, more than its tiles)
-        constexpr int kSteps = R / kRows, kFlight = kSteps < 4 ? kSteps : 4;
-#pragma unroll 1
-        for (int s0 = 0; s0 < kSteps; s0 += kFlight) {
-          uint4 x[kFlight][2];
-#pragma unroll
-          for (int y = 0; y < kFlight; ++y) {
-            const int r = r0 + (s0 + y) * kRows + sub, node = r / t.group;
-            x[y][0] = x[y][1] = make_uint4(0, 0, 0, 0);
-            if (node < len) {
-              const uint4 *q = reinterpret_cast<const uint4 *>(q0 + node * t.q_st + (r - node * t.group) * t.q_sh);
-              x[y][0] = __ldg(q), x[y][1] = __ldg(q + 1);
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < kFlight; ++y) {
-            const int row = (s0 + y) * kRows + sub;
-            const uint32_t u8[8] = {x[y][0].x, x[y][0].y, x[y][0].z, x[y][0].w, x[y][1].x, x[y][1].y, x[y][1].z, x[y][1].w};
-            if (tree) {
-              uint8_t *d = dst + (e0 >> 6) * (R * 128) + row * 128;
-              const int chunk = (e0 & 63) >> 3;
-              *reinterpret_cast<uint4 *>(d + ((chunk ^ (row & 7)) << 4)) = x[y][0];
-              *reinterpret_cast<uint4 *>(d + (((chunk + 1) ^ (row & 7)) << 4)) = x[y][1];
-              if (lane % kPer == 0) s_factor[slot][row] = c;
-              continue;
-            }
-            float most = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              most = fmaxf(most, fmaxf(fabsf(unpack_lo<F16>(u8[j])), fabsf(unpack_lo<F16>(u8[j] >> 16))));
-#pragma unroll
-            for (int o = 1; o < kPer; o <<= 1) most = fmaxf(most, __shfl_xor_sync(DC_FULL_MASK, most, o));
-            // the power of two that brings the row's largest to 128..256 (rows below 2^-100 count as of that
-            // size; a row with an infinity becomes NaN)
-            const int e = max((int)(__float_as_uint(most) >> 23), 27);
-            const float mul = __uint_as_float(e < 255 ? (uint32_t)(261 - e) << 23 : 0x7FC00000u);
-            if (lane % kPer == 0) s_factor[slot][row] = c * __uint_as_float((uint32_t)min(e - 7, 254) << 23);
-            uint8_t *d = dst + row * D + (((e0 >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
-            uint32_t h[NP][4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              // (fp16 holds either type's elements of that size but for what lies below 2^-24)
-              uint32_t f = pack2<true>(unpack_lo<F16>(u8[j]) * mul, unpack_lo<F16>(u8[j] >> 16) * mul);
-#pragma unroll
-              for (int k = 0; k < NP; ++k) {
-                uint16_t y;
-                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(y) : "r"(f));
-                if (k + 1 < NP) {
-                  uint32_t back;
-                  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(y));
-                  f = hsub2(f, back);
-                }
-                h[k][j >> 1] = j & 1 ? h[k][j >> 1] | (uint32_t)y << 16 : y;
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < NP; ++k)
-              *reinterpret_cast<uint4 *>(d + k * G::kQPart) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
-          }
-        }
-        fence_proxy_async();
+      if (u.ntiles == 0) {  // the end
+        if (lane == 0) mbar_arrive(factors_bar(unit));
+        break;
+      }
+      if (lane == 0) {
+        const uint8_t *src = p.q_parts + (((int64_t)u.n * t.kv_heads + u.h) * p.mtiles + u.mt) * quant_q_bytes(NP, R, D);
+        const uint32_t bytes = u.tree ? G::kQTree : G::kQBytes, q_bar = smem_u32(&b.q_full[qb]);
+        mbar_arrive_expect_tx(q_bar, bytes);
+        bulk_load(sbase + G::kQ + qb * G::kQBytes, src + (u.tree ? G::kQBytes : 0), bytes, q_bar);
+        mbar_arrive_expect_tx(factors_bar(unit), R * 4);
+        bulk_load(smem_u32(s_factor[slot]), src + G::kQBytes + G::kQTree + (u.tree ? R * 4 : 0), R * 4, factors_bar(unit));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(factors_bar(unit));
-      if (ntiles == 0) break;
     }
-  } else if (warp == kScoreWarp) {
+  } else if (warp == G::kScoreWarp) {
     // ------------------------------------------------------------ tensor core: S^T = K Q^T
     constexpr uint32_t kId = (1u << 4) | (8u << 24) | (uint32_t)(R >> 3) << 17;  // fp32 += e4m3 e4m3, M = 128, N = R
     constexpr uint32_t kId16 = F16 ? idesc_f16(128, R) : idesc_bf16(128, R);
@@ -633,11 +581,13 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
     int ks = 0, k_phase = 0;
     for (int unit = 0; ok; ++unit) {
       const int qb = unit & 1;
-      ok = __all_sync(DC_FULL_MASK, bar_wait(factors_bar(unit), (unit / kAhead) & 1, &s_abort, t.err));
+      ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
       if (!ok) break;
       const int ntiles = uni(unit_at(unit).ntiles);
       const bool tree = uni(unit_at(unit).tree);
       if (ntiles == 0) break;
+      ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (unit >> 1) & 1, &s_abort, t.err));
+      if (!ok) break;
       const uint32_t sq = desc_lo(sbase + G::kQ + qb * G::kQBytes);
       for (int i = 0; i < ntiles; ++i, ++g) {
         const int sb = g % G::kNS;
@@ -673,7 +623,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
       mbar_drain(smem_u32(&b.done[0]), 0);
     }
     __syncwarp();
-  } else if (warp == kOutWarp) {
+  } else if (warp == G::kOutWarp) {
     // ------------------------------------------------------------ tensor core: O^T += V^T P^T
     constexpr uint32_t kId =  // B e5m2; both M- and N-major
         (1u << 4) | (8u << 24) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t)(3 * R >> 3) << 17;
@@ -728,11 +678,11 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftRegs));
     // ------------------------------------------------------------ softmax, output
     // Each team of groups takes every kTeams-th tile, with references, sums and O of its own; a unit's
     // tiles i, i + kTeams, ... make a partial result of their own, whichever team has them.
-    constexpr int C = kCols;
+    constexpr int C = G::kCols;
     const int group = warp >> 2, quad = warp & 3, tok = tid & (kGroup - 1);
     const int team = group / G::kParts, col0 = group % G::kParts * C;  // this group's rows: columns col0 .. col0 + C - 1
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + col0;
@@ -980,24 +930,27 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
                   make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         } else {
-          uint32_t parts[3][C / 4];
 #pragma unroll
-          for (int k = 0; k < C; k += 4) {
-            float e[4];
+          for (int k0 = 0; k0 < C; k0 += 16) {  // rows of a store
+            uint32_t parts[3][4];
 #pragma unroll
-            for (int z = 0; z < 4; z += 2) {
-              const int at = (k + z) / 2;
-              const float2 v = apart(x[at]);
-              e[z] = ex2(v.x), e[z + 1] = ex2(v.y);
-              l[at] = fma2(both(e[z], e[z + 1]), inv2, l[at]);
+            for (int k = 0; k < 16; k += 4) {
+              float e[4];
+#pragma unroll
+              for (int z = 0; z < 4; z += 2) {
+                const int at = (k0 + k + z) / 2;
+                const float2 v = apart(x[at]);
+                e[z] = ex2(v.x), e[z + 1] = ex2(v.y);
+                l[at] = fma2(both(e[z], e[z + 1]), inv2, l[at]);
+              }
+              split4(e, parts[0][k / 4], parts[1][k / 4], parts[2][k / 4]);
             }
-            split4(e, parts[0][k / 4], parts[1][k / 4], parts[2][k / 4]);
-          }
 #pragma unroll
-          for (int y = 0; y < 3; ++y) {
-            const int col = y * R + col0;  // of the parts side by side
-            *reinterpret_cast<uint4 *>(pbuf + (col >> 6) * G::kPAtom + tok * 64 + ((((col & 63) >> 4) ^ ((tok >> 1) & 3)) << 4)) =
-                make_uint4(parts[y][0], parts[y][1], parts[y][2], parts[y][3]);
+            for (int y = 0; y < 3; ++y) {
+              const int col = y * R + col0 + k0;  // of the parts side by side
+              *reinterpret_cast<uint4 *>(pbuf + (col >> 6) * G::kPAtom + tok * 64 + ((((col & 63) >> 4) ^ ((tok >> 1) & 3)) << 4)) =
+                  make_uint4(parts[y][0], parts[y][1], parts[y][2], parts[y][3]);
+            }
           }
         }
         fence_proxy_async();
@@ -1033,13 +986,81 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kLoadWarp) asm volatile("cp.async.wait_all;" ::: "memory");
-  if (s_abort && warp == kLoadWarp && lane == 0) {
+  if (warp == G::kLoadWarp) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (s_abort && warp == G::kPrepWarp && lane == 0)
+    for (int i = 0; i < 2; ++i) mbar_drain(smem_u32(&b.q_full[i]), 0), mbar_drain(smem_u32(&b.q_full[i]), 1);
+  if (s_abort && warp == G::kLoadWarp && lane == 0) {
     // after an expired wait: copies in flight land before the block gives its memory back
     for (int x = max(0, g - G::kNK); x < g; ++x) mbar_drain(smem_u32(&b.k_full[x % G::kNK]), (x / G::kNK) & 1);
     for (int x = max(0, g - G::kNV); x < g; ++x) mbar_drain(smem_u32(&b.v_full[x % G::kNV]), (x / G::kNV) & 1);
   }
-  if (warp == kScoreWarp) tmem_dealloc(tmem, G::kTmem);
+  if (warp == G::kScoreWarp) tmem_dealloc(tmem, G::kTmem);
+}
+
+// Q as the units' products take it: of each row tile of a K/V head the rows' parts of
+// e4m3 (NP of R x D bytes), the rows in 16 bits ([64-element block][row]), both swizzled as
+// shared memory has them, then the rows' factors, of either form.  A warp a row.
+// (Once for each row tile, in a kernel of its own: by a warp of the attention's blocks a
+// unit's Q took up to 30,000 cycles, more than its tiles.)
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) k_quant_q(const QuantAttnParams p) {
+  constexpr int NP = F16 ? 3 : 2, E = D / 32;
+  const TreeAttnParams &t = p.t;
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, R = p.R;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);  // row of all row tiles
+  if (i >= (int64_t)t.N * t.kv_heads * p.mtiles * R) return;
+  const int64_t item = i / R, pair = item / p.mtiles;
+  const int row = (int)(i - item * R), mt = (int)(item - pair * p.mtiles);
+  const int n = (int)(pair / t.kv_heads), h = (int)(pair - (int64_t)n * t.kv_heads);
+  const int r = mt * R + row, node = r / t.group;
+  const int len = t.tree_len ? min(max(t.tree_len[n], 0), t.T) : t.T;
+  uint32_t x[E / 2];
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) x[k] = 0u;
+  if (node < len) {
+    const uint16_t *q = t.q + n * t.q_sn + node * t.q_st + (h * t.group + r - node * t.group) * t.q_sh + lane * E;
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) x[k] = __ldg(reinterpret_cast<const uint32_t *>(q) + k);
+  }
+  float most = 0.f;
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) most = fmaxf(most, fmaxf(fabsf(unpack_lo<F16>(x[k])), fabsf(unpack_lo<F16>(x[k] >> 16))));
+  most = warp_max(most);
+  // the power of two that brings the row's largest to 128..256 (rows below 2^-100 count as of that size; a
+  // row with an infinity becomes NaN)
+  const int e = max((int)(__float_as_uint(most) >> 23), 27);
+  const float mul = __uint_as_float(e < 255 ? (uint32_t)(261 - e) << 23 : 0x7FC00000u), c = t.scale * kLog2e;
+  uint8_t *dst = p.q_parts + item * quant_q_bytes(NP, R, D);
+  const int at = lane * E;
+  const int off = row * D + (((at >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4) + (at & 15);
+  uint16_t part[NP][E / 2];
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    // (fp16 holds either type's elements of that size but for what lies below 2^-24)
+    uint32_t f = pack2<true>(unpack_lo<F16>(x[k]) * mul, unpack_lo<F16>(x[k] >> 16) * mul);
+#pragma unroll
+    for (int y = 0; y < NP; ++y) {
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(part[y][k]) : "r"(f));
+      uint32_t back;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(part[y][k]));
+      f = hsub2(f, back);
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < NP; ++y) {
+    if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst + y * R * D + off) = part[y][0] | (uint32_t)part[y][1] << 16;
+    else *reinterpret_cast<uint16_t *>(dst + y * R * D + off) = part[y][0];
+  }
+  dst += NP * R * D;
+  uint8_t *wide = dst + (at >> 6) * (R * 128) + row * 128 + ((((at & 63) >> 3) ^ (row & 7)) << 4) + (at & 7) * 2;
+  if constexpr (E == 4) *reinterpret_cast<uint2 *>(wide) = make_uint2(x[0], x[1]);
+  else *reinterpret_cast<uint32_t *>(wide) = x[0];
+  if (lane == 0) {
+    float *factor = reinterpret_cast<float *>(dst + 2 * R * D);
+    factor[row] = c * __uint_as_float((uint32_t)min(e - 7, 254) << 23);
+    factor[R + row] = c;
+  }
 }
 
 // The output of each row from its units: sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M)
@@ -1057,7 +1078,7 @@ __global__ void __launch_bounds__(256, 6) k_quant_join(const QuantAttnParams p) 
   int ctx, len;
   const int nc = context_chunks(p, n, ctx, len);
   const int h = hq / t.group, r = node * t.group + hq - h * t.group, mt = r / p.R, row = r - mt * p.R;
-  const int teams = kGroups * kCols / p.R;  // partial results of a unit
+  const int teams = kQuantRows / p.R;  // partial results of a unit
   const int64_t first = (((int64_t)n * t.kv_heads + h) * p.mtiles + mt) * p.slots * teams * p.R + row;
   const float *po = p.part_o + first * D + lane * E;
   const float2 *ml = p.part_ml + first;
@@ -1131,13 +1152,16 @@ cudaError_t launch(const QuantAttnParams &p, const QuantMaps &maps, unsigned gri
   const cudaError_t e =
       cudaFuncSetAttribute(k_quant_attn<D, R, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k_quant_attn<D, R, F16><<<grid, kThreads, smem, st>>>(p, maps);
-  return cudaGetLastError();
+  return launch_ex(k_quant_attn<D, R, F16>, dim3(grid), dim3(Geom8<D, R, F16 ? 3 : 2>::kThreads), smem, st, true, 0, p, maps);
 }
 
 template <int D, bool F16>
 cudaError_t launch_all(const QuantAttnParams &p, const QuantMaps &maps, unsigned grid, cudaStream_t st) {
-  const cudaError_t e = p.R == 16   ? launch<D, 16, F16>(p, maps, grid, st)
+  const int64_t q_rows = (int64_t)p.t.N * p.t.kv_heads * p.mtiles * p.R;
+  k_quant_q<D, F16><<<(unsigned)((q_rows + 7) / 8), 256, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = p.R == 16   ? launch<D, 16, F16>(p, maps, grid, st)
                         : p.R == 32 ? launch<D, 32, F16>(p, maps, grid, st)
                                     : launch<D, 64, F16>(p, maps, grid, st);
   if (e != cudaSuccess) return e;
