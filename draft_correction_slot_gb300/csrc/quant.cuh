@@ -14,10 +14,14 @@ namespace {
 // falls below e4m3's least step, 2^-9.
 constexpr int kScaleLow = -64, kScaleHigh = 64;
 
+// Two finite values to e4m3, to nearest even, at most 448.
+__device__ __forceinline__ uint32_t finite_e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
 // Two values to e4m3, to nearest even.  Infinities become NaN like NaN itself:
 // a largest finite value in their place would pass for data.
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
-  uint32_t r = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  uint32_t r = finite_e4m3x2(a, b);
   if ((__float_as_uint(a) & 0x7F800000u) == 0x7F800000u) r |= 0x7Fu;
   if ((__float_as_uint(b) & 0x7F800000u) == 0x7F800000u) r |= 0x7F00u;
   return r;

@@ -7,11 +7,15 @@
 //   s = need (no token of the block committed before), else max(s0, need)
 //   new payload rn(x / s);  committed payload y: rn(y s0 / s) where s > s0.
 //
-// A warp has a block: 16 bytes of a token a lane, so 32 / (D / 8) tokens a step,
-// eight steps in flight.  What fits in these stays in registers between the
-// maximum and the rounding; longer blocks are read again (from L1 or L2).
+// A warp has a block: 16 bytes of a token a lane, so 32 / (D / 8) tokens a step, four
+// (append) or eight (commit) steps in flight.  What fits in these stays in registers
+// between the maximum and the rounding; longer blocks are read again (from L1 or L2).
 // Nothing is shared between warps, so a request's result depends on its own
 // tokens alone.
+// Append: 8 prompts of up to 2000 tokens, 16 layers x 8 heads of 64, blocks of 64: 127 us,
+// 3.8 TB/s of the 6.8 that a copy reaches; bound by the chain lengths, page, tokens, maximum, rounding
+// of each warp.  Commit: 32 trees of 64 nodes, 16 layers: 17 us with its call, bound
+// by latency as tree_commit.cu's.
 #include "kernels.h"
 #include "quant.cuh"
 
@@ -20,13 +24,14 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxNodes = 256;
-constexpr int kSteps = 8;  // 16-byte loads in flight a lane
+constexpr int kAppendSteps = 4;  // 8 prompts of up to 2000 tokens: 127 us; 140 with 8 steps, 200 with 16 (fewer warps an SM)
 
-__device__ __forceinline__ void unpack8(const uint4 &w, bool f16, float (&x)[8]) {
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (f16) {
+    if constexpr (F16) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     } else {
@@ -37,12 +42,13 @@ __device__ __forceinline__ void unpack8(const uint4 &w, bool f16, float (&x)[8])
 
 // One block's `count` new tokens, the first at place `old` of the block; row(i)
 // is the i-th one's source.  dst: the block's first token in the cache.
-template <class Row>
-__device__ __forceinline__ void write_block(int D, bool f16, int old, int count, Row row, uint8_t *dst, int64_t stride,
+template <int D, bool F16, int kSteps, class Row>
+__device__ __forceinline__ void write_block(int old, int count, Row row, uint8_t *dst, int64_t stride,
                                             float *scale) {
-  const int lane = threadIdx.x & 31, per = D / 8, step = 32 / per, sub = lane / per, e = (lane - sub * per) * 8;
+  constexpr int per = D / 8, step = 32 / per;
+  const int lane = threadIdx.x & 31, sub = lane / per, e = lane % per * 8;
   uint4 w[kSteps];
-  float most = 0.f;
+  float most = 0.f, odd = 0.f;  // (odd becomes NaN with an infinity or NaN)
   for (int i0 = 0; i0 < count; i0 += step * kSteps) {
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
@@ -51,8 +57,19 @@ __device__ __forceinline__ void write_block(int D, bool f16, int old, int count,
     }
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
+      if (i0 + k * step >= count) break;
       float x[8];
-      unpack8(w[k], f16, x);
+      unpack8<F16>(w[k], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) odd = fmaf(x[j], 0.f, odd), most = fmaxf(most, fabsf(x[j]));
+    }
+  }
+  const bool finite = !__any_sync(DC_FULL_MASK, odd != odd);
+  if (!finite) {  // rare: once more over what does count
+    most = 0.f;
+    for (int i = sub; i < count; i += step) {
+      float x[8];
+      unpack8<F16>(__ldg(reinterpret_cast<const uint4 *>(row(i) + e)), x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]) < INFINITY ? fabsf(x[j]) : 0.f);
     }
@@ -76,6 +93,10 @@ __device__ __forceinline__ void write_block(int D, bool f16, int old, int count,
       *at = make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
     }
   }
+  // A power of two (any scale that was made here) is divided by exactly by its inverse; divisions
+  // of 8 elements took as long as all the rest (8 prompts of up to 2000 tokens: 183 us with them).
+  const bool power = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
+  const float inv = power ? 1.f / s : 1.f;
   const bool kept = count <= step * kSteps;
   for (int i0 = 0; i0 < count; i0 += step * kSteps) {
 #pragma unroll
@@ -86,11 +107,14 @@ __device__ __forceinline__ void write_block(int D, bool f16, int old, int count,
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       const int i = i0 + k * step + sub;
+      if (i0 + k * step >= count) break;
       float x[8];
-      unpack8(w[k], f16, x);
+      unpack8<F16>(w[k], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = power ? x[j] * inv : x[j] / s;
       uint32_t r[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) r[j] = to_e4m3x2(x[2 * j] / s, x[2 * j + 1] / s);
+      for (int j = 0; j < 4; ++j) r[j] = finite ? finite_e4m3x2(x[2 * j], x[2 * j + 1]) : to_e4m3x2(x[2 * j], x[2 * j + 1]);
       if (i < count) *reinterpret_cast<uint2 *>(dst + (old + i) * stride + e) = make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
     }
   }
@@ -114,19 +138,20 @@ struct Side {
 
 // The new tokens of request n in the block of position pos (the first of them)
 // up to position `end`; row(i): source of the token at pos + i.  -> error bits
-template <class Row>
+template <int D, bool F16, int kSteps, class Row>
 __device__ __forceinline__ int write_at(const QuantWriteParams &p, const Side &a, int n, int h, int pos, int end, Row row) {
   const int block = 1 << p.scale_shift, b0 = pos & ~(block - 1);
   if ((pos >> p.page_shift) >= p.max_pages) return kErrBadPage;
   const int page = __ldg(p.page_table + n * p.pt_stride + (pos >> p.page_shift));
   if (page < 0 || page >= p.num_pages) return kErrBadPage;
   const int slot = b0 & ((1 << p.page_shift) - 1);
-  write_block(p.head_dim, p.f16, pos - b0, min(end, b0 + block) - pos, row, a.cache + page * a.cp + slot * a.ct + h * a.ch,
+  write_block<D, F16, kSteps>(pos - b0, min(end, b0 + block) - pos, row, a.cache + page * a.cp + slot * a.ct + h * a.ch,
               a.ct, a.scale + page * a.sp + (slot >> p.scale_shift) * a.sb + h * a.ss);
   return 0;
 }
 
 // One block (of threads) a request, layer and K or V; each walks the tree itself.
+template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) k_quant_commit(const QuantWriteParams p) {
   __shared__ int s_tok[kMaxNodes], s_par[kMaxNodes], s_want[kMaxNodes], s_path[kMaxNodes];
   __shared__ int s_count;
@@ -175,13 +200,14 @@ __global__ void __launch_bounds__(kThreads) k_quant_commit(const QuantWriteParam
   for (int u = tid >> 5; u < blocks * p.kv_heads; u += kWarps) {
     const int b = u / p.kv_heads, h = u - b * p.kv_heads;
     const int pos = max(ctx, (first + b) << p.scale_shift);
-    bad |= write_at(p, a, n, h, pos, ctx + count,
+    bad |= write_at<D, F16, 8>(p, a, n, h, pos, ctx + count,
                     [&](int i) { return rows + s_path[pos - ctx + i] * a.st + h * a.sh; });
   }
   if (bad) atomicOr(p.err, bad);
 }
 
 // A warp a block of tokens and head; blockIdx.y: the layer's K or V.
+template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantWriteParams p) {
   const int lane = threadIdx.x & 31, capacity = p.max_pages << p.page_shift;
   int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -217,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantWriteParam
       const Side a(p, blockIdx.y >> 1, blockIdx.y & 1);
       const int pos = max(ctx, ((ctx >> p.scale_shift) + rel) << p.scale_shift);
       const uint16_t *rows = a.fresh + (int64_t)(row0 + pos - ctx) * a.st + h * a.sh;
-      bad |= write_at(p, a, n0 + src, h, pos, ctx + len, [&](int i) { return rows + i * a.st; });
+      bad |= write_at<D, F16, kAppendSteps>(p, a, n0 + src, h, pos, ctx + len, [&](int i) { return rows + i * a.st; });
       if (!first_warp) break;
     }
     b -= all;
@@ -229,15 +255,19 @@ __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantWriteParam
 }  // namespace
 
 cudaError_t launch_quant_commit(const QuantWriteParams &p, cudaStream_t st) {
-  k_quant_commit<<<dim3(p.N, p.layers, 2), kThreads, 0, st>>>(p);
+  const auto kernel = p.head_dim == 128 ? (p.f16 ? k_quant_commit<128, true> : k_quant_commit<128, false>)
+                                        : (p.f16 ? k_quant_commit<64, true> : k_quant_commit<64, false>);
+  kernel<<<dim3(p.N, p.layers, 2), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_quant_append(const QuantWriteParams &p, cudaStream_t st) {
+  const auto kernel = p.head_dim == 128 ? (p.f16 ? k_quant_append<128, true> : k_quant_append<128, false>)
+                                        : (p.f16 ? k_quant_append<64, true> : k_quant_append<64, false>);
   // a request's tokens lie in at most total / block + 2 blocks
   const int64_t blocks = ((int64_t)p.total >> p.scale_shift) + 2ll * p.N;
   const int64_t grid = (blocks * p.kv_heads + kWarps - 1) / kWarps;
-  k_quant_append<<<dim3((unsigned)grid, p.layers * 2), kThreads, 0, st>>>(p);
+  kernel<<<dim3((unsigned)grid, p.layers * 2), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -31,6 +31,8 @@
 // scales, 12-15 the units' Q parts and the tree's K and V.  After an expired wait the
 // softmax and preparing warps run their loops to the end without waiting or
 // storing, so that their barriers stay complete.
+#include <type_traits>
+
 #include "launch.h"
 #include "quant.cuh"
 #include "tma_map.h"
@@ -502,23 +504,37 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
           __syncwarp();
         } else {
           const int used = min(boxes, (end - tok0 + box - 1) >> box_shift);  // copies of the tile
-          // (the pages first, then all copies by one lane: a shuffle and an election between copies cost 130 cycles each)
-          int pg[kTile / 16];
-#pragma unroll
-          for (int r = 0; r < kTile / 16; ++r)
-            if (r < boxes) pg[r] = uni(lane == at + r ? page : 0);
           const int slot = tok0 & (page_size - 1);
-          if (elect_one()) {
-            mbar_arrive_expect_tx(k_bar, used * box_bytes);
-            mbar_arrive_expect_tx(v_bar, used * box_bytes);
+          // (the pages first, then all copies by one lane: a shuffle and an election between copies cost 130 cycles each)
+          auto copies = [&](auto number) {
+            constexpr int kBoxes = decltype(number)::value;
+            int pg[kBoxes];
 #pragma unroll
-            for (int r = 0; r < kTile / 16; ++r)
-              if (r < used) {  // (used <= boxes)
-                tma_load_4d(k_dst + r * box_bytes, &maps.k, 0, slot, h, pg[r], k_bar);
-                tma_load_4d(v_dst + r * box_bytes, &maps.v, 0, slot, h, pg[r], v_bar);
+            for (int r = 0; r < kBoxes; ++r) pg[r] = uni(lane == at + r ? page : 0);
+            if (elect_one()) {
+              mbar_arrive_expect_tx(k_bar, used * box_bytes);
+              mbar_arrive_expect_tx(v_bar, used * box_bytes);
+              if (used == kBoxes) {
+#pragma unroll
+                for (int r = 0; r < kBoxes; ++r) {
+                  tma_load_4d(k_dst + r * (G::kTileBytes / kBoxes), &maps.k, 0, slot, h, pg[r], k_bar);
+                  tma_load_4d(v_dst + r * (G::kTileBytes / kBoxes), &maps.v, 0, slot, h, pg[r], v_bar);
+                }
+              } else {
+#pragma unroll
+                for (int r = 0; r < kBoxes; ++r)
+                  if (r < used) {
+                    tma_load_4d(k_dst + r * (G::kTileBytes / kBoxes), &maps.k, 0, slot, h, pg[r], k_bar);
+                    tma_load_4d(v_dst + r * (G::kTileBytes / kBoxes), &maps.v, 0, slot, h, pg[r], v_bar);
+                  }
               }
-          }
-          __syncwarp();
+            }
+            __syncwarp();
+          };
+          if (boxes == 1) copies(std::integral_constant<int, 1>());
+          else if (boxes == 2) copies(std::integral_constant<int, 2>());
+          else if (boxes == 4) copies(std::integral_constant<int, 4>());
+          else copies(std::integral_constant<int, 8>());
           const int pg_j = __shfl_sync(DC_FULL_MASK, page, at + box_j);
           if (lane < 16 && tok_j < kTile && tok0 + tok_j < end) {
             const float *src = scale_h + pg_j * sp;
