@@ -24,13 +24,27 @@
 // The tree's own nodes are a unit of their own with 16-bit operands, 64 nodes a
 // tile in a tile's place.  Units (request, K/V head, row tile, chunk of the
 // context or tree) are dealt to one persistent block an SM; each leaves its rows'
-// unnormalised output, reference and sum, and a second kernel joins them.
+// unnormalised output, reference and sum, and a last kernel joins them.  A first
+// one makes the parts of Q.
 //
-// Roles: warps 0-7 softmax and output (two groups of four, half of the rows each;
-// thread = token = TMEM lane), 8 the tensor core, 9 and 10 TMA for K and V with the
-// scales, 12-15 the units' Q parts and the tree's K and V.  After an expired wait the
-// softmax and preparing warps run their loops to the end without waiting or
-// storing, so that their barriers stay complete.
+// Softmax: four groups of four warps, 16 rows a thread (thread = token = TMEM
+// lane); 64 rows take all four, 32 or 16 rows two or one, and the groups then
+// are teams that take the tiles in turn, each with references, sums and O of its own.
+// (Two groups of 32 rows a thread, with twice the registers: 669 us for 8 x 64 at 32000 where
+// four took 528.  The next tile's scores fetched under this one's exponentials: 542 for
+// 484, registers spilled.)
+//
+// Every other role has a warp, so that each one's chain of waits and issues (200 cycles
+// a wait, 60 a product or copy) runs beside the others': with S and O issued by one
+// warp, that warp took 2050 cycles a tile of 16 rows.  A tile of 32 KB is due every 1400 cycles at
+// HBM's rate.  It takes 1750 for 4 rows (48 requests of up to 24001 tokens: 271 us, 5.0 TB/s), where the
+// loading warp is what bounds it, and 2700 for 64 rows (32 x 16 to 8000: 129 us; 8 x 64 to 32000: 447 us),
+// where the softmax chain does: wait, scores, vote, exponentials and parts, store.
+//
+// Roles: warps 0-15 softmax and output, 16 the products S, 17 the products O, 18
+// TMA for K and V and the scales, 19 the list of the block's units and their Q.  A
+// softmax group's warps vote on every unit and tile whether a wait has expired, and
+// leave together, so that their barriers stay complete.
 #include <type_traits>
 
 #include "launch.h"
@@ -443,256 +457,256 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   const auto units_bar = [&](int unit) { return smem_u32(&b.units[unit & (kUnits - 1)]); };
   const auto factors_bar = [&](int unit) { return smem_u32(&b.factors[unit & (kAhead - 1)]); };
   if (warp >= G::kScoreWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
-  if (warp == G::kLoadWarp) {
-    // ------------------------------------------------------------ TMA for K and V, the scales
-    const int page_size = 1 << t.page_shift, box_shift = min(t.page_shift, 7), box = 1 << box_shift, boxes = kTile >> box_shift;
-    const uint32_t box_bytes = box * D;
-    // lanes 0-7 fetch K's scales of a tile, 8-15 V's: block j of the tile, in box box_j; its place in its
-    // page is its place in the box where a box is a page
-    const int j = lane & 7, tok_j = j << p.scale_shift, box_j = min(tok_j, kTile - 1) >> box_shift;
-    const float *scale = lane < 8 ? p.k_scale : p.v_scale;
-    const int64_t sp = lane < 8 ? p.ks_sp : p.vs_sp, sb = lane < 8 ? p.ks_sb : p.vs_sb, ss = lane < 8 ? p.ks_sh : p.vs_sh;
-    scale += ((tok_j & (box - 1)) >> p.scale_shift) * sb;
-    bool ok = true;
-    int ks = 0, k_phase = 1, vs = 0, v_phase = 1;  // (a wait for phase 1 of a new barrier is over at once)
-    for (int unit = 0; ok; ++unit) {
-      ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
-      if (!ok) break;
-      const QuantUnit &u = unit_at(unit);
-      const int ntiles = uni(u.ntiles), n = uni(u.n), h = uni(u.h), tile0 = uni(u.tile0), ctx = uni(u.ctx);
-      const bool tree = uni(u.tree);
-      if (ntiles == 0) break;
-      const float *scale_h = scale + h * ss;
-      const int32_t *table = t.page_table + n * t.pt_stride;
-      const int end = tree ? 0 : min(ctx, (tile0 + ntiles) * kTile);
-      auto pages_from = [&](int tok) {  // lane l: page of the l-th box from token `tok` on
-        tok += lane * box;
-        int page = 0;
-        if (tok < end) page = __ldg(table + (tok >> t.page_shift));
-        return page;
-      };
-      int tok0 = tile0 * kTile, at = 0;
-      int page = pages_from(tok0), page_next = pages_from(tok0 + 32 * box);
-      for (int i = 0; i < ntiles; ++i, ++g, tok0 += kTile) {
-        if (at == 32) {
-          at = 0, page = page_next;
-          page_next = pages_from(tok0 + 32 * box);
-        }
-        if (at == 0 && (page < 0 || page >= t.num_pages)) {
-          atomicOr(t.err, kErrBadPage);
-          page = 0;
-        }
-        const uint32_t k_bar = smem_u32(&b.k_full[ks]), v_bar = smem_u32(&b.v_full[vs]);
-        const uint32_t k_empty = smem_u32(&b.k_empty[ks]);
-        ok = __all_sync(DC_FULL_MASK, bar_wait3(k_empty, k_phase, smem_u32(&b.v_empty[vs]), v_phase, k_empty, k_phase,
-                                                &s_abort, t.err));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+    if (warp == G::kLoadWarp) {
+      // ------------------------------------------------------------ TMA for K and V, the scales
+      const int page_size = 1 << t.page_shift, box_shift = min(t.page_shift, 7), box = 1 << box_shift, boxes = kTile >> box_shift;
+      const uint32_t box_bytes = box * D;
+      // lanes 0-7 fetch K's scales of a tile, 8-15 V's: block j of the tile, in box box_j; its place in its
+      // page is its place in the box where a box is a page
+      const int j = lane & 7, tok_j = j << p.scale_shift, box_j = min(tok_j, kTile - 1) >> box_shift;
+      const float *scale = lane < 8 ? p.k_scale : p.v_scale;
+      const int64_t sp = lane < 8 ? p.ks_sp : p.vs_sp, sb = lane < 8 ? p.ks_sb : p.vs_sb, ss = lane < 8 ? p.ks_sh : p.vs_sh;
+      scale += ((tok_j & (box - 1)) >> p.scale_shift) * sb;
+      bool ok = true;
+      int ks = 0, k_phase = 1, vs = 0, v_phase = 1;  // (a wait for phase 1 of a new barrier is over at once)
+      for (int unit = 0; ok; ++unit) {
+        ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
         if (!ok) break;
-        const uint32_t k_dst = sbase + G::kK + ks * G::kTileBytes, v_dst = sbase + G::kV + vs * G::kTileBytes;
-        if (tree) {
-          const int bytes = (D / 64) * 128 * t.tree_box;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(k_bar, bytes);
-            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(v_bar), "r"(bytes) : "memory");
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              tma_load_4d(k_dst + c * kTreeNodes * 128, &maps.k_new, c * 64, i * kTreeNodes, h, n, k_bar);
-              tma_load_4d(v_dst + c * kTreeNodes * 128, &maps.v_new, c * 64, i * kTreeNodes, h, n, v_bar);
-            }
-            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 33;" ::"r"(v_bar) : "memory");
+        const QuantUnit &u = unit_at(unit);
+        const int ntiles = uni(u.ntiles), n = uni(u.n), h = uni(u.h), tile0 = uni(u.tile0), ctx = uni(u.ctx);
+        const bool tree = uni(u.tree);
+        if (ntiles == 0) break;
+        const float *scale_h = scale + h * ss;
+        const int32_t *table = t.page_table + n * t.pt_stride;
+        const int end = tree ? 0 : min(ctx, (tile0 + ntiles) * kTile);
+        auto pages_from = [&](int tok) {  // lane l: page of the l-th box from token `tok` on
+          tok += lane * box;
+          int page = 0;
+          if (tok < end) page = __ldg(table + (tok >> t.page_shift));
+          return page;
+        };
+        int tok0 = tile0 * kTile, at = 0;
+        int page = pages_from(tok0), page_next = pages_from(tok0 + 32 * box);
+        for (int i = 0; i < ntiles; ++i, ++g, tok0 += kTile) {
+          if (at == 32) {
+            at = 0, page = page_next;
+            page_next = pages_from(tok0 + 32 * box);
           }
-          __syncwarp();
-        } else {
-          const int used = min(boxes, (end - tok0 + box - 1) >> box_shift);  // copies of the tile
-          const int slot = tok0 & (page_size - 1);
-          // (the pages first, then all copies by one lane: a shuffle and an election between copies cost 130 cycles each)
-          auto copies = [&](auto number) {
-            constexpr int kBoxes = decltype(number)::value;
-            int pg[kBoxes];
-#pragma unroll
-            for (int r = 0; r < kBoxes; ++r) pg[r] = uni(lane == at + r ? page : 0);
+          if (at == 0 && (page < 0 || page >= t.num_pages)) {
+            atomicOr(t.err, kErrBadPage);
+            page = 0;
+          }
+          const uint32_t k_bar = smem_u32(&b.k_full[ks]), v_bar = smem_u32(&b.v_full[vs]);
+          const uint32_t k_empty = smem_u32(&b.k_empty[ks]);
+          ok = __all_sync(DC_FULL_MASK, bar_wait3(k_empty, k_phase, smem_u32(&b.v_empty[vs]), v_phase, k_empty, k_phase,
+                                                  &s_abort, t.err));
+          if (!ok) break;
+          const uint32_t k_dst = sbase + G::kK + ks * G::kTileBytes, v_dst = sbase + G::kV + vs * G::kTileBytes;
+          if (tree) {
+            const int bytes = (D / 64) * 128 * t.tree_box;
             if (elect_one()) {
-              mbar_arrive_expect_tx(k_bar, used * box_bytes);
-              mbar_arrive_expect_tx(v_bar, used * box_bytes);
-              if (used == kBoxes) {
+              mbar_arrive_expect_tx(k_bar, bytes);
+              asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(v_bar), "r"(bytes) : "memory");
 #pragma unroll
-                for (int r = 0; r < kBoxes; ++r) {
-                  tma_load_4d(k_dst + r * (G::kTileBytes / kBoxes), &maps.k, 0, slot, h, pg[r], k_bar);
-                  tma_load_4d(v_dst + r * (G::kTileBytes / kBoxes), &maps.v, 0, slot, h, pg[r], v_bar);
-                }
-              } else {
+              for (int c = 0; c < D / 64; ++c) {
+                tma_load_4d(k_dst + c * kTreeNodes * 128, &maps.k_new, c * 64, i * kTreeNodes, h, n, k_bar);
+                tma_load_4d(v_dst + c * kTreeNodes * 128, &maps.v_new, c * 64, i * kTreeNodes, h, n, v_bar);
+              }
+              asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 33;" ::"r"(v_bar) : "memory");
+            }
+            __syncwarp();
+          } else {
+            const int used = min(boxes, (end - tok0 + box - 1) >> box_shift);  // copies of the tile
+            const int slot = tok0 & (page_size - 1);
+            // (the pages first, then all copies by one lane: a shuffle and an election between copies cost 130 cycles each)
+            auto copies = [&](auto number) {
+              constexpr int kBoxes = decltype(number)::value;
+              int pg[kBoxes];
 #pragma unroll
-                for (int r = 0; r < kBoxes; ++r)
-                  if (r < used) {
+              for (int r = 0; r < kBoxes; ++r) pg[r] = uni(lane == at + r ? page : 0);
+              if (elect_one()) {
+                mbar_arrive_expect_tx(k_bar, used * box_bytes);
+                mbar_arrive_expect_tx(v_bar, used * box_bytes);
+                if (used == kBoxes) {
+#pragma unroll
+                  for (int r = 0; r < kBoxes; ++r) {
                     tma_load_4d(k_dst + r * (G::kTileBytes / kBoxes), &maps.k, 0, slot, h, pg[r], k_bar);
                     tma_load_4d(v_dst + r * (G::kTileBytes / kBoxes), &maps.v, 0, slot, h, pg[r], v_bar);
                   }
+                } else {
+#pragma unroll
+                  for (int r = 0; r < kBoxes; ++r)
+                    if (r < used) {
+                      tma_load_4d(k_dst + r * (G::kTileBytes / kBoxes), &maps.k, 0, slot, h, pg[r], k_bar);
+                      tma_load_4d(v_dst + r * (G::kTileBytes / kBoxes), &maps.v, 0, slot, h, pg[r], v_bar);
+                    }
+                }
               }
+              __syncwarp();
+            };
+            if (boxes == 1) copies(std::integral_constant<int, 1>());
+            else if (boxes == 2) copies(std::integral_constant<int, 2>());
+            else if (boxes == 4) copies(std::integral_constant<int, 4>());
+            else copies(std::integral_constant<int, 8>());
+            const int pg_j = __shfl_sync(DC_FULL_MASK, page, at + box_j);
+            if (lane < 16 && tok_j < kTile && tok0 + tok_j < end) {
+              const float *src = scale_h + pg_j * sp;
+              if (page_size > kTile) src += (slot >> p.scale_shift) * sb;
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[vs][lane >> 3][j])), "l"(src)
+                           : "memory");
             }
-            __syncwarp();
-          };
-          if (boxes == 1) copies(std::integral_constant<int, 1>());
-          else if (boxes == 2) copies(std::integral_constant<int, 2>());
-          else if (boxes == 4) copies(std::integral_constant<int, 4>());
-          else copies(std::integral_constant<int, 8>());
-          const int pg_j = __shfl_sync(DC_FULL_MASK, page, at + box_j);
-          if (lane < 16 && tok_j < kTile && tok0 + tok_j < end) {
-            const float *src = scale_h + pg_j * sp;
-            if (page_size > kTile) src += (slot >> p.scale_shift) * sb;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&s_scale[vs][lane >> 3][j])), "l"(src)
-                         : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_bar) : "memory");
+            at += boxes;
           }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_bar) : "memory");
-          at += boxes;
+          if (++ks == G::kNK) ks = 0, k_phase ^= 1;
+          if (++vs == G::kNV) vs = 0, v_phase ^= 1;
         }
-        if (++ks == G::kNK) ks = 0, k_phase ^= 1;
-        if (++vs == G::kNV) vs = 0, v_phase ^= 1;
       }
-    }
-  } else if (warp == G::kPrepWarp) {
-    // ------------------------------------------------------------ units, their Q
-    const bool flag = blockIdx.x == 0;
-    QuantUnits it(p, flag);
-    QuantUnit w;
-    bool ok = true, more = true;
-    int made = 0;
-    pdl_wait();  // k_quant_q's Q
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    for (int unit = 0; ok; ++unit) {
-      const int qb = unit & 1, slot = unit & (kAhead - 1);
-      // Units are published ahead of their Q, up to nine: the loads of short ones run that far ahead.
-      for (int k = 0; k < 2 && more && made <= unit + 8; ++k) {
-        do more = it.next(w, flag);
-        while (more && w.ntiles == 0);
-        if (!more) w.ntiles = 0;
-        if (lane == 0) {
-          s_unit[made & (kUnits - 1)] = w;
-          mbar_arrive(units_bar(made));
+    } else if (warp == G::kPrepWarp) {
+      // ------------------------------------------------------------ units, their Q
+      const bool flag = blockIdx.x == 0;
+      QuantUnits it(p, flag);
+      QuantUnit w;
+      bool ok = true, more = true;
+      int made = 0;
+      pdl_wait();  // k_quant_q's Q
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      for (int unit = 0; ok; ++unit) {
+        const int qb = unit & 1, slot = unit & (kAhead - 1);
+        // Units are published ahead of their Q, up to nine: the loads of short ones run that far ahead.
+        for (int k = 0; k < 2 && more && made <= unit + 8; ++k) {
+          do more = it.next(w, flag);
+          while (more && w.ntiles == 0);
+          if (!more) w.ntiles = 0;
+          if (lane == 0) {
+            s_unit[made & (kUnits - 1)] = w;
+            mbar_arrive(units_bar(made));
+          }
+          ++made;
+          __syncwarp();
         }
-        ++made;
+        if (unit >= 2) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_empty[qb]), ((unit >> 1) - 1) & 1, &s_abort, t.err));
+        if (!ok) break;
+        const QuantUnit &u = unit_at(unit);
+        if (u.ntiles == 0) {  // the end
+          if (lane == 0) mbar_arrive(factors_bar(unit));
+          break;
+        }
+        if (lane == 0) {
+          const uint8_t *src = p.q_parts + (((int64_t)u.n * t.kv_heads + u.h) * p.mtiles + u.mt) * quant_q_bytes(NP, R, D);
+          const uint32_t bytes = u.tree ? G::kQTree : G::kQBytes, q_bar = smem_u32(&b.q_full[qb]);
+          mbar_arrive_expect_tx(q_bar, bytes);
+          bulk_load(sbase + G::kQ + qb * G::kQBytes, src + (u.tree ? G::kQBytes : 0), bytes, q_bar);
+          mbar_arrive_expect_tx(factors_bar(unit), R * 4);
+          bulk_load(smem_u32(s_factor[slot]), src + G::kQBytes + G::kQTree + (u.tree ? R * 4 : 0), R * 4, factors_bar(unit));
+        }
         __syncwarp();
       }
-      if (unit >= 2) ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_empty[qb]), ((unit >> 1) - 1) & 1, &s_abort, t.err));
-      if (!ok) break;
-      const QuantUnit &u = unit_at(unit);
-      if (u.ntiles == 0) {  // the end
-        if (lane == 0) mbar_arrive(factors_bar(unit));
-        break;
+    } else if (warp == G::kScoreWarp) {
+      // ------------------------------------------------------------ tensor core: S^T = K Q^T
+      constexpr uint32_t kId = (1u << 4) | (8u << 24) | (uint32_t)(R >> 3) << 17;  // fp32 += e4m3 e4m3, M = 128, N = R
+      constexpr uint32_t kId16 = F16 ? idesc_f16(128, R) : idesc_bf16(128, R);
+      bool ok = true;
+      int ks = 0, k_phase = 0;
+      for (int unit = 0; ok; ++unit) {
+        const int qb = unit & 1;
+        ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
+        if (!ok) break;
+        const int ntiles = uni(unit_at(unit).ntiles);
+        const bool tree = uni(unit_at(unit).tree);
+        if (ntiles == 0) break;
+        ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (unit >> 1) & 1, &s_abort, t.err));
+        if (!ok) break;
+        const uint32_t sq = desc_lo(sbase + G::kQ + qb * G::kQBytes);
+        for (int i = 0; i < ntiles; ++i, ++g) {
+          const int sb = g % G::kNS;
+          const uint32_t k_bar = smem_u32(&b.k_full[ks]);
+          ok = __all_sync(DC_FULL_MASK, bar_wait3(k_bar, k_phase, k_bar, k_phase, g >= G::kNS ? smem_u32(&b.s_free[sb]) : k_bar,
+                                                  g >= G::kNS ? (g / G::kNS - 1) & 1 : k_phase, &s_abort, t.err));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sk = desc_lo(sbase + G::kK + ks * G::kTileBytes), to = tmem + G::kS + sb * R;
+          if (elect_one()) {
+            if (tree) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(to, sk + (((k >> 2) * (kTreeNodes * 128) + (k & 3) * 32) >> 4),
+                       sq + (((k >> 2) * (R * 128) + (k & 3) * 32) >> 4), kId16, k > 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int x = 0; x < NP; ++x)
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                  mma8<G::kHi, G::kHi>(to, sk + k * 2, sq + ((x * G::kQPart) >> 4) + k * 2, kId, (x > 0 || k > 0) ? 1u : 0u);
+            }
+            mma_commit(smem_u32(&b.s_full[sb]));
+            mma_commit(smem_u32(&b.k_empty[ks]));
+            if (i == ntiles - 1) mma_commit(smem_u32(&b.q_empty[qb]));
+          }
+          __syncwarp();
+          if (++ks == G::kNK) ks = 0, k_phase ^= 1;
+        }
       }
-      if (lane == 0) {
-        const uint8_t *src = p.q_parts + (((int64_t)u.n * t.kv_heads + u.h) * p.mtiles + u.mt) * quant_q_bytes(NP, R, D);
-        const uint32_t bytes = u.tree ? G::kQTree : G::kQBytes, q_bar = smem_u32(&b.q_full[qb]);
-        mbar_arrive_expect_tx(q_bar, bytes);
-        bulk_load(sbase + G::kQ + qb * G::kQBytes, src + (u.tree ? G::kQBytes : 0), bytes, q_bar);
-        mbar_arrive_expect_tx(factors_bar(unit), R * 4);
-        bulk_load(smem_u32(s_factor[slot]), src + G::kQBytes + G::kQTree + (u.tree ? R * 4 : 0), R * 4, factors_bar(unit));
+      if (elect_one()) {  // the lane that issued: nothing is in flight when the block frees its TMEM
+        mma_commit(smem_u32(&b.done[0]));
+        mbar_drain(smem_u32(&b.done[0]), 0);
+      }
+      __syncwarp();
+    } else if (warp == G::kOutWarp) {
+      // ------------------------------------------------------------ tensor core: O^T += V^T P^T
+      constexpr uint32_t kId =  // B e5m2; both M- and N-major
+          (1u << 4) | (8u << 24) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t)(3 * R >> 3) << 17;
+      constexpr uint32_t kId16 = (F16 ? idesc_f16(128, R) : idesc_bf16(128, R)) | (1u << 15) | (1u << 16);
+      bool ok = true;
+      int vs = 0, v_phase = 0;
+      int begun[G::kTeams] = {};  // units that each team has begun
+      for (int unit = 0; ok; ++unit) {
+        ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
+        if (!ok) break;
+        const int ntiles = uni(unit_at(unit).ntiles);
+        const bool tree = uni(unit_at(unit).tree);
+        if (ntiles == 0) break;
+        for (int i = 0; i < ntiles; ++i, ++g) {
+          const int team = g % G::kTeams, pb = g % G::kNP;
+          const bool first = i < G::kTeams;
+          int mine = 0;
+#pragma unroll
+          for (int k = 0; k < G::kTeams; ++k)
+            if (k == team) mine = (begun[k] += first) - 1;
+          const uint32_t v_bar = smem_u32(&b.v_full[vs]);
+          const bool wait_o = first && mine >= 2;
+          ok = __all_sync(DC_FULL_MASK, bar_wait3(v_bar, v_phase, smem_u32(&b.p_full[pb]), (g / G::kNP) & 1,
+                                                  wait_o ? smem_u32(&b.o_free[team][mine & 1]) : v_bar,
+                                                  wait_o ? ((mine >> 1) - 1) & 1 : v_phase, &s_abort, t.err));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t to = tmem + G::kO + (team * 2 + (mine & 1)) * 3 * R;
+          const uint32_t sv = sbase + G::kV + vs * G::kTileBytes, sp = sbase + G::kP + pb * G::kPBytes;
+          const uint32_t a = desc_lo(sv, tree ? kTreeNodes * 128 : G::kTileBytes), bd = desc_lo(sp, tree ? 16 : G::kPAtom);
+          if (elect_one()) {
+            if (tree) {
+#pragma unroll
+              for (int k = 0; k < kTreeNodes / 16; ++k)
+                mma_ss(to, a + k * (2048 >> 4), bd + k * (2048 >> 4), kId16, (!first || k > 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int k = 0; k < kTile / 32; ++k)
+                mma8<G::kHi, G::kHiP>(to, a + k * (32 * D >> 4), bd + k * (2048 >> 4), kId, (!first || k > 0) ? 1u : 0u);
+            }
+            mma_commit(smem_u32(&b.v_empty[vs]));
+            mma_commit(smem_u32(&b.pv_done[pb]));
+          }
+          __syncwarp();
+          if (++vs == G::kNV) vs = 0, v_phase ^= 1;
+        }
+      }
+      if (elect_one()) {
+        mma_commit(smem_u32(&b.done[1]));
+        mbar_drain(smem_u32(&b.done[1]), 0);
       }
       __syncwarp();
     }
-  } else if (warp == G::kScoreWarp) {
-    // ------------------------------------------------------------ tensor core: S^T = K Q^T
-    constexpr uint32_t kId = (1u << 4) | (8u << 24) | (uint32_t)(R >> 3) << 17;  // fp32 += e4m3 e4m3, M = 128, N = R
-    constexpr uint32_t kId16 = F16 ? idesc_f16(128, R) : idesc_bf16(128, R);
-    bool ok = true;
-    int ks = 0, k_phase = 0;
-    for (int unit = 0; ok; ++unit) {
-      const int qb = unit & 1;
-      ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
-      if (!ok) break;
-      const int ntiles = uni(unit_at(unit).ntiles);
-      const bool tree = uni(unit_at(unit).tree);
-      if (ntiles == 0) break;
-      ok = __all_sync(DC_FULL_MASK, bar_wait(smem_u32(&b.q_full[qb]), (unit >> 1) & 1, &s_abort, t.err));
-      if (!ok) break;
-      const uint32_t sq = desc_lo(sbase + G::kQ + qb * G::kQBytes);
-      for (int i = 0; i < ntiles; ++i, ++g) {
-        const int sb = g % G::kNS;
-        const uint32_t k_bar = smem_u32(&b.k_full[ks]);
-        ok = __all_sync(DC_FULL_MASK, bar_wait3(k_bar, k_phase, k_bar, k_phase, g >= G::kNS ? smem_u32(&b.s_free[sb]) : k_bar,
-                                                g >= G::kNS ? (g / G::kNS - 1) & 1 : k_phase, &s_abort, t.err));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sk = desc_lo(sbase + G::kK + ks * G::kTileBytes), to = tmem + G::kS + sb * R;
-        if (elect_one()) {
-          if (tree) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(to, sk + (((k >> 2) * (kTreeNodes * 128) + (k & 3) * 32) >> 4),
-                     sq + (((k >> 2) * (R * 128) + (k & 3) * 32) >> 4), kId16, k > 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int x = 0; x < NP; ++x)
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k)
-                mma8<G::kHi, G::kHi>(to, sk + k * 2, sq + ((x * G::kQPart) >> 4) + k * 2, kId, (x > 0 || k > 0) ? 1u : 0u);
-          }
-          mma_commit(smem_u32(&b.s_full[sb]));
-          mma_commit(smem_u32(&b.k_empty[ks]));
-          if (i == ntiles - 1) mma_commit(smem_u32(&b.q_empty[qb]));
-        }
-        __syncwarp();
-        if (++ks == G::kNK) ks = 0, k_phase ^= 1;
-      }
-    }
-    if (elect_one()) {  // the lane that issued: nothing is in flight when the block frees its TMEM
-      mma_commit(smem_u32(&b.done[0]));
-      mbar_drain(smem_u32(&b.done[0]), 0);
-    }
-    __syncwarp();
-  } else if (warp == G::kOutWarp) {
-    // ------------------------------------------------------------ tensor core: O^T += V^T P^T
-    constexpr uint32_t kId =  // B e5m2; both M- and N-major
-        (1u << 4) | (8u << 24) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t)(3 * R >> 3) << 17;
-    constexpr uint32_t kId16 = (F16 ? idesc_f16(128, R) : idesc_bf16(128, R)) | (1u << 15) | (1u << 16);
-    bool ok = true;
-    int vs = 0, v_phase = 0;
-    int begun[G::kTeams] = {};  // units that each team has begun
-    for (int unit = 0; ok; ++unit) {
-      ok = __all_sync(DC_FULL_MASK, bar_wait(units_bar(unit), (unit / kUnits) & 1, &s_abort, t.err));
-      if (!ok) break;
-      const int ntiles = uni(unit_at(unit).ntiles);
-      const bool tree = uni(unit_at(unit).tree);
-      if (ntiles == 0) break;
-      for (int i = 0; i < ntiles; ++i, ++g) {
-        const int team = g % G::kTeams, pb = g % G::kNP;
-        const bool first = i < G::kTeams;
-        int mine = 0;
-#pragma unroll
-        for (int k = 0; k < G::kTeams; ++k)
-          if (k == team) mine = (begun[k] += first) - 1;
-        const uint32_t v_bar = smem_u32(&b.v_full[vs]);
-        const bool wait_o = first && mine >= 2;
-        ok = __all_sync(DC_FULL_MASK, bar_wait3(v_bar, v_phase, smem_u32(&b.p_full[pb]), (g / G::kNP) & 1,
-                                                wait_o ? smem_u32(&b.o_free[team][mine & 1]) : v_bar,
-                                                wait_o ? ((mine >> 1) - 1) & 1 : v_phase, &s_abort, t.err));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t to = tmem + G::kO + (team * 2 + (mine & 1)) * 3 * R;
-        const uint32_t sv = sbase + G::kV + vs * G::kTileBytes, sp = sbase + G::kP + pb * G::kPBytes;
-        const uint32_t a = desc_lo(sv, tree ? kTreeNodes * 128 : G::kTileBytes), bd = desc_lo(sp, tree ? 16 : G::kPAtom);
-        if (elect_one()) {
-          if (tree) {
-#pragma unroll
-            for (int k = 0; k < kTreeNodes / 16; ++k)
-              mma_ss(to, a + k * (2048 >> 4), bd + k * (2048 >> 4), kId16, (!first || k > 0) ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < kTile / 32; ++k)
-              mma8<G::kHi, G::kHiP>(to, a + k * (32 * D >> 4), bd + k * (2048 >> 4), kId, (!first || k > 0) ? 1u : 0u);
-          }
-          mma_commit(smem_u32(&b.v_empty[vs]));
-          mma_commit(smem_u32(&b.pv_done[pb]));
-        }
-        __syncwarp();
-        if (++vs == G::kNV) vs = 0, v_phase ^= 1;
-      }
-    }
-    if (elect_one()) {
-      mma_commit(smem_u32(&b.done[1]));
-      mbar_drain(smem_u32(&b.done[1]), 0);
-    }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftRegs));
     // ------------------------------------------------------------ softmax, output
