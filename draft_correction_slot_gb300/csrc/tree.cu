@@ -103,10 +103,11 @@ int most_chunks(int64_t max_tiles, int items, int sms, int cap) {
   return most;
 }
 
-// The same for the attention on a cache in 8 bits, whose tiles are short and whose units' borders
-// cost as much.  Measured at 8 / 16 / 24 / 32 / 64 tiles: 32 requests x 16 nodes, 64 rows, to 8000
-// tokens: 153 / 139 / 143 / 137 / 135 us; 8 x 64, five tiles of 64 rows, to 32000: 542 / 485 / 447 /
-// 451 / 448 us; 48 x 1, 4 rows, to 24001: 403 / 336 / 316 / 307 / 286 us.
+// The same for the attention on a cache in 8 bits, whose tiles are short beside its units' borders.
+// Measured at 16 / 24 / 32 / 48 / 64 / 128 tiles, the mean of six draws of the lengths: 32 requests x
+// 16 nodes, 64 rows, to 8000 tokens: 139 / 139 / 136 / 147 / 129 / 129 us; 8 x 64, five tiles of 64
+// rows, to 32000: 581 / 553 / 538 / 539 / 534 / 545 us; 48 x 1, 4 rows, to 24001: 327 / 306 / 297 / 291
+// / 278 / 280 us.
 int quant_chunk_cap(const dcoco_tree_config &c) { return c.max_batch == 1 ? 1 << 30 : 64; }
 int most_quant_chunks(int64_t max_tiles, int items, int sms, int cap) {
   const int64_t scan = max_tiles < 64 * dc::kTreeMaxChunks ? max_tiles : 64 * dc::kTreeMaxChunks;

@@ -37,8 +37,8 @@
 // Every other role has a warp, so that each one's chain of waits and issues (200 cycles
 // a wait, 60 a product or copy) runs beside the others': with S and O issued by one
 // warp, that warp took 2050 cycles a tile of 16 rows.  A tile of 32 KB is due every 1400 cycles at
-// HBM's rate.  It takes 1750 for 4 rows (48 requests of up to 24001 tokens: 271 us, 5.0 TB/s), where the
-// loading warp is what bounds it, and 2700 for 64 rows (32 x 16 to 8000: 129 us; 8 x 64 to 32000: 447 us),
+// HBM's rate.  It takes 1750 for 4 rows (48 requests of up to 24001 tokens: 266 us, 5.1 TB/s), where the
+// loading warp is what bounds it, and 2700 for 64 rows (32 x 16 to 8000: 123 us; 8 x 64 to 32000: 525 us),
 // where the softmax chain does: wait, scores, vote, exponentials and parts, store.
 //
 // Roles: warps 0-15 softmax and output, 16 the products S, 17 the products O, 18

@@ -481,11 +481,20 @@ typedef struct {
 /* As dcoco_tree_create, for a cache in 8 bits whose scales cover scale_tokens
  * tokens: a power of two, 16..page_size (else EUNSUPPORTED).  On such a handle
  * dcoco_tree_attention and _commit answer EUNSUPPORTED, and the _quant calls do so on
- * a handle for 16 bits; status, launches and destroy are the same calls. */
+ * a handle for 16 bits; status, launches and destroy are the same calls.
+ * The workspace holds, for every request, K/V head and 64 rows (nodes x (q_heads /
+ * kv_heads)) of the largest call, (4 head_dim + 8) x 64 bytes for each chunk of the
+ * context and the tree, and up to 5 head_dim + 8 bytes a row of q.  A chunk has up to 64
+ * tiles of 128 tokens, shorter ones where a full batch would not fill the GPU, and a
+ * request at most 63. */
 int dcoco_tree_create_quant(const dcoco_tree_config *cfg, int scale_tokens, dcoco_tree_handle **out);
 
 /* dcoco_tree_attention with k_cache and v_cache in 8 bits; their strides are
- * multiples of 16 (elements, one byte each).  All else as there. */
+ * multiples of 16 (elements, one byte each).  Scales outside 2^-100 .. 2^100 may lose
+ * their values.  All else as there, but for the roundings: the weights of the context's tokens
+ * keep 2^-10 of themselves, those of the nodes are rounded to the handle's type; q's
+ * elements keep 2^-17 of their row's largest.  A NaN of the cache or of q reaches the rows
+ * that see it, and no others; so does an infinity of q, as NaN.  Three launches. */
 int dcoco_tree_attention_quant(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_attention_args *in,
                                const dcoco_quant_scales *scales, void *out, float *lse, void *stream);
 
@@ -530,8 +539,8 @@ typedef struct {
  * The rows follow from one another: first does not decrease and stays within
  * 0..tokens.  A request whose rows or lengths do not (or would not fit its page
  * table) is left out, new_len = ctx_len (clamped), and recorded in the status word, as is a
- * page outside the pool, whose tokens are not written.  No page may belong to
- * two requests.  One launch.  Errors: as dcoco_tree_commit; tokens < 0: EINVAL;
+ * page outside the pool, whose tokens are not written.  No page that is written may
+ * belong to two requests (full pages may: dcoco_pages_fork).  One launch.  Errors: as dcoco_tree_commit; tokens < 0: EINVAL;
  * layers outside 1..32767: EINVAL. */
 int dcoco_tree_append_quant(dcoco_tree_handle *h, int batch, const dcoco_tree_append_args *in,
                             const dcoco_quant_scales *scales, int32_t *new_len, void *stream);
