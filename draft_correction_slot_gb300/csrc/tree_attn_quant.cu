@@ -171,6 +171,16 @@ __device__ __forceinline__ void warp_col_sums(float (&v)[N], float *dst) {
   for (int k = 0; k < kLeft; ++k) dst[col + k] = v[k];
 }
 
+__device__ __forceinline__ float lg2(float x) {  // of normal numbers
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 __device__ __forceinline__ float rcp(float x) {  // within an ulp
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -419,8 +429,9 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   __shared__ QuantUnit s_unit[kUnits];                     // the block's units in turn; ntiles 0: the end
   __shared__ uint32_t s_odd[kAhead][8];                    // tree units: nodes whose V holds an infinity or NaN
   __shared__ float s_scale[G::kNV][2][8];                  // a V stage's tile: K and V scales of its blocks
-  // of each group: its rows' references less kTop, rescale factors, and what its warps put together
-  __shared__ __align__(16) float s_mb[G::kGroups][G::kCols], s_f[G::kGroups][G::kCols], s_part[G::kGroups][4][G::kCols];
+  // of each group: kTop less its rows' references (what the scores are added to), rescale factors, and what
+  // its warps put together
+  __shared__ __align__(16) float s_nref[G::kGroups][G::kCols], s_f[G::kGroups][G::kCols], s_part[G::kGroups][4][G::kCols];
   const int tid = threadIdx.x, warp = __shfl_sync(DC_FULL_MASK, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
 
@@ -441,7 +452,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < 64) s_mb[tid / G::kCols][tid % G::kCols] = kNone;
+  if (tid < 64) s_nref[tid / G::kCols][tid % G::kCols] = -kNone;
   if (warp == G::kLoadWarp && lane < 4)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k + lane)) : "memory");
   if (warp == G::kScoreWarp) tmem_alloc(smem_u32(&s_tmem), G::kTmem);
@@ -716,7 +727,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
     const int group = warp >> 2, quad = warp & 3, tok = tid & (kGroup - 1);
     const int team = group / G::kParts, col0 = group % G::kParts * C;  // this group's rows: columns col0 .. col0 + C - 1
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + col0;
-    float *const mb_of = s_mb[group], *const f_of = s_f[group];
+    float *const nref_of = s_nref[group], *const f_of = s_f[group];
     uint32_t(*const s_word)[C] = reinterpret_cast<uint32_t(*)[C]>(s_part[group]);  // mask words (a tile's step between uses of s_part)
     bool ok = true;
     auto wait = [&](unsigned long long *bar, int phase) {
@@ -825,7 +836,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
             const int blk = tok >> p.scale_shift;
             ks = s_scale[vs][0][blk];
             const float f = s_scale[vs][1][blk];
-            lvs = __log2f(f), inv = rcp(f);
+            lvs = lg2(f), inv = rcp(f);
           } else if (col0 == 0 && ok) {
             // past the end lies what a page or a copy left: zeros in its place, since a zero weight does not cancel NaN
             uint4 *row = reinterpret_cast<uint4 *>(smem + G::kV + vs * G::kTileBytes + tok * D);
@@ -871,10 +882,10 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
           float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
           for (int k = 0; k < C; k += 4) {
-            const float4 mb = *reinterpret_cast<const float4 *>(mb_of + k);
-            x[k / 2] = add2(x[k / 2], both(-mb.x, -mb.y)), x[k / 2 + 1] = add2(x[k / 2 + 1], both(-mb.z, -mb.w));
+            const float4 r = *reinterpret_cast<const float4 *>(nref_of + k);
+            x[k / 2] = add2(x[k / 2], both(r.x, r.y)), x[k / 2 + 1] = add2(x[k / 2 + 1], both(r.z, r.w));
             const float2 a = apart(x[k / 2]), c = apart(x[k / 2 + 1]);
-            g0 = fmaxf(g0, fmaxf(a.x, a.y)), g1 = fmaxf(g1, fmaxf(c.x, c.y));
+            g0 = max3(g0, a.x, a.y), g1 = max3(g1, c.x, c.y);
           }
           grow = fmaxf(g0, g1);
         };
@@ -909,10 +920,10 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
           if (tok < C) {
             const float m = fmaxf(fmaxf(s_part[group][0][tok], s_part[group][1][tok]),
                                   fmaxf(s_part[group][2][tok], s_part[group][3][tok]));
-            const float old = mb_of[tok];
-            const bool grown = m - old > kGrow;  // (the others stay: a row's result hangs on its own scores)
-            mb_of[tok] = grown ? m - kTop : old;
-            f_of[tok] = grown ? ex2(old - m + kTop) : 1.f;
+            const float old = nref_of[tok];
+            const bool grown = m + old > kGrow;  // (the others stay: a row's result hangs on its own scores)
+            nref_of[tok] = grown ? kTop - m : old;
+            f_of[tok] = grown ? ex2(kTop - m - old) : 1.f;
           }
           soft_sync(group);
           if (i > first) {
@@ -935,8 +946,8 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
           // (the words anew: s_part took their place)
 #pragma unroll
           for (int k = 0; k < C; k += 4) {
-            const float4 mb = *reinterpret_cast<const float4 *>(mb_of + k);
-            x[k / 2] = add2(x[k / 2], both(-mb.x, -mb.y)), x[k / 2 + 1] = add2(x[k / 2 + 1], both(-mb.z, -mb.w));
+            const float4 r = *reinterpret_cast<const float4 *>(nref_of + k);
+            x[k / 2] = add2(x[k / 2], both(r.x, r.y)), x[k / 2 + 1] = add2(x[k / 2 + 1], both(r.z, r.w));
           }
         }
         tc_fence_before();
@@ -1000,8 +1011,8 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
       soft_sync(group);
       if (tok < C) {
         const float *s4 = s_part[group][0] + tok;
-        if (ok) p.part_ml[slot_of(u, first) + tok] = make_float2(mb_of[tok], (s4[0] + s4[C]) + (s4[2 * C] + s4[3 * C]));
-        mb_of[tok] = kNone;  // no reference yet: any score outgrows it
+        if (ok) p.part_ml[slot_of(u, first) + tok] = make_float2(-nref_of[tok], (s4[0] + s4[C]) + (s4[2 * C] + s4[3 * C]));
+        nref_of[tok] = -kNone;  // no reference yet: any score outgrows it
       }
       soft_sync(group);
       done_g = x_g, done_unit = unit, done_i = first, ++begun;
