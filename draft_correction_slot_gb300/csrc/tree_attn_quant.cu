@@ -37,9 +37,9 @@
 // Every other role has a warp, so that each one's chain of waits and issues (200 cycles
 // a wait, 60 a product or copy) runs beside the others': with S and O issued by one
 // warp, that warp took 2050 cycles a tile of 16 rows.  A tile of 32 KB is due every 1400 cycles at
-// HBM's rate.  It takes 1750 for 4 rows (48 requests of up to 24001 tokens: 266 us, 5.1 TB/s), where the
-// loading warp is what bounds it, and 2700 for 64 rows (32 x 16 to 8000: 123 us; 8 x 64 to 32000: 525 us),
-// where the softmax chain does: wait, scores, vote, exponentials and parts, store.
+// HBM's rate.  It takes 1750 for 4 rows (48 requests of up to 24001 tokens: 271 us, 5.0 TB/s), where the
+// loading warp is what bounds it, and 2700 for 64 rows (32 x 16 to 8000: 128 us; 8 x 64 to 32000: 534 us;
+// means of six draws of the lengths), where the softmax chain does: wait, scores, vote, exponentials and parts, store.
 //
 // Roles: warps 0-15 softmax and output, 16 the products S, 17 the products O, 18
 // TMA for K and V and the scales, 19 the list of the block's units and their Q.  A
@@ -1042,18 +1042,18 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
 // e4m3 (NP of R x D bytes), the rows in 16 bits ([64-element block][row]), both swizzled as
 // shared memory has them, then the rows' factors, of either form.  A warp a row.
 // (Once for each row tile, in a kernel of its own: by a warp of the attention's blocks a
-// unit's Q took up to 30,000 cycles, more than its tiles.)
+// unit's Q took up to 30,000 cycles, more than its tiles.)  Bound by latency: 16,384 rows some 5 us, of
+// which the attention's start hides a part.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) k_quant_q(const QuantAttnParams p) {
   constexpr int NP = F16 ? 3 : 2, E = D / 32;
   const TreeAttnParams &t = p.t;
   pdl_trigger();
-  const int lane = threadIdx.x & 31, R = p.R;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);  // row of all row tiles
-  if (i >= (int64_t)t.N * t.kv_heads * p.mtiles * R) return;
-  const int64_t item = i / R, pair = item / p.mtiles;
-  const int row = (int)(i - item * R), mt = (int)(item - pair * p.mtiles);
-  const int n = (int)(pair / t.kv_heads), h = (int)(pair - (int64_t)n * t.kv_heads);
+  const int lane = threadIdx.x & 31, R = p.R, shift = R == 64 ? 6 : R == 32 ? 5 : 4;
+  const uint32_t i = blockIdx.x * 8u + (threadIdx.x >> 5);  // row of all row tiles (at most 2^30; whole blocks)
+  const uint32_t item = i >> shift, pair = item / (uint32_t)p.mtiles;
+  const int row = (int)(i & (uint32_t)(R - 1)), mt = (int)(item - pair * p.mtiles);
+  const int n = (int)(pair / (uint32_t)t.kv_heads), h = (int)(pair - (uint32_t)n * t.kv_heads);
   const int r = mt * R + row, node = r / t.group;
   const int len = t.tree_len ? min(max(t.tree_len[n], 0), t.T) : t.T;
   uint32_t x[E / 2];
@@ -1072,7 +1072,7 @@ __global__ void __launch_bounds__(256) k_quant_q(const QuantAttnParams p) {
   // row with an infinity becomes NaN)
   const int e = max((int)(__float_as_uint(most) >> 23), 27);
   const float mul = __uint_as_float(e < 255 ? (uint32_t)(261 - e) << 23 : 0x7FC00000u), c = t.scale * kLog2e;
-  uint8_t *dst = p.q_parts + item * quant_q_bytes(NP, R, D);
+  uint8_t *dst = p.q_parts + (int64_t)item * quant_q_bytes(NP, R, D);
   const int at = lane * E;
   const int off = row * D + (((at >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4) + (at & 15);
   uint16_t part[NP][E / 2];
@@ -1199,7 +1199,7 @@ cudaError_t launch(const QuantAttnParams &p, const QuantMaps &maps, unsigned gri
 template <int D, bool F16>
 cudaError_t launch_all(const QuantAttnParams &p, const QuantMaps &maps, unsigned grid, cudaStream_t st) {
   const int64_t q_rows = (int64_t)p.t.N * p.t.kv_heads * p.mtiles * p.R;
-  k_quant_q<D, F16><<<(unsigned)((q_rows + 7) / 8), 256, 0, st>>>(p);
+  k_quant_q<D, F16><<<(unsigned)(q_rows / 8), 256, 0, st>>>(p);  // (R is a multiple of 8)
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = p.R == 16   ? launch<D, 16, F16>(p, maps, grid, st)
