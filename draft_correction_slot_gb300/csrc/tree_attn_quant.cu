@@ -1134,10 +1134,11 @@ __global__ void __launch_bounds__(256, 6) k_quant_join(const QuantAttnParams p) 
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= f0;
     const int k1 = min(live - k0, 32);
+    const uint32_t holds = __ballot_sync(DC_FULL_MASK, a.y != 0.f);  // (an empty one was not written)
 #pragma unroll 4
     for (int k = 0; k < k1; ++k) {
       const float f = __shfl_sync(DC_FULL_MASK, wk, k);
-      if (f == 0.f) continue;  // (an empty one holds nothing; NaN goes on)
+      if (!((holds >> k) & 1u)) continue;  // by its sum, not by f: a NaN counts however little its tokens weigh
       const float *src = po + (int64_t)(k0 + k) * p.R * D;
       if constexpr (E == 4) {
         const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));

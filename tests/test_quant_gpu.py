@@ -438,6 +438,26 @@ def test_attention_refusals(env):
     assert v.status() == dc.DCOCO_OK
 
 
+@pytest.mark.parametrize("T", [2, 6, 16])
+@pytest.mark.parametrize("max_batch", [1, 200])  # partial results of one tile, and of several teams
+def test_attention_nan_of_a_light_token(env, T, max_batch):
+    """A NaN of V reaches the rows that see it however little its token weighs: here its scores, and those of all the
+    tokens that share its partial result, lie hundreds below the rows' largest."""
+    torch, dc = env
+    a = Attn(torch, 71, [1000], T, 1, 4, 128, 16, 16, torch.bfloat16, mask="none", poison=False)
+    a.k_scale[torch.from_numpy(a.table[0, 8:63]).long().cuda()] *= 64.0  # tokens 128 and on: scores of hundreds
+    v = a.verifier(dc, max_batch=max_batch)
+    clean, lse = a.run(v, scale=1.0)
+    a.check(clean, lse, scale=1.0)
+    for token, e in ((37, 7), (400, 90)):  # (the second one beside heavier ones in its tile)
+        a.v_cache.view(torch.uint8)[int(a.table[0, token // 16]), token % 16, 0, e] = 0x7F
+    out, lse2 = a.run(v, scale=1.0)
+    keep = torch.ones(128, dtype=torch.bool, device="cuda")
+    keep[[7, 90]] = False
+    assert bool(torch.isnan(out[..., ~keep]).all())
+    assert torch.equal(out[..., keep], clean[..., keep]) and torch.equal(lse, lse2)
+
+
 # ------------------------------------------------------------------ writing
 class Cache:
     """A random cache of all layers on the GPU and its copy in 64 bits."""
