@@ -19,7 +19,13 @@
 //     nothing that fp16 kept.
 // The scales never touch an operand: ks multiplies a score (a thread has a
 // token), log2(vs) is added to it, and the sum takes its weights divided by vs.
-// So a row's reference is the largest log2 of weight x vs.
+// So a row's reference is the largest log2 of weight x vs.  A token of a small vs
+// may lie far below it and still be most of the sum, whose value lies anywhere
+// between 1 / vs of the least and of the largest scale.  With scales of 2^-80 .. 2^80 it is
+// 2^-73 .. 2^119, and a weight that ex2 flushes (below 2^-126 of the reference) is below
+// 2^-25 of it if vs >= kSmallScale; below that a token's weights for the sum are exponentials of
+// their own.  Where a reference moves by up to 2 x 80 octaves and more, sums follow by the
+// factor's root, twice.
 //
 // The tree's own nodes are a unit of their own with 16-bit operands, 64 nodes a
 // tile in a tile's place.  Units (request, K/V head, row tile, chunk of the
@@ -59,6 +65,7 @@ constexpr int kGroup = 128;    // softmax threads of a group
 constexpr int kTreeNodes = kQuantNodes;  // nodes of a tree tile
 constexpr int kAhead = 16, kUnits = 32;  // units whose row factors and odd nodes are kept; whose description is
 constexpr float kTop = 7.f;     // log2 of a weight at its row's reference
+constexpr float kSmallScale = -28.f;  // log2 of a V scale, see above
 constexpr float kGrow = kTop + kRescale;  // log2 of the largest weight: 2^15 fits fp16 and e5m2
 
 struct QuantMaps {
@@ -836,7 +843,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
             const int blk = tok >> p.scale_shift;
             ks = s_scale[vs][0][blk];
             const float f = s_scale[vs][1][blk];
-            lvs = lg2(f), inv = rcp(f);
+            lvs = lg2(f), inv = lvs < kSmallScale ? 0.f : rcp(f);
           } else if (col0 == 0 && ok) {
             // past the end lies what a page or a copy left: zeros in its place, since a zero weight does not cancel NaN
             uint4 *row = reinterpret_cast<uint4 *>(smem + G::kV + vs * G::kTileBytes + tok * D);
@@ -923,12 +930,15 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
             const float old = nref_of[tok];
             const bool grown = m + old > kGrow;  // (the others stay: a row's result hangs on its own scores)
             nref_of[tok] = grown ? kTop - m : old;
-            f_of[tok] = grown ? ex2(kTop - m - old) : 1.f;
+            f_of[tok] = grown ? ex2(0.5f * (kTop - m - old)) : 1.f;  // (the factor's root)
           }
           soft_sync(group);
           if (i > first) {
 #pragma unroll
-            for (int k = 0; k < C / 2; ++k) l[k] = mul2(l[k], both(f_of[2 * k], f_of[2 * k + 1]));
+            for (int k = 0; k < C / 2; ++k) {
+              const f32x2 f = both(f_of[2 * k], f_of[2 * k + 1]);
+              l[k] = mul2(mul2(l[k], f), f);
+            }
             // this team's last product
             wait(&b.pv_done[(x_g - G::kTeams) % G::kNP], (x_g - G::kTeams) / G::kNP);
             tc_fence_after();
@@ -939,7 +949,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
                 float o[8];
                 tmem_ld<8>(to_o + part * R + k0, o);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] *= f_of[k0 + k];
+                for (int k = 0; k < 8; ++k) o[k] *= f_of[k0 + k] * f_of[k0 + k];
                 tmem_st<8>(to_o + part * R + k0, o);
               }
           }
@@ -955,6 +965,13 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
         if (lane == 0 && ok) mbar_arrive(smem_u32(&b.s_free[sb]));
         uint8_t *pbuf = smem + G::kP + pb * G::kPBytes;
         const f32x2 inv2 = both(inv, inv);
+        if (lvs < kSmallScale) {  // (rare: V below 2^-19, blocks of zeros; inv is 0)
+#pragma unroll
+          for (int k = 0; k < C / 2; ++k) {
+            const float2 v = apart(x[k]);
+            l[k] = add2(l[k], both(ex2(v.x - lvs), ex2(v.y - lvs)));
+          }
+        }
         if (tree) {
 #pragma unroll
           for (int k = 0; k < C; k += 8) {
@@ -1129,8 +1146,10 @@ __global__ void __launch_bounds__(256, 6) k_quant_join(const QuantAttnParams p) 
   // 32 partial results at a time, one a lane
   for (int k0 = 0; k0 < live; k0 += 32) {
     const float2 a = k0 + lane < live ? __ldcg(&ml[(int64_t)(k0 + lane) * p.R]) : make_float2(kNone, 0.f);
-    const float top = fmaxf(M, warp_max(a.x)), f0 = ex2(M - top), wk = a.y != 0.f ? ex2(a.x - top) : 0.f;
-    M = top, L = fmaf(L, f0, warp_sum(wk * a.y));
+    // factors' roots: a sum is multiplied by them one after the other (see the top of this file)
+    const float top = fmaxf(M, warp_max(a.x)), r0 = ex2(0.5f * (M - top)), f0 = r0 * r0;
+    const float rk = a.y != 0.f ? ex2(0.5f * (a.x - top)) : 0.f, wk = rk * rk;
+    M = top, L = L * r0 * r0 + warp_sum(a.y * rk * rk);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= f0;
     const int k1 = min(live - k0, 32);

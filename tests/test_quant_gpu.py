@@ -458,6 +458,23 @@ def test_attention_nan_of_a_light_token(env, T, max_batch):
     assert torch.equal(out[..., keep], clean[..., keep]) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("ends", [(-64, 64), (-80, 80), (-80, -80), (80, 80)])
+@pytest.mark.parametrize("how", ["mixed", "tiles", "rise", "fall"])
+@pytest.mark.parametrize("max_batch", [2, 200])
+def test_attention_scales_at_both_ends(env, ends, how, max_batch):
+    """V scales as far apart as they may be, within a tile, from tile to tile and from chunk to chunk: the tokens of
+    the small ones count in the sum of the weights all the same."""
+    torch, dc = env
+    a = Attn(torch, 18, [2000, 300], 3, 1, 4, 128, 16, 16, torch.bfloat16)
+    rng = np.random.default_rng(3)
+    for n in range(2):
+        b = np.arange(-(-a.ctx[n] // 16))
+        low = {"mixed": rng.random(len(b)) < 0.5, "tiles": b // 8 % 2 == 0, "rise": b < len(b) / 2, "fall": b > len(b) / 2}[how]
+        s = np.exp2(np.where(low, ends[0], ends[1])).astype(np.float32)
+        a.v_scale[torch.from_numpy(a.table[n, b]).long().cuda(), 0, 0] = torch.from_numpy(s).cuda()
+    a.check(*a.run(a.verifier(dc, max_batch=max_batch)))
+
+
 # ------------------------------------------------------------------ writing
 class Cache:
     """A random cache of all layers on the GPU and its copy in 64 bits."""
