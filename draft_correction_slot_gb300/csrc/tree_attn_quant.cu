@@ -13,10 +13,11 @@
 //   Q: a row times a power of two that brings its largest element to 128..256,
 //     then 2 parts of e4m3 (bf16: exact but for elements below 2^-10 of the
 //     largest, whose error is below 2^-18 of it) or 3 (fp16); all into one S.
-//   P: rounded to fp16 (2^-11), then 3 parts of e5m2, N columns of their own: the
-//     first two to nearest, each leaving its error to the next, so that 2^-11 of
-//     a weight is lost once more; the third times 2^7, below whose least step lies
-//     nothing that fp16 kept.
+//   P: rounded to fp16 (2^-11 of a weight, or 2^-32 of its row's reference), then 3
+//     parts of e5m2, N columns of their own: each the nearest to what is left, the
+//     second times 2^4, the third times 2^8. Together they are that fp16 number, to the bit, for
+//     any up to 2^15, its subnormals too (without the 2^4 a weight 2^-20 of its row's largest
+//     kept 8 bits, one of 2^-25 three).
 // The scales never touch an operand: ks multiplies a score (a thread has a
 // token), log2(vs) is added to it, and the sum takes its weights divided by vs.
 // So a row's reference is the largest log2 of weight x vs.  A token of a small vs
@@ -282,9 +283,9 @@ __device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32
   for (int i = 0; i < 2; ++i) {
     const uint32_t p = pack2<true>(e[2 * i], e[2 * i + 1]);
     h[i] = top_bytes(p);
-    const uint32_t r = hsub2(p, h[i]);
+    const uint32_t r = hmul2(hsub2(p, h[i]), 0x4C004C00u);  // 2^4
     m[i] = top_bytes(r);
-    l[i] = hmul2(hsub2(r, m[i]), 0x58005800u) + 0x00800080u;  // 2^7
+    l[i] = hmul2(hsub2(r, m[i]), 0x4C004C00u) + 0x00800080u;
   }
   hi = __byte_perm(h[0], h[1], 0x7531), mid = __byte_perm(m[0], m[1], 0x7531), lo = __byte_perm(l[0], l[1], 0x7531);
 }
@@ -767,7 +768,8 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
           tmem_wait<8>(y), tmem_wait<8>(z);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            x[k] = __float_as_uint(fmaf(__uint_as_float(z[k]), 0.0078125f, __uint_as_float(x[k]) + __uint_as_float(y[k])));
+            x[k] = __float_as_uint(fmaf(__uint_as_float(z[k]), 0.00390625f,
+                                        fmaf(__uint_as_float(y[k]), 0.0625f, __uint_as_float(x[k]))));
         }
         if (tok < D && ok) {
 #pragma unroll

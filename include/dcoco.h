@@ -492,10 +492,12 @@ int dcoco_tree_create_quant(const dcoco_tree_config *cfg, int scale_tokens, dcoc
 /* dcoco_tree_attention with k_cache and v_cache in 8 bits; their strides are
  * multiples of 16 (elements, one byte each).  K's scales outside 2^-100 .. 2^100 and
  * V's outside 2^-80 .. 2^80 may lose their tokens' part in lse and out; within, scales
- * of one request may differ as they like.  All else as there, but for the roundings: the weights of the context's tokens
- * keep 2^-10 of themselves, those of the nodes are rounded to the handle's type; q's
- * elements keep 2^-17 of their row's largest.  A NaN of the cache or of q reaches the rows
- * that see it, and no others; so does an infinity of q, as NaN.  Three launches. */
+ * of one request may differ as they like.  All else as there, but for the
+ * roundings: in out a context token's weight is off by up to 2^-11 of itself, or 2^-31 of
+ * the row's largest product of weight and V scale where that is more (lse has fp32 weights); a
+ * node's is rounded to the handle's type; q's elements keep 2^-17 of their row's largest.
+ * A NaN of the cache or of q reaches the rows that see it, and no others; so does an infinity
+ * of q, as NaN.  Three launches. */
 int dcoco_tree_attention_quant(dcoco_tree_handle *h, int batch, int nodes, const dcoco_tree_attention_args *in,
                                const dcoco_quant_scales *scales, void *out, float *lse, void *stream);
 

@@ -100,3 +100,18 @@ def test_reference_pool():
     p.free([1, 0, 1])
     assert p.refs == [1, 1, 0, 1, 1, 0]
     assert p.compact() == 4 and p.table[2] == [0, 1, 2] and p.cache[2] == "c" and p.refs == [1, 1, 1, 1, 0, 0]
+
+
+def test_weight_parts():
+    """What the attention makes of a weight: fp16 into three parts of e5m2 (three significant bits, 2^4 and 2^8 times
+    in the second and third), whose sum is the fp16 number for every one up to 2^15."""
+    f16 = np.float16
+    top = lambda x: ((x.view(np.uint16).astype(np.uint32) + 0x80) & 0xFF00).astype(np.uint16).view(f16)  # noqa: E731
+    p = np.arange(f16(2.0 ** 15).view(np.uint16) + 1, dtype=np.uint16).view(f16)
+    hi = top(p)
+    rest = (p - hi) * f16(16)
+    mid = top(rest)
+    lo = top((rest - mid) * f16(16))
+    assert hi.dtype == rest.dtype == mid.dtype == lo.dtype == f16
+    assert np.isfinite([hi, mid, lo]).all()
+    assert (hi.astype(np.float64) + mid.astype(np.float64) / 16 + lo.astype(np.float64) / 256 == p.astype(np.float64)).all()

@@ -475,6 +475,25 @@ def test_attention_scales_at_both_ends(env, ends, how, max_batch):
     a.check(*a.run(a.verifier(dc, max_batch=max_batch)))
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("octaves", [3, 12, 17, 20, 23, 25])
+def test_attention_light_token_decides(env, dtype, octaves):
+    """Two tokens: a heavy one whose value is zero, and one lighter by so many octaves, which is all the output."""
+    torch, dc = env
+    a = Attn(torch, 19, [2], 16, 1, 4, 64, 16, 16, getattr(torch, dtype), mask="none")
+    page, e4m3 = int(a.table[0, 0]), torch.float8_e4m3fn
+    k, v = torch.zeros(2, 64, device="cuda"), torch.zeros(2, 64, device="cuda")
+    k[1, 0] = -128
+    v[1] = torch.linspace(-448, 448, 64, device="cuda")
+    a.k_cache.view(torch.uint8)[page, :2, 0] = k.to(e4m3).view(torch.uint8)
+    a.v_cache.view(torch.uint8)[page, :2, 0] = v.to(e4m3).view(torch.uint8)
+    a.k_scale[page], a.v_scale[page] = 2.0 ** -3, 2.0 ** 8
+    a.q.zero_()
+    a.q[0, :, :, 0] = torch.linspace(1, 1.2, 64, device="cuda").view(16, 4).to(a.dtype)
+    scale = octaves * math.log(2) / 16
+    a.check(*a.run(a.verifier(dc), scale=scale), scale=scale)
+
+
 # ------------------------------------------------------------------ writing
 class Cache:
     """A random cache of all layers on the GPU and its copy in 64 bits."""
