@@ -1090,7 +1090,9 @@ __global__ void __launch_bounds__(256) k_quant_q(const QuantAttnParams p) {
   // the power of two that brings the row's largest to 128..256 (rows below 2^-100 count as of that size; a
   // row with an infinity becomes NaN)
   const int e = max((int)(__float_as_uint(most) >> 23), 27);
-  const float mul = __uint_as_float(e < 255 ? (uint32_t)(261 - e) << 23 : 0x7FC00000u), c = t.scale * kLog2e;
+  const float mul = __uint_as_float(e < 255 ? (uint32_t)(261 - e) << 23 : 0x7FC00000u);
+  // (the factors too: products with the 16-bit form, the tree's, may all be -inf, and the row would pass for empty)
+  const float c = e < 255 ? t.scale * kLog2e : mul;
   uint8_t *dst = p.q_parts + (int64_t)item * quant_q_bytes(NP, R, D);
   const int at = lane * E;
   const int off = row * D + (((at >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4) + (at & 15);

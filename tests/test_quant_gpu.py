@@ -494,6 +494,27 @@ def test_attention_light_token_decides(env, dtype, octaves):
     a.check(*a.run(a.verifier(dc), scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("ctx", [0, 40])
+def test_attention_infinite_queries_are_nan(env, value, ctx):
+    """A query that holds an infinity gives NaN, not the zeros of a row that sees nothing, whatever sign the
+    products have; a row that does see nothing stays empty."""
+    torch, dc = env
+    a = Attn(torch, 20, [ctx, ctx], 3, 1, 2, 64, 16, 16, torch.bfloat16, mask="causal", poison=False)
+    a.k_new[..., 7] = torch.tensor([1.0, -1.0], device="cuda").view(2, 1, 1).to(a.dtype)
+    clean, _ = a.run(a.verifier(dc))
+    a.q[:, 1, 0, 7] = value
+    out, lse = a.run(a.verifier(dc))
+    hit = torch.zeros(2, 3, 2, dtype=torch.bool, device="cuda")
+    hit[:, 1, 0] = True
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+    assert torch.equal(out[~hit], clean[~hit])
+    if ctx == 0:
+        a.mask = torch.zeros(1, 3, 1, dtype=torch.int32, device="cuda")
+        out, lse = a.run(a.verifier(dc))
+        assert (out == 0).all() and bool(torch.isneginf(lse).all())
+
+
 # ------------------------------------------------------------------ writing
 class Cache:
     """A random cache of all layers on the GPU and its copy in 64 bits."""
