@@ -56,6 +56,7 @@
 
 #include "launch.h"
 #include "quant.cuh"
+#include "ring.h"
 #include "tma_map.h"
 #include "tree_attn.cuh"
 
@@ -64,7 +65,7 @@ namespace {
 
 constexpr int kGroup = 128;    // softmax threads of a group
 constexpr int kTreeNodes = kQuantNodes;  // nodes of a tree tile
-constexpr int kAhead = 16, kUnits = 32;  // units whose row factors and odd nodes are kept; whose description is
+constexpr int kAhead = kAheadUnits, kUnits = 32;  // units whose row factors and odd nodes are kept; whose description is
 constexpr float kTop = 7.f;     // log2 of a weight at its row's reference
 constexpr float kSmallScale = -28.f;  // log2 of a V scale, see above
 constexpr float kGrow = kTop + kRescale;  // log2 of the largest weight: 2^15 fits fp16 and e5m2
@@ -470,7 +471,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   const uint32_t tmem = __shfl_sync(DC_FULL_MASK, s_tmem, 0);
   pdl_trigger();
 
-  int g = 0;  // tiles that this role has begun
+  int g = 0;  // tiles that this role has begun (of the list's warp: units whose Q it has)
   // Unit number `unit` as the preparing warp has published it.
   const auto unit_at = [&](int unit) -> const QuantUnit & { return s_unit[unit & (kUnits - 1)]; };
   const auto units_bar = [&](int unit) { return smem_u32(&b.units[unit & (kUnits - 1)]); };
@@ -620,6 +621,7 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
           mbar_arrive_expect_tx(factors_bar(unit), R * 4);
           bulk_load(smem_u32(s_factor[slot]), src + G::kQBytes + G::kQTree + (u.tree ? R * 4 : 0), R * 4, factors_bar(unit));
         }
+        ++g;
         __syncwarp();
       }
     } else if (warp == G::kScoreWarp) {
@@ -1047,12 +1049,13 @@ k_quant_attn(const QuantAttnParams p, const __grid_constant__ QuantMaps maps) {
   __syncthreads();
   tc_fence_after();
   if (warp == G::kLoadWarp) asm volatile("cp.async.wait_all;" ::: "memory");
+  // after an expired wait: copies in flight land before the block gives its memory back
   if (s_abort && warp == G::kPrepWarp && lane == 0)
-    for (int i = 0; i < 2; ++i) mbar_drain(smem_u32(&b.q_full[i]), 0), mbar_drain(smem_u32(&b.q_full[i]), 1);
+    unit_copies(g, [&](int i, int parity) { mbar_drain(smem_u32(&b.q_full[i]), parity); },
+                [&](int i, int parity) { mbar_drain(smem_u32(&b.factors[i]), parity); });
   if (s_abort && warp == G::kLoadWarp && lane == 0) {
-    // after an expired wait: copies in flight land before the block gives its memory back
-    for (int x = max(0, g - G::kNK); x < g; ++x) mbar_drain(smem_u32(&b.k_full[x % G::kNK]), (x / G::kNK) & 1);
-    for (int x = max(0, g - G::kNV); x < g; ++x) mbar_drain(smem_u32(&b.v_full[x % G::kNV]), (x / G::kNV) & 1);
+    last_uses(g, G::kNK, [&](int i, int parity) { mbar_drain(smem_u32(&b.k_full[i]), parity); });
+    last_uses(g, G::kNV, [&](int i, int parity) { mbar_drain(smem_u32(&b.v_full[i]), parity); });
   }
   if (warp == G::kScoreWarp) tmem_dealloc(tmem, G::kTmem);
 }

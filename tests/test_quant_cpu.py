@@ -115,3 +115,46 @@ def test_weight_parts():
     assert hi.dtype == rest.dtype == mid.dtype == lo.dtype == f16
     assert np.isfinite([hi, mid, lo]).all()
     assert (hi.astype(np.float64) + mid.astype(np.float64) / 16 + lo.astype(np.float64) / 256 == p.astype(np.float64)).all()
+
+
+def test_copies_in_flight_are_waited_for(tmp_path):
+    """What a block whose waits have expired waits for before it returns: every copy begun for its units, whichever
+    of them are still in flight, and nothing else (a wait for a phase that has not begun would run to its limit)."""
+    import os
+    import subprocess
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "draft_correction_slot_gb300", "csrc")
+    (tmp_path / "model.cpp").write_text("""
+#include <cstdio>
+#include <initializer_list>
+#include "ring.h"
+// A ring of barriers: uses begun and completed on each; a use begins after the one before it on its barrier.
+struct Ring {
+  int slots, begun[32] = {}, waits = 0;
+  bool bad = false, landed[32] = {};
+  void wait(int i, int parity) {  // for the phase of that parity: the one in flight, not the one before or to come
+    ++waits;
+    if (i >= slots || begun[i] == 0 || ((begun[i] - 1) & 1) != parity) bad = true;
+    else landed[i] = true;
+  }
+};
+int main() {
+  for (int units = 0; units < 200; ++units) {
+    Ring q{2}, factors{dc::kAheadUnits};
+    for (int u = 0; u < units; ++u) ++q.begun[u % 2], ++factors.begun[u % dc::kAheadUnits];
+    dc::unit_copies(units, [&](int i, int p) { q.wait(i, p); }, [&](int i, int p) { factors.wait(i, p); });
+    for (Ring *r : {&q, &factors}) {
+      if (r->bad || r->waits > r->slots) return printf("%d units: a wait for nothing\\n", units), 1;
+      for (int i = 0; i < r->slots; ++i)
+        if (r->begun[i] > 0 && !r->landed[i]) return printf("%d units: a copy in flight\\n", units), 1;
+    }
+  }
+}
+""")
+    exe = str(tmp_path / "model")
+    subprocess.check_call(["g++", "-std=c++17", "-I", csrc, str(tmp_path / "model.cpp"), "-o", exe])
+    assert subprocess.run([exe]).returncode == 0
+    # the kernel's rings that copies complete on are these, and K's and V's
+    src = open(os.path.join(csrc, "tree_attn_quant.cu")).read()
+    tail = src[src.index("if (s_abort && warp == G::kPrepWarp"):src.index("tmem_dealloc(tmem, G::kTmem)")]
+    for ring in ("q_full", "factors", "k_full", "v_full"):
+        assert f"mbar_drain(smem_u32(&b.{ring}[i]), parity)" in tail
