@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxNodes = 256;
+constexpr int kTailBlocks = 8;  // see k_quant_append
 constexpr int kAppendSteps = 4;  // 8 prompts of up to 2000 tokens: 127 us; 140 with 8 steps, 200 with 16 (fewer warps an SM)
 
 template <bool F16>
@@ -206,48 +207,78 @@ __global__ void __launch_bounds__(kThreads) k_quant_commit(const QuantWriteParam
   if (bad) atomicOr(p.err, bad);
 }
 
-// A warp a block of tokens and head; blockIdx.y: the layer's K or V.
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) k_quant_append(const QuantWriteParams p) {
-  const int lane = threadIdx.x & 31, capacity = p.max_pages << p.page_shift;
-  int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int h = (int)(u % p.kv_heads);
-  int64_t b = u / p.kv_heads;  // block of tokens, over all requests
-  const bool first_warp = u == 0 && blockIdx.y == 0;
-  int bad = 0;
-  for (int n0 = 0; n0 < p.N; n0 += 32) {
-    const int n = n0 + lane;
-    int ctx = 0, row0 = 0, len = 0, blocks = 0;
+// The most blocks of `scale` tokens that requests with rows of their own lie in.
+__host__ __device__ inline int64_t append_blocks(const QuantWriteParams &p) {
+  return ((int64_t)p.total >> p.scale_shift) + 2ll * p.N;
+}
+
+// 32 requests' rows, one a lane: what it has before, its first row, how many rows and blocks of
+// tokens, and the blocks up to and with it.  A request with lengths out of range has none.
+struct AppendLanes {
+  int ctx = 0, row0 = 0, len = 0, blocks = 0, upto = 0, all = 0;
+  bool bad = false;
+  __device__ AppendLanes(const QuantWriteParams &p, int n) {
+    const int lane = threadIdx.x & 31, capacity = p.max_pages << p.page_shift;
     if (n < p.N) {
       ctx = p.ctx_len[n], row0 = p.first[n], len = p.first[n + 1] - row0;
-      if (ctx < 0 || ctx > capacity || row0 < 0 || len < 0 || row0 > p.total || len > p.total - row0 || len > capacity - ctx) {
-        bad |= kErrBadLength;  // a request with lengths out of range is left out
-        ctx = min(max(ctx, 0), capacity), len = 0;
-      }
+      bad = ctx < 0 || ctx > capacity || row0 < 0 || len < 0 || row0 > p.total || len > p.total - row0 || len > capacity - ctx;
+      if (bad) ctx = min(max(ctx, 0), capacity), len = 0;
       if (len > 0) blocks = ((ctx + len - 1) >> p.scale_shift) - (ctx >> p.scale_shift) + 1;
-      if (first_warp) p.new_len[n] = ctx + len;
     }
-    int upto = blocks;
+    upto = blocks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(DC_FULL_MASK, upto, o);
       if (lane >= o) upto += y;
     }
-    const int all = __shfl_sync(DC_FULL_MASK, upto, 31);
-    if (b >= 0 && b < all) {
-      const int src = __ffs(__ballot_sync(DC_FULL_MASK, upto > b)) - 1;
-      const int rel = (int)b - __shfl_sync(DC_FULL_MASK, upto - blocks, src);
-      ctx = __shfl_sync(DC_FULL_MASK, ctx, src);
-      row0 = __shfl_sync(DC_FULL_MASK, row0, src);
-      len = __shfl_sync(DC_FULL_MASK, len, src);
-      const Side a(p, blockIdx.y >> 1, blockIdx.y & 1);
-      const int pos = max(ctx, ((ctx >> p.scale_shift) + rel) << p.scale_shift);
-      const uint16_t *rows = a.fresh + (int64_t)(row0 + pos - ctx) * a.st + h * a.sh;
-      bad |= write_at<D, F16, kAppendSteps>(p, a, n0 + src, h, pos, ctx + len, [&](int i) { return rows + i * a.st; });
-      if (!first_warp) break;
+    all = __shfl_sync(DC_FULL_MASK, upto, 31);
+  }
+  // Block b of theirs (of the requests from n0 on), head h.  -> error bits
+  template <int D, bool F16>
+  __device__ __forceinline__ int write(const QuantWriteParams &p, int n0, int b, int h) const {
+    const int src = __ffs(__ballot_sync(DC_FULL_MASK, upto > b)) - 1;
+    const int rel = b - __shfl_sync(DC_FULL_MASK, upto - blocks, src);
+    const int c = __shfl_sync(DC_FULL_MASK, ctx, src), r = __shfl_sync(DC_FULL_MASK, row0, src);
+    const int end = c + __shfl_sync(DC_FULL_MASK, len, src);
+    const Side a(p, blockIdx.y >> 1, blockIdx.y & 1);
+    const int pos = max(c, ((c >> p.scale_shift) + rel) << p.scale_shift);
+    const uint16_t *rows = a.fresh + (int64_t)(r + pos - c) * a.st + h * a.sh;
+    return write_at<D, F16, kAppendSteps>(p, a, n0 + src, h, pos, end, [&](int i) { return rows + i * a.st; });
+  }
+};
+
+// A warp a block of tokens and head; blockIdx.y: the layer's K or V.
+// (64 registers a thread: the 80 that it would take leave three blocks an SM; 187 us where 138.)
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 4) k_quant_append(const QuantWriteParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), covered = append_blocks(p);
+  const int h = (int)(u % p.kv_heads);
+  const int64_t b = u / p.kv_heads;  // block of tokens, over all requests
+  const bool first_warp = u == 0 && blockIdx.y == 0;
+  int64_t base = 0;                  // blocks of the requests before n0
+  int bad = 0;
+  for (int n0 = 0; n0 < p.N; n0 += 32) {
+    const AppendLanes w(p, n0 + lane);
+    if (w.bad) bad |= kErrBadLength;
+    if (first_warp && n0 + lane < p.N) p.new_len[n0 + lane] = w.ctx + w.len;
+    if (b >= base && b < base + w.all && b < covered) {
+      bad |= w.write<D, F16>(p, n0, (int)(b - base), h);
+      if (!first_warp && b >= kTailBlocks) break;
     }
-    b -= all;
-    if (b < 0 && !first_warp) break;
+    base += w.all;
+  }
+  // Where rows go back (first decreases), requests may share rows and have more blocks than
+  // the grid: what lies past it is taken by the warps of the first few, which have seen them all.
+  const int tail = (int)min(covered, (int64_t)kTailBlocks);
+  if (b < tail && base > covered) {
+    base = 0;
+    int64_t t = covered + b;
+    for (int n0 = 0; n0 < p.N; n0 += 32) {
+      const AppendLanes w(p, n0 + lane);
+      for (; t < base + w.all; t += tail) bad |= w.write<D, F16>(p, n0, (int)(t - base), h);
+      base += w.all;
+    }
   }
   if (bad && (first_warp || (bad & kErrBadPage))) atomicOr(p.err, bad);
 }
@@ -264,9 +295,7 @@ cudaError_t launch_quant_commit(const QuantWriteParams &p, cudaStream_t st) {
 cudaError_t launch_quant_append(const QuantWriteParams &p, cudaStream_t st) {
   const auto kernel = p.head_dim == 128 ? (p.f16 ? k_quant_append<128, true> : k_quant_append<128, false>)
                                         : (p.f16 ? k_quant_append<64, true> : k_quant_append<64, false>);
-  // a request's tokens lie in at most total / block + 2 blocks
-  const int64_t blocks = ((int64_t)p.total >> p.scale_shift) + 2ll * p.N;
-  const int64_t grid = (blocks * p.kv_heads + kWarps - 1) / kWarps;
+  const int64_t grid = (append_blocks(p) * p.kv_heads + kWarps - 1) / kWarps;
   kernel<<<dim3((unsigned)grid, p.layers * 2), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }

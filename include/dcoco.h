@@ -539,12 +539,13 @@ typedef struct {
 /* Append prompts, or pieces of them: request n's rows go to cache positions
  * ctx_len[n] .. of every layer.  Any number of tokens (max_tree does not matter).
  *   new_len: int32 [batch], ctx_len + the request's rows; not ctx_len itself (EINVAL)
- * The rows follow from one another: first does not decrease and stays within
- * 0..tokens.  A request whose rows or lengths do not (or would not fit its page
- * table) is left out, new_len = ctx_len (clamped), and recorded in the status word, as is a
- * page outside the pool, whose tokens are not written.  No page that is written may
- * belong to two requests (full pages may: dcoco_pages_fork).  One launch.  Errors: as dcoco_tree_commit; tokens < 0: EINVAL;
- * layers outside 1..32767: EINVAL. */
+ * A request's rows and lengths lie in 0..tokens and fit its page table, and its rows end
+ * no earlier than they begin.  One of which that is not so is left out, new_len = ctx_len
+ * (clamped), and recorded in the status word, as is a page outside the pool, whose tokens are not
+ * written.  first is meant to grow; where it goes back, requests may share rows, and all that are
+ * not left out are written, more slowly beyond the `tokens` rows that there are.  No page that is
+ * written may belong to two requests (full pages may: dcoco_pages_fork).  One launch.  Errors: as
+ * dcoco_tree_commit; tokens < 0: EINVAL; layers outside 1..32767: EINVAL. */
 int dcoco_tree_append_quant(dcoco_tree_handle *h, int batch, const dcoco_tree_append_args *in,
                             const dcoco_quant_scales *scales, int32_t *new_len, void *stream);
 

@@ -651,6 +651,33 @@ def test_append_flags(env):
         c.check()
 
 
+@pytest.mark.parametrize("first", [[0, 4000, 0, 4000], [0, 700] * 20 + [0], [0, 3000, 3000, 10, 2900, 5, 3000], [0, 20, 0, 20, 0, 20, 0, 20]])
+def test_append_rows_that_go_back(env, first):
+    """A request whose rows end before they begin is left out; all others are written to their last token, also where
+    requests share rows and have more of them together than there are."""
+    torch, dc = env
+    rng = np.random.default_rng(len(first))
+    N, D, page = len(first) - 1, 64, 16
+    total = max(first)
+    width = -(-(total + 20) // page)
+    ctx = rng.integers(0, 20, N)
+    table = rng.permutation(N * width).reshape(N, width).astype(np.int32)
+    new = [fresh(torch, rng, 2, total, 1, D).bfloat16().cuda() for _ in "kv"]
+    c = Cache(torch, rng, 2, N * width, page, 1, D, page, False)
+    v = dc.QuantTreeVerifier(1, 1, D, page, width, max_batch=N, max_tree=1, scale_tokens=page)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+    got = v.append(i32(first), *new, **c.gpu, page_table=i32(table), ctx_len=i32(ctx)).tolist()
+    assert v.status() == dc.DCOCO_EDEVICE
+    rows = [f64(x) for x in new]
+    for n in range(N):
+        count = max(0, first[n + 1] - first[n])
+        assert got[n] == ctx[n] + count
+        for layer in range(2):
+            for name, x in zip("kv", rows):
+                c.write(name, layer, page, table[n], int(ctx[n]), x[layer, first[n]:first[n] + count])
+    c.check()
+
+
 def test_write_refusals(env):
     torch, dc = env
     v = dc.QuantTreeVerifier(1, 1, 64, 16, 2, max_batch=2, max_tree=4, scale_tokens=16)
