@@ -625,8 +625,9 @@ int dcoco_pages_compact(dcoco_pages_handle *h, const dcoco_pages_state *s, int p
                         int32_t *live, void *stream);
 
 /* As dcoco_tree_status, _launches and _destroy.  DCOCO_EDEVICE: a call named rows
- * that it could not serve, a table entry outside the pool or to a page that
- * nobody holds, or free pages ran out. */
+ * that it could not serve, a table entry that it followed was outside the pool or to a page that
+ * nobody holds (such an entry stays, and goes to the copy of a fork, as it is, and no
+ * count changes), or free pages ran out.  To a fork a page that the same call gives out is held. */
 int dcoco_pages_status(dcoco_pages_handle *h);
 long long dcoco_pages_launches(const dcoco_pages_handle *h);
 void dcoco_pages_destroy(dcoco_pages_handle *h);

@@ -917,6 +917,33 @@ def test_pool_flags_bad_state(env):
     assert int(p.refs[int(keep[1, 2])]) == 1
 
 
+def test_pool_flags_entries_nobody_holds(env):
+    """An entry to a page that nobody holds is recorded, wherever the page lies, and left as it is."""
+    torch, dc = env
+    for page in (1, 15):  # below the pages in use after compaction, above
+        w = Watched(env, 20, 16, 4, 4)
+        p = w.pool
+        assert p.reserve(w.i32([0, 1, 2]), w.i32([64, 64, 48])).tolist() == [1, 1, 1]
+        p.lens.copy_(w.i32([64, 64, 40, 0]))
+        p.free(w.i32([0]))
+        assert p.status() == dc.DCOCO_OK and p.refs.tolist() == [0] * 4 + [1] * 7 + [0] * 9
+        held = p.table[1, 1].item()
+        p.table[1, 1] = page
+        assert int(p.compact()) == 7 and p.status() == dc.DCOCO_EDEVICE and int(p.table[1, 1]) == page
+        assert p.compact().tolist() == [7]  # the other entries are in order
+        assert p.table[2, :3].tolist() == [1, 2, 3] and p.refs.tolist() == [1] * 7 + [0] * 13 and held == 5
+    # a fork: of a full page, and of the one filled in part
+    for row, at in ((0, 1), (0, 2)):
+        w = Watched(env, 20, 16, 4, 4)
+        p = w.pool
+        assert p.reserve(w.i32([0]), w.i32([40])).tolist() == [1]
+        p.lens[0] = 40
+        p.table[row, at] = 17
+        assert p.fork(w.i32([0]), w.i32([1])).tolist() == [1] and p.status() == dc.DCOCO_EDEVICE
+        assert int(p.refs[17]) == 0
+        assert p.refs[:5].tolist() == ([2, 1, 1, 1, 0] if at == 1 else [2, 2, 1, 1, 0])
+
+
 def test_pool_refusals(env):
     torch, dc = env
     w = Watched(env, 8, 16, 4, 4)
