@@ -657,10 +657,17 @@ def _planes_for(handle, planes) -> tuple:
     return planes.count, planes.packed
 
 
+def _row_list(rows, name: str) -> tuple:
+    """The shape of a list of rows: one axis."""
+    if rows.dim() != 1:
+        raise ValueError(f"{name} must have one axis")
+    return rows.shape
+
+
 def dcoco_pages_reserve(handle, rows, tokens, page_table, held, refs, *, done=None, stream=None) -> None:
     """Give each listed row pages for so many tokens.  rows, tokens and done int32 [count]; the pool's state:
     page_table int32 [max_rows, >= max_pages], held int32 [max_rows], refs int32 [num_pages]."""
-    n, i32 = rows.shape, torch.int32
+    n, i32 = _row_list(rows, "rows"), torch.int32
     _check(_lib.dcoco_pages_reserve(handle, _pool_state(handle, page_table, held, None, refs), n[0],
                                     _dense(rows, "rows", n, i32), _dense(tokens, "tokens", n, i32),
                                     _dense_or_none(done, "done", n, i32), _stream(stream)), "dcoco_pages_reserve")
@@ -669,7 +676,7 @@ def dcoco_pages_reserve(handle, rows, tokens, page_table, held, refs, *, done=No
 def dcoco_pages_fork(handle, planes, src, dst, page_table, held, lens, refs, *, done=None, stream=None) -> None:
     """Rows dst become copies of rows src (int32 [count]): full pages shared, the partly filled one copied in all
     planes.  lens int32 [max_rows]: the rows' tokens."""
-    n, i32 = src.shape, torch.int32
+    n, i32 = _row_list(src, "src"), torch.int32
     _check(_lib.dcoco_pages_fork(handle, _pool_state(handle, page_table, held, lens, refs), *_planes_for(handle, planes),
                                  n[0], _dense(src, "src", n, i32), _dense(dst, "dst", n, i32),
                                  _dense_or_none(done, "done", n, i32), _stream(stream)), "dcoco_pages_fork")
@@ -677,8 +684,9 @@ def dcoco_pages_fork(handle, planes, src, dst, page_table, held, lens, refs, *, 
 
 def dcoco_pages_free(handle, rows, page_table, held, lens, refs, *, stream=None) -> None:
     """The listed rows (int32 [count]) hold nothing any more."""
-    _check(_lib.dcoco_pages_free(handle, _pool_state(handle, page_table, held, lens, refs), rows.shape[0],
-                                 _dense(rows, "rows", rows.shape, torch.int32), _stream(stream)), "dcoco_pages_free")
+    n = _row_list(rows, "rows")
+    _check(_lib.dcoco_pages_free(handle, _pool_state(handle, page_table, held, lens, refs), n[0],
+                                 _dense(rows, "rows", n, torch.int32), _stream(stream)), "dcoco_pages_free")
 
 
 def dcoco_pages_compact(handle, planes, page_table, held, refs, *, live, page_table_out=None, refs_out=None,

@@ -158,3 +158,15 @@ int main() {
     tail = src[src.index("if (s_abort && warp == G::kPrepWarp"):src.index("tmem_dealloc(tmem, G::kTmem)")]
     for ring in ("q_full", "factors", "k_full", "v_full"):
         assert f"mbar_drain(smem_u32(&b.{ring}[i]), parity)" in tail
+
+
+def test_lists_of_rows_have_one_axis(dc):
+    import torch
+    h = dc._PagesHandle()
+    h.sizes = (8, 4, 4)
+    x = torch.zeros(2, 2, dtype=torch.int32)
+    for rows in (x, x[0, 0]):
+        for call in (lambda: dc.dcoco_pages_free(h, rows, x, x, x, x), lambda: dc.dcoco_pages_reserve(h, rows, rows, x, x, x),
+                     lambda: dc.dcoco_pages_fork(h, None, rows, rows, x, x, x, x)):
+            with pytest.raises(ValueError, match="one axis"):
+                call()

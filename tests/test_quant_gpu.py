@@ -977,6 +977,18 @@ def test_pool_refusals(env):
     assert p.reserve(w.i32([]), w.i32([])).tolist() == [] and dc.dcoco_pages_launches(p.handle) == 0
 
 
+def test_pool_lists_have_one_axis(env):
+    """A list of rows of another shape is refused, not cut off."""
+    torch, dc = env
+    w = Watched(env, 8, 16, 4, 4)
+    p, two = w.pool, w.i32([0, 1, 2, 3]).view(2, 2)
+    for rows in (two, two[0, 0]):
+        for call in (lambda: p.free(rows), lambda: p.reserve(rows, rows), lambda: p.fork(rows, rows)):
+            with pytest.raises(ValueError):
+                call()
+    assert dc.dcoco_pages_launches(p.handle) == 0 and p.status() == dc.DCOCO_OK
+
+
 def test_pool_out_of_place(env):
     """Compaction into other arrays leaves the state as it was, but for the pages' content."""
     torch, dc = env
