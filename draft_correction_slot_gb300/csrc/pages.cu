@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kPlan) k_pages_fork_plan(const Pool q, const W
     bool ok = false;
     if (i < count) {
       const int a = src[i], b = dst[i];
-      // the row forked into is empty, named once, and no fork's source
+      // the row forked into is empty and named once, and the source is not forked into
       ok = a >= 0 && a < q.max_rows && b >= 0 && b < q.max_rows && w.claim[b] == i && w.claim[a] == kNoRow && q.held[b] == 0;
       if (ok) {
         const int n = q.len[a], held = q.held[a];

@@ -605,9 +605,9 @@ int dcoco_pages_reserve(dcoco_pages_handle *h, const dcoco_pages_state *s, int c
  * fill in part.  Pages that src holds past its tokens are its own.  dst rows hold
  * nothing before (free them first); a row may be the source of many.
  *   done: as above
- * A fork gets nothing where dst[i] holds pages, is named before or is a source in
- * the same call, where a row is out of range, and where free pages run out (in
- * the list's order); recorded in the status word. */
+ * A fork gets nothing where dst[i] holds pages or is named before, where src[i] is
+ * forked into in the same call (whether that is served or not), where a row is out of range, and
+ * where free pages run out (in the list's order); recorded in the status word. */
 int dcoco_pages_fork(dcoco_pages_handle *h, const dcoco_pages_state *s, int planes_count, const dcoco_page_plane *planes,
                      int count, const int32_t *src, const int32_t *dst, int32_t *done, void *stream);
 

@@ -989,6 +989,24 @@ def test_pool_lists_have_one_axis(env):
     assert dc.dcoco_pages_launches(p.handle) == 0 and p.status() == dc.DCOCO_OK
 
 
+def test_pool_forks_in_a_row(env):
+    """A row cannot be forked into and be a source in one call: the fork into it is served, the one from it is not."""
+    torch, dc = env
+    w = Watched(env, 20, 16, 4, 4)
+    w.pool.reserve(w.i32([0]), w.i32([40]))
+    w.ref.reserve([0], [40])
+    w.set_len(0, 40)
+    for order in ([0, 1], [1, 0]):
+        src, dst = np.array([0, 1])[order].tolist(), np.array([1, 2])[order].tolist()
+        want = [int(a == 0) for a in src]
+        assert w.ref.fork(src, dst) == want and w.pool.fork(w.i32(src), w.i32(dst)).tolist() == want
+        assert w.pool.status() == dc.DCOCO_EDEVICE
+        w.check()
+        w.ref.free([1])
+        w.pool.free(w.i32([1]))
+        w.check()
+
+
 def test_pool_out_of_place(env):
     """Compaction into other arrays leaves the state as it was, but for the pages' content."""
     torch, dc = env
