@@ -10,9 +10,10 @@
 // The plan is a scan over the counts, 16 KB a step of 1024 threads; a fork stops
 // as soon as it has enough free pages.  The copy is bound by HBM: a warp moves
 // 4 KB a step, all its loads in flight before the first store.  2000 of 8001 pages of 263
-// KB (K, V, scales of 8 layers) compacted: 132 us, 8.0 TB/s with what stays in L2; 48
-// of 64 rows freed and forked anew, 33 KB a copied page and layer: 25 us, of which the
-// calls' host part and three dependent launches are 17.
+// KB (K, V, scales of 8 layers) compacted: 134 us, 7.8 TB/s with what stays in L2; 48
+// of 64 rows freed and forked anew, 33 KB a copied page and layer: 24 us, of which the
+// calls' host part and three dependent launches are 17.  48 rows reserve a page each among 8200: 6 us; among
+// 2^20, all held but the last: 220 us, the scan.
 #include <cuda_runtime.h>
 
 #include <new>

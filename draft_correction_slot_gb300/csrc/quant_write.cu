@@ -12,10 +12,10 @@
 // between the maximum and the rounding; longer blocks are read again (from L1 or L2).
 // Nothing is shared between warps, so a request's result depends on its own
 // tokens alone.
-// Append: 8 prompts of up to 2000 tokens, 16 layers x 8 heads of 64, blocks of 64: 127 us,
-// 3.8 TB/s of the 6.8 that a copy reaches; bound by the chain lengths, page, tokens, maximum, rounding
-// of each warp.  Commit: 32 trees of 64 nodes, 16 layers: 17 us with its call, bound
-// by latency as tree_commit.cu's.
+// Append: 8 prompts of up to 2000 tokens, 16 layers x 8 heads of 64, blocks of 64: 138 us (132 to
+// 174 by the draw of the lengths), 3.5 TB/s of the 6.8 that a copy reaches; bound by the chain lengths,
+// page, tokens, maximum, rounding of each warp.  Commit: 32 trees of 64 nodes, 16 layers: 18 us with
+// its call, bound by latency as tree_commit.cu's.
 #include "kernels.h"
 #include "quant.cuh"
 
@@ -25,7 +25,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxNodes = 256;
 constexpr int kTailBlocks = 8;  // see k_quant_append
-constexpr int kAppendSteps = 4;  // 8 prompts of up to 2000 tokens: 127 us; 140 with 8 steps, 200 with 16 (fewer warps an SM)
+constexpr int kAppendSteps = 4;  // 8 prompts of up to 2000 tokens, mean of six draws: 156 us; 175 with 8 steps, 220 with 16 (fewer warps an SM)
 
 template <bool F16>
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
@@ -95,7 +95,7 @@ __device__ __forceinline__ void write_block(int old, int count, Row row, uint8_t
     }
   }
   // A power of two (any scale that was made here) is divided by exactly by its inverse; divisions
-  // of 8 elements took as long as all the rest (8 prompts of up to 2000 tokens: 183 us with them).
+  // of 8 elements took as long as all the rest (8 prompts of up to 2000 tokens: 183 us with them, 169 without).
   const bool power = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
   const float inv = power ? 1.f / s : 1.f;
   const bool kept = count <= step * kSteps;

@@ -108,6 +108,11 @@ int most_chunks(int64_t max_tiles, int items, int sms, int cap) {
 // 16 nodes, 64 rows, to 8000 tokens: 139 / 139 / 136 / 147 / 129 / 129 us; 8 x 64, five tiles of 64
 // rows, to 32000: 581 / 553 / 538 / 539 / 534 / 545 us; 48 x 1, 4 rows, to 24001: 327 / 306 / 297 / 291
 // / 278 / 280 us.
+//
+// The handle's batch counts here too, and long chunks make its price higher than the other
+// cap's: 8 K/V heads of 128, in a graph, on a handle for 32 against one for the call's requests (and the
+// cache in 16 bits on a handle for 32): one request of 8000 tokens x 1 node x 4 heads 50 us (38; 30), x 16
+// nodes 103 (34; 35), x 64 x 5 108 (67; 89); four requests: 51 (44; 37), 103 (60; 39), 185 (186; 99).
 int quant_chunk_cap(const dcoco_tree_config &c) { return c.max_batch == 1 ? 1 << 30 : 64; }
 int most_quant_chunks(int64_t max_tiles, int items, int sms, int cap) {
   const int64_t scan = max_tiles < 64 * dc::kTreeMaxChunks ? max_tiles : 64 * dc::kTreeMaxChunks;

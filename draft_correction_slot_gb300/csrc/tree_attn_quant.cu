@@ -38,15 +38,17 @@
 // lane); 64 rows take all four, 32 or 16 rows two or one, and the groups then
 // are teams that take the tiles in turn, each with references, sums and O of its own.
 // (Two groups of 32 rows a thread, with twice the registers: 669 us for 8 x 64 at 32000 where
-// four took 528.  The next tile's scores fetched under this one's exponentials: 542 for
-// 484, registers spilled.)
+// four took 528 on the same lengths.  The next tile's scores fetched under this one's
+// exponentials: 542 for 484, registers spilled.)
 //
 // Every other role has a warp, so that each one's chain of waits and issues (200 cycles
 // a wait, 60 a product or copy) runs beside the others': with S and O issued by one
 // warp, that warp took 2050 cycles a tile of 16 rows.  A tile of 32 KB is due every 1400 cycles at
-// HBM's rate.  It takes 1750 for 4 rows (48 requests of up to 24001 tokens: 271 us, 5.0 TB/s), where the
-// loading warp is what bounds it, and 2700 for 64 rows (32 x 16 to 8000: 128 us; 8 x 64 to 32000: 534 us;
-// means of six draws of the lengths), where the softmax chain does: wait, scores, vote, exponentials and parts, store.
+// HBM's rate.  It takes 1750 for 4 rows (48 requests of up to 24001 tokens: 288 us, 260 to 299), where the
+// loading warp is what bounds it, and 2700 for 64 rows (32 x 16 to 8000: 133 us, 123 to 138; 8 x 64 to 32000: 536
+// us, 457 to 589; mean and range of six draws of the lengths, L2 flushed before each call), where the softmax
+// chain does: wait, scores, vote, exponentials and parts, store.  For 32 x 16 that is some 85 us of
+// the kernel's 125; units' borders, the trees' units and the blocks' uneven ends are the rest.
 //
 // Roles: warps 0-15 softmax and output, 16 the products S, 17 the products O, 18
 // TMA for K and V and the scales, 19 the list of the block's units and their Q.  A

@@ -492,7 +492,9 @@ int dcoco_tree_create_quant(const dcoco_tree_config *cfg, int scale_tokens, dcoc
 /* dcoco_tree_attention with k_cache and v_cache in 8 bits; their strides are
  * multiples of 16 (elements, one byte each).  K's scales outside 2^-100 .. 2^100 and
  * V's outside 2^-80 .. 2^80 may lose their tokens' part in lse and out; within, scales
- * of one request may differ as they like.  All else as there, but for the
+ * of one request may differ as they like.  Faster than dcoco_tree_attention where a K/V head
+ * has few rows (nodes x heads of its group) and contexts are long; from some 64 rows on, on
+ * short contexts, and for calls much smaller than their handle it is not.  All else as there, but for the
  * roundings: in out a context token's weight is off by up to 2^-11 of itself, or 2^-31 of
  * the row's largest product of weight and V scale where that is more (lse has fp32 weights); a
  * node's is rounded to the handle's type; q's elements keep 2^-17 of their row's largest.
